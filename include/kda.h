@@ -336,6 +336,125 @@ kda_status kda_combine_pairs(const float* M, const float* S_tilde, int n_pairs, 
                              int n_seq, int H, int d, cudaStream_t stream);
 
 /*
+ * Attention cache.  No counterpart on the pages: a hybrid stack runs its delta-rule layers
+ * next to layers of softmax attention, and these entry points keep the latter's keys and
+ * values in pages and attend over them.  128 channels a head; H query heads share
+ * n_kv_heads key/value heads (query head h reads head h / (H / n_kv_heads)).
+ *
+ * The cache of one layer (all pointers device memory, the struct itself host memory):
+ *   k, v          pages of keys / values, logically [n_pages][n_kv_heads][page_size][128];
+ *                 *_stride are the element strides of the first three dimensions (the last is
+ *                 contiguous), so pages may hold tokens or heads outermost and k and v may be
+ *                 interleaved in one allocation.  Bases 16-byte aligned, strides positive
+ *                 multiples of 16 bytes (a dimension of extent 1 too).
+ *   page_size     16, 32, 64 or 128 tokens
+ *   dtype         KDA_KV_BF16: the rows as they are, no scales.
+ *                 KDA_KV_E4M3: 8-bit floats with one power-of-two scale per row (token and
+ *                 head): the row's values are code * 2^(byte - 127); byte 255 marks a row of NaN.
+ *   k_scale, v_scale  E4M3 only: scale bytes, logically [n_pages][n_kv_heads][page_size], with
+ *                 strides *_scale_stride of the first two dimensions (positive multiples of
+ *                 16; the last contiguous), bases 16-byte aligned.
+ * Page tables are device int32 [n_seq][max_pages], row i the pages of sequence i in order:
+ * token j of the sequence is slot j % page_size of page table[i][j / page_size].
+ */
+typedef enum { KDA_KV_BF16 = 0, KDA_KV_E4M3 = 1 } kda_kv_dtype;
+#define KDA_KV_SCALE_MIN_EXP (-40)
+#define KDA_KV_SCALE_MAX_EXP 40
+typedef struct {
+  void* k;
+  void* v;
+  uint8_t* k_scale;
+  uint8_t* v_scale;
+  int64_t k_stride[3];
+  int64_t v_stride[3];
+  int64_t k_scale_stride[2];
+  int64_t v_scale_stride[2];
+  int64_t n_pages;
+  int n_kv_heads;
+  int page_size;
+  int dtype;
+} kda_kv_cache;
+
+/*
+ * kda_kv_append -- write new tokens' keys and values into their pages (quantising them for an
+ * E4M3 cache).
+ *
+ *   k, v        [total_tokens, n_kv_heads, d] bf16, packed over sequences; element strides of
+ *               the first two dimensions in k_stride / v_stride (host arrays of 2; positive
+ *               multiples of 8; rows of a fused projection may be passed as they lie)
+ *   cu_seqlens  [n_seq + 1] int32: sequence i owns rows [cu[i], cu[i+1])
+ *   kv_start    [n_seq] int32: tokens already in the cache; row cu[i] + t becomes token
+ *               kv_start[i] + t of sequence i
+ * E4M3: a row's scale is 2^e with the smallest whole e in [KDA_KV_SCALE_MIN_EXP,
+ * KDA_KV_SCALE_MAX_EXP] that has max|x| <= 448 * 2^e, its codes are x / 2^e (exact) rounded to
+ * the nearest e4m3, ties to even.  A row holding a NaN, an infinity or a value above
+ * 448 * 2^KDA_KV_SCALE_MAX_EXP becomes a row of NaN: byte 255, codes 0.
+ * A table entry -1 leaves its tokens unwritten.  Another entry outside [0, n_pages), a position
+ * beyond the table, a negative kv_start or offsets that run backwards: KDA_ERR_DEVICE_CHECK,
+ * the row is skipped.  Two rows with the same destination: either one may remain.
+ */
+kda_status kda_kv_append(const kda_kv_cache* cache, const kda_bf16* k, const int64_t* k_stride, const kda_bf16* v,
+                         const int64_t* v_stride, const int32_t* page_table, int n_seq, int max_pages,
+                         const int32_t* cu_seqlens, const int32_t* kv_start, int64_t total_tokens, int d,
+                         int* dev_status, cudaStream_t stream);
+
+/*
+ * kda_kv_read -- the inverse: tokens kv_start[i] .. kv_start[i] + (cu[i+1] - cu[i]) of each
+ * sequence from the pages into packed rows k, v [total_tokens, n_kv_heads, d] bf16
+ * (contiguous).  E4M3 values are exact in bf16; a row of NaN reads as NaN.  Any page outside
+ * [0, n_pages), -1 included: KDA_ERR_DEVICE_CHECK, the row is left unwritten.
+ */
+kda_status kda_kv_read(const kda_kv_cache* cache, kda_bf16* k, kda_bf16* v, const int32_t* page_table, int n_seq,
+                       int max_pages, const int32_t* cu_seqlens, const int32_t* kv_start, int64_t total_tokens, int d,
+                       int* dev_status, cudaStream_t stream);
+
+/*
+ * kda_attn_prefill_paged -- causal attention of a chunk of new tokens over the paged cache
+ * (their own keys and values are in it already: kda_kv_append first).
+ *
+ *   q           [total_tokens, H, d] bf16 packed over sequences; element strides of the first
+ *               two dimensions in q_stride (host array of 2, positive multiples of 8)
+ *   cu_seqlens  [n_seq + 1] int32; sequence i has n_i = cu[i+1] - cu[i] >= 0 new tokens
+ *   kv_len      [n_seq] int32: tokens in the cache, the new ones included; new token t of
+ *               sequence i stands at position p = kv_len[i] - n_i + t
+ *   scale       softmax scale on q . k, finite
+ *   window      0: token p sees keys 0 .. p.  w > 0: it sees keys j with p - w < j <= p, and
+ *   n_sink      the first n_sink tokens (j < n_sink, j <= p) besides
+ *   o           [total_tokens, H, d] bf16: sum_j softmax(scale q . k_j)_j v_j over the visible
+ *               keys (sums and statistics in fp32)
+ *   lse         [total_tokens, H] fp32 or NULL: log sum_j exp(scale q . k_j)
+ * A row that sees nothing (p < 0) gets o = 0 and lse = -inf.  Keys that a row does not see
+ * never reach its result, whatever they hold; a NaN or infinity in the value row of a key
+ * that it sees makes the row non-finite.
+ * Only pages with visible keys are read.  One outside [0, n_pages), a kv_len outside
+ * [0, max_pages * page_size] or offsets that run backwards: KDA_ERR_DEVICE_CHECK; the rows
+ * concerned are undefined (of a bad kv_len or offsets: unwritten).
+ *   workspace   kda_attn_prefill_workspace_size(...) bytes, 256-byte aligned; its contents
+ *               need no preparation and mean nothing between calls
+ * Long rows of keys are split over the GPU and joined in a fixed order: a call gives the same
+ * bits each time, but a sequence's last bits may depend on what else is in the batch.
+ */
+size_t kda_attn_prefill_workspace_size(int n_seq, int64_t total_tokens, int H, int n_kv_heads, int d);
+kda_status kda_attn_prefill_paged(const kda_bf16* q, const int64_t* q_stride, const kda_kv_cache* cache,
+                                  const int32_t* page_table, int n_seq, int max_pages, const int32_t* cu_seqlens,
+                                  const int32_t* kv_len, int64_t total_tokens, int H, int d, float scale, int window,
+                                  int n_sink, kda_bf16* o, float* lse, void* workspace, size_t workspace_bytes,
+                                  int* dev_status, cudaStream_t stream);
+
+/*
+ * kda_attn_decode_paged -- the same for a decode (n_tok = 1) or verify (n_tok <= 4) step.
+ *   q, o        [B, n_tok, H, d] bf16 (q_stride: element strides of the first three dimensions)
+ *   lse         [B, n_tok, H] fp32 or NULL
+ *   kv_len      [B] int32, the step's tokens included; 0 (an idle slot) gives o = 0
+ * Every other argument and the errors are those of kda_attn_prefill_paged.
+ */
+size_t kda_attn_decode_workspace_size(int B, int n_tok, int H, int n_kv_heads, int d);
+kda_status kda_attn_decode_paged(const kda_bf16* q, const int64_t* q_stride, const kda_kv_cache* cache,
+                                 const int32_t* page_table, int B, int n_tok, int max_pages, const int32_t* kv_len,
+                                 int H, int d, float scale, int window, int n_sink, kda_bf16* o, float* lse,
+                                 void* workspace, size_t workspace_bytes, int* dev_status, cudaStream_t stream);
+
+/*
  * kda_debug_stall_next_prefill -- test hook for the bounded waits (no counterpart on the
  * pages).  The next prefill launch of this process runs a test instance of the kernel
  * whose prep warps withhold their first hand-off of chunk `chunk` (counted within each

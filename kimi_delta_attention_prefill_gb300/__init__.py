@@ -10,8 +10,10 @@ Functions mirror the C entry points: :func:`prefill` (``kda_prefill``, or
 :func:`decode` (``kda_decode``), :func:`decode_paged` (``kda_decode_paged``),
 :func:`decode_fused` (``kda_decode_fused``), :func:`prefill_pairs` (``kda_prefill_pairs``),
 :func:`combine_pairs` (``kda_combine_pairs``), :func:`prefill_noalloc`
-(``kda_prefill_noalloc``), the workspace-size queries, and :func:`status_string`
-(``kda_status_string``).  The cross-device split's exchange is in :mod:`.kcp`.  Tensors are torch CUDA tensors (pinned
+(``kda_prefill_noalloc``), the attention cache's :func:`kv_append` (``kda_kv_append``),
+:func:`kv_read` (``kda_kv_read``), :func:`attn_prefill_paged` (``kda_attn_prefill_paged``) and
+:func:`attn_decode_paged` (``kda_attn_decode_paged``), the workspace-size queries, and
+:func:`status_string` (``kda_status_string``).  The cross-device split's exchange is in :mod:`.kcp`.  Tensors are torch CUDA tensors (pinned
 host tensors for :func:`prefill_host`); the launch goes to the current torch stream
 unless ``stream`` is given.
 """
@@ -33,6 +35,12 @@ _lib = None
 _lock = threading.Lock()
 
 _c_int, _c_i64, _c_sz, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
+
+
+class _KvCache(ctypes.Structure):  # kda_kv_cache
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("k_stride", _c_i64 * 3),
+                ("v_stride", _c_i64 * 3), ("k_scale_stride", _c_i64 * 2), ("v_scale_stride", _c_i64 * 2),
+                ("n_pages", _c_i64), ("n_kv_heads", _c_int), ("page_size", _c_int), ("dtype", _c_int)]
 
 
 class KdaLibraryError(RuntimeError):
@@ -103,6 +111,24 @@ def library():
             lib.kda_prefill_noalloc.restype = _c_int
             lib.kda_prefill_noalloc.argtypes = ([_vp] * 7 + [_c_int, _c_i64] + [_vp, _vp, _c_i64] + [_vp] * 3 +
                                                 [_c_int, _c_int, _c_int, _vp, _vp])
+            cache = ctypes.POINTER(_KvCache)
+            strides = ctypes.POINTER(_c_i64)
+            lib.kda_kv_append.restype = _c_int
+            lib.kda_kv_append.argtypes = [cache, _vp, strides, _vp, strides, _vp, _c_int, _c_int, _vp, _vp, _c_i64,
+                                          _c_int, _vp, _vp]
+            lib.kda_kv_read.restype = _c_int
+            lib.kda_kv_read.argtypes = [cache, _vp, _vp, _vp, _c_int, _c_int, _vp, _vp, _c_i64, _c_int, _vp, _vp]
+            lib.kda_attn_prefill_workspace_size.restype = _c_sz
+            lib.kda_attn_prefill_workspace_size.argtypes = [_c_int, _c_i64, _c_int, _c_int, _c_int]
+            lib.kda_attn_prefill_paged.restype = _c_int
+            lib.kda_attn_prefill_paged.argtypes = ([_vp, strides, cache, _vp, _c_int, _c_int, _vp, _vp, _c_i64, _c_int,
+                                                    _c_int, ctypes.c_float, _c_int, _c_int] +
+                                                   [_vp, _vp, _vp, _c_sz, _vp, _vp])
+            lib.kda_attn_decode_workspace_size.restype = _c_sz
+            lib.kda_attn_decode_workspace_size.argtypes = [_c_int] * 5
+            lib.kda_attn_decode_paged.restype = _c_int
+            lib.kda_attn_decode_paged.argtypes = ([_vp, strides, cache, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _c_int,
+                                                   ctypes.c_float, _c_int, _c_int] + [_vp, _vp, _vp, _c_sz, _vp, _vp])
             _lib = lib
     return _lib
 
@@ -556,3 +582,214 @@ def combine_pairs(M, S_tilde, S_in=None, entry=None, stream=None):
     if st != 0:
         raise KdaError(st, "kda_combine_pairs")
     return entry
+
+
+# ------------------------------------------------------------------------ attention cache
+def _rows_of(t, name, dtype, lead):
+    """A tensor ``lead + [128]`` whose last dimension is contiguous; the others may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    shape = tuple(lead) + (HEAD_DIM,)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t
+
+
+def _row_strides(t):
+    # torch gives dimensions of extent 1 any stride; the library wants a sound one
+    packed = [1] * t.dim()
+    for i in range(t.dim() - 2, -1, -1):
+        packed[i] = packed[i + 1] * max(t.shape[i + 1], 1)
+    s = [t.stride(i) if t.shape[i] > 1 else packed[i] for i in range(t.dim() - 1)]
+    return (_c_i64 * len(s))(*s)
+
+
+def _kv_cache(k_pool, v_pool, k_scale, v_scale):
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+        raise ValueError("k_pool must be a tensor [n_pages, n_kv_heads, page_size, 128]")
+    if k_pool.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise TypeError(f"k_pool must be torch.bfloat16 or torch.float8_e4m3fn, got {k_pool.dtype}")
+    lead = tuple(k_pool.shape[:3])
+    _rows_of(k_pool, "k_pool", k_pool.dtype, lead)
+    _rows_of(v_pool, "v_pool", k_pool.dtype, lead)
+    c = _KvCache(k=_ptr(k_pool), v=_ptr(v_pool), k_stride=_row_strides(k_pool), v_stride=_row_strides(v_pool),
+                 n_pages=lead[0], n_kv_heads=lead[1], page_size=lead[2], dtype=0)
+    if k_pool.dtype == torch.float8_e4m3fn:
+        c.dtype = 1
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t is None:
+                raise ValueError(f"{name} is required for a float8_e4m3fn cache")
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if not t.is_cuda:
+                raise ValueError(f"{name} must be a CUDA tensor")
+            if t.dtype != torch.uint8:
+                raise TypeError(f"{name} must be torch.uint8, got {t.dtype}")
+            if tuple(t.shape) != lead:
+                raise ValueError(f"{name} must have shape {lead}, got {tuple(t.shape)}")
+            if t.numel() and t.stride(-1) != 1:
+                raise ValueError(f"{name} must be contiguous in its last dimension")
+            setattr(c, name, _ptr(t))
+            setattr(c, name + "_stride", _row_strides(t))
+    elif k_scale is not None or v_scale is not None:
+        raise ValueError("k_scale / v_scale belong to a float8_e4m3fn cache")
+    return c
+
+
+def _page_table(page_table):
+    _need(page_table, "page_table", torch.int32)
+    if page_table.dim() != 2:
+        raise ValueError(f"page_table must have shape [sequences, pages], got {tuple(page_table.shape)}")
+    return tuple(page_table.shape)
+
+
+def kv_append(k, v, k_pool, v_pool, page_table, cu_seqlens, kv_start, k_scale=None, v_scale=None, dev_status=None,
+              stream=None):
+    """Write new tokens' keys and values into the paged attention cache (``kda_kv_append``).
+
+    k, v ``[T, Hkv, 128]`` bf16, packed over sequences (token and head dimensions may be
+    strided); k_pool, v_pool ``[n_pages, Hkv, page_size, 128]`` bf16 or float8_e4m3fn (any
+    strides over the first three dimensions; page_size 16, 32, 64 or 128), with k_scale,
+    v_scale ``[n_pages, Hkv, page_size]`` uint8 for float8_e4m3fn: a row's values are
+    ``code * 2**(scale - 127)``, scale 255 marks a row of NaN.  page_table ``[N, max_pages]``
+    int32 (-1: tokens there are not written); cu_seqlens ``[N + 1]``, kv_start ``[N]`` int32:
+    row ``cu[i] + t`` becomes token ``kv_start[i] + t`` of sequence i.  Updates the pools (and
+    scales) in place.
+    """
+    c = _kv_cache(k_pool, v_pool, k_scale, v_scale)
+    n_seq, max_pages = _page_table(page_table)
+    T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
+    _rows_of(k, "k", torch.bfloat16, (T, c.n_kv_heads))
+    _rows_of(v, "v", torch.bfloat16, (T, c.n_kv_heads))
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (n_seq + 1,))
+    _need(kv_start, "kv_start", torch.int32, (n_seq,))
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32)
+    st = library().kda_kv_append(ctypes.byref(c), _ptr(k), _row_strides(k), _ptr(v), _row_strides(v),
+                                 _ptr(page_table), n_seq, max_pages, _ptr(cu_seqlens), _ptr(kv_start), T, HEAD_DIM,
+                                 _ptr(dev_status), _stream_handle(stream))
+    if st != 0:
+        raise KdaError(st, "kda_kv_append")
+
+
+def kv_read(k_pool, v_pool, page_table, cu_seqlens, kv_start, total_tokens, k_scale=None, v_scale=None, k=None, v=None,
+            dev_status=None, stream=None):
+    """Read ranges of cached tokens back as packed bf16 rows (``kda_kv_read``).
+
+    Rows ``cu[i] .. cu[i + 1]`` of the result are tokens ``kv_start[i] ..`` of sequence i;
+    ``total_tokens`` is ``cu[N]``.  The cache's arguments are those of :func:`kv_append`.
+    Returns ``(k, v)``, each ``[total_tokens, Hkv, 128]`` bf16 (float8 values are exact in bf16).
+    """
+    c = _kv_cache(k_pool, v_pool, k_scale, v_scale)
+    n_seq, max_pages = _page_table(page_table)
+    T = int(total_tokens)
+    shape = (T, c.n_kv_heads, HEAD_DIM)
+    if k is None:
+        k = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device)
+    if v is None:
+        v = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device)
+    _need(k, "k", torch.bfloat16, shape)
+    _need(v, "v", torch.bfloat16, shape)
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (n_seq + 1,))
+    _need(kv_start, "kv_start", torch.int32, (n_seq,))
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32)
+    st = library().kda_kv_read(ctypes.byref(c), _ptr(k), _ptr(v), _ptr(page_table), n_seq, max_pages, _ptr(cu_seqlens),
+                               _ptr(kv_start), T, HEAD_DIM, _ptr(dev_status), _stream_handle(stream))
+    if st != 0:
+        raise KdaError(st, "kda_kv_read")
+    return k, v
+
+
+def attn_prefill_workspace_size(n_seq, total_tokens, H, n_kv_heads, d=HEAD_DIM) -> int:
+    return int(library().kda_attn_prefill_workspace_size(int(n_seq), int(total_tokens), int(H), int(n_kv_heads), int(d)))
+
+
+def attn_decode_workspace_size(B, n_tok, H, n_kv_heads, d=HEAD_DIM) -> int:
+    return int(library().kda_attn_decode_workspace_size(int(B), int(n_tok), int(H), int(n_kv_heads), int(d)))
+
+
+def _attn_outputs(q, o, lse, return_lse):
+    if o is None:
+        o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    _need(o, "o", torch.bfloat16, q.shape)
+    if lse is None and return_lse:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    if lse is not None:
+        _need(lse, "lse", torch.float32, q.shape[:-1])
+    return o, lse
+
+
+def attn_prefill_paged(q, k_pool, v_pool, page_table, cu_seqlens, kv_len, k_scale=None, v_scale=None, scale=None,
+                       window=0, n_sink=0, o=None, lse=None, return_lse=False, workspace=None, dev_status=None,
+                       stream=None):
+    """Causal attention of a chunk of new tokens over the paged cache (``kda_attn_prefill_paged``).
+
+    q ``[T, H, 128]`` bf16, packed over sequences (token and head dimensions may be strided; H a
+    multiple of the cache's heads); the cache as in :func:`kv_append`, the new tokens already in
+    it; cu_seqlens ``[N + 1]`` int32; kv_len ``[N]`` int32 the tokens in the cache, new ones
+    included.  ``scale`` defaults to 1 / sqrt(128).  With ``window`` > 0 a token sees the last
+    ``window`` keys up to itself and the first ``n_sink`` of the sequence.  Returns o
+    ``[T, H, 128]`` bf16, or ``(o, lse)`` with ``return_lse`` or ``lse`` given (``[T, H]`` fp32).
+    """
+    c = _kv_cache(k_pool, v_pool, k_scale, v_scale)
+    n_seq, max_pages = _page_table(page_table)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a tensor [T, H, 128]")
+    T, H, _ = q.shape
+    _rows_of(q, "q", torch.bfloat16, (T, H))
+    _need(cu_seqlens, "cu_seqlens", torch.int32, (n_seq + 1,))
+    _need(kv_len, "kv_len", torch.int32, (n_seq,))
+    o, lse = _attn_outputs(q, o, lse, return_lse)
+    if workspace is None:
+        workspace = torch.empty(attn_prefill_workspace_size(n_seq, T, H, c.n_kv_heads), dtype=torch.uint8,
+                                device=q.device)
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32)
+    st = library().kda_attn_prefill_paged(_ptr(q), _row_strides(q), ctypes.byref(c), _ptr(page_table), n_seq, max_pages,
+                                          _ptr(cu_seqlens), _ptr(kv_len), T, H, HEAD_DIM,
+                                          HEAD_DIM ** -0.5 if scale is None else float(scale), int(window), int(n_sink),
+                                          _ptr(o), _ptr(lse), _ptr(workspace),
+                                          workspace.numel() * workspace.element_size(), _ptr(dev_status),
+                                          _stream_handle(stream))
+    if st != 0:
+        raise KdaError(st, "kda_attn_prefill_paged")
+    return o if lse is None else (o, lse)
+
+
+def attn_decode_paged(q, k_pool, v_pool, page_table, kv_len, k_scale=None, v_scale=None, scale=None, window=0, n_sink=0,
+                      o=None, lse=None, return_lse=False, workspace=None, dev_status=None, stream=None):
+    """:func:`attn_prefill_paged` for a decode or verify step (``kda_attn_decode_paged``): q
+    ``[B, n_tok, H, 128]`` bf16 with n_tok <= 4, the last n_tok tokens of each sequence; kv_len
+    ``[B]`` int32 includes them (0: an idle slot, o = 0).  Returns o ``[B, n_tok, H, 128]``
+    bf16, or ``(o, lse)`` with lse ``[B, n_tok, H]`` fp32.
+    """
+    c = _kv_cache(k_pool, v_pool, k_scale, v_scale)
+    n_seq, max_pages = _page_table(page_table)
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a tensor [B, n_tok, H, 128]")
+    B, n_tok, H, _ = q.shape
+    _rows_of(q, "q", torch.bfloat16, (B, n_tok, H))
+    if B != n_seq:
+        raise ValueError(f"page_table must have {B} rows, got {n_seq}")
+    _need(kv_len, "kv_len", torch.int32, (B,))
+    o, lse = _attn_outputs(q, o, lse, return_lse)
+    if workspace is None:
+        workspace = torch.empty(attn_decode_workspace_size(B, n_tok, H, c.n_kv_heads), dtype=torch.uint8,
+                                device=q.device)
+    if dev_status is not None:
+        _need(dev_status, "dev_status", torch.int32)
+    st = library().kda_attn_decode_paged(_ptr(q), _row_strides(q), ctypes.byref(c), _ptr(page_table), B, n_tok, max_pages,
+                                         _ptr(kv_len), H, HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else float(scale),
+                                         int(window), int(n_sink), _ptr(o), _ptr(lse), _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(), _ptr(dev_status),
+                                         _stream_handle(stream))
+    if st != 0:
+        raise KdaError(st, "kda_attn_decode_paged")
+    return o if lse is None else (o, lse)

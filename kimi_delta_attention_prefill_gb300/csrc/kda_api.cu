@@ -45,6 +45,10 @@ std::atomic<int> g_stall_chunk{-1};
 
 }  // namespace
 
+namespace kda {
+int current_device_status(int* sms) { return current_device(sms); }
+}  // namespace kda
+
 extern "C" {
 
 const char* kda_status_string(int status) {

@@ -1,0 +1,131 @@
+// kda_attn.h -- the attention cache's shared pieces: the cache as the kernels see it, the
+// tiles of keys that a block of query rows has to visit, and the launches.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <cstddef>
+#include <cstdint>
+
+#include "kda_internal.h"
+
+namespace kda {
+
+// One layer's cache (kda_kv_cache, checked on the host).
+struct KvCache {
+  void* k = nullptr;
+  void* v = nullptr;
+  uint8_t* ks = nullptr;  // scale bytes (e4m3 only)
+  uint8_t* vs = nullptr;
+  int64_t k_stride[3] = {0, 0, 0};  // elements: page, head, token
+  int64_t v_stride[3] = {0, 0, 0};
+  int64_t ks_stride[2] = {0, 0};  // bytes: page, head
+  int64_t vs_stride[2] = {0, 0};
+  int64_t n_pages = 0;
+  int heads = 0;
+  int page_size = 0;
+  int page_log2 = 0;
+  bool e4m3 = false;
+};
+
+struct KvRows {  // kda_kv_append / kda_kv_read
+  KvCache cache;
+  void* k = nullptr;
+  void* v = nullptr;
+  int64_t k_stride[2] = {0, 0};  // elements: token, head
+  int64_t v_stride[2] = {0, 0};
+  const int32_t* page_table = nullptr;
+  const int32_t* cu = nullptr;
+  const int32_t* start = nullptr;
+  int n_seq = 0;
+  int max_pages = 0;
+  int64_t tokens = 0;
+  int* status = nullptr;
+  cudaStream_t stream = nullptr;
+};
+cudaError_t launch_kv_append(const KvRows& a);
+cudaError_t launch_kv_read(const KvRows& a);
+
+struct AttnArgs {
+  const void* q = nullptr;
+  int64_t q_stride[3] = {0, 0, 0};  // elements: sequence (decode only), token, head
+  KvCache cache;
+  const int32_t* page_table = nullptr;
+  const int32_t* cu = nullptr;  // prefill; nullptr: decode, n_tok tokens of each sequence
+  const int32_t* kv_len = nullptr;
+  int n_seq = 0;
+  int n_tok = 0;
+  int max_pages = 0;
+  int64_t tokens = 0;
+  int H = 0;
+  float scale_log2 = 0.f;  // softmax scale in log2 units
+  int window = 0;
+  int n_sink = 0;
+  void* o = nullptr;
+  float* lse = nullptr;
+  void* workspace = nullptr;
+  int* status = nullptr;
+  cudaStream_t stream = nullptr;
+};
+size_t attn_prefill_workspace(int n_seq, int64_t tokens, int H, int kv_heads, int num_sms);
+size_t attn_decode_workspace(int n_seq, int n_tok, int H, int kv_heads, int num_sms);
+cudaError_t launch_attn_prefill(const AttnArgs& a, int num_sms);
+cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms);
+
+// The split of the work over blocks, and the workspace that joins it (kda_attn_common.cu).
+// The items -- (sequence, row tile) x kv head -- lie one after the other on a line of key
+// tiles; block c of the first C takes [c W / C, (c + 1) W / C) of its W tiles.  Parts of items
+// that two or more blocks share go to slots of the workspace: block c's first part, of an item
+// begun by an earlier block, to slot 2c, its last part, of an item that a later block goes on
+// with, to slot 2c + 1, and desc[c] = {sequence, head, first row, last block} names the latter.
+struct AttnSplit {
+  int4* desc = nullptr;        // [grid], .w = -1: none
+  float2* part_ml = nullptr;   // [2 grid][part_rows] (maximum, sum)
+  float* part_o = nullptr;     // [2 grid][part_rows][128] unnormalised
+  int64_t* plan_total = nullptr;   // prefill: tiles of all items of one kv head
+  int64_t* plan_start = nullptr;   // [items + 1] where each begins on one kv head's line
+  int2* plan_item = nullptr;       // [items] {sequence, first row}
+  int* plan_items = nullptr;       // number of items
+  int64_t max_items = 0;
+  int grid = 0;
+  int part_rows = 0;
+  int min_tiles = 1;
+};
+size_t attn_split_bytes(int grid, int part_rows, int64_t max_items);
+void attn_split_layout(AttnSplit* s, void* workspace, int grid, int part_rows, int64_t max_items);
+// Most row tiles that `tokens` tokens of n_seq sequences can make.
+inline int64_t attn_max_items(int n_seq, int64_t tokens, int group, int rows) { return tokens * group / rows + n_seq; }
+// Prefill: lists the items (row tiles of `rows` rows, key tiles of `tile` keys) in the workspace.
+cudaError_t launch_attn_plan(const AttnArgs& a, const AttnSplit& s, int rows, int tile);
+// Joins the parts of split items in block order.
+cudaError_t launch_attn_join(const AttnArgs& a, const AttnSplit& s);
+// Tensor maps of the cache, one box per (page, kv head): min(page_size, tile) tokens.
+bool make_cache_maps(const KvCache& c, int tile, struct CUtensorMap_st* k, struct CUtensorMap_st* v,
+                     struct CUtensorMap_st* ks, struct CUtensorMap_st* vs);
+
+// The key tiles (of `tile` keys) that rows at positions p_first .. p_last have to visit: the
+// tiles [0, sink) of the first tokens, then [lo, hi) up to the last visible key.
+struct KeyTiles {
+  int sink, lo, hi;
+  __host__ __device__ int count() const { return sink + hi - lo; }
+  // key tile of the i-th visit
+  __host__ __device__ int at(int i) const { return i < sink ? i : lo + (i - sink); }
+};
+__host__ __device__ inline KeyTiles key_tiles(int p_first, int p_last, int window, int n_sink, int tile) {
+  KeyTiles t{0, 0, 0};
+  if (p_last < 0) return t;
+  t.hi = p_last / tile + 1;
+  if (window > 0) {
+    const int64_t first = static_cast<int64_t>(p_first < 0 ? 0 : p_first) - window + 1;
+    t.lo = first > 0 ? static_cast<int>(first / tile) : 0;
+    const int s = n_sink > 0 ? (n_sink - 1) / tile + 1 : 0;
+    t.sink = s < t.lo ? s : t.lo;
+  }
+  return t;
+}
+
+// Whether the row at position p sees key j (window = 0: no window).
+__device__ __forceinline__ bool sees(int p, int j, int window, int n_sink) {
+  return j <= p && (window == 0 || p - j < window || j < n_sink);
+}
+
+}  // namespace kda

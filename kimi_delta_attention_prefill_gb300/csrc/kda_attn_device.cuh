@@ -1,0 +1,273 @@
+// kda_attn_device.cuh -- device code shared by the attention kernels: the walk of a block over
+// its share of the work, scale bytes, and TMA loads of the cache's maps.
+#pragma once
+
+#include <cstdint>
+
+#include "kda_attn.h"
+#include "kda_ptx.cuh"
+
+namespace kda {
+
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3,
+                                            int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %6, %7}], [%2];\n" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4)
+      : "memory");
+}
+
+// Programmatic dependent launch: let the next kernel of the stream start its blocks / wait for
+// the previous kernel's end and its writes.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Two e4m3 codes (low 16 bits) as two f16 values, exactly.
+__device__ __forceinline__ uint32_t e4m3_half2(uint32_t pair) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
+  return r;
+}
+
+// Scale bytes of E4M3 rows: 2^(b - 127), NaN for 255 (what is written lies in [87, 167]; other
+// bytes keep their meaning as far as 32 bits go).
+__device__ __forceinline__ float scale_value(uint32_t b) {
+  return __uint_as_float(b == 255 ? 0x7fffffffu : b == 0 ? 0x00400000u : b << 23);
+}
+__device__ __forceinline__ float scale_inverse(uint32_t b) {
+  return __uint_as_float(b == 255 ? 0x7fffffffu : b == 254 ? 0x00400000u : (254u - b) << 23);
+}
+__device__ __forceinline__ float scale_exponent(uint32_t b) {
+  return b == 255 ? __uint_as_float(0x7fffffffu) : static_cast<float>(static_cast<int>(b) - 127);
+}
+
+__device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }
+
+// Queries against E4M3 keys are f16, as the codes are: a row times 2^-e with its largest value
+// (bf16 magnitude bits `top`) in [2^8, 2^9) is exact down to 2^-22 of that value.
+__device__ __forceinline__ int query_exponent(uint32_t top) {
+  const int e = static_cast<int>(top >> 7) - 127 - 8;
+  return top >= 0x7f80u || top == 0 ? 0 : max(e, -100);
+}
+
+__device__ __forceinline__ float lse_of(float m, float l) {  // m in log2 units
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
+// One (sequence, kv head, row tile): rows [row0, row0 + tile rows) of the sequence's
+// rows = n_tok G rows, row r = token r / G, query head head * G + r % G.
+struct Item {
+  int seq = 0, head = 0, row0 = 0, rows = 0;
+  int G = 1, n_tok = 0, len = 0;
+  int64_t base = 0;  // packed row of the sequence's first token
+  int last_row = 0;  // last live row of the tile
+  KeyTiles tiles{0, 0, 0};
+  __device__ int p_of_row(int row) const { return len - n_tok + row / G; }
+  __device__ int p_first() const { return p_of_row(row0); }
+  __device__ int p_last() const { return p_of_row(last_row); }
+  __device__ int64_t q_offset(const AttnArgs& a, int row) const {
+    const int t = row / G, g = row - t * G;
+    const int64_t s = a.cu ? (base + t) * a.q_stride[1] : static_cast<int64_t>(seq) * a.q_stride[0] + t * a.q_stride[1];
+    return s + (static_cast<int64_t>(head) * G + g) * a.q_stride[2];
+  }
+  __device__ int64_t o_row(const AttnArgs& a, int row) const {
+    const int t = row / G, g = row - t * G;
+    return (base + t) * a.H + static_cast<int64_t>(head) * G + g;
+  }
+};
+
+// A kv_len that the table cannot hold, or offsets that run backwards.
+__device__ __forceinline__ bool seq_bad(const AttnArgs& a, int len, int64_t first, int64_t end) {
+  return len < 0 || len > static_cast<int64_t>(a.max_pages) * a.cache.page_size || first < 0 || end < first || end > a.tokens;
+}
+
+// Fills an item's sequence part; false: the sequence is bad or has no new tokens.
+__device__ inline bool item_sequence(const AttnArgs& a, int seq, Item* w) {
+  const int64_t first = a.cu ? a.cu[seq] : static_cast<int64_t>(seq) * a.n_tok;
+  const int64_t end = a.cu ? a.cu[seq + 1] : first + a.n_tok;
+  w->seq = seq;
+  w->len = a.kv_len[seq];
+  w->base = first;
+  w->n_tok = static_cast<int>(end - first);
+  w->G = a.H / a.cache.heads;
+  w->rows = w->n_tok * w->G;
+  return !seq_bad(a, w->len, first, end) && end > first;
+}
+// The tiles of its row tile [row0, row0 + n); never none: a tile that sees nothing has one
+// visit, which writes its rows' zeros.
+__device__ inline void item_tiles(const AttnArgs& a, int row0, int n, int tile, Item* w) {
+  w->row0 = row0;
+  w->last_row = min(row0 + n, w->rows) - 1;
+  w->tiles = key_tiles(w->p_first(), w->p_last(), a.window, a.n_sink, tile);
+  if (w->tiles.count() == 0) w->tiles.hi = w->tiles.lo + 1;
+}
+
+// A block's way along the line of key tiles (AttnSplit).  In decode every sequence's row tiles
+// visit the same key tiles, so the line needs only the sequences' counts, which each block adds
+// up by itself; in prefill it comes from the plan.
+template <int kRows, int kTileKeys>
+struct ItemWalk {
+  const AttnArgs& a;
+  const AttnSplit& s;
+  Item item;
+  int begin = 0, end = 0;   // key tile visits of the item that are this block's
+  int64_t pos = 0, stop = 0, at = 0;  // on the line: where we are, the share's end, where the item begins
+  int64_t blocks = 1, total = 0;
+  int64_t idx = 0;  // prefill: the plan's item
+  int unit = 0, n_units = 1;  // decode: head and row tile within the sequence
+
+  __device__ ItemWalk(const AttnArgs& a_, const AttnSplit& s_) : a(a_), s(s_) {}
+
+  __device__ int decode_count(int seq) {  // key tiles of a row tile of the sequence; 0: bad
+    const int len = a.kv_len[seq];
+    if (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.cache.page_size) {
+      if (blockIdx.x == 0) report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
+      return 0;
+    }
+    const int n = key_tiles(len - a.n_tok, len - 1, a.window, a.n_sink, kTileKeys).count();
+    return n > 0 ? n : 1;
+  }
+
+  // Takes this block's share; false: there is none.  Called by all kThreads threads.
+  template <int kThreads>
+  __device__ bool start(int tid) {
+    __shared__ int64_t sh_sum[kThreads / 32 + 1];
+    __shared__ int64_t sh_at;
+    __shared__ int sh_seq;
+    const int warp = tid >> 5, lane = tid & 31;
+    const int rows = a.n_tok * (a.H / a.cache.heads);
+    n_units = a.cu ? a.cache.heads : a.cache.heads * ((rows + kRows - 1) / kRows);
+    if (tid == 0) s.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
+    int64_t sum = 0;
+    if (a.cu) {
+      sum = *s.plan_total;
+      __syncthreads();
+    } else {
+      for (int i = tid; i < a.n_seq; i += kThreads) sum += decode_count(i);
+#pragma unroll
+      for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+      if (lane == 0) sh_sum[warp] = sum;
+      __syncthreads();
+      sum = 0;
+#pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) sum += sh_sum[i];
+      __syncthreads();
+    }
+    total = sum * n_units;
+    blocks = total / s.min_tiles;
+    blocks = blocks < 1 ? 1 : blocks > gridDim.x ? gridDim.x : blocks;
+    if (total == 0 || blockIdx.x >= blocks) return false;
+    pos = blockIdx.x * total / blocks;
+    stop = (blockIdx.x + 1) * total / blocks;
+    const int64_t target = pos / n_units;
+    if (a.cu) {
+      int64_t lo = 0, hi = *s.plan_items;  // plan_start[lo] <= target < plan_start[hi]
+      while (hi - lo > 1) {
+        const int64_t mid = (lo + hi) >> 1;
+        if (s.plan_start[mid] <= target) lo = mid; else hi = mid;
+      }
+      idx = lo;
+      load_plan();
+    } else {
+      int64_t run = 0;
+      for (int b = 0; b < a.n_seq; b += kThreads) {
+        const int i = b + tid;
+        const int64_t c = i < a.n_seq ? decode_count(i) : 0;
+        int64_t incl = c;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+          const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
+          if (lane >= off) incl += up;
+        }
+        if (lane == 31) sh_sum[warp] = incl;
+        __syncthreads();
+        int64_t before = run, all = run;
+#pragma unroll
+        for (int k = 0; k < kThreads / 32; ++k) {
+          if (k < warp) before += sh_sum[k];
+          all += sh_sum[k];
+        }
+        incl += before;
+        if (incl - c <= target && target < incl) { sh_seq = i; sh_at = incl - c; }
+        __syncthreads();
+        run = all;
+        if (run > target) break;
+      }
+      item_sequence(a, sh_seq, &item);
+      item_tiles(a, 0, rows, kTileKeys, &item);
+      at = sh_at * n_units;
+      unit = static_cast<int>((pos - at) / item.tiles.count());
+      at += static_cast<int64_t>(unit) * item.tiles.count();
+      set_unit();
+    }
+    clip();
+    return true;
+  }
+
+  __device__ void set_unit() {  // decode: heads outermost, so that row tiles of a head are neighbours
+    const int n_rt = n_units / a.cache.heads;
+    item.head = unit / n_rt;
+    item.row0 = (unit - item.head * n_rt) * kRows;
+    item.last_row = min(item.row0 + kRows, item.rows) - 1;
+  }
+  __device__ void load_plan() {
+    const int2 d = s.plan_item[idx];
+    item_sequence(a, d.x, &item);
+    item_tiles(a, d.y, kRows, kTileKeys, &item);
+    at = s.plan_start[idx] * n_units;
+    item.head = static_cast<int>((pos - at) / item.tiles.count());
+    at += static_cast<int64_t>(item.head) * item.tiles.count();
+  }
+  __device__ void clip() {
+    const int n = item.tiles.count();
+    begin = static_cast<int>(pos - at);
+    end = stop - at < n ? static_cast<int>(stop - at) : n;
+  }
+  // The next item of the share; false: the share is done.
+  __device__ bool next() {
+    const int n = item.tiles.count();
+    pos = at + end;
+    if (pos >= stop) return false;
+    at += n;
+    if (a.cu) {
+      if (++item.head == a.cache.heads) {
+        ++idx;
+        load_plan();
+      }
+    } else if (++unit == n_units) {
+      unit = 0;
+      int seq = item.seq + 1;
+      while (decode_count(seq) == 0) ++seq;  // there is one: the share goes on
+      item_sequence(a, seq, &item);
+      item_tiles(a, 0, item.rows, kTileKeys, &item);
+      set_unit();
+    } else {
+      set_unit();
+    }
+    clip();
+    return true;
+  }
+  // Slot of the part at hand, or -1 when the block has the whole item.  Thread 0 also names the
+  // parts of an item that begins here and ends in a later block.
+  __device__ int part_slot() const {
+    const int n = item.tiles.count();
+    if (begin == 0 && end == n) return -1;
+    if (begin > 0) return 2 * blockIdx.x;
+    if (threadIdx.x == 0) {
+      // the block that has the item's last tile: c1 = ceil(E C / W) - 1
+      const int64_t e = at + n;
+      s.desc[blockIdx.x] = make_int4(item.seq, item.head, item.row0, static_cast<int>((e * blocks + total - 1) / total - 1));
+    }
+    return 2 * blockIdx.x + 1;
+  }
+};
+
+}  // namespace kda

@@ -1,0 +1,538 @@
+// kda_attn_short.cu -- attention of few query rows a sequence over the paged cache.
+//
+// The mathematics: one pass over the keys with the running maximum m and sum l of a softmax,
+//     x_j = scale log2(e) q . k_j,   m' = max(m, max_j x_j),   l <- l 2^(m-m') + sum_j 2^(x_j-m'),
+//     O <- O 2^(m-m') + sum_j 2^(x_j-m') v_j,                  o = O / l,  lse = ln 2 (m + log2 l).
+// E4M3 rows stand for code * 2^e.  The key's scale multiplies x_j; the value's joins the
+// exponent, y_j = x_j + ev_j with m the maximum of the y_j, so P_j = 2^(y_j - m) <= 1 is
+// already the weight of the codes (exact in f16) and l sums P_j 2^-ev_j.  A large value row
+// therefore costs the others no precision, and nothing is rescaled tile by tile.
+//
+// Bound by the cache's bytes: every key and value row is read once per (sequence, kv head),
+// whatever the number of query heads that share it.  The H / kv_heads query heads of a kv
+// head and the tokens of the step are the rows of one block (row r = token r / G, head r % G),
+// 16 rows to a warp's mma.sync tile; at up to 64 rows the products need a small share of even
+// the warp-level tensor rate (16 padded rows: 8 KFLOP per key against 512 bytes), so tcgen05's
+// 128-row tiles would add latency and win nothing.
+//
+// Blocks: 4 warps compute, 1 warp issues the copies (TMA, one box per page and tile of 64
+// keys, 128-byte swizzle) into a ring of stages.  With up to 16 rows the 4 warps split the
+// keys of a tile (each with its own m, l, O, joined once at the end), with up to 32 rows two
+// and two, with more each warp has 16 rows and all keys.
+//
+// Work: the (sequence, head, row tile) items lie one after the other on a line of key tiles,
+// and every block takes an equal share of that line, whole items or parts of them: ragged
+// lengths and few long sequences fill the GPU alike.  A block has at most two partial items
+// (its first and its last); their O, m, l go to the workspace and a second kernel, launched
+// to overlap this one's tail, joins an item's parts in order.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cstdint>
+#include <cstring>
+
+#include "kda_attn.h"
+#include "kda_attn_device.cuh"
+#include "kda_ptx.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kTile = 64;  // keys a stage
+constexpr int kWarps = 4;
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kTileRows = 16;
+constexpr int kMaxRows = kWarps * kTileRows;
+constexpr int kMinTiles = 4;  // fewest key tiles of a block's share: below that the joining costs more than it spreads
+
+template <bool kE4m3>
+struct Stage {
+  static constexpr int kBytes = kE4m3 ? kTile * 128 : kTile * 256;  // one of K, V
+  static constexpr int kScales = kE4m3 ? 4 * 128 : 0;               // a 128-byte slot per page of the tile
+  static constexpr int kTotal = 2 * kBytes + 2 * kScales;
+  static constexpr int kCount = kE4m3 ? 5 : 3;
+};
+constexpr int kJoinBytes = 32 * 64 * 4 + 32 * 4 * 4;  // one warp's O and its (m, l) pairs
+template <bool kE4m3>
+constexpr int smem_bytes() {
+  return 1024 + Stage<kE4m3>::kTotal * Stage<kE4m3>::kCount + kJoinBytes;
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+  return v;
+}
+template <bool kHalf>
+__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (kHalf)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Bits 0 / 1: the low / high half of a pair is NaN or infinite; such halves are cleared.
+template <bool kHalf>
+__device__ __forceinline__ uint32_t take_nonfinite(uint32_t& w) {
+  constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
+  uint32_t f = 0;
+  if ((w & e) == e) { f |= 1; w &= 0xffff0000u; }
+  if ((w & (e << 16)) == (e << 16)) { f |= 2; w &= 0x0000ffffu; }
+  return f;
+}
+
+struct ShortParams {
+  CUtensorMap tk, tv, tks, tvs;
+  AttnArgs a;
+  AttnSplit s;
+};
+
+template <bool kE4m3, int kRG>
+__global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_constant__ ShortParams p) {
+  using St = Stage<kE4m3>;
+  constexpr int kKG = kWarps / kRG;            // warps that split a tile's keys
+  constexpr int kKeys = kTile / kKG;           // keys of a warp
+  constexpr int kNT = kKeys / 8;               // its 8-key column tiles
+  constexpr int kRT = kRG * kTileRows;         // rows of an item
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ alignas(8) uint64_t full[St::kCount], empty[St::kCount];
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const AttnArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < St::kCount; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], kWarps); }
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  ItemWalk<kRT, kTile> walk(p.a, p.s);
+  const bool any = walk.template start<kThreads>(tid);  // has the barriers that publish the mbarriers
+  if (!any) return;
+  const int P = min(a.cache.page_size, kTile), n_blk = kTile / P;
+
+  if (warp == kWarps) {  // ------------------------------------------------------ copies
+    int it = 0;
+    const int blk = lane;
+    do {
+      const Item& w = walk.item;
+      const KeyTiles kt = w.tiles;
+      const int p_first = w.p_first(), p_last = w.p_last();
+      for (int i = walk.begin; i < walk.end; ++i, ++it) {
+        const int j0 = kt.at(i) * kTile + blk * P;  // first key of this lane's page block
+        int page = -1;
+        if (blk < n_blk && j0 <= p_last) {
+          page = a.page_table[static_cast<int64_t>(w.seq) * a.max_pages + (j0 >> a.cache.page_log2)];
+          if (page < 0 || page >= a.cache.n_pages) {
+            const bool needed = a.window == 0 || j0 + P - 1 > p_first - a.window || j0 < a.n_sink;
+            if (needed) report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
+            page = -1;  // out of the tensor map's range: the copy fills with zeros
+          }
+        }
+        const int s = it % St::kCount;
+        if (it >= St::kCount && !mbar_wait(&empty[s], ((it / St::kCount) - 1) & 1)) {
+          report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+          return;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], 2 * St::kBytes + (kE4m3 ? 2 * kTile : 0));
+        __syncwarp();
+        if (blk < n_blk) {
+          uint8_t* st = sm + s * St::kTotal;
+          const int slot = j0 & (a.cache.page_size - 1);
+          if constexpr (kE4m3) {
+            tma_load_4d(st + blk * P * 128, &p.tk, &full[s], 0, slot, w.head, page);
+            tma_load_4d(st + St::kBytes + blk * P * 128, &p.tv, &full[s], 0, slot, w.head, page);
+            tma_load_3d(st + 2 * St::kBytes + blk * 128, &p.tks, &full[s], slot, w.head, page);
+            tma_load_3d(st + 2 * St::kBytes + St::kScales + blk * 128, &p.tvs, &full[s], slot, w.head, page);
+          } else {
+            tma_load_5d(st + blk * P * 256, &p.tk, &full[s], 0, slot, 0, w.head, page);
+            tma_load_5d(st + St::kBytes + blk * P * 256, &p.tv, &full[s], 0, slot, 0, w.head, page);
+          }
+        }
+      }
+    } while (walk.next());
+    return;
+  }
+
+  // -------------------------------------------------------------------------- products
+  const int g = lane >> 2, t = lane & 3;
+  const int rg = warp / kKG, kg = warp % kKG;
+  float* join = reinterpret_cast<float*>(sm + St::kTotal * St::kCount);
+  const int p_log = 31 - __clz(P);
+  int it = 0;
+  bool dead = false;
+  do {
+    const Item& w = walk.item;
+    const KeyTiles kt = w.tiles;
+    // this thread's rows g and g + 8 of the warp's 16: position, query fragments
+    int pos[2];
+    float cs[2];  // scale in log2 units (times the query row's own power of two)
+    uint32_t qf[8][4];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int row = w.row0 + rg * kTileRows + g + 8 * r;
+      const bool live = row < w.rows;
+      pos[r] = live ? w.p_of_row(row) : -1;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + w.q_offset(a, live ? row : 0);
+      cs[r] = a.scale_log2;
+      if constexpr (kE4m3) {
+        // channel order of the codes' 16-byte loads: this thread's chunks t and t + 4, 4 channels a step
+        uint32_t x[16];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const uint4 u = live ? *reinterpret_cast<const uint4*>(q + (c >> 1) * 64 + 16 * t + (c & 1) * 8) : make_uint4(0, 0, 0, 0);
+          x[4 * c] = u.x; x[4 * c + 1] = u.y; x[4 * c + 2] = u.z; x[4 * c + 3] = u.w;
+        }
+        uint32_t top = 0;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) top = max(top, max(x[c] & 0x7fffu, (x[c] >> 16) & 0x7fffu));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = query_exponent(top);
+        const float inv = pow2i(-e);
+        cs[r] *= pow2i(e);
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          qf[c >> 1][r + 2 * (c & 1)] = pack_half2(__uint_as_float(x[c] << 16) * inv, __uint_as_float(x[c] & 0xffff0000u) * inv);
+      } else {
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+          qf[s][r] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 2 * t) : 0;
+          qf[s][r + 2] = live ? *reinterpret_cast<const uint32_t*>(q + 16 * s + 8 + 2 * t) : 0;
+        }
+      }
+    }
+    float o[16][4];
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    const int p_first = w.p_first(), p_last = w.p_last();
+
+    for (int i = walk.begin; i < walk.end; ++i, ++it) {
+      const int s = it % St::kCount;
+      // after a wait that ran out the loop goes on without waiting, so that every barrier is still met
+      if (!dead && !mbar_wait(&full[s], (it / St::kCount) & 1)) dead = true;
+      const uint32_t kb = smem_u32(sm + s * St::kTotal), vb = kb + St::kBytes;
+      const int key0 = kt.at(i) * kTile + kg * kKeys;  // first key of this warp
+      float x[kNT][4];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[n][e] = 0.f;
+      // ---- q . k
+      if constexpr (kE4m3) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) {
+          const uint32_t row = kg * kKeys + n * 8 + g;
+          const uint4 u0 = lds128(kb + sw128(row, 16 * t)), u1 = lds128(kb + sw128(row, 64 + 16 * t));
+          const uint32_t c[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            mma16816<true>(x[n], qf[e], e4m3_half2(c[e]), e4m3_half2(c[e] >> 16));
+        }
+      } else {
+#pragma unroll
+        for (int n = 0; n < kNT; n += 2) {
+          const uint32_t row = kg * kKeys + n * 8 + (lane & 7) + ((lane >> 4) << 3);
+          const uint32_t base = kb + (row >> p_log) * (P * 256), rr = row & (P - 1);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            uint32_t b[4];
+            const uint32_t byte = 32 * (e & 3) + 16 * ((lane >> 3) & 1);
+            ldsm4(base + (e >> 2) * (P * 128) + sw128(rr, byte), b);
+            mma16816<false>(x[n], qf[e], b[0], b[1]);
+            mma16816<false>(x[n + 1], qf[e], b[2], b[3]);
+          }
+        }
+      }
+      // ---- scaled scores; hidden ones to -inf
+      float rv[kE4m3 ? kNT : 1][2];  // 2^-ev
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+        if constexpr (kE4m3) {
+          const uint32_t key = kg * kKeys + n * 8 + 2 * t;
+          const uint8_t* sc = sm + s * St::kTotal + 2 * St::kBytes + (key >> p_log) * 128 + (key & (P - 1));
+          const uint32_t k2 = *reinterpret_cast<const uint16_t*>(sc), v2 = *reinterpret_cast<const uint16_t*>(sc + St::kScales);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t kbyte = (k2 >> (8 * h)) & 255u, vbyte = (v2 >> (8 * h)) & 255u;
+            const float ks = scale_value(kbyte), ev = scale_exponent(vbyte);
+            rv[n][h] = scale_inverse(vbyte);
+            x[n][h] = fmaf(x[n][h] * ks, cs[0], ev);
+            x[n][h + 2] = fmaf(x[n][h + 2] * ks, cs[1], ev);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[n][e] *= cs[e >> 1];
+        }
+      }
+      const int t_first = kt.at(i) * kTile, t_last = t_first + kTile - 1;
+      const bool edge = t_last > p_first || (a.window > 0 && t_first <= p_last - a.window && t_last >= a.n_sink);
+      if (edge) {
+#pragma unroll
+        for (int n = 0; n < kNT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (!sees(pos[e >> 1], key0 + n * 8 + 2 * t + (e & 1), a.window, a.n_sink)) x[n][e] = -INFINITY;
+      }
+      // ---- running maximum and sum
+      float corr[2], base[2];
+      bool moved = false;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float mx = x[0][2 * r];
+#pragma unroll
+        for (int n = 0; n < kNT; ++n) mx = fmaxf(mx, fmaxf(x[n][2 * r], x[n][2 * r + 1]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[r], mx);
+        base[r] = mn == -INFINITY ? 0.f : mn;
+        corr[r] = exp2_fast(m[r] - base[r]);
+        moved |= mn != m[r];
+        m[r] = mn;
+        l[r] *= corr[r];
+      }
+      uint32_t pf[kNT][2];
+#pragma unroll
+      for (int n = 0; n < kNT; ++n) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const float p0 = exp2_fast(x[n][2 * r] - base[r]), p1 = exp2_fast(x[n][2 * r + 1] - base[r]);
+          // weights rounded once, to the values' type: f16 2^-11, bf16 2^-8 at most; l keeps 32 bits
+          if constexpr (kE4m3) {
+            // a hidden key's scale may be NaN, its weight is 0 whatever the scale says
+            l[r] += (p0 == 0.f ? 0.f : p0 * rv[n][0]) + (p1 == 0.f ? 0.f : p1 * rv[n][1]);
+            pf[n][r] = pack_half2(p0, p1);
+          } else {
+            l[r] += p0 + p1;
+            pf[n][r] = pack_bf162(p0, p1);
+          }
+        }
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int n = 0; n < 16; ++n) {
+          o[n][0] *= corr[0]; o[n][1] *= corr[0];
+          o[n][2] *= corr[1]; o[n][3] *= corr[1];
+        }
+      }
+      // ---- P V
+#pragma unroll
+      for (int n = 0; n < kNT; n += 2) {  // 16 keys
+        const uint32_t pa[4] = {pf[n][0], pf[n][1], pf[n + 1][0], pf[n + 1][1]};
+        uint32_t bad = 0;  // bits: keys 2t, 2t + 1, 2t + 8, 2t + 9 have a non-finite value
+        if constexpr (kE4m3) {
+          const uint32_t row = kg * kKeys + n * 8 + 2 * t;
+          uint32_t c[4][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const uint4 u = lds128(vb + sw128(row + (r & 1) + 8 * (r >> 1), 16 * g));
+            c[r][0] = u.x; c[r][1] = u.y; c[r][2] = u.z; c[r][3] = u.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {  // 4 channels: column tiles 4e .. 4e + 3
+            const uint32_t a0 = __byte_perm(c[0][e], c[1][e], 0x5140), a1 = __byte_perm(c[0][e], c[1][e], 0x7362);
+            const uint32_t b0 = __byte_perm(c[2][e], c[3][e], 0x5140), b1 = __byte_perm(c[2][e], c[3][e], 0x7362);
+            uint32_t ba[4] = {e4m3_half2(a0), e4m3_half2(a0 >> 16), e4m3_half2(a1), e4m3_half2(a1 >> 16)};
+            uint32_t bb[4] = {e4m3_half2(b0), e4m3_half2(b0 >> 16), e4m3_half2(b1), e4m3_half2(b1 >> 16)};
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              if (edge) bad |= take_nonfinite<true>(ba[q]) | (take_nonfinite<true>(bb[q]) << 2);
+              mma16816<true>(o[4 * e + q], pa, ba[q], bb[q]);
+            }
+          }
+        } else {
+          const uint32_t row = kg * kKeys + n * 8 + (lane & 15);
+          const uint32_t base_v = vb + (row >> p_log) * (P * 256), rr = row & (P - 1);
+#pragma unroll
+          for (int c = 0; c < 16; c += 2) {
+            uint32_t b[4];
+            ldsm4t(base_v + (c >> 3) * (P * 128) + sw128(rr, 16 * ((c & 7) + (lane >> 4))), b);
+            if (edge) {
+              bad |= take_nonfinite<false>(b[0]) | (take_nonfinite<false>(b[1]) << 2);
+              bad |= take_nonfinite<false>(b[2]) | (take_nonfinite<false>(b[3]) << 2);
+            }
+            mma16816<false>(o[c], pa, b[0], b[1]);
+            mma16816<false>(o[c + 1], pa, b[2], b[3]);
+          }
+        }
+        if (edge) {
+          // 0 * NaN must not reach a row that does not see the key: the values were cleared, and
+          // the rows that do see it become NaN here.
+          bad |= __shfl_xor_sync(0xffffffffu, bad, 4);
+          bad |= __shfl_xor_sync(0xffffffffu, bad, 8);
+          bad |= __shfl_xor_sync(0xffffffffu, bad, 16);
+          if (bad) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if ((bad >> e) & 1) {
+                const int key = key0 + n * 8 + 2 * t + (e & 1) + 8 * (e >> 1);
+#pragma unroll
+                for (int r = 0; r < 2; ++r)
+                  if (sees(pos[r], key, a.window, a.n_sink)) l[r] = __uint_as_float(0x7fffffffu);
+              }
+          }
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+    }
+
+    // ---- one row's sum lies over the 4 lanes that share it
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+    }
+    // ---- join the warps that split the keys, in order
+#pragma unroll
+    for (int k = 1; k < kKG; ++k) {
+#pragma unroll
+      for (int q = 0; q < kRG; ++q) {  // one buffer: the row groups take turns
+        if (rg == q && kg == k) {
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) join[(n * 4 + e) * 32 + lane] = o[n][e];
+          reinterpret_cast<float4*>(join + 64 * 32)[lane] = make_float4(m[0], m[1], l[0], l[1]);
+        }
+        named_bar_sync(1, kWarps * 32);
+        if (rg == q && kg == 0) {
+          const float4 ml = reinterpret_cast<const float4*>(join + 64 * 32)[lane];
+          const float om[2] = {ml.x, ml.y}, ol[2] = {ml.z, ml.w};
+          float c0[2], c1[2];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float mn = fmaxf(m[r], om[r]), b = mn == -INFINITY ? 0.f : mn;
+            c0[r] = exp2_fast(m[r] - b); c1[r] = exp2_fast(om[r] - b);
+            m[r] = mn;
+            l[r] = l[r] * c0[r] + ol[r] * c1[r];
+          }
+#pragma unroll
+          for (int n = 0; n < 16; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[n][e] = o[n][e] * c0[e >> 1] + join[(n * 4 + e) * 32 + lane] * c1[e >> 1];
+        }
+        named_bar_sync(1, kWarps * 32);
+      }
+    }
+    if (kg == 0) {
+      const int slot = walk.part_slot();
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int lr = rg * kTileRows + g + 8 * r, row = w.row0 + lr;
+        if (row >= w.rows) continue;
+        // channels of o[n][2r], o[n][2r + 1]: bf16 8n + 2t, + 1; e4m3 32t + n, 32t + 16 + n
+        if (slot >= 0) {
+          float* dst = p.s.part_o + (static_cast<int64_t>(slot) * p.s.part_rows + lr) * 128;
+          if constexpr (kE4m3) {
+#pragma unroll
+            for (int n = 0; n < 16; n += 4) {
+              *reinterpret_cast<float4*>(dst + 32 * t + n) = make_float4(o[n][2 * r], o[n + 1][2 * r], o[n + 2][2 * r], o[n + 3][2 * r]);
+              *reinterpret_cast<float4*>(dst + 32 * t + 16 + n) =
+                  make_float4(o[n][2 * r + 1], o[n + 1][2 * r + 1], o[n + 2][2 * r + 1], o[n + 3][2 * r + 1]);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < 16; ++n) *reinterpret_cast<float2*>(dst + 8 * n + 2 * t) = make_float2(o[n][2 * r], o[n][2 * r + 1]);
+          }
+          if (t == 0) p.s.part_ml[static_cast<int64_t>(slot) * p.s.part_rows + lr] = make_float2(m[r], l[r]);
+        } else {
+          const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
+          const int64_t orow = w.o_row(a, row);
+          uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + orow * 128);
+          if constexpr (kE4m3) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int n = 0; n < 16; n += 8)
+                *reinterpret_cast<uint4*>(dst + 16 * t + 8 * h + n / 2) =
+                    make_uint4(pack_bf162(o[n][2 * r + h] * inv, o[n + 1][2 * r + h] * inv),
+                               pack_bf162(o[n + 2][2 * r + h] * inv, o[n + 3][2 * r + h] * inv),
+                               pack_bf162(o[n + 4][2 * r + h] * inv, o[n + 5][2 * r + h] * inv),
+                               pack_bf162(o[n + 6][2 * r + h] * inv, o[n + 7][2 * r + h] * inv));
+          } else {
+#pragma unroll
+            for (int n = 0; n < 16; ++n) dst[4 * n + t] = pack_bf162(o[n][2 * r] * inv, o[n][2 * r + 1] * inv);
+          }
+          if (a.lse && t == 0) a.lse[orow] = lse_of(m[r], l[r]);
+        }
+      }
+    }
+  } while (walk.next());
+  if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+}
+
+template <bool kE4m3, int kRG>
+cudaError_t launch_short(const ShortParams& p, int grid) {
+  constexpr int bytes = smem_bytes<kE4m3>();
+  auto kern = attn_short_kernel<kE4m3, kRG>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<grid, kThreads, bytes, p.a.stream>>>(p);
+  return cudaGetLastError();
+}
+
+int row_groups(int rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : 4; }
+
+}  // namespace
+
+size_t attn_decode_workspace(int n_seq, int n_tok, int H, int kv_heads, int num_sms) {
+  return attn_split_bytes(2 * num_sms, kTileRows * row_groups(n_tok * (H / kv_heads)), 0);
+}
+
+cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms) {
+  const int G = a.H / a.cache.heads, rg = row_groups(a.n_tok * G);
+  ShortParams p;
+  memset(&p, 0, sizeof(p));
+  p.a = a;
+  const int grid = 2 * num_sms;
+  attn_split_layout(&p.s, a.workspace, grid, kTileRows * rg, 0);
+  p.s.min_tiles = kMinTiles;
+  if (!make_cache_maps(a.cache, kTile, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
+  cudaError_t e;
+  if (a.cache.e4m3)
+    e = rg == 1 ? launch_short<true, 1>(p, grid) : rg == 2 ? launch_short<true, 2>(p, grid) : launch_short<true, 4>(p, grid);
+  else
+    e = rg == 1 ? launch_short<false, 1>(p, grid) : rg == 2 ? launch_short<false, 2>(p, grid) : launch_short<false, 4>(p, grid);
+  if (e != cudaSuccess) return e;
+  return launch_attn_join(p.a, p.s);
+}
+
+size_t attn_prefill_workspace(int n_seq, int64_t tokens, int H, int kv_heads, int num_sms) {
+  return attn_split_bytes(2 * num_sms, kMaxRows, attn_max_items(n_seq, tokens, H / kv_heads, kMaxRows));
+}
+
+cudaError_t launch_attn_prefill(const AttnArgs& a, int num_sms) {
+  const int G = a.H / a.cache.heads;
+  ShortParams p;
+  memset(&p, 0, sizeof(p));
+  p.a = a;
+  const int grid = 2 * num_sms;
+  attn_split_layout(&p.s, a.workspace, grid, kMaxRows, attn_max_items(a.n_seq, a.tokens, G, kMaxRows));
+  p.s.min_tiles = kMinTiles;
+  if (!make_cache_maps(a.cache, kTile, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
+  cudaError_t e = launch_attn_plan(a, p.s, kMaxRows, kTile);
+  if (e != cudaSuccess) return e;
+  e = a.cache.e4m3 ? launch_short<true, 4>(p, grid) : launch_short<false, 4>(p, grid);
+  if (e != cudaSuccess) return e;
+  return launch_attn_join(p.a, p.s);
+}
+
+}  // namespace kda

@@ -11,6 +11,9 @@ constexpr int kHeadDim = 128;
 constexpr int kChunk = 64;
 constexpr int kMaxDecodeTokens = 4;
 
+// kda_status of the current device (KDA_OK: an sm_103 part); fills its SM count (kda_api.cu).
+int current_device_status(int* sms);
+
 // Device-side error report: the first non-zero code wins.
 __device__ __forceinline__ void report_status(int* status, int code) {
   if (status) atomicCAS(status, 0, code);
