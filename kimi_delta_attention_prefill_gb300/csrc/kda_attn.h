@@ -71,6 +71,10 @@ size_t attn_decode_workspace(int n_seq, int n_tok, int H, int kv_heads, int num_
 cudaError_t launch_attn_prefill(const AttnArgs& a, int num_sms);
 cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms);
 
+// Many rows a sequence: kda_attn_chunk.cu.
+size_t attn_chunk_workspace(int n_seq, int64_t tokens, int group, int num_sms);
+cudaError_t launch_attn_chunk(const AttnArgs& a, int num_sms);
+
 // The split of the work over blocks, and the workspace that joins it (kda_attn_common.cu).
 // The items -- (sequence, row tile) x kv head -- lie one after the other on a line of key
 // tiles; block c of the first C takes [c W / C, (c + 1) W / C) of its W tiles.  Parts of items
@@ -98,8 +102,9 @@ inline int64_t attn_max_items(int n_seq, int64_t tokens, int group, int rows) { 
 cudaError_t launch_attn_plan(const AttnArgs& a, const AttnSplit& s, int rows, int tile);
 // Joins the parts of split items in block order.
 cudaError_t launch_attn_join(const AttnArgs& a, const AttnSplit& s);
-// Tensor maps of the cache, one box per (page, kv head): min(page_size, tile) tokens.
-bool make_cache_maps(const KvCache& c, int tile, struct CUtensorMap_st* k, struct CUtensorMap_st* v,
+// Tensor maps of the cache, one box per (page, kv head): min(page_size, tile) tokens, bf16 rows
+// in `panels` (1 or 2) panels of 64 channels.
+bool make_cache_maps(const KvCache& c, int tile, int panels, struct CUtensorMap_st* k, struct CUtensorMap_st* v,
                      struct CUtensorMap_st* ks, struct CUtensorMap_st* vs);
 
 // The key tiles (of `tile` keys) that rows at positions p_first .. p_last have to visit: the

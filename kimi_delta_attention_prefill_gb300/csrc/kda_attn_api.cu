@@ -78,7 +78,11 @@ kda_status check_attn(const void* q, const int64_t* qs, int n_strides, const kda
       !aligned(kv_len, 4) || !aligned(lse, 4) || !aligned(status, 4) || !aligned(workspace, 256))
     return KDA_ERR_ALIGNMENT;
   a->q = q; a->page_table = page_table; a->kv_len = kv_len; a->n_seq = n_seq; a->max_pages = max_pages;
-  a->tokens = tokens; a->H = H; a->scale_log2 = scale * 1.4426950408889634f; a->window = window; a->n_sink = n_sink;
+  a->tokens = tokens; a->H = H; a->scale_log2 = scale * 1.4426950408889634f;
+  // a window no sequence can outgrow is none, and the kernels' 32-bit positions need no more first tokens than fit
+  const int64_t most = static_cast<int64_t>(max_pages) * cache->page_size;
+  a->window = window >= most ? 0 : window;
+  a->n_sink = static_cast<int>(n_sink < most ? n_sink : most);
   a->o = const_cast<void*>(o); a->lse = const_cast<float*>(lse); a->workspace = const_cast<void*>(workspace);
   return KDA_OK;
 }

@@ -1,0 +1,651 @@
+// kda_attn_chunk.cu -- attention of a chunk of new tokens over the paged cache (tcgen05).
+//
+// The mathematics is that of kda_attn_short.cu (one pass with a running maximum); here the
+// rows are many, so the products bound it: 4 * 128 FLOPs per visible (query head, key).
+//
+// A block (one per SM) holds 256 query rows of one kv head -- row r is token r / G, query head
+// r % G of the head's group, so 8 tokens of a group of 12 fill 96 rows and no tile is padded
+// by the group -- as two 128-row tiles A and B, and visits key tiles of 128:
+//     S = Q K^T    tcgen05, both operands in shared memory, S (fp32) in TMEM
+//     P = 2^(S c - m c), rounded to the values' type, over S's first 64 columns
+//     O += P V     tcgen05, P from TMEM, V from shared memory (MN-major)
+// TMEM: S_A, S_B, O_A, O_B, 128 columns each: all 512.
+//
+// Warps: two groups of four for the softmax of A and of B (thread = row = TMEM lane: a row's
+// maximum and sum need no exchange), one warp that issues the products, one the copies, two
+// that bring the next item's queries; for an E4M3 cache four more turn the codes into f16
+// tiles (exact).  The tensor core runs P V and the next Q K^T of one tile while the other
+// tile is in its softmax.
+//
+// The maximum is lazy: O is rescaled only when a row's maximum has grown by more than 2^8
+// since the last time (weights stay below 2^8, far inside every type here), which random
+// rows do in their first tiles only.
+//
+// Work is split as in kda_attn_short.cu: equal shares of the line of key tiles, at most two
+// partial items a block, joined by attn_join_kernel.
+#include <cuda_runtime.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cstdint>
+#include <cstring>
+
+#include "kda_attn.h"
+#include "kda_attn_device.cuh"
+#include "kda_ptx.cuh"
+
+namespace kda {
+
+namespace {
+
+constexpr int kTile = 128;
+constexpr int kRows = 256;
+constexpr int kPanel = kTile * 128;     // 64 channels of 128 rows, 16-bit
+constexpr int kSlot = 2 * kPanel;       // one tile of K or V (or 128 rows of Q) as 16-bit values
+constexpr int kStage = kTile * 128 + 8 * 128;  // a tile of codes and a 128-byte slot of scale bytes per page
+constexpr float kLazy = 8.f;
+
+template <bool kE4m3>
+struct Cfg {
+  static constexpr int kThreads = kE4m3 ? 512 : 384;
+  static constexpr int kSlots = kE4m3 ? 3 : 5;
+  static constexpr int kStages = kE4m3 ? 3 : 0;
+  static constexpr int kSmQ = 0;
+  static constexpr int kSmKV = 2 * kSlot;
+  static constexpr int kSmStage = kSmKV + kSlots * kSlot;
+  static constexpr int kSmVec = kSmStage + kStages * kStage;          // [2 tiles][ks, ev, 2^-ev][128] floats
+  static constexpr int kSmExp = kSmVec + (kE4m3 ? 2 * 3 * 512 : 0);   // [2 items][256] query row scales
+  static constexpr int kSmBytes = kSmExp + (kE4m3 ? 2048 : 0) + 1024;
+};
+
+struct Bars {
+  uint64_t full[5], empty[5];      // slots of K / V tiles
+  uint64_t vok[5];                 // bf16: an edge tile's values have been looked through
+  uint64_t st_full[3], st_empty[3];  // stages of codes
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], pv_done[2], o_full[2];
+  uint64_t drain;
+  uint32_t bad[5][4];              // edge tiles: keys with a non-finite value row
+  uint32_t tmem;
+};
+
+struct ChunkParams {
+  CUtensorMap tk, tv, tks, tvs;
+  AttnArgs a;
+  AttnSplit s;
+};
+
+using Walk = ItemWalk<kRows, kTile>;
+
+// Whether some row of the item does not see some key of key tile t.
+__device__ __forceinline__ bool edge_tile(const AttnArgs& a, int t, int p_first, int p_last) {
+  const int first = t * kTile, last = first + kTile - 1;
+  return last > p_first || (a.window > 0 && first <= p_last - a.window && last >= a.n_sink);
+}
+
+// ---------------------------------------------------------------------------- copies
+template <bool kE4m3>
+__device__ void load_warp(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b, int lane) {
+  using C = Cfg<kE4m3>;
+  const AttnArgs& a = p.a;
+  const int P = min(a.cache.page_size, kTile), n_blk = kTile / P;
+  const int blk = kE4m3 ? lane : lane >> 1, panel = kE4m3 ? 0 : lane & 1;
+  constexpr int kRing = kE4m3 ? C::kStages : C::kSlots;
+  uint64_t* full = kE4m3 ? b.st_full : b.full;
+  uint64_t* empty = kE4m3 ? b.st_empty : b.empty;
+  uint32_t n = 0;
+  do {
+    const Item& w = walk.item;
+    const int p_first = w.p_first(), p_last = w.p_last();
+    for (int i = walk.begin; i < walk.end; ++i) {
+      const int j0 = w.tiles.at(i) * kTile + blk * P;
+      int page = -1;
+      if (blk < n_blk && j0 <= p_last) {
+        page = a.page_table[static_cast<int64_t>(w.seq) * a.max_pages + (j0 >> a.cache.page_log2)];
+        if (page < 0 || page >= a.cache.n_pages) {
+          const bool needed = a.window == 0 || j0 + P - 1 > p_first - a.window || j0 < a.n_sink;
+          if (needed) report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
+          page = -1;  // out of the tensor map's range: the copy fills with zeros
+        }
+      }
+      const int slot = j0 & (a.cache.page_size - 1);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv, ++n) {
+        const uint32_t s = n % kRing;
+        if (n >= kRing && !mbar_wait(&empty[s], (n / kRing - 1) & 1)) {
+          report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+          return;
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], kE4m3 ? kTile * 128 + kTile : kSlot);
+        __syncwarp();
+        if (blk < n_blk) {
+          if constexpr (kE4m3) {
+            uint8_t* st = sm + C::kSmStage + s * kStage;
+            tma_load_4d(st + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, w.head, page);
+            tma_load_3d(st + kTile * 128 + blk * 128, kv ? &p.tvs : &p.tks, &full[s], slot, w.head, page);
+          } else {
+            uint8_t* st = sm + C::kSmKV + s * kSlot;
+            tma_load_5d(st + panel * kPanel + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, panel, w.head, page);
+          }
+        }
+      }
+    }
+  } while (walk.next());
+}
+
+// -------------------------------------------------------------------------- products
+template <bool kE4m3>
+__device__ void mma_thread(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b) {
+  using C = Cfg<kE4m3>;
+  const AttnArgs& a = p.a;
+  const uint32_t tmem = b.tmem;
+  const uint32_t id_qk = idesc_f16(128, 128, !kE4m3, false, false), id_pv = idesc_f16(128, 128, !kE4m3, false, true);
+  const uint64_t dq = smem_desc(smem_u32(sm + C::kSmQ), 16, 1024, kSwizzle128B);
+  const uint64_t dk = smem_desc(smem_u32(sm + C::kSmKV), 16, 1024, kSwizzle128B);
+  const uint64_t dv = smem_desc(smem_u32(sm + C::kSmKV), kPanel, 1024, kSwizzle128B);
+  bool dead = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead && !mbar_wait(bar, parity & 1)) dead = true;
+    tc_fence_after();
+  };
+  uint32_t n = 0, items = 0, vok = 0;   // ring position (K: even, V: odd), items, vok phases of the slots
+  uint32_t tiles[2] = {0, 0};           // tiles begun of A and B
+  auto qk = [&](int t, uint32_t slot) {
+    if (dead) return;
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      mma_f16(tmem + 128 * t, dq + ((t * kSlot + (kk >> 2) * kPanel + 32 * (kk & 3)) >> 4),
+              dk + ((slot * kSlot + (kk >> 2) * kPanel + 32 * (kk & 3)) >> 4), id_qk, kk > 0);
+    mma_commit(&b.s_full[t]);
+  };
+  do {
+    const Item& w = walk.item;
+    const int halves = w.last_row - w.row0 >= 128 ? 2 : 1;
+    const int p_first = w.p_first(), p_last = w.p_last();
+    wait(&b.q_full, items);
+    {
+      const uint32_t s = n % C::kSlots;
+      wait(&b.full[s], n / C::kSlots);
+      for (int t = 0; t < halves; ++t) qk(t, s);  // S is free: the last P V over it is done (below)
+      if (!dead) mma_commit(&b.empty[s]);
+      if (!dead && walk.end - walk.begin == 1) mma_commit(&b.q_empty);
+    }
+    for (int i = walk.begin; i < walk.end; ++i, n += 2) {
+      const uint32_t sv = (n + 1) % C::kSlots, sk = (n + 2) % C::kSlots;
+      const bool more = i + 1 < walk.end;
+      for (int t = 0; t < halves; ++t) {
+        wait(&b.p_full[t], tiles[t]);
+        if (t == 0) {
+          wait(&b.full[sv], (n + 1) / C::kSlots);
+          if (!kE4m3 && edge_tile(a, w.tiles.at(i), p_first, p_last)) {
+            wait(&b.vok[sv], vok >> sv);
+            vok ^= 1u << sv;
+          }
+        }
+        if (!dead) {
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_f16_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, dv + ((sv * kSlot + kk * 2048) >> 4), id_pv,
+                       kk > 0 || i > walk.begin);
+          mma_commit(&b.pv_done[t]);
+          if (t == halves - 1) mma_commit(&b.empty[sv]);
+          if (!more) mma_commit(&b.o_full[t]);
+        }
+        if (more && t == 0) wait(&b.full[sk], (n + 2) / C::kSlots);
+        // P lies over S: the next scores may be written once this product has read it
+        wait(&b.pv_done[t], tiles[t]);
+        ++tiles[t];
+        if (more) qk(t, sk);
+      }
+      if (more && !dead) {
+        mma_commit(&b.empty[sk]);
+        if (i + 2 == walk.end) mma_commit(&b.q_empty);
+      }
+    }
+    ++items;
+  } while (walk.next());
+  // nothing of this block's may be in flight when it ends
+  mma_commit(&b.drain);
+  if (!mbar_wait(&b.drain, 0)) dead = true;
+  if (dead) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+}
+
+// --------------------------------------------------------------------------- queries
+// Two warps bring an item's 256 query rows (16 lanes a row), zero past the last, and in a bf16
+// cache's edge tiles look the values through (see the softmax).  A negative scale is the same
+// as negated queries and a scale of 0 as zero queries with any scale, so the softmax's scale c
+// is positive.
+template <bool kE4m3>
+__device__ void query_warps(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b, int tid) {
+  using C = Cfg<kE4m3>;
+  const AttnArgs& a = p.a;
+  const int lane = tid & 31, sub = tid & 15, grp = tid >> 4;  // 4 groups of 16 lanes
+  const uint32_t flip = !kE4m3 && a.scale_log2 < 0.f ? 0x80008000u : 0u;
+  const bool zero = !kE4m3 && a.scale_log2 == 0.f;
+  float* qexp = reinterpret_cast<float*>(sm + C::kSmExp);
+  uint32_t n = 0, items = 0;
+  bool dead = false;
+  do {
+    const Item& w = walk.item;
+    if (items > 0 && !dead && !mbar_wait(&b.q_empty, (items - 1) & 1)) dead = true;
+    constexpr int kBatch = 8;
+    for (int r0 = grp; r0 < kRows; r0 += 4 * kBatch) {
+      uint4 x[kBatch];
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int row = w.row0 + r0 + 4 * u;
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (row < w.rows && !zero)
+          x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + w.q_offset(a, row)) + sub);
+      }
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const int r = r0 + 4 * u;
+        if constexpr (kE4m3) {
+          uint32_t top = max(max(x[u].x & 0x7fffu, (x[u].x >> 16) & 0x7fffu), max(x[u].y & 0x7fffu, (x[u].y >> 16) & 0x7fffu));
+          top = max(top, max(max(x[u].z & 0x7fffu, (x[u].z >> 16) & 0x7fffu), max(x[u].w & 0x7fffu, (x[u].w >> 16) & 0x7fffu)));
+#pragma unroll
+          for (int off = 8; off; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
+          const int e = query_exponent(top);
+          const float inv = pow2i(-e);
+          if (sub == 0) qexp[(items & 1) * kRows + r] = pow2i(e);
+          auto half = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv); };
+          x[u] = make_uint4(half(x[u].x), half(x[u].y), half(x[u].z), half(x[u].w));
+        } else {
+          x[u].x ^= flip; x[u].y ^= flip; x[u].z ^= flip; x[u].w ^= flip;
+        }
+        uint8_t* dst = sm + C::kSmQ + (r >> 7) * kSlot + (sub >> 3) * kPanel;
+        *reinterpret_cast<uint4*>(dst + sw128(r & 127, 16 * (sub & 7))) = x[u];
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&b.q_full);
+    ++items;
+    if constexpr (!kE4m3) {
+      const int p_first = w.p_first(), p_last = w.p_last();
+      for (int i = walk.begin; i < walk.end; ++i, n += 2) {
+        if (!edge_tile(a, w.tiles.at(i), p_first, p_last)) continue;
+        const uint32_t s = (n + 1) % C::kSlots;
+        if (!dead && !mbar_wait(&b.full[s], ((n + 1) / C::kSlots) & 1)) dead = true;
+        // thread = 2 keys: a row of 128 values with a NaN or an infinity is cleared and noted
+        for (int q = 0; q < 2; ++q) {
+          const int key = tid + 64 * q;
+          uint8_t* v = sm + C::kSmKV + s * kSlot;
+          bool bad = false;
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * kPanel + sw128(key, 16 * (c & 7)));
+            auto has = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
+            bad |= has(x.x) | has(x.y) | has(x.z) | has(x.w);
+          }
+          if (bad) {
+#pragma unroll 4
+            for (int c = 0; c < 16; ++c)
+              *reinterpret_cast<uint4*>(v + (c >> 3) * kPanel + sw128(key, 16 * (c & 7))) = make_uint4(0, 0, 0, 0);
+          }
+          const uint32_t m = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) b.bad[s][2 * q + (tid >> 5)] = m;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.vok[s]);
+      }
+    }
+  } while (walk.next());
+  if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+}
+
+// ------------------------------------------------------------------- codes to f16 tiles
+// Four warps, thread = key: 16 codes at a time to two 16-byte pieces of the f16 tile, and the
+// key's scales as the floats that the softmax needs.
+__device__ void convert_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b, int tid) {
+  using C = Cfg<true>;
+  const AttnArgs& a = p.a;
+  const int lane = tid & 31, warp = tid >> 5;
+  const int p_log = min(a.cache.page_log2, 7);
+  const int sc_at = kTile * 128 + (tid >> p_log) * 128 + (tid & ((1 << p_log) - 1));
+  uint32_t n = 0;
+  bool dead = false;
+  do {
+    const Item& w = walk.item;
+    const int p_first = w.p_first(), p_last = w.p_last();
+    for (int i = walk.begin; i < walk.end; ++i) {
+      const bool edge = edge_tile(a, w.tiles.at(i), p_first, p_last);
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv, ++n) {
+        const uint32_t st = n % C::kStages, s = n % C::kSlots;
+        if (!dead && !mbar_wait(&b.st_full[st], (n / C::kStages) & 1)) dead = true;
+        const uint8_t* src = sm + C::kSmStage + st * kStage;
+        uint4 c[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) c[k] = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
+        const uint32_t byte = src[sc_at];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.st_empty[st]);
+        if (kv && edge) {  // a code of NaN: its row is cleared and noted (see the softmax)
+          uint32_t nan = 0;
+          auto has = [](uint32_t u) {  // a byte 0x7f or 0xff
+            u = (u & 0x7f7f7f7fu) + 0x01010101u;
+            return u & 0x80808080u;
+          };
+#pragma unroll
+          for (int k = 0; k < 8; ++k) nan |= has(c[k].x) | has(c[k].y) | has(c[k].z) | has(c[k].w);
+          if (nan) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) c[k] = make_uint4(0, 0, 0, 0);
+          }
+          const uint32_t m = __ballot_sync(0xffffffffu, nan != 0);
+          if (n >= C::kSlots && !dead && !mbar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) dead = true;
+          if (lane == 0) b.bad[s][warp] = m;
+        } else if (n >= C::kSlots && !dead && !mbar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) {
+          dead = true;
+        }
+        float* vec = reinterpret_cast<float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 384;
+        if (kv) {
+          vec[128 + tid] = scale_exponent(byte);
+          vec[256 + tid] = scale_inverse(byte);
+        } else {
+          vec[tid] = scale_value(byte);
+        }
+        uint8_t* dst = sm + C::kSmKV + s * kSlot;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          uint8_t* row = dst + (k >> 2) * kPanel;
+          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3))) =
+              make_uint4(e4m3_half2(c[k].x), e4m3_half2(c[k].x >> 16), e4m3_half2(c[k].y), e4m3_half2(c[k].y >> 16));
+          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3) + 16)) =
+              make_uint4(e4m3_half2(c[k].z), e4m3_half2(c[k].z >> 16), e4m3_half2(c[k].w), e4m3_half2(c[k].w >> 16));
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.full[s]);
+      }
+    }
+  } while (walk.next());
+  if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+}
+
+// ---------------------------------------------------------------------------- softmax
+template <bool kE4m3>
+__device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b, int t, int tid) {
+  using C = Cfg<kE4m3>;
+  const AttnArgs& a = p.a;
+  const int lane = tid & 31;
+  const uint32_t tl = static_cast<uint32_t>(tid & 96) << 16;
+  const uint32_t ts = b.tmem + tl + 128 * t, to = b.tmem + tl + 256 + 128 * t;
+  uint32_t n = 0, tiles = 0, items = 0, vphase = 0, seen = 0;  // seen: items of the block, items: those with rows here
+  bool dead = false;
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (!dead && !mbar_wait(bar, parity & 1)) dead = true;
+  };
+  do {
+    const Item& w = walk.item;
+    const int row = w.row0 + 128 * t + tid;
+    if (w.row0 + 128 * t > w.last_row) {  // no rows of this tile
+      if constexpr (!kE4m3) {
+        const int pf = w.p_first(), pl = w.p_last();
+        for (int i = walk.begin; i < walk.end; ++i, n += 2)
+          if (edge_tile(a, w.tiles.at(i), pf, pl)) vphase ^= 1u << ((n + 1) % C::kSlots);
+      } else {
+        n += 2 * (walk.end - walk.begin);
+      }
+      ++seen;
+      continue;
+    }
+    const bool live = row < w.rows;
+    const int pos = live ? w.p_of_row(row) : -1;
+    const int p_first = w.p_first(), p_last = w.p_last();
+    // scores to log2 units: bf16 S c (c > 0), e4m3 S ks c + ev
+    const float sc = fabsf(a.scale_log2);
+    const float c = kE4m3 ? a.scale_log2 : (sc == 0.f ? 1.f : sc);
+    float crow = c;
+    float m = -INFINITY;            // the reference that P is taken against (bf16: in units of S)
+    uint64_t l2 = f32x2(0.f, 0.f);
+    for (int i = walk.begin; i < walk.end; ++i, n += 2) {
+      const int kt = w.tiles.at(i);
+      const bool edge = edge_tile(a, kt, p_first, p_last);
+      const uint32_t sv = (n + 1) % C::kSlots;
+      wait(&b.s_full[t], tiles);
+      ++tiles;
+      tc_fence_after();
+      float s[4][32];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) tmem_ld32(ts + 32 * g, s[g]);
+      const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 384;
+      if constexpr (kE4m3) {
+        if (i == walk.begin) crow = c * reinterpret_cast<const float*>(sm + C::kSmExp)[(seen & 1) * kRows + 128 * t + tid];
+        wait(&b.full[sv], (n + 1) / C::kSlots);  // the value scales come with the values
+        const uint64_t c2 = f32x2(crow, crow);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float4 ks = *reinterpret_cast<const float4*>(vec + 32 * g + e);
+            const float4 ev = *reinterpret_cast<const float4*>(vec + 128 + 32 * g + e);
+            const float2 y0 = unpack_f32x2(fma_f32x2(mul_f32x2(f32x2(s[g][e], s[g][e + 1]), f32x2(ks.x, ks.y)), c2, f32x2(ev.x, ev.y)));
+            const float2 y1 = unpack_f32x2(fma_f32x2(mul_f32x2(f32x2(s[g][e + 2], s[g][e + 3]), f32x2(ks.z, ks.w)), c2, f32x2(ev.z, ev.w)));
+            s[g][e] = y0.x; s[g][e + 1] = y0.y; s[g][e + 2] = y1.x; s[g][e + 3] = y1.y;
+          }
+      }
+      if (edge) {
+        const int first = kt * kTile;
+        const int hi = pos - first;                                            // columns past it are hidden
+        const int lo = a.window > 0 && pos >= a.window ? max(pos - a.window + 1 - first, 0) : 0;  // those before it too, but for
+        const int sink = a.n_sink - first;                                     // the first tokens
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const int col = 32 * g + e;
+            if (col > hi || (col < lo && col >= sink)) s[g][e] = -INFINITY;
+          }
+        // 0 * NaN must not reach a row that does not see the key: such value rows were cleared,
+        // and the rows that do see one become NaN here.
+        if constexpr (!kE4m3) {
+          wait(&b.vok[sv], vphase >> sv);
+          vphase ^= 1u << sv;
+        }
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const uint32_t bad = b.bad[sv][g];
+          if (bad)
+            for (int e = 0; e < 32; ++e)
+              if (((bad >> e) & 1) && sees(pos, first + 32 * g + e, a.window, a.n_sink)) l2 = f32x2(__uint_as_float(0x7fffffffu), 0.f);
+        }
+      }
+      float mx[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        mx[g] = fmaxf(s[g][0], s[g][1]);
+#pragma unroll
+        for (int e = 2; e < 32; e += 2) mx[g] = fmaxf(mx[g], fmaxf(s[g][e], s[g][e + 1]));
+      }
+      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      const float unit = kE4m3 ? 1.f : c;
+      const bool grow = (top - m) * unit > kLazy;  // also from -inf to anything; never for nothing visible
+      if (__any_sync(0xffffffffu, grow)) {
+        const float mn = grow ? top : m;
+        const float f = grow ? exp2_fast((m - mn) * unit) : 1.f;
+        m = mn;
+        l2 = mul_f32x2(l2, f32x2(f, f));
+        if (i > walk.begin) {
+          // The scores' barrier stands for every product issued before them, the last P V among them.
+#pragma unroll 1
+          for (int g = 0; g < 8; ++g) {
+            float o[16];
+            tmem_ld16(to + 16 * g, o);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) o[e] *= f;
+            tmem_st16(to + 16 * g, o);
+          }
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : m * unit;
+      const uint64_t u2 = f32x2(unit, unit), nb2 = f32x2(-base, -base);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        float pk[32];
+#pragma unroll
+        for (int e = 0; e < 64; e += 2) {
+          const int g = 2 * h + (e >> 5), k = e & 31;
+          const uint64_t x = kE4m3 ? add_f32x2(f32x2(s[g][k], s[g][k + 1]), nb2) : fma_f32x2(f32x2(s[g][k], s[g][k + 1]), u2, nb2);
+          const float2 y = unpack_f32x2(x);
+          const float p0 = exp2_fast(y.x), p1 = exp2_fast(y.y);
+          // weights rounded once, to the values' type: f16 2^-11, bf16 2^-8; the sum keeps 32 bits
+          if constexpr (kE4m3) {
+            float2 rv = *reinterpret_cast<const float2*>(vec + 256 + 64 * h + e);
+            if (edge) {  // a hidden key's scale may be NaN; its weight is 0 whatever it says
+              rv.x = p0 == 0.f ? 0.f : rv.x;
+              rv.y = p1 == 0.f ? 0.f : rv.y;
+            }
+            l2 = fma_f32x2(f32x2(p0, p1), f32x2(rv.x, rv.y), l2);
+            pk[e >> 1] = __uint_as_float(pack_half2(p0, p1));
+          } else {
+            l2 = add_f32x2(l2, f32x2(p0, p1));
+            pk[e >> 1] = __uint_as_float(pack_bf162(p0, p1));
+          }
+        }
+        tmem_st32(ts + 32 * h, pk);
+      }
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&b.p_full[t]);
+    }
+    // ---- the item's (or part's) rows
+    wait(&b.o_full[t], items);
+    ++items;
+    ++seen;
+    tc_fence_after();
+    const float2 lp = unpack_f32x2(l2);
+    const float l = lp.x + lp.y;
+    const float ml = kE4m3 ? m : m * c;
+    const int slot = walk.part_slot();
+    if (slot >= 0) {
+      const int64_t at = static_cast<int64_t>(slot) * p.s.part_rows + 128 * t + tid;
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+        float o[32];
+        tmem_ld32(to + 32 * g, o);
+        float4* dst = reinterpret_cast<float4*>(p.s.part_o + at * 128 + 32 * g);
+        if (live)
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) dst[e >> 2] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+      }
+      if (live) p.s.part_ml[at] = make_float2(ml, l);
+    } else {
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      const int64_t orow = live ? w.o_row(a, row) : 0;
+#pragma unroll 1
+      for (int g = 0; g < 4; ++g) {
+        float o[32];
+        tmem_ld32(to + 32 * g, o);
+        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * 128 + 32 * g);
+        if (live)
+#pragma unroll
+          for (int e = 0; e < 32; e += 8)
+            dst[e >> 3] = make_uint4(pack_bf162(o[e] * inv, o[e + 1] * inv), pack_bf162(o[e + 2] * inv, o[e + 3] * inv),
+                                     pack_bf162(o[e + 4] * inv, o[e + 5] * inv), pack_bf162(o[e + 6] * inv, o[e + 7] * inv));
+      }
+      if (live && a.lse) a.lse[orow] = lse_of(ml, l);
+    }
+    tc_fence_before();
+  } while (walk.next());
+  if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+}
+
+template <bool kE4m3>
+__global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1) attn_chunk_kernel(const __grid_constant__ ChunkParams p) {
+  using C = Cfg<kE4m3>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Bars b;
+  uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < 5; ++i) {
+      mbar_init(&b.full[i], kE4m3 ? 4 : 1);
+      mbar_init(&b.empty[i], 1);
+      mbar_init(&b.vok[i], 2);
+    }
+    for (int i = 0; i < 3; ++i) { mbar_init(&b.st_full[i], 1); mbar_init(&b.st_empty[i], 4); }
+    mbar_init(&b.q_full, 2);
+    mbar_init(&b.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&b.s_full[i], 1);
+      mbar_init(&b.p_full[i], 4);
+      mbar_init(&b.pv_done[i], 1);
+      mbar_init(&b.o_full[i], 1);
+    }
+    mbar_init(&b.drain, 1);
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  Walk walk(p.a, p.s);
+  const bool any = walk.template start<C::kThreads>(tid);  // has the barrier that publishes the mbarriers
+  if (!any) return;
+  if (warp == 8) {
+    tmem_alloc(&b.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  // registers: 168 a thread at launch of 384 (504 of each group's thread), 128 of 512 (512)
+  if (warp < 8) {
+    if constexpr (kE4m3) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n" ::: "memory");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n" ::: "memory");
+    softmax_group<kE4m3>(p, walk, sm, b, warp >> 2, tid & 127);
+  } else {
+    if constexpr (kE4m3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
+    if (warp == 8) {
+      if (elect_one_sync()) mma_thread<kE4m3>(p, walk, sm, b);
+      __syncwarp();
+    } else if (warp == 9) {
+      load_warp<kE4m3>(p, walk, sm, b, tid & 31);
+    } else if (warp < 12) {
+      query_warps<kE4m3>(p, walk, sm, b, tid - 320);
+    } else {
+      if constexpr (kE4m3) convert_group(p, walk, sm, b, tid - 384);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(b.tmem, 512);
+}
+
+template <bool kE4m3>
+cudaError_t launch_chunk(const ChunkParams& p) {
+  constexpr int bytes = Cfg<kE4m3>::kSmBytes;
+  auto kern = attn_chunk_kernel<kE4m3>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  kern<<<p.s.grid, Cfg<kE4m3>::kThreads, bytes, p.a.stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t attn_chunk_workspace(int n_seq, int64_t tokens, int group, int num_sms) {
+  return attn_split_bytes(num_sms, kRows, attn_max_items(n_seq, tokens, group, kRows));
+}
+
+cudaError_t launch_attn_chunk(const AttnArgs& a, int num_sms) {
+  const int G = a.H / a.cache.heads;
+  ChunkParams p;
+  memset(&p, 0, sizeof(p));
+  p.a = a;
+  attn_split_layout(&p.s, a.workspace, num_sms, kRows, attn_max_items(a.n_seq, a.tokens, G, kRows));
+  p.s.min_tiles = 1;
+  if (!make_cache_maps(a.cache, kTile, 1, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
+  cudaError_t e = launch_attn_plan(a, p.s, kRows, kTile);
+  if (e != cudaSuccess) return e;
+  e = a.cache.e4m3 ? launch_chunk<true>(p) : launch_chunk<false>(p);
+  if (e != cudaSuccess) return e;
+  return launch_attn_join(p.a, p.s);
+}
+
+}  // namespace kda

@@ -25,8 +25,9 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// One pool: bf16 rows as two 64-channel panels (5-D), e4m3 rows whole (4-D), 128-byte swizzle.
-bool rows_map(CUtensorMap* m, const void* base, const int64_t* stride, const KvCache& c, int tile) {
+// One pool: bf16 rows as two 64-channel panels (5-D), `panels` of them a box, e4m3 rows whole
+// (4-D), 128-byte swizzle.
+bool rows_map(CUtensorMap* m, const void* base, const int64_t* stride, const KvCache& c, int tile, int panels) {
   const cuuint32_t box_tok = static_cast<cuuint32_t>(c.page_size < tile ? c.page_size : tile);
   const cuuint64_t P = c.page_size, H = c.heads, N = c.n_pages > 0 ? c.n_pages : 1;
   const cuuint32_t es[5] = {1, 1, 1, 1, 1};
@@ -42,7 +43,7 @@ bool rows_map(CUtensorMap* m, const void* base, const int64_t* stride, const KvC
     const cuuint64_t dims[5] = {64, P, 2, H, N};
     const cuuint64_t st[4] = {2 * static_cast<cuuint64_t>(stride[2]), 128, 2 * static_cast<cuuint64_t>(stride[1]),
                               2 * static_cast<cuuint64_t>(stride[0])};
-    const cuuint32_t box[5] = {64, box_tok, 2, 1, 1};
+    const cuuint32_t box[5] = {64, box_tok, static_cast<cuuint32_t>(panels), 1, 1};
     r = encode_fn()(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, st, box, es,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
@@ -176,9 +177,10 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
-bool make_cache_maps(const KvCache& c, int tile, CUtensorMap* k, CUtensorMap* v, CUtensorMap* ks, CUtensorMap* vs) {
+bool make_cache_maps(const KvCache& c, int tile, int panels, CUtensorMap* k, CUtensorMap* v, CUtensorMap* ks,
+                     CUtensorMap* vs) {
   if (!encode_fn()) return false;
-  if (!rows_map(k, c.k, c.k_stride, c, tile) || !rows_map(v, c.v, c.v_stride, c, tile)) return false;
+  if (!rows_map(k, c.k, c.k_stride, c, tile, panels) || !rows_map(v, c.v, c.v_stride, c, tile, panels)) return false;
   return !c.e4m3 || (scale_map(ks, c.ks, c.ks_stride, c, tile) && scale_map(vs, c.vs, c.vs_stride, c, tile));
 }
 

@@ -505,7 +505,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms) {
   const int grid = 2 * num_sms;
   attn_split_layout(&p.s, a.workspace, grid, kTileRows * rg, 0);
   p.s.min_tiles = kMinTiles;
-  if (!make_cache_maps(a.cache, kTile, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
+  if (!make_cache_maps(a.cache, kTile, 2, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
   cudaError_t e;
   if (a.cache.e4m3)
     e = rg == 1 ? launch_short<true, 1>(p, grid) : rg == 2 ? launch_short<true, 2>(p, grid) : launch_short<true, 4>(p, grid);
@@ -515,19 +515,26 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms) {
   return launch_attn_join(p.a, p.s);
 }
 
+namespace {
+// Chunks of up to 64 rows (tokens x shared heads) a sequence on average stay with this kernel.
+bool short_chunks(int n_seq, int64_t tokens, int group) { return tokens * group <= static_cast<int64_t>(kMaxRows) * n_seq; }
+}  // namespace
+
 size_t attn_prefill_workspace(int n_seq, int64_t tokens, int H, int kv_heads, int num_sms) {
+  if (!short_chunks(n_seq, tokens, H / kv_heads)) return attn_chunk_workspace(n_seq, tokens, H / kv_heads, num_sms);
   return attn_split_bytes(2 * num_sms, kMaxRows, attn_max_items(n_seq, tokens, H / kv_heads, kMaxRows));
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, int num_sms) {
   const int G = a.H / a.cache.heads;
+  if (!short_chunks(a.n_seq, a.tokens, G)) return launch_attn_chunk(a, num_sms);
   ShortParams p;
   memset(&p, 0, sizeof(p));
   p.a = a;
   const int grid = 2 * num_sms;
   attn_split_layout(&p.s, a.workspace, grid, kMaxRows, attn_max_items(a.n_seq, a.tokens, G, kMaxRows));
   p.s.min_tiles = kMinTiles;
-  if (!make_cache_maps(a.cache, kTile, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
+  if (!make_cache_maps(a.cache, kTile, 2, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
   cudaError_t e = launch_attn_plan(a, p.s, kMaxRows, kTile);
   if (e != cudaSuccess) return e;
   e = a.cache.e4m3 ? launch_short<true, 4>(p, grid) : launch_short<false, 4>(p, grid);
