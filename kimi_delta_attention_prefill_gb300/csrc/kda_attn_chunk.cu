@@ -61,12 +61,12 @@ struct Cfg {
 
 struct Bars {
   uint64_t full[5], empty[5];      // slots of K / V tiles
-  uint64_t vok[5];                 // bf16: an edge tile's values have been looked through
+  uint64_t v_ask, v_ok;            // bf16: an edge tile's values are there / have been looked through
   uint64_t st_full[3], st_empty[3];  // stages of codes
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], pv_done[2], o_full[2];
   uint64_t drain;
-  uint32_t bad[5][4];              // edge tiles: keys with a non-finite value row
+  uint32_t bad[5][4];              // edge tiles, by slot: keys with a non-finite value row
   uint32_t tmem;
 };
 
@@ -113,7 +113,7 @@ __device__ void load_warp(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const uint32_t s = n % kRing;
-        if (n >= kRing && !mbar_wait(&empty[s], (n / kRing - 1) & 1)) {
+        if (n >= kRing && !bar_wait(&empty[s], (n / kRing - 1) & 1)) {
           report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
           return;
         }
@@ -146,10 +146,10 @@ __device__ void mma_thread(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& 
   const uint64_t dv = smem_desc(smem_u32(sm + C::kSmKV), kPanel, 1024, kSwizzle128B);
   bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!dead && !mbar_wait(bar, parity & 1)) dead = true;
+    if (!dead && !bar_wait(bar, parity & 1)) dead = true;
     tc_fence_after();
   };
-  uint32_t n = 0, items = 0, vok = 0;   // ring position (K: even, V: odd), items, vok phases of the slots
+  uint32_t n = 0, items = 0, edges = 0;  // ring position (K: even, V: odd), items, edge tiles (bf16)
   uint32_t tiles[2] = {0, 0};           // tiles begun of A and B
   auto qk = [&](int t, uint32_t slot) {
     if (dead) return;
@@ -174,14 +174,18 @@ __device__ void mma_thread(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& 
     for (int i = walk.begin; i < walk.end; ++i, n += 2) {
       const uint32_t sv = (n + 1) % C::kSlots, sk = (n + 2) % C::kSlots;
       const bool more = i + 1 < walk.end;
+      // Edge tiles one after the other: asked for here, where the barrier's every phase is seen, so
+      // that the warps that look the values through need not follow the ring.
+      const bool edge = !kE4m3 && edge_tile(a, w.tiles.at(i), p_first, p_last);
+      if (edge) {
+        wait(&b.full[sv], (n + 1) / C::kSlots);
+        mbar_arrive(&b.v_ask);
+      }
       for (int t = 0; t < halves; ++t) {
         wait(&b.p_full[t], tiles[t]);
         if (t == 0) {
           wait(&b.full[sv], (n + 1) / C::kSlots);
-          if (!kE4m3 && edge_tile(a, w.tiles.at(i), p_first, p_last)) {
-            wait(&b.vok[sv], vok >> sv);
-            vok ^= 1u << sv;
-          }
+          if (edge) wait(&b.v_ok, edges++);
         }
         if (!dead) {
 #pragma unroll
@@ -207,7 +211,7 @@ __device__ void mma_thread(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& 
   } while (walk.next());
   // nothing of this block's may be in flight when it ends
   mma_commit(&b.drain);
-  if (!mbar_wait(&b.drain, 0)) dead = true;
+  if (!bar_wait(&b.drain, 0)) dead = true;
   if (dead) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
@@ -224,11 +228,11 @@ __device__ void query_warps(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars&
   const uint32_t flip = !kE4m3 && a.scale_log2 < 0.f ? 0x80008000u : 0u;
   const bool zero = !kE4m3 && a.scale_log2 == 0.f;
   float* qexp = reinterpret_cast<float*>(sm + C::kSmExp);
-  uint32_t n = 0, items = 0;
+  uint32_t n = 0, items = 0, edges = 0;
   bool dead = false;
   do {
     const Item& w = walk.item;
-    if (items > 0 && !dead && !mbar_wait(&b.q_empty, (items - 1) & 1)) dead = true;
+    if (items > 0 && !dead && !bar_wait(&b.q_empty, (items - 1) & 1)) dead = true;
     constexpr int kBatch = 8;
     for (int r0 = grp; r0 < kRows; r0 += 4 * kBatch) {
       uint4 x[kBatch];
@@ -268,7 +272,7 @@ __device__ void query_warps(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars&
       for (int i = walk.begin; i < walk.end; ++i, n += 2) {
         if (!edge_tile(a, w.tiles.at(i), p_first, p_last)) continue;
         const uint32_t s = (n + 1) % C::kSlots;
-        if (!dead && !mbar_wait(&b.full[s], ((n + 1) / C::kSlots) & 1)) dead = true;
+        if (!dead && !bar_wait(&b.v_ask, edges++ & 1)) dead = true;
         // thread = 2 keys: a row of 128 values with a NaN or an infinity is cleared and noted
         for (int q = 0; q < 2; ++q) {
           const int key = tid + 64 * q;
@@ -290,7 +294,7 @@ __device__ void query_warps(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars&
         }
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&b.vok[s]);
+        if (lane == 0) mbar_arrive(&b.v_ok);
       }
     }
   } while (walk.next());
@@ -316,7 +320,7 @@ __device__ void convert_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const uint32_t st = n % C::kStages, s = n % C::kSlots;
-        if (!dead && !mbar_wait(&b.st_full[st], (n / C::kStages) & 1)) dead = true;
+        if (!dead && !bar_wait(&b.st_full[st], (n / C::kStages) & 1)) dead = true;
         const uint8_t* src = sm + C::kSmStage + st * kStage;
         uint4 c[8];
 #pragma unroll
@@ -337,9 +341,9 @@ __device__ void convert_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
             for (int k = 0; k < 8; ++k) c[k] = make_uint4(0, 0, 0, 0);
           }
           const uint32_t m = __ballot_sync(0xffffffffu, nan != 0);
-          if (n >= C::kSlots && !dead && !mbar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) dead = true;
+          if (n >= C::kSlots && !dead && !bar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) dead = true;
           if (lane == 0) b.bad[s][warp] = m;
-        } else if (n >= C::kSlots && !dead && !mbar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) {
+        } else if (n >= C::kSlots && !dead && !bar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) {
           dead = true;
         }
         float* vec = reinterpret_cast<float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 384;
@@ -375,10 +379,10 @@ __device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
   const int lane = tid & 31;
   const uint32_t tl = static_cast<uint32_t>(tid & 96) << 16;
   const uint32_t ts = b.tmem + tl + 128 * t, to = b.tmem + tl + 256 + 128 * t;
-  uint32_t n = 0, tiles = 0, items = 0, vphase = 0, seen = 0;  // seen: items of the block, items: those with rows here
+  uint32_t n = 0, tiles = 0, items = 0, edges = 0, seen = 0;  // seen: items of the block, items: those with rows here
   bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (!dead && !mbar_wait(bar, parity & 1)) dead = true;
+    if (!dead && !bar_wait(bar, parity & 1)) dead = true;
   };
   do {
     const Item& w = walk.item;
@@ -387,7 +391,7 @@ __device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
       if constexpr (!kE4m3) {
         const int pf = w.p_first(), pl = w.p_last();
         for (int i = walk.begin; i < walk.end; ++i, n += 2)
-          if (edge_tile(a, w.tiles.at(i), pf, pl)) vphase ^= 1u << ((n + 1) % C::kSlots);
+          if (edge_tile(a, w.tiles.at(i), pf, pl)) ++edges;
       } else {
         n += 2 * (walk.end - walk.begin);
       }
@@ -444,8 +448,7 @@ __device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
         // 0 * NaN must not reach a row that does not see the key: such value rows were cleared,
         // and the rows that do see one become NaN here.
         if constexpr (!kE4m3) {
-          wait(&b.vok[sv], vphase >> sv);
-          vphase ^= 1u << sv;
+          wait(&b.v_ok, edges++);
         }
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -567,9 +570,10 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1) attn_chunk_kernel(con
     for (int i = 0; i < 5; ++i) {
       mbar_init(&b.full[i], kE4m3 ? 4 : 1);
       mbar_init(&b.empty[i], 1);
-      mbar_init(&b.vok[i], 2);
     }
     for (int i = 0; i < 3; ++i) { mbar_init(&b.st_full[i], 1); mbar_init(&b.st_empty[i], 4); }
+    mbar_init(&b.v_ask, 1);
+    mbar_init(&b.v_ok, 2);
     mbar_init(&b.q_full, 2);
     mbar_init(&b.q_empty, 1);
     for (int i = 0; i < 2; ++i) {

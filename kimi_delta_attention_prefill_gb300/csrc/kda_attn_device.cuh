@@ -30,6 +30,21 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Wait for a barrier's phase, given up after two seconds (false): then the caller reports
+// KDA_ERR_TIMEOUT, stops waiting and leaves in order.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
+  for (int i = 0; i < 64; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0, t1;
+  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
+  do {
+    for (int i = 0; i < 16; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t1));
+  } while (t1 - t0 < 2000000000ull);
+  return false;
+}
+
 // Two e4m3 codes (low 16 bits) as two f16 values, exactly.
 __device__ __forceinline__ uint32_t e4m3_half2(uint32_t pair) {
   uint32_t r;

@@ -144,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           }
         }
         const int s = it % St::kCount;
-        if (it >= St::kCount && !mbar_wait(&empty[s], ((it / St::kCount) - 1) & 1)) {
+        if (it >= St::kCount && !bar_wait(&empty[s], ((it / St::kCount) - 1) & 1)) {
           report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
           return;
         }
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
     for (int i = walk.begin; i < walk.end; ++i, ++it) {
       const int s = it % St::kCount;
       // after a wait that ran out the loop goes on without waiting, so that every barrier is still met
-      if (!dead && !mbar_wait(&full[s], (it / St::kCount) & 1)) dead = true;
+      if (!dead && !bar_wait(&full[s], (it / St::kCount) & 1)) dead = true;
       const uint32_t kb = smem_u32(sm + s * St::kTotal), vb = kb + St::kBytes;
       const int key0 = kt.at(i) * kTile + kg * kKeys;  // first key of this warp
       float x[kNT][4];

@@ -222,6 +222,19 @@ def test_prefill(fp8, page, layout, H, Hkv, new, past):
         check(o, lse, reference(c, torch.split(q, new), new, lens, window, sink, D ** -0.5))
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("new,past,window,sink", [([700, 64, 300], [2500, 900, 0], 1100, 4), ([900], [3100], 0, 0),
+                                                  ([130, 1500], [1700, 20], 640, 200)])
+def test_prefill_edges_far_apart(fp8, new, past, window, sink):
+    """Masked tiles with runs of whole tiles between them, longer than the ring of stages."""
+    g = gen(window)
+    lens = [a + b for a, b in zip(new, past)]
+    c = Cache(lens, 1, 128, fp8, g)
+    q = torch.randn(sum(new), 2, D, generator=g).to(torch.bfloat16)
+    o, lse = run_prefill(c, q.cuda(), new, lens, window, sink)
+    check(o, lse, reference(c, torch.split(q, new), new, lens, window, sink, D ** -0.5))
+
+
 def test_prefill_rows_before_the_first_token():
     """More new tokens than the cache holds: the first rows see nothing."""
     g = gen(31)
