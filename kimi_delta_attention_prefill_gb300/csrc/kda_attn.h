@@ -92,7 +92,8 @@ struct AttnSplit {
   int64_t max_items = 0;
   int grid = 0;
   int part_rows = 0;
-  int min_tiles = 1;
+  int min_tiles = 1;  // least share of a block
+  int item_cost = 0;  // what an item costs besides its key tiles, in key tiles
 };
 size_t attn_split_bytes(int grid, int part_rows, int64_t max_items);
 void attn_split_layout(AttnSplit* s, void* workspace, int grid, int part_rows, int64_t max_items);

@@ -45,6 +45,7 @@ constexpr int kPanel = kTile * 128;     // 64 channels of 128 rows, 16-bit
 constexpr int kSlot = 2 * kPanel;       // one tile of K or V (or 128 rows of Q) as 16-bit values
 constexpr int kStage = kTile * 128 + 8 * 128;  // a tile of codes and a 128-byte slot of scale bytes per page
 constexpr float kLazy = 8.f;
+constexpr int kMinTiles = 4, kItemCost = 3;
 
 template <bool kE4m3>
 struct Cfg {
@@ -59,13 +60,28 @@ struct Cfg {
   static constexpr int kSmBytes = kSmExp + (kE4m3 ? 2048 : 0) + 1024;
 };
 
+// One item (or part) of the block's share, as the copy warp hands it to the others.
+struct Job {
+  int head, row0, rows, last_row, len, n_tok;
+  int sink, lo;         // its key tiles
+  int begin, end;       // the visits that are this block's; none: the share is done
+  int p_first, p_last;  // positions of its first and last row
+  int slot;             // of the workspace, -1: whole
+  int seq;
+  int64_t base;
+  __device__ int tile(int i) const { return i < sink ? i : lo + (i - sink); }
+};
+constexpr int kJobs = 4;
+
 struct Bars {
   uint64_t full[5], empty[5];      // slots of K / V tiles
   uint64_t v_ask, v_ok;            // bf16: an edge tile's values are there / have been looked through
   uint64_t st_full[3], st_empty[3];  // stages of codes
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2], pv_done[2], o_full[2];
+  uint64_t job_full[kJobs], job_empty[kJobs];
   uint64_t drain;
+  Job job[kJobs];
   uint32_t bad[5][4];              // edge tiles, by slot: keys with a non-finite value row
   uint32_t tmem;
 };
@@ -78,6 +94,24 @@ struct ChunkParams {
 
 using Walk = ItemWalk<kRows, kTile>;
 
+// The jobs in order, for one warp (or its one thread at work): next() waits for the next.
+struct JobFeed {
+  Bars& b;
+  bool& dead;
+  uint32_t k = 0;
+  __device__ const Job* next() {
+    if (!dead && !bar_wait(&b.job_full[k % kJobs], (k / kJobs) & 1)) dead = true;
+    const Job* j = &b.job[k % kJobs];
+    return dead || j->begin == j->end ? nullptr : j;
+  }
+  // By one thread, when its warp needs nothing of the job any more.
+  __device__ void done() { mbar_arrive(&b.job_empty[k % kJobs]); }
+};
+__device__ __forceinline__ int64_t job_q_offset(const AttnArgs& a, const Job& j, int row) {
+  const int G = a.H / a.cache.heads, t = row / G, g = row - t * G;
+  return (j.base + t) * a.q_stride[1] + (static_cast<int64_t>(j.head) * G + g) * a.q_stride[2];
+}
+
 // Whether some row of the item does not see some key of key tile t.
 __device__ __forceinline__ bool edge_tile(const AttnArgs& a, int t, int p_first, int p_last) {
   const int first = t * kTile, last = first + kTile - 1;
@@ -85,8 +119,9 @@ __device__ __forceinline__ bool edge_tile(const AttnArgs& a, int t, int p_first,
 }
 
 // ---------------------------------------------------------------------------- copies
+// The copy warp is furthest ahead of all: it walks the share and hands out the jobs.
 template <bool kE4m3>
-__device__ void load_warp(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b, int lane) {
+__device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) {
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
   const int P = min(a.cache.page_size, kTile), n_blk = kTile / P;
@@ -94,15 +129,31 @@ __device__ void load_warp(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b
   constexpr int kRing = kE4m3 ? C::kStages : C::kSlots;
   uint64_t* full = kE4m3 ? b.st_full : b.full;
   uint64_t* empty = kE4m3 ? b.st_empty : b.empty;
-  uint32_t n = 0;
-  do {
+  uint32_t n = 0, k = 0;
+  Walk walk(p.a, p.s);
+  bool more = walk.start_plan();
+  for (;; ++k) {
+    if (k >= kJobs && !bar_wait(&b.job_empty[k % kJobs], (k / kJobs - 1) & 1)) break;
     const Item& w = walk.item;
-    const int p_first = w.p_first(), p_last = w.p_last();
-    for (int i = walk.begin; i < walk.end; ++i) {
-      const int j0 = w.tiles.at(i) * kTile + blk * P;
+    if (lane == 0) {
+      Job& j = b.job[k % kJobs];
+      j.begin = j.end = 0;
+      if (more) {
+        j.head = w.head; j.row0 = w.row0; j.rows = w.rows; j.last_row = w.last_row; j.len = w.len; j.n_tok = w.n_tok;
+        j.sink = w.tiles.sink; j.lo = w.tiles.lo; j.begin = walk.begin; j.end = walk.end;
+        j.p_first = w.p_first(); j.p_last = w.p_last(); j.slot = walk.part_slot(true); j.seq = w.seq; j.base = w.base;
+      }
+      mbar_arrive(&b.job_full[k % kJobs]);
+    }
+    if (!more) return;
+    const int p_first = w.p_first(), p_last = w.p_last(), begin = walk.begin, end = walk.end, head = w.head;
+    const int32_t* table = a.page_table + static_cast<int64_t>(w.seq) * a.max_pages;
+    const KeyTiles kt = w.tiles;
+    for (int i = begin; i < end; ++i) {
+      const int j0 = kt.at(i) * kTile + blk * P;
       int page = -1;
       if (blk < n_blk && j0 <= p_last) {
-        page = a.page_table[static_cast<int64_t>(w.seq) * a.max_pages + (j0 >> a.cache.page_log2)];
+        page = table[j0 >> a.cache.page_log2];
         if (page < 0 || page >= a.cache.n_pages) {
           const bool needed = a.window == 0 || j0 + P - 1 > p_first - a.window || j0 < a.n_sink;
           if (needed) report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
@@ -122,21 +173,23 @@ __device__ void load_warp(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b
         if (blk < n_blk) {
           if constexpr (kE4m3) {
             uint8_t* st = sm + C::kSmStage + s * kStage;
-            tma_load_4d(st + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, w.head, page);
-            tma_load_3d(st + kTile * 128 + blk * 128, kv ? &p.tvs : &p.tks, &full[s], slot, w.head, page);
+            tma_load_4d(st + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, head, page);
+            tma_load_3d(st + kTile * 128 + blk * 128, kv ? &p.tvs : &p.tks, &full[s], slot, head, page);
           } else {
             uint8_t* st = sm + C::kSmKV + s * kSlot;
-            tma_load_5d(st + panel * kPanel + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, panel, w.head, page);
+            tma_load_5d(st + panel * kPanel + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, panel, head, page);
           }
         }
       }
     }
-  } while (walk.next());
+    more = walk.next();
+  }
+  report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
 // -------------------------------------------------------------------------- products
 template <bool kE4m3>
-__device__ void mma_thread(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b) {
+__device__ void mma_thread(const ChunkParams& p, uint8_t* sm, Bars& b) {
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
   const uint32_t tmem = b.tmem;
@@ -159,24 +212,26 @@ __device__ void mma_thread(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& 
               dk + ((slot * kSlot + (kk >> 2) * kPanel + 32 * (kk & 3)) >> 4), id_qk, kk > 0);
     mma_commit(&b.s_full[t]);
   };
-  do {
-    const Item& w = walk.item;
+  JobFeed feed{b, dead};
+  while (const Job* jp = feed.next()) {
+    const Job w = *jp;
+    feed.done();
+    ++feed.k;
     const int halves = w.last_row - w.row0 >= 128 ? 2 : 1;
-    const int p_first = w.p_first(), p_last = w.p_last();
     wait(&b.q_full, items);
     {
       const uint32_t s = n % C::kSlots;
       wait(&b.full[s], n / C::kSlots);
       for (int t = 0; t < halves; ++t) qk(t, s);  // S is free: the last P V over it is done (below)
       if (!dead) mma_commit(&b.empty[s]);
-      if (!dead && walk.end - walk.begin == 1) mma_commit(&b.q_empty);
+      if (!dead && w.end - w.begin == 1) mma_commit(&b.q_empty);
     }
-    for (int i = walk.begin; i < walk.end; ++i, n += 2) {
+    for (int i = w.begin; i < w.end; ++i, n += 2) {
       const uint32_t sv = (n + 1) % C::kSlots, sk = (n + 2) % C::kSlots;
-      const bool more = i + 1 < walk.end;
+      const bool more = i + 1 < w.end;
       // Edge tiles one after the other: asked for here, where the barrier's every phase is seen, so
       // that the warps that look the values through need not follow the ring.
-      const bool edge = !kE4m3 && edge_tile(a, w.tiles.at(i), p_first, p_last);
+      const bool edge = !kE4m3 && edge_tile(a, w.tile(i), w.p_first, w.p_last);
       if (edge) {
         wait(&b.full[sv], (n + 1) / C::kSlots);
         mbar_arrive(&b.v_ask);
@@ -191,7 +246,7 @@ __device__ void mma_thread(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& 
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk)
             mma_f16_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, dv + ((sv * kSlot + kk * 2048) >> 4), id_pv,
-                       kk > 0 || i > walk.begin);
+                       kk > 0 || i > w.begin);
           mma_commit(&b.pv_done[t]);
           if (t == halves - 1) mma_commit(&b.empty[sv]);
           if (!more) mma_commit(&b.o_full[t]);
@@ -204,11 +259,11 @@ __device__ void mma_thread(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& 
       }
       if (more && !dead) {
         mma_commit(&b.empty[sk]);
-        if (i + 2 == walk.end) mma_commit(&b.q_empty);
+        if (i + 2 == w.end) mma_commit(&b.q_empty);
       }
     }
     ++items;
-  } while (walk.next());
+  }
   // nothing of this block's may be in flight when it ends
   mma_commit(&b.drain);
   if (!bar_wait(&b.drain, 0)) dead = true;
@@ -221,7 +276,7 @@ __device__ void mma_thread(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& 
 // as negated queries and a scale of 0 as zero queries with any scale, so the softmax's scale c
 // is positive.
 template <bool kE4m3>
-__device__ void query_warps(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b, int tid) {
+__device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
   const int lane = tid & 31, sub = tid & 15, grp = tid >> 4;  // 4 groups of 16 lanes
@@ -230,8 +285,9 @@ __device__ void query_warps(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars&
   float* qexp = reinterpret_cast<float*>(sm + C::kSmExp);
   uint32_t n = 0, items = 0, edges = 0;
   bool dead = false;
-  do {
-    const Item& w = walk.item;
+  JobFeed feed{b, dead};
+  while (const Job* jp = feed.next()) {
+    const Job& w = *jp;
     if (items > 0 && !dead && !bar_wait(&b.q_empty, (items - 1) & 1)) dead = true;
     constexpr int kBatch = 8;
     for (int r0 = grp; r0 < kRows; r0 += 4 * kBatch) {
@@ -241,7 +297,7 @@ __device__ void query_warps(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars&
         const int row = w.row0 + r0 + 4 * u;
         x[u] = make_uint4(0, 0, 0, 0);
         if (row < w.rows && !zero)
-          x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + w.q_offset(a, row)) + sub);
+          x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + job_q_offset(a, w, row)) + sub);
       }
 #pragma unroll
       for (int u = 0; u < kBatch; ++u) {
@@ -268,9 +324,9 @@ __device__ void query_warps(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars&
     if (lane == 0) mbar_arrive(&b.q_full);
     ++items;
     if constexpr (!kE4m3) {
-      const int p_first = w.p_first(), p_last = w.p_last();
-      for (int i = walk.begin; i < walk.end; ++i, n += 2) {
-        if (!edge_tile(a, w.tiles.at(i), p_first, p_last)) continue;
+      const int begin = w.begin, end = w.end;
+      for (int i = begin; i < end; ++i, n += 2) {
+        if (!edge_tile(a, w.tile(i), w.p_first, w.p_last)) continue;
         const uint32_t s = (n + 1) % C::kSlots;
         if (!dead && !bar_wait(&b.v_ask, edges++ & 1)) dead = true;
         // thread = 2 keys: a row of 128 values with a NaN or an infinity is cleared and noted
@@ -297,14 +353,17 @@ __device__ void query_warps(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars&
         if (lane == 0) mbar_arrive(&b.v_ok);
       }
     }
-  } while (walk.next());
+    __syncwarp();
+    if (lane == 0) feed.done();
+    ++feed.k;
+  }
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
 // ------------------------------------------------------------------- codes to f16 tiles
 // Four warps, thread = key: 16 codes at a time to two 16-byte pieces of the f16 tile, and the
 // key's scales as the floats that the softmax needs.
-__device__ void convert_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b, int tid) {
+__device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
   using C = Cfg<true>;
   const AttnArgs& a = p.a;
   const int lane = tid & 31, warp = tid >> 5;
@@ -312,11 +371,12 @@ __device__ void convert_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
   const int sc_at = kTile * 128 + (tid >> p_log) * 128 + (tid & ((1 << p_log) - 1));
   uint32_t n = 0;
   bool dead = false;
-  do {
-    const Item& w = walk.item;
-    const int p_first = w.p_first(), p_last = w.p_last();
-    for (int i = walk.begin; i < walk.end; ++i) {
-      const bool edge = edge_tile(a, w.tiles.at(i), p_first, p_last);
+  JobFeed feed{b, dead};
+  while (const Job* jp = feed.next()) {
+    const Job& w = *jp;
+    const int begin = w.begin, end = w.end;
+    for (int i = begin; i < end; ++i) {
+      const bool edge = edge_tile(a, w.tile(i), w.p_first, w.p_last);
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const uint32_t st = n % C::kStages, s = n % C::kSlots;
@@ -367,13 +427,16 @@ __device__ void convert_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
         if (lane == 0) mbar_arrive(&b.full[s]);
       }
     }
-  } while (walk.next());
+    __syncwarp();
+    if (lane == 0) feed.done();
+    ++feed.k;
+  }
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
 // ---------------------------------------------------------------------------- softmax
 template <bool kE4m3>
-__device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bars& b, int t, int tid) {
+__device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t, int tid) {
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
   const int lane = tid & 31;
@@ -384,42 +447,47 @@ __device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead && !bar_wait(bar, parity & 1)) dead = true;
   };
-  do {
-    const Item& w = walk.item;
+  JobFeed feed{b, dead};
+  while (const Job* jp = feed.next()) {
+    const Job& w = *jp;
+    const int begin = w.begin, end = w.end;
     const int row = w.row0 + 128 * t + tid;
     if (w.row0 + 128 * t > w.last_row) {  // no rows of this tile
       if constexpr (!kE4m3) {
-        const int pf = w.p_first(), pl = w.p_last();
-        for (int i = walk.begin; i < walk.end; ++i, n += 2)
-          if (edge_tile(a, w.tiles.at(i), pf, pl)) ++edges;
-      } else {
-        n += 2 * (walk.end - walk.begin);
+        for (int i = begin; i < end; ++i)
+          if (edge_tile(a, w.tile(i), w.p_first, w.p_last)) ++edges;
       }
+      n += 2 * (end - begin);
       ++seen;
+      __syncwarp();
+      if (lane == 0) feed.done();
+      ++feed.k;
       continue;
     }
     const bool live = row < w.rows;
-    const int pos = live ? w.p_of_row(row) : -1;
-    const int p_first = w.p_first(), p_last = w.p_last();
+    const int G = a.H / a.cache.heads;
+    const int pos = live ? w.len - w.n_tok + row / G : -1;
     // scores to log2 units: bf16 S c (c > 0), e4m3 S ks c + ev
     const float sc = fabsf(a.scale_log2);
     const float c = kE4m3 ? a.scale_log2 : (sc == 0.f ? 1.f : sc);
     float crow = c;
     float m = -INFINITY;            // the reference that P is taken against (bf16: in units of S)
     uint64_t l2 = f32x2(0.f, 0.f);
-    for (int i = walk.begin; i < walk.end; ++i, n += 2) {
-      const int kt = w.tiles.at(i);
-      const bool edge = edge_tile(a, kt, p_first, p_last);
+    for (int i = begin; i < end; ++i, n += 2) {
+      const int kt = w.tile(i);
+      const bool edge = edge_tile(a, kt, w.p_first, w.p_last);
       const uint32_t sv = (n + 1) % C::kSlots;
       wait(&b.s_full[t], tiles);
       ++tiles;
       tc_fence_after();
       float s[4][32];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) tmem_ld32(ts + 32 * g, s[g]);
+      for (int g = 0; g < 4; ++g) tmem_ld32_async(ts + 32 * g, s[g]);
+#pragma unroll
+      for (int g = 0; g < 4; ++g) tmem_wait_ld32(s[g]);
       const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 384;
       if constexpr (kE4m3) {
-        if (i == walk.begin) crow = c * reinterpret_cast<const float*>(sm + C::kSmExp)[(seen & 1) * kRows + 128 * t + tid];
+        if (i == begin) crow = c * reinterpret_cast<const float*>(sm + C::kSmExp)[(seen & 1) * kRows + 128 * t + tid];
         wait(&b.full[sv], (n + 1) / C::kSlots);  // the value scales come with the values
         const uint64_t c2 = f32x2(crow, crow);
 #pragma unroll
@@ -473,7 +541,7 @@ __device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
         const float f = grow ? exp2_fast((m - mn) * unit) : 1.f;
         m = mn;
         l2 = mul_f32x2(l2, f32x2(f, f));
-        if (i > walk.begin) {
+        if (i > begin) {
           // The scores' barrier stands for every product issued before them, the last P V among them.
 #pragma unroll 1
           for (int g = 0; g < 8; ++g) {
@@ -525,7 +593,7 @@ __device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
     const float2 lp = unpack_f32x2(l2);
     const float l = lp.x + lp.y;
     const float ml = kE4m3 ? m : m * c;
-    const int slot = walk.part_slot();
+    const int slot = w.slot;
     if (slot >= 0) {
       const int64_t at = static_cast<int64_t>(slot) * p.s.part_rows + 128 * t + tid;
 #pragma unroll 1
@@ -540,7 +608,7 @@ __device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
       if (live) p.s.part_ml[at] = make_float2(ml, l);
     } else {
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t orow = live ? w.o_row(a, row) : 0;
+      const int64_t orow = live ? (w.base + row / G) * a.H + static_cast<int64_t>(w.head) * G + row % G : 0;
 #pragma unroll 1
       for (int g = 0; g < 4; ++g) {
         float o[32];
@@ -555,7 +623,10 @@ __device__ void softmax_group(const ChunkParams& p, Walk& walk, uint8_t* sm, Bar
       if (live && a.lse) a.lse[orow] = lse_of(ml, l);
     }
     tc_fence_before();
-  } while (walk.next());
+    __syncwarp();
+    if (lane == 0) feed.done();
+    ++feed.k;
+  }
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
@@ -582,13 +653,13 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1) attn_chunk_kernel(con
       mbar_init(&b.pv_done[i], 1);
       mbar_init(&b.o_full[i], 1);
     }
+    // a job is read by the product thread, the two query warps, the eight softmax warps and the converters
+    for (int i = 0; i < kJobs; ++i) { mbar_init(&b.job_full[i], 1); mbar_init(&b.job_empty[i], kE4m3 ? 15 : 11); }
     mbar_init(&b.drain, 1);
     fence_mbar_init();
+    p.s.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
   }
   pdl_launch_dependents();
-  Walk walk(p.a, p.s);
-  const bool any = walk.template start<C::kThreads>(tid);  // has the barrier that publishes the mbarriers
-  if (!any) return;
   if (warp == 8) {
     tmem_alloc(&b.tmem, 512);
     tmem_relinquish();
@@ -600,19 +671,19 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1) attn_chunk_kernel(con
   if (warp < 8) {
     if constexpr (kE4m3) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n" ::: "memory");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n" ::: "memory");
-    softmax_group<kE4m3>(p, walk, sm, b, warp >> 2, tid & 127);
+    softmax_group<kE4m3>(p, sm, b, warp >> 2, tid & 127);
   } else {
     if constexpr (kE4m3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
     if (warp == 8) {
-      if (elect_one_sync()) mma_thread<kE4m3>(p, walk, sm, b);
+      if (elect_one_sync()) mma_thread<kE4m3>(p, sm, b);
       __syncwarp();
     } else if (warp == 9) {
-      load_warp<kE4m3>(p, walk, sm, b, tid & 31);
+      load_warp<kE4m3>(p, sm, b, tid & 31);
     } else if (warp < 12) {
-      query_warps<kE4m3>(p, walk, sm, b, tid - 320);
+      query_warps<kE4m3>(p, sm, b, tid - 320);
     } else {
-      if constexpr (kE4m3) convert_group(p, walk, sm, b, tid - 384);
+      if constexpr (kE4m3) convert_group(p, sm, b, tid - 384);
     }
   }
   tc_fence_before();
@@ -643,7 +714,8 @@ cudaError_t launch_attn_chunk(const AttnArgs& a, int num_sms) {
   memset(&p, 0, sizeof(p));
   p.a = a;
   attn_split_layout(&p.s, a.workspace, num_sms, kRows, attn_max_items(a.n_seq, a.tokens, G, kRows));
-  p.s.min_tiles = 1;
+  p.s.min_tiles = kMinTiles;
+  p.s.item_cost = kItemCost;
   if (!make_cache_maps(a.cache, kTile, 1, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
   cudaError_t e = launch_attn_plan(a, p.s, kRows, kTile);
   if (e != cudaSuccess) return e;

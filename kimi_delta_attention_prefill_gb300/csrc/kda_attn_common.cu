@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
         item_sequence(a, b + lo, &w);
         d = make_int2(b + lo, static_cast<int>(k - first_item[lo]) * rows);
         item_tiles(a, d.y, rows, tile, &w);
-        count = w.tiles.count();
+        count = w.tiles.count() + s.item_cost;
       }
       int64_t sum;
       const int64_t before = block_scan(count, sh, &sum);

@@ -125,7 +125,9 @@ __device__ inline void item_tiles(const AttnArgs& a, int row0, int n, int tile, 
   if (w->tiles.count() == 0) w->tiles.hi = w->tiles.lo + 1;
 }
 
-// A block's way along the line of key tiles (AttnSplit).  In decode every sequence's row tiles
+// A block's way along the line (AttnSplit).  An item takes its key tiles' length on it and before
+// them item_cost more, for what an item costs whatever its length (queries, output); a border
+// that falls into that stretch is a border before the first tile.  In decode every sequence's row tiles
 // visit the same key tiles, so the line needs only the sequences' counts, which each block adds
 // up by itself; in prefill it comes from the plan.
 template <int kRows, int kTileKeys>
@@ -136,19 +138,46 @@ struct ItemWalk {
   int begin = 0, end = 0;   // key tile visits of the item that are this block's
   int64_t pos = 0, stop = 0, at = 0;  // on the line: where we are, the share's end, where the item begins
   int64_t blocks = 1, total = 0;
-  int64_t idx = 0;  // prefill: the plan's item
+  int idx = 0;      // prefill: the plan's item
   int unit = 0, n_units = 1;  // decode: head and row tile within the sequence
 
   __device__ ItemWalk(const AttnArgs& a_, const AttnSplit& s_) : a(a_), s(s_) {}
 
-  __device__ int decode_count(int seq) {  // key tiles of a row tile of the sequence; 0: bad
+  __device__ int length() const { return item.tiles.count() + s.item_cost; }  // the item's on the line
+  __device__ int decode_length(int seq) {  // of a row tile of the sequence; 0: bad
     const int len = a.kv_len[seq];
     if (len < 0 || len > static_cast<int64_t>(a.max_pages) * a.cache.page_size) {
       if (blockIdx.x == 0) report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
       return 0;
     }
     const int n = key_tiles(len - a.n_tok, len - 1, a.window, a.n_sink, kTileKeys).count();
-    return n > 0 ? n : 1;
+    return (n > 0 ? n : 1) + s.item_cost;
+  }
+
+  // Prefill, by any one thread or warp: the block's share from the plan.
+  __device__ bool start_plan() {
+    n_units = a.cache.heads;
+    total = *s.plan_total * n_units;
+    return total > 0 && take_share() && find_plan();
+  }
+  __device__ bool take_share() {
+    blocks = total / s.min_tiles;
+    blocks = blocks < 1 ? 1 : blocks > gridDim.x ? gridDim.x : blocks;
+    if (blockIdx.x >= blocks) return false;
+    pos = blockIdx.x * total / blocks;
+    stop = (blockIdx.x + 1) * total / blocks;
+    return true;
+  }
+  __device__ bool find_plan() {
+    const int64_t target = pos / n_units;
+    int lo = 0, hi = *s.plan_items;  // plan_start[lo] <= target < plan_start[hi]
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s.plan_start[mid] <= target) lo = mid; else hi = mid;
+    }
+    idx = lo;
+    load_plan();
+    return clip();
   }
 
   // Takes this block's share; false: there is none.  Called by all kThreads threads.
@@ -166,7 +195,7 @@ struct ItemWalk {
       sum = *s.plan_total;
       __syncthreads();
     } else {
-      for (int i = tid; i < a.n_seq; i += kThreads) sum += decode_count(i);
+      for (int i = tid; i < a.n_seq; i += kThreads) sum += decode_length(i);
 #pragma unroll
       for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
       if (lane == 0) sh_sum[warp] = sum;
@@ -177,25 +206,15 @@ struct ItemWalk {
       __syncthreads();
     }
     total = sum * n_units;
-    blocks = total / s.min_tiles;
-    blocks = blocks < 1 ? 1 : blocks > gridDim.x ? gridDim.x : blocks;
-    if (total == 0 || blockIdx.x >= blocks) return false;
-    pos = blockIdx.x * total / blocks;
-    stop = (blockIdx.x + 1) * total / blocks;
+    if (total == 0 || !take_share()) return false;
     const int64_t target = pos / n_units;
     if (a.cu) {
-      int64_t lo = 0, hi = *s.plan_items;  // plan_start[lo] <= target < plan_start[hi]
-      while (hi - lo > 1) {
-        const int64_t mid = (lo + hi) >> 1;
-        if (s.plan_start[mid] <= target) lo = mid; else hi = mid;
-      }
-      idx = lo;
-      load_plan();
+      return find_plan();
     } else {
       int64_t run = 0;
       for (int b = 0; b < a.n_seq; b += kThreads) {
         const int i = b + tid;
-        const int64_t c = i < a.n_seq ? decode_count(i) : 0;
+        const int64_t c = i < a.n_seq ? decode_length(i) : 0;
         int64_t incl = c;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -219,12 +238,11 @@ struct ItemWalk {
       item_sequence(a, sh_seq, &item);
       item_tiles(a, 0, rows, kTileKeys, &item);
       at = sh_at * n_units;
-      unit = static_cast<int>((pos - at) / item.tiles.count());
-      at += static_cast<int64_t>(unit) * item.tiles.count();
+      unit = static_cast<int>((pos - at) / length());
+      at += static_cast<int64_t>(unit) * length();
       set_unit();
     }
-    clip();
-    return true;
+    return clip();
   }
 
   __device__ void set_unit() {  // decode: heads outermost, so that row tiles of a head are neighbours
@@ -238,20 +256,20 @@ struct ItemWalk {
     item_sequence(a, d.x, &item);
     item_tiles(a, d.y, kRows, kTileKeys, &item);
     at = s.plan_start[idx] * n_units;
-    item.head = static_cast<int>((pos - at) / item.tiles.count());
-    at += static_cast<int64_t>(item.head) * item.tiles.count();
+    item.head = pos > at ? static_cast<int>((pos - at) / length()) : 0;
+    at += static_cast<int64_t>(item.head) * length();
   }
-  __device__ void clip() {
+  __device__ bool clip() {  // false: nothing of the item's tiles is in the share
     const int n = item.tiles.count();
-    begin = static_cast<int>(pos - at);
-    end = stop - at < n ? static_cast<int>(stop - at) : n;
+    const int64_t first = at + s.item_cost;
+    begin = pos > first ? static_cast<int>(pos - first) : 0;
+    end = stop - first < n ? static_cast<int>(stop - first) : n;
+    return end > begin;
   }
   // The next item of the share; false: the share is done.
   __device__ bool next() {
-    const int n = item.tiles.count();
-    pos = at + end;
-    if (pos >= stop) return false;
-    at += n;
+    at += length();
+    if (at >= stop) return false;
     if (a.cu) {
       if (++item.head == a.cache.heads) {
         ++idx;
@@ -260,25 +278,24 @@ struct ItemWalk {
     } else if (++unit == n_units) {
       unit = 0;
       int seq = item.seq + 1;
-      while (decode_count(seq) == 0) ++seq;  // there is one: the share goes on
+      while (decode_length(seq) == 0) ++seq;  // there is one: the share goes on
       item_sequence(a, seq, &item);
       item_tiles(a, 0, item.rows, kTileKeys, &item);
       set_unit();
     } else {
       set_unit();
     }
-    clip();
-    return true;
+    return clip();
   }
-  // Slot of the part at hand, or -1 when the block has the whole item.  Thread 0 also names the
-  // parts of an item that begins here and ends in a later block.
-  __device__ int part_slot() const {
+  // Slot of the part at hand, or -1 when the block has the whole item.  The thread that says
+  // `names` also names the parts of an item that begins here and ends in a later block.
+  __device__ int part_slot(bool names) const {
     const int n = item.tiles.count();
     if (begin == 0 && end == n) return -1;
     if (begin > 0) return 2 * blockIdx.x;
-    if (threadIdx.x == 0) {
+    if (names) {
       // the block that has the item's last tile: c1 = ceil(E C / W) - 1
-      const int64_t e = at + n;
+      const int64_t e = at + length();
       s.desc[blockIdx.x] = make_int4(item.seq, item.head, item.row0, static_cast<int>((e * blocks + total - 1) / total - 1));
     }
     return 2 * blockIdx.x + 1;

@@ -47,6 +47,7 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTileRows = 16;
 constexpr int kMaxRows = kWarps * kTileRows;
 constexpr int kMinTiles = 4;  // fewest key tiles of a block's share: below that the joining costs more than it spreads
+constexpr int kItemCost = 1;
 
 template <bool kE4m3>
 struct Stage {
@@ -433,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
       }
     }
     if (kg == 0) {
-      const int slot = walk.part_slot();
+      const int slot = walk.part_slot(tid == 0);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int lr = rg * kTileRows + g + 8 * r, row = w.row0 + lr;
@@ -505,6 +506,7 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms) {
   const int grid = 2 * num_sms;
   attn_split_layout(&p.s, a.workspace, grid, kTileRows * rg, 0);
   p.s.min_tiles = kMinTiles;
+  p.s.item_cost = kItemCost;
   if (!make_cache_maps(a.cache, kTile, 2, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
   cudaError_t e;
   if (a.cache.e4m3)
@@ -534,6 +536,7 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, int num_sms) {
   const int grid = 2 * num_sms;
   attn_split_layout(&p.s, a.workspace, grid, kMaxRows, attn_max_items(a.n_seq, a.tokens, G, kMaxRows));
   p.s.min_tiles = kMinTiles;
+  p.s.item_cost = kItemCost;
   if (!make_cache_maps(a.cache, kTile, 2, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
   cudaError_t e = launch_attn_plan(a, p.s, kMaxRows, kTile);
   if (e != cudaSuccess) return e;
