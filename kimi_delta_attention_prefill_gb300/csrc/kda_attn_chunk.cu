@@ -107,11 +107,6 @@ struct JobFeed {
   // By one thread, when its warp needs nothing of the job any more.
   __device__ void done() { mbar_arrive(&b.job_empty[k % kJobs]); }
 };
-__device__ __forceinline__ int64_t job_q_offset(const AttnArgs& a, const Job& j, int row) {
-  const int G = a.H / a.cache.heads, t = row / G, g = row - t * G;
-  return (j.base + t) * a.q_stride[1] + (static_cast<int64_t>(j.head) * G + g) * a.q_stride[2];
-}
-
 // Whether some row of the item does not see some key of key tile t.
 __device__ __forceinline__ bool edge_tile(const AttnArgs& a, int t, int p_first, int p_last) {
   const int first = t * kTile, last = first + kTile - 1;
@@ -280,8 +275,9 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
   const int lane = tid & 31, sub = tid & 15, grp = tid >> 4;  // 4 groups of 16 lanes
-  const uint32_t flip = !kE4m3 && a.scale_log2 < 0.f ? 0x80008000u : 0u;
-  const bool zero = !kE4m3 && a.scale_log2 == 0.f;
+  const int G = a.H / a.cache.heads;
+  const uint32_t q_at = smem_u32(sm + C::kSmQ) + (sub >> 3) * kPanel;
+  auto q_piece = [&](int r) { return q_at + (r >> 7) * kSlot + sw128(r & 127, 16 * (sub & 7)); };  // this lane's 8 channels
   float* qexp = reinterpret_cast<float*>(sm + C::kSmExp);
   uint32_t n = 0, items = 0, edges = 0;
   bool dead = false;
@@ -289,34 +285,40 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
   while (const Job* jp = feed.next()) {
     const Job& w = *jp;
     if (items > 0 && !dead && !bar_wait(&b.q_empty, (items - 1) & 1)) dead = true;
-    constexpr int kBatch = 8;
-    for (int r0 = grp; r0 < kRows; r0 += 4 * kBatch) {
-      uint4 x[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int row = w.row0 + r0 + 4 * u;
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (row < w.rows && !zero)
-          x[u] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + job_q_offset(a, w, row)) + sub);
+    // every piece is on its way before any is waited for; zeros past the last row
+    {
+      const int first = w.row0 + grp;
+      int tok = first / G, g = first - tok * G;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (w.base + tok) * a.q_stride[1] +
+                            (static_cast<int64_t>(w.head) * G + g) * a.q_stride[2] + 8 * sub;
+      const int n_rows = w.rows - w.row0;
+#pragma unroll 4
+      for (int r = grp; r < kRows; r += 4) {
+        cp_async16(q_piece(r), src, r < n_rows);
+        src += 4 * a.q_stride[2];
+        for (g += 4; g >= G; g -= G) src += a.q_stride[1] - G * a.q_stride[2];
       }
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int r = r0 + 4 * u;
+    }
+    cp_async_wait_all();
+    if (kE4m3 || a.scale_log2 <= 0.f) {  // in place: each thread its own pieces
+#pragma unroll 4
+      for (int r = grp; r < kRows; r += 4) {
+        uint4 x = lds128(q_piece(r));
         if constexpr (kE4m3) {
-          uint32_t top = max(max(x[u].x & 0x7fffu, (x[u].x >> 16) & 0x7fffu), max(x[u].y & 0x7fffu, (x[u].y >> 16) & 0x7fffu));
-          top = max(top, max(max(x[u].z & 0x7fffu, (x[u].z >> 16) & 0x7fffu), max(x[u].w & 0x7fffu, (x[u].w >> 16) & 0x7fffu)));
+          uint32_t top = max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu), max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu));
+          top = max(top, max(max(x.z & 0x7fffu, (x.z >> 16) & 0x7fffu), max(x.w & 0x7fffu, (x.w >> 16) & 0x7fffu)));
 #pragma unroll
           for (int off = 8; off; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
           const int e = query_exponent(top);
           const float inv = pow2i(-e);
           if (sub == 0) qexp[(items & 1) * kRows + r] = pow2i(e);
           auto half = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv); };
-          x[u] = make_uint4(half(x[u].x), half(x[u].y), half(x[u].z), half(x[u].w));
+          x = make_uint4(half(x.x), half(x.y), half(x.z), half(x.w));
         } else {
-          x[u].x ^= flip; x[u].y ^= flip; x[u].z ^= flip; x[u].w ^= flip;
+          const uint32_t flip = 0x80008000u;
+          x = a.scale_log2 == 0.f ? make_uint4(0, 0, 0, 0) : make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
         }
-        uint8_t* dst = sm + C::kSmQ + (r >> 7) * kSlot + (sub >> 3) * kPanel;
-        *reinterpret_cast<uint4*>(dst + sw128(r & 127, 16 * (sub & 7))) = x[u];
+        sts128(q_piece(r), x);
       }
     }
     fence_proxy_async_smem();
