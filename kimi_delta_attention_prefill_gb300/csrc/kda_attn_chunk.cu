@@ -12,10 +12,10 @@
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each: all 512.
 //
 // Warps: two groups of four for the softmax of A and of B (thread = row = TMEM lane: a row's
-// maximum and sum need no exchange), one warp that issues the products, one the copies, two
-// that bring the next item's queries; for an E4M3 cache four more turn the codes into f16
-// tiles (exact).  The tensor core runs P V and the next Q K^T of one tile while the other
-// tile is in its softmax.
+// maximum and sum need no exchange), one warp each that issues A's and B's products, one for
+// the copies; the others bring the next item's queries and, for an E4M3 cache, turn the codes
+// into f16 tiles (exact).  The tensor core runs P V and the next Q K^T of one tile while the
+// other tile is in its softmax.
 //
 // The maximum is lazy: O is rescaled only when a row's maximum has grown by more than 2^8
 // since the last time (weights stay below 2^8, far inside every type here), which random
@@ -39,24 +39,24 @@ namespace kda {
 
 namespace {
 
+constexpr int kThreads = 512;
 constexpr int kTile = 128;
 constexpr int kRows = 256;
 constexpr int kPanel = kTile * 128;     // 64 channels of 128 rows, 16-bit
 constexpr int kSlot = 2 * kPanel;       // one tile of K or V (or 128 rows of Q) as 16-bit values
 constexpr int kStage = kTile * 128 + 8 * 128;  // a tile of codes and a 128-byte slot of scale bytes per page
-constexpr float kLazy = 8.f;
 constexpr int kMinTiles = 4, kItemCost = 3;
 
 template <bool kE4m3>
 struct Cfg {
-  static constexpr int kThreads = kE4m3 ? 512 : 384;
+  static constexpr int kQueryWarps = kE4m3 ? 1 : 4;
   static constexpr int kSlots = kE4m3 ? 3 : 5;
   static constexpr int kStages = kE4m3 ? 3 : 0;
   static constexpr int kSmQ = 0;
   static constexpr int kSmKV = 2 * kSlot;
   static constexpr int kSmStage = kSmKV + kSlots * kSlot;
-  static constexpr int kSmVec = kSmStage + kStages * kStage;          // [2 tiles][ks, ev, 2^-ev][128] floats
-  static constexpr int kSmExp = kSmVec + (kE4m3 ? 2 * 3 * 512 : 0);   // [2 items][256] query row scales
+  static constexpr int kSmVec = kSmStage + kStages * kStage;          // [2 tiles][2^ek, ev][128] floats (wide tiles)
+  static constexpr int kSmExp = kSmVec + (kE4m3 ? 2 * 2 * 512 : 0);   // [2 items][256] query row scales
   static constexpr int kSmBytes = kSmExp + (kE4m3 ? 2048 : 0) + 1024;
 };
 
@@ -73,16 +73,26 @@ struct Job {
 };
 constexpr int kJobs = 4;
 
+// E4M3: what the f16 tiles of a key tile were scaled by (see convert_group).
+struct TileScale {
+  float k;        // 2^E of the keys
+  float v;        // E of the values
+  int wide;       // the scales of the keys (1), the values (2) lie too far apart: code tiles, per-key scales
+  int bad;        // some value row holds a NaN: look at bad[]
+};
+
 struct Bars {
   uint64_t full[5], empty[5];      // slots of K / V tiles
   uint64_t v_ask, v_ok;            // bf16: an edge tile's values are there / have been looked through
   uint64_t st_full[3], st_empty[3];  // stages of codes
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], pv_done[2], o_full[2];
+  uint64_t s_full[2], p_full[2][2], pv_done[2], o_full[2];
   uint64_t job_full[kJobs], job_empty[kJobs];
-  uint64_t drain;
+  uint64_t drain[2];
   Job job[kJobs];
   uint32_t bad[5][4];              // edge tiles, by slot: keys with a non-finite value row
+  TileScale tile[2];               // e4m3, by tile parity
+  int reduce[2][4];
   uint32_t tmem;
 };
 
@@ -183,90 +193,119 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
 }
 
 // -------------------------------------------------------------------------- products
+// One warp issues tile A's products, another tile B's: what a warp spends between its products
+// (barriers, its own instruction fetch) passes behind the other's.  The whole warp walks, so that
+// addresses and descriptors stay in uniform registers; one lane issues.
 template <bool kE4m3>
-__device__ void mma_thread(const ChunkParams& p, uint8_t* sm, Bars& b) {
+__device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
-  const uint32_t tmem = b.tmem;
-  const uint32_t id_qk = idesc_f16(128, 128, !kE4m3, false, false), id_pv = idesc_f16(128, 128, !kE4m3, false, true);
-  const uint64_t dq = smem_desc(smem_u32(sm + C::kSmQ), 16, 1024, kSwizzle128B);
+  const uint32_t leader = elect_one_sync();
+  constexpr uint32_t id_qk = idesc_f16(128, 128, !kE4m3, false, false), id_pv = idesc_f16(128, 128, !kE4m3, false, true);
+  const uint64_t dq = smem_desc(smem_u32(sm + C::kSmQ) + t * kSlot, 16, 1024, kSwizzle128B);
   const uint64_t dk = smem_desc(smem_u32(sm + C::kSmKV), 16, 1024, kSwizzle128B);
   const uint64_t dv = smem_desc(smem_u32(sm + C::kSmKV), kPanel, 1024, kSwizzle128B);
   bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead && !bar_wait(bar, parity & 1)) dead = true;
-    tc_fence_after();
   };
-  uint32_t n = 0, items = 0, edges = 0;  // ring position (K: even, V: odd), items, edge tiles (bf16)
-  uint32_t tiles[2] = {0, 0};           // tiles begun of A and B
-  auto qk = [&](int t, uint32_t slot) {
-    if (dead) return;
-#pragma unroll
-    for (int kk = 0; kk < 8; ++kk)
-      mma_f16(tmem + 128 * t, dq + ((t * kSlot + (kk >> 2) * kPanel + 32 * (kk & 3)) >> 4),
-              dk + ((slot * kSlot + (kk >> 2) * kPanel + 32 * (kk & 3)) >> 4), id_qk, kk > 0);
-    mma_commit(&b.s_full[t]);
+  auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+  uint32_t items = 0, edges = 0, tiles = 0;
+  uint32_t sk = 0, pk = 0;  // the ring's slot and phase of the next tile to be used
+  auto step = [&] {
+    if (++sk == C::kSlots) { sk = 0; pk ^= 1; }
   };
   JobFeed feed{b, dead};
   while (const Job* jp = feed.next()) {
-    const Job w = *jp;
-    feed.done();
+    const int begin = uniform(jp->begin), end = uniform(jp->end), sink = uniform(jp->sink), lo = uniform(jp->lo);
+    const int p_first = uniform(jp->p_first), p_last = uniform(jp->p_last);
+    const bool mine = uniform(jp->last_row) - uniform(jp->row0) >= 128 * t;  // the item has rows of this tile
+    __syncwarp();
+    if (leader) feed.done();
     ++feed.k;
-    const int halves = w.last_row - w.row0 >= 128 ? 2 : 1;
     wait(&b.q_full, items);
-    {
-      const uint32_t s = n % C::kSlots;
-      wait(&b.full[s], n / C::kSlots);
-      for (int t = 0; t < halves; ++t) qk(t, s);  // S is free: the last P V over it is done (below)
-      if (!dead) mma_commit(&b.empty[s]);
-      if (!dead && w.end - w.begin == 1) mma_commit(&b.q_empty);
-    }
-    for (int i = w.begin; i < w.end; ++i, n += 2) {
-      const uint32_t sv = (n + 1) % C::kSlots, sk = (n + 2) % C::kSlots;
-      const bool more = i + 1 < w.end;
-      // Edge tiles one after the other: asked for here, where the barrier's every phase is seen, so
-      // that the warps that look the values through need not follow the ring.
-      const bool edge = !kE4m3 && edge_tile(a, w.tile(i), w.p_first, w.p_last);
-      if (edge) {
-        wait(&b.full[sv], (n + 1) / C::kSlots);
-        mbar_arrive(&b.v_ask);
-      }
-      for (int t = 0; t < halves; ++t) {
-        wait(&b.p_full[t], tiles[t]);
-        if (t == 0) {
-          wait(&b.full[sv], (n + 1) / C::kSlots);
-          if (edge) wait(&b.v_ok, edges++);
-        }
-        if (!dead) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ta(tmem + 256 + 128 * t, tmem + 128 * t + 8 * kk, dv + ((sv * kSlot + kk * 2048) >> 4), id_pv,
-                       kk > 0 || i > w.begin);
-          mma_commit(&b.pv_done[t]);
-          if (t == halves - 1) mma_commit(&b.empty[sv]);
-          if (!more) mma_commit(&b.o_full[t]);
-        }
-        if (more && t == 0) wait(&b.full[sk], (n + 2) / C::kSlots);
-        // P lies over S: the next scores may be written once this product has read it
-        wait(&b.pv_done[t], tiles[t]);
-        ++tiles[t];
-        if (more) qk(t, sk);
-      }
-      if (more && !dead) {
-        mma_commit(&b.empty[sk]);
-        if (i + 2 == w.end) mma_commit(&b.q_empty);
-      }
-    }
     ++items;
+    // An edge tile's values are looked through by other warps before they are used.  Edge tiles
+    // are asked for one by one here, where every phase of the barrier is seen, so that those
+    // warps need not follow the ring.
+    bool edge = false;
+    auto values = [&](int i, uint32_t slot, uint32_t phase) {
+      wait(&b.full[slot], phase);
+      edge = !kE4m3 && edge_tile(a, i < sink ? i : lo + (i - sink), p_first, p_last);
+      if (edge && leader) mbar_arrive(&b.v_ask);
+    };
+    if (!mine) {  // only keeps the other warps' counts
+      if (leader) mbar_arrive(&b.q_empty);
+      for (int i = begin; i < end; ++i) {
+        wait(&b.full[sk], pk);
+        if (leader) mbar_arrive(&b.empty[sk]);
+        step();
+        values(i, sk, pk);
+        if (edge) wait(&b.v_ok, edges++);
+        if (leader) mbar_arrive(&b.empty[sk]);
+        step();
+      }
+      continue;
+    }
+    auto qk = [&](uint32_t slot, bool last) {
+      __syncwarp();
+      tc_fence_after();
+      const uint64_t db = dk + slot * (kSlot >> 4);
+#pragma unroll
+      for (int kk = 0; kk < 8; ++kk) {
+        const uint32_t off = ((kk >> 2) * kPanel + 32 * (kk & 3)) >> 4;
+        mma_f16_if(leader, 128 * t, dq + off, db + off, id_qk, kk > 0);
+      }
+      mma_commit_if(leader, &b.s_full[t]);
+      mma_commit_if(leader, &b.empty[slot]);
+      if (last) mma_commit_if(leader, &b.q_empty);
+    };
+    wait(&b.full[sk], pk);
+    qk(sk, end - begin == 1);  // S is free: the last P V over it is done (below)
+    step();
+    values(begin, sk, pk);
+    // The tensor core has products queued while this warp waits: what can be waited for early is
+    // waited for behind a product, so that nothing but the softmax comes before P V.
+    for (int i = begin; i < end; ++i) {
+      const uint32_t sv = sk;
+      step();
+      const bool more = i + 1 < end;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // the weights come in two halves of 64 keys
+        wait(&b.p_full[t][h], tiles);
+        if (h == 0 && edge) wait(&b.v_ok, edges++);
+        __syncwarp();
+        tc_fence_after();
+        const uint64_t db = dv + sv * (kSlot >> 4) + h * (4 * 2048 >> 4);
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+          mma_f16_ta_if(leader, 256 + 128 * t, 128 * t + 32 * h + 8 * kk, db + kk * (2048 >> 4), id_pv,
+                        kk > 0 || h > 0 || i > begin);
+      }
+      mma_commit_if(leader, &b.pv_done[t]);
+      mma_commit_if(leader, &b.empty[sv]);
+      if (more) {
+        wait(&b.full[sk], pk);
+        // P lies over S: the next scores may be written once this product has read it
+        wait(&b.pv_done[t], tiles);
+        qk(sk, i + 2 == end);
+        step();
+        values(i + 1, sk, pk);
+      } else {
+        mma_commit_if(leader, &b.o_full[t]);
+        wait(&b.pv_done[t], tiles);
+      }
+      ++tiles;
+    }
   }
   // nothing of this block's may be in flight when it ends
-  mma_commit(&b.drain);
-  if (!bar_wait(&b.drain, 0)) dead = true;
-  if (dead) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+  mma_commit_if(leader, &b.drain[t]);
+  if (!bar_wait(&b.drain[t], 0)) dead = true;
+  if (dead && leader) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
 // --------------------------------------------------------------------------- queries
-// Two warps bring an item's 256 query rows (16 lanes a row), zero past the last, and in a bf16
+// One warp (bf16: four) brings an item's 256 query rows, 16 lanes a row, zero past the last, and in a bf16
 // cache's edge tiles look the values through (see the softmax).  A negative scale is the same
 // as negated queries and a scale of 0 as zero queries with any scale, so the softmax's scale c
 // is positive.
@@ -274,7 +313,8 @@ template <bool kE4m3>
 __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
-  const int lane = tid & 31, sub = tid & 15, grp = tid >> 4;  // 4 groups of 16 lanes
+  const int lane = tid & 31, sub = tid & 15, grp = tid >> 4;
+  constexpr int kGroups = 2 * C::kQueryWarps;  // of 16 lanes
   const int G = a.H / a.cache.heads;
   const uint32_t q_at = smem_u32(sm + C::kSmQ) + (sub >> 3) * kPanel;
   auto q_piece = [&](int r) { return q_at + (r >> 7) * kSlot + sw128(r & 127, 16 * (sub & 7)); };  // this lane's 8 channels
@@ -293,30 +333,31 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
                             (static_cast<int64_t>(w.head) * G + g) * a.q_stride[2] + 8 * sub;
       const int n_rows = w.rows - w.row0;
 #pragma unroll 4
-      for (int r = grp; r < kRows; r += 4) {
+      for (int r = grp; r < kRows; r += kGroups) {
         cp_async16(q_piece(r), src, r < n_rows);
-        src += 4 * a.q_stride[2];
-        for (g += 4; g >= G; g -= G) src += a.q_stride[1] - G * a.q_stride[2];
+        src += kGroups * a.q_stride[2];
+        for (g += kGroups; g >= G; g -= G) src += a.q_stride[1] - G * a.q_stride[2];
       }
     }
     cp_async_wait_all();
     if (kE4m3 || a.scale_log2 <= 0.f) {  // in place: each thread its own pieces
 #pragma unroll 4
-      for (int r = grp; r < kRows; r += 4) {
+      for (int r = grp; r < kRows; r += kGroups) {
         uint4 x = lds128(q_piece(r));
+        if (a.scale_log2 == 0.f) x = make_uint4(0, 0, 0, 0);
         if constexpr (kE4m3) {
           uint32_t top = max(max(x.x & 0x7fffu, (x.x >> 16) & 0x7fffu), max(x.y & 0x7fffu, (x.y >> 16) & 0x7fffu));
           top = max(top, max(max(x.z & 0x7fffu, (x.z >> 16) & 0x7fffu), max(x.w & 0x7fffu, (x.w >> 16) & 0x7fffu)));
 #pragma unroll
           for (int off = 8; off; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
           const int e = query_exponent(top);
-          const float inv = pow2i(-e);
+          const float inv = a.scale_log2 < 0.f ? -pow2i(-e) : pow2i(-e);
           if (sub == 0) qexp[(items & 1) * kRows + r] = pow2i(e);
           auto half = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv); };
           x = make_uint4(half(x.x), half(x.y), half(x.z), half(x.w));
-        } else {
+        } else if (a.scale_log2 < 0.f) {
           const uint32_t flip = 0x80008000u;
-          x = a.scale_log2 == 0.f ? make_uint4(0, 0, 0, 0) : make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
+          x = make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
         }
         sts128(q_piece(r), x);
       }
@@ -331,25 +372,22 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
         if (!edge_tile(a, w.tile(i), w.p_first, w.p_last)) continue;
         const uint32_t s = (n + 1) % C::kSlots;
         if (!dead && !bar_wait(&b.v_ask, edges++ & 1)) dead = true;
-        // thread = 2 keys: a row of 128 values with a NaN or an infinity is cleared and noted
-        for (int q = 0; q < 2; ++q) {
-          const int key = tid + 64 * q;
-          uint8_t* v = sm + C::kSmKV + s * kSlot;
-          bool bad = false;
-#pragma unroll 4
-          for (int c = 0; c < 16; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * kPanel + sw128(key, 16 * (c & 7)));
-            auto has = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
-            bad |= has(x.x) | has(x.y) | has(x.z) | has(x.w);
-          }
-          if (bad) {
-#pragma unroll 4
-            for (int c = 0; c < 16; ++c)
-              *reinterpret_cast<uint4*>(v + (c >> 3) * kPanel + sw128(key, 16 * (c & 7))) = make_uint4(0, 0, 0, 0);
-          }
-          const uint32_t m = __ballot_sync(0xffffffffu, bad);
-          if (lane == 0) b.bad[s][2 * q + (tid >> 5)] = m;
+        // thread = key: a row of 128 values with a NaN or an infinity is cleared and noted
+        uint8_t* v = sm + C::kSmKV + s * kSlot;
+        bool bad = false;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * kPanel + sw128(tid, 16 * (c & 7)));
+          auto has = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
+          bad |= has(x.x) | has(x.y) | has(x.z) | has(x.w);
         }
+        if (bad) {
+#pragma unroll 4
+          for (int c = 0; c < 16; ++c)
+            *reinterpret_cast<uint4*>(v + (c >> 3) * kPanel + sw128(tid, 16 * (c & 7))) = make_uint4(0, 0, 0, 0);
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, bad);
+        if (lane == 0) b.bad[s][tid >> 5] = m;
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.v_ok);
@@ -363,8 +401,12 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
 }
 
 // ------------------------------------------------------------------- codes to f16 tiles
-// Four warps, thread = key: 16 codes at a time to two 16-byte pieces of the f16 tile, and the
-// key's scales as the floats that the softmax needs.
+// Four warps, thread = key.  With E the largest scale exponent of the tile's keys (values), a row
+// becomes code * 2^(e - E) in f16: exact for e >= E - 15 (codes go down to 2^-9, f16 to 2^-24),
+// so that one factor 2^E serves the whole tile and the softmax has no per-key work.  Where a row's
+// scale lies further below (all-zero rows aside) the tile is "wide": its rows stay plain codes and
+// the softmax takes every key's scale by itself.  Rows past the last position, which may hold
+// anything, become zeros; so do value rows that hold a NaN, noted in bad[].
 __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
   using C = Cfg<true>;
   const AttnArgs& a = p.a;
@@ -378,51 +420,82 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
     const Job& w = *jp;
     const int begin = w.begin, end = w.end;
     for (int i = begin; i < end; ++i) {
-      const bool edge = edge_tile(a, w.tile(i), w.p_first, w.p_last);
+      const bool past = w.tile(i) * kTile + tid > w.p_last;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const uint32_t st = n % C::kStages, s = n % C::kSlots;
         if (!dead && !bar_wait(&b.st_full[st], (n / C::kStages) & 1)) dead = true;
         const uint8_t* src = sm + C::kSmStage + st * kStage;
         uint4 c[8];
+        uint32_t any = 0, nan = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) c[k] = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
+        for (int k = 0; k < 8; ++k) {
+          c[k] = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
+          any |= (c[k].x | c[k].y | c[k].z | c[k].w) & 0x7f7f7f7fu;
+          auto has = [](uint32_t u) { return ((u & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };  // a byte 0x7f or 0xff
+          nan |= has(c[k].x) | has(c[k].y) | has(c[k].z) | has(c[k].w);
+        }
         const uint32_t byte = src[sc_at];
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.st_empty[st]);
-        if (kv && edge) {  // a code of NaN: its row is cleared and noted (see the softmax)
-          uint32_t nan = 0;
-          auto has = [](uint32_t u) {  // a byte 0x7f or 0xff
-            u = (u & 0x7f7f7f7fu) + 0x01010101u;
-            return u & 0x80808080u;
-          };
+        const bool bad = (nan || byte == 255) && !past;
+        const bool counts = any && !past && !bad;
+        const int e = static_cast<int>(byte) - 127;
+        const uint32_t bad_keys = __ballot_sync(0xffffffffu, bad);
+        const int hi = __reduce_max_sync(0xffffffffu, counts ? e : -1000), lo = __reduce_min_sync(0xffffffffu, counts ? e : 1000);
+        if (n >= C::kSlots && !dead && !bar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) dead = true;
+        if (lane == 0) {
+          b.reduce[kv][warp] = (hi + 1000) | ((lo + 1000) << 12) | (bad_keys ? 1 << 24 : 0);
+          if (kv) b.bad[s][warp] = bad_keys;
+        }
+        named_bar_sync(2, 128);
+        int top = -1000, low = 1000, bads = 0;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) nan |= has(c[k].x) | has(c[k].y) | has(c[k].z) | has(c[k].w);
-          if (nan) {
-#pragma unroll
-            for (int k = 0; k < 8; ++k) c[k] = make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < 4; ++k) {
+          const int r = b.reduce[kv][k];
+          top = max(top, (r & 4095) - 1000);
+          low = min(low, ((r >> 12) & 4095) - 1000);
+          bads |= r >> 24;
+        }
+        if (top < -500) top = low = 0;
+        const bool wide = low < top - 15;
+        TileScale& ts = b.tile[(n >> 1) & 1];
+        if (tid == 0) {
+          if (kv) {
+            ts.v = wide ? 0.f : static_cast<float>(top);
+            ts.wide |= wide ? 2 : 0;
+            ts.bad = bads;
+          } else {
+            ts.k = wide ? 1.f : pow2i(top);
+            ts.wide = wide ? 1 : 0;
           }
-          const uint32_t m = __ballot_sync(0xffffffffu, nan != 0);
-          if (n >= C::kSlots && !dead && !bar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) dead = true;
-          if (lane == 0) b.bad[s][warp] = m;
-        } else if (n >= C::kSlots && !dead && !bar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) {
-          dead = true;
         }
-        float* vec = reinterpret_cast<float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 384;
-        if (kv) {
-          vec[128 + tid] = scale_exponent(byte);
-          vec[256 + tid] = scale_inverse(byte);
-        } else {
-          vec[tid] = scale_value(byte);
+        float* vec = reinterpret_cast<float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
+        // per-key scales, for a tile that is wide in either way: those of the side that is not are in the tile
+        if (kv) vec[128 + tid] = wide ? static_cast<float>(counts ? e : low) : 0.f;  // a zero row must not raise m
+        else vec[tid] = wide && counts ? pow2i(e) : 1.f;
+        // the row's factor as an f16 pair; NaN for a key row that holds one
+        const int r = wide || !counts ? 0 : max(e - top, -24);
+        __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>(r >= -14 ? (15 + r) << 10 : 1 << (24 + r))));
+        if (past || (bad && kv)) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) c[k] = make_uint4(0, 0, 0, 0);
+        } else if (bad) {
+          f = __half2half2(__ushort_as_half(0x7fff));
         }
+        auto out = [&](uint32_t pair) {
+          const uint32_t h = e4m3_half2(pair);
+          const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h), f);
+          return *reinterpret_cast<const uint32_t*>(&y);
+        };
         uint8_t* dst = sm + C::kSmKV + s * kSlot;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           uint8_t* row = dst + (k >> 2) * kPanel;
           *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3))) =
-              make_uint4(e4m3_half2(c[k].x), e4m3_half2(c[k].x >> 16), e4m3_half2(c[k].y), e4m3_half2(c[k].y >> 16));
+              make_uint4(out(c[k].x), out(c[k].x >> 16), out(c[k].y), out(c[k].y >> 16));
           *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3) + 16)) =
-              make_uint4(e4m3_half2(c[k].z), e4m3_half2(c[k].z >> 16), e4m3_half2(c[k].w), e4m3_half2(c[k].w >> 16));
+              make_uint4(out(c[k].z), out(c[k].z >> 16), out(c[k].w), out(c[k].w >> 16));
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -437,18 +510,25 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
 }
 
 // ---------------------------------------------------------------------------- softmax
+// Scores are taken to log2 units as y = S u + off: u the softmax scale (e4m3: times the query
+// row's and the tile's powers of two), off the values' E of an e4m3 tile, by which the weights
+// 2^(y - m) are those of the scaled tile; the row's sum takes 2^-off back.
 template <bool kE4m3>
 __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t, int tid) {
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
+  // A row's reference m follows its maximum only when that has grown by this much (log2): bf16
+  // weights have 32-bit range and may grow far without harm, f16 weights end at 2^16.
+  constexpr float kLazy = kE4m3 ? 8.f : 32.f;
   const int lane = tid & 31;
   const uint32_t tl = static_cast<uint32_t>(tid & 96) << 16;
-  const uint32_t ts = b.tmem + tl + 128 * t, to = b.tmem + tl + 256 + 128 * t;
+  const uint32_t ts = tl + 128 * t, to = tl + 256 + 128 * t;
   uint32_t n = 0, tiles = 0, items = 0, edges = 0, seen = 0;  // seen: items of the block, items: those with rows here
   bool dead = false;
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (!dead && !bar_wait(bar, parity & 1)) dead = true;
   };
+  const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);  // the queries have its sign (0: are 0)
   JobFeed feed{b, dead};
   while (const Job* jp = feed.next()) {
     const Job& w = *jp;
@@ -469,12 +549,8 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
     const bool live = row < w.rows;
     const int G = a.H / a.cache.heads;
     const int pos = live ? w.len - w.n_tok + row / G : -1;
-    // scores to log2 units: bf16 S c (c > 0), e4m3 S ks c + ev
-    const float sc = fabsf(a.scale_log2);
-    const float c = kE4m3 ? a.scale_log2 : (sc == 0.f ? 1.f : sc);
-    float crow = c;
-    float m = -INFINITY;            // the reference that P is taken against (bf16: in units of S)
-    uint64_t l2 = f32x2(0.f, 0.f);
+    float crow = scale;
+    float m = -INFINITY, l = 0.f;
     for (int i = begin; i < end; ++i, n += 2) {
       const int kt = w.tile(i);
       const bool edge = edge_tile(a, kt, w.p_first, w.p_last);
@@ -485,29 +561,33 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       float s[4][32];
 #pragma unroll
       for (int g = 0; g < 4; ++g) tmem_ld32_async(ts + 32 * g, s[g]);
+      float u = crow, off = 0.f;
+      int wide = 0, bad = edge;
+      if constexpr (kE4m3) {
+        if (i == begin) crow = scale * reinterpret_cast<const float*>(sm + C::kSmExp)[(seen & 1) * kRows + 128 * t + tid];
+        wait(&b.full[sv], (n + 1) / C::kSlots);  // the value scales come with the values
+        const TileScale& sc = b.tile[(n >> 1) & 1];
+        u = crow * sc.k;
+        off = sc.v;
+        wide = sc.wide;
+        bad = sc.bad;
+      }
 #pragma unroll
       for (int g = 0; g < 4; ++g) tmem_wait_ld32(s[g]);
-      const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 384;
-      if constexpr (kE4m3) {
-        if (i == begin) crow = c * reinterpret_cast<const float*>(sm + C::kSmExp)[(seen & 1) * kRows + 128 * t + tid];
-        wait(&b.full[sv], (n + 1) / C::kSlots);  // the value scales come with the values
-        const uint64_t c2 = f32x2(crow, crow);
+      if (kE4m3 && wide) {  // y of the codes, key by key; then u = 1, off = 0
+        const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 ks = *reinterpret_cast<const float4*>(vec + 32 * g + e);
-            const float4 ev = *reinterpret_cast<const float4*>(vec + 128 + 32 * g + e);
-            const float2 y0 = unpack_f32x2(fma_f32x2(mul_f32x2(f32x2(s[g][e], s[g][e + 1]), f32x2(ks.x, ks.y)), c2, f32x2(ev.x, ev.y)));
-            const float2 y1 = unpack_f32x2(fma_f32x2(mul_f32x2(f32x2(s[g][e + 2], s[g][e + 3]), f32x2(ks.z, ks.w)), c2, f32x2(ev.z, ev.w)));
-            s[g][e] = y0.x; s[g][e + 1] = y0.y; s[g][e + 2] = y1.x; s[g][e + 3] = y1.y;
-          }
+          for (int e = 0; e < 32; ++e) s[g][e] = fmaf(s[g][e] * vec[32 * g + e], u, vec[128 + 32 * g + e] + off);
+        u = 1.f;
+        off = 0.f;
       }
       if (edge) {
         const int first = kt * kTile;
-        const int hi = pos - first;                                            // columns past it are hidden
+        const int hi = pos - first;                                                                  // columns past it are hidden
         const int lo = a.window > 0 && pos >= a.window ? max(pos - a.window + 1 - first, 0) : 0;  // those before it too, but for
-        const int sink = a.n_sink - first;                                     // the first tokens
+        const int sink = a.n_sink - first;                                                           // the first tokens
 #pragma unroll
         for (int g = 0; g < 4; ++g)
 #pragma unroll
@@ -515,19 +595,39 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
             const int col = 32 * g + e;
             if (col > hi || (col < lo && col >= sink)) s[g][e] = -INFINITY;
           }
+        if constexpr (!kE4m3) wait(&b.v_ok, edges++);
+      }
+      if (bad) {
         // 0 * NaN must not reach a row that does not see the key: such value rows were cleared,
         // and the rows that do see one become NaN here.
-        if constexpr (!kE4m3) {
-          wait(&b.v_ok, edges++);
-        }
-#pragma unroll
+#pragma unroll 1
         for (int g = 0; g < 4; ++g) {
-          const uint32_t bad = b.bad[sv][g];
-          if (bad)
-            for (int e = 0; e < 32; ++e)
-              if (((bad >> e) & 1) && sees(pos, first + 32 * g + e, a.window, a.n_sink)) l2 = f32x2(__uint_as_float(0x7fffffffu), 0.f);
+          const uint32_t keys = b.bad[sv][g];
+          for (int e = 0; keys >> e && e < 32; ++e)
+            if (((keys >> e) & 1) && sees(pos, kt * kTile + 32 * g + e, a.window, a.n_sink)) l = __uint_as_float(0x7fffffffu);
         }
       }
+      // a quarter's weights, packed, and their sum
+      uint64_t u2 = f32x2(u, u), nb2;
+      auto quarter = [&](const float (&x)[32], float (&pk)[16], uint64_t& sum) {
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 y = unpack_f32x2(fma_f32x2(f32x2(x[e], x[e + 1]), u2, nb2));
+          const float p0 = exp2_fast(y.x), p1 = exp2_fast(y.y);
+          sum = e == 0 ? f32x2(p0, p1) : add_f32x2(sum, f32x2(p0, p1));
+          // rounded once, to the values' type: f16 2^-11, bf16 2^-8; the sum keeps 32 bits
+          pk[e >> 1] = __uint_as_float(kE4m3 ? pack_half2(p0, p1) : pack_bf162(p0, p1));
+        }
+      };
+      auto base = [&] {
+        const float nb = off - (m == -INFINITY ? 0.f : m);
+        nb2 = f32x2(nb, nb);
+      };
+      // The first quarter against the present reference, while the maximum is found: mostly it stays.
+      float pk[16];
+      uint64_t sum0, sum1, sum2, sum3;
+      base();
+      quarter(s[0], pk, sum0);
       float mx[4];
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
@@ -535,14 +635,12 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
 #pragma unroll
         for (int e = 2; e < 32; e += 2) mx[g] = fmaxf(mx[g], fmaxf(s[g][e], s[g][e + 1]));
       }
-      const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-      const float unit = kE4m3 ? 1.f : c;
-      const bool grow = (top - m) * unit > kLazy;  // also from -inf to anything; never for nothing visible
+      const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), u, off);
+      const bool grow = top - m > kLazy;  // also from -inf to anything; never for nothing visible
       if (__any_sync(0xffffffffu, grow)) {
-        const float mn = grow ? top : m;
-        const float f = grow ? exp2_fast((m - mn) * unit) : 1.f;
-        m = mn;
-        l2 = mul_f32x2(l2, f32x2(f, f));
+        const float f = grow ? exp2_fast(m - top) : 1.f;
+        m = grow ? top : m;
+        l *= f;
         if (i > begin) {
           // The scores' barrier stands for every product issued before them, the last P V among them.
 #pragma unroll 1
@@ -554,47 +652,41 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
             tmem_st16(to + 16 * g, o);
           }
         }
+        base();
+        quarter(s[0], pk, sum0);
       }
-      const float base = m == -INFINITY ? 0.f : m * unit;
-      const uint64_t u2 = f32x2(unit, unit), nb2 = f32x2(-base, -base);
+      auto give = [&](int h) {
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.p_full[t][h]);
+      };
+      tmem_st16(ts, pk);
+      quarter(s[1], pk, sum1);
+      tmem_st16(ts + 16, pk);
+      give(0);
+      quarter(s[2], pk, sum2);
+      tmem_st16(ts + 32, pk);
+      quarter(s[3], pk, sum3);
+      tmem_st16(ts + 48, pk);
+      float2 sum = unpack_f32x2(add_f32x2(add_f32x2(sum0, sum1), add_f32x2(sum2, sum3)));
+      if (kE4m3 && wide) {  // the sum of 2^(y - ev - m), key by key
+        const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
+        const float v = b.tile[(n >> 1) & 1].v, nb = m == -INFINITY ? 0.f : m;
+        sum.x = sum.y = 0.f;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float pk[32];
+        for (int g = 0; g < 4; ++g)
 #pragma unroll
-        for (int e = 0; e < 64; e += 2) {
-          const int g = 2 * h + (e >> 5), k = e & 31;
-          const uint64_t x = kE4m3 ? add_f32x2(f32x2(s[g][k], s[g][k + 1]), nb2) : fma_f32x2(f32x2(s[g][k], s[g][k + 1]), u2, nb2);
-          const float2 y = unpack_f32x2(x);
-          const float p0 = exp2_fast(y.x), p1 = exp2_fast(y.y);
-          // weights rounded once, to the values' type: f16 2^-11, bf16 2^-8; the sum keeps 32 bits
-          if constexpr (kE4m3) {
-            float2 rv = *reinterpret_cast<const float2*>(vec + 256 + 64 * h + e);
-            if (edge) {  // a hidden key's scale may be NaN; its weight is 0 whatever it says
-              rv.x = p0 == 0.f ? 0.f : rv.x;
-              rv.y = p1 == 0.f ? 0.f : rv.y;
-            }
-            l2 = fma_f32x2(f32x2(p0, p1), f32x2(rv.x, rv.y), l2);
-            pk[e >> 1] = __uint_as_float(pack_half2(p0, p1));
-          } else {
-            l2 = add_f32x2(l2, f32x2(p0, p1));
-            pk[e >> 1] = __uint_as_float(pack_bf162(p0, p1));
-          }
-        }
-        tmem_st32(ts + 32 * h, pk);
+          for (int e = 0; e < 32; ++e) sum.x += exp2_fast(s[g][e] - vec[128 + 32 * g + e] - v - nb);
       }
-      tmem_wait_st();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&b.p_full[t]);
+      give(1);
+      l = fmaf(sum.x + sum.y, kE4m3 && !wide ? exp2_fast(-off) : 1.f, l);
     }
     // ---- the item's (or part's) rows
     wait(&b.o_full[t], items);
     ++items;
     ++seen;
     tc_fence_after();
-    const float2 lp = unpack_f32x2(l2);
-    const float l = lp.x + lp.y;
-    const float ml = kE4m3 ? m : m * c;
     const int slot = w.slot;
     if (slot >= 0) {
       const int64_t at = static_cast<int64_t>(slot) * p.s.part_rows + 128 * t + tid;
@@ -607,7 +699,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
 #pragma unroll
           for (int e = 0; e < 32; e += 4) dst[e >> 2] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
       }
-      if (live) p.s.part_ml[at] = make_float2(ml, l);
+      if (live) p.s.part_ml[at] = make_float2(m, l);
     } else {
       const float inv = l == 0.f ? 0.f : 1.f / l;
       const int64_t orow = live ? (w.base + row / G) * a.H + static_cast<int64_t>(w.head) * G + row % G : 0;
@@ -622,7 +714,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
             dst[e >> 3] = make_uint4(pack_bf162(o[e] * inv, o[e + 1] * inv), pack_bf162(o[e + 2] * inv, o[e + 3] * inv),
                                      pack_bf162(o[e + 4] * inv, o[e + 5] * inv), pack_bf162(o[e + 6] * inv, o[e + 7] * inv));
       }
-      if (live && a.lse) a.lse[orow] = lse_of(ml, l);
+      if (live && a.lse) a.lse[orow] = lse_of(m, l);
     }
     tc_fence_before();
     __syncwarp();
@@ -633,7 +725,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
 }
 
 template <bool kE4m3>
-__global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1) attn_chunk_kernel(const __grid_constant__ ChunkParams p) {
+__global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_constant__ ChunkParams p) {
   using C = Cfg<kE4m3>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ Bars b;
@@ -642,50 +734,52 @@ __global__ void __launch_bounds__(Cfg<kE4m3>::kThreads, 1) attn_chunk_kernel(con
   if (tid == 0) {
     for (int i = 0; i < 5; ++i) {
       mbar_init(&b.full[i], kE4m3 ? 4 : 1);
-      mbar_init(&b.empty[i], 1);
+      mbar_init(&b.empty[i], 2);
     }
     for (int i = 0; i < 3; ++i) { mbar_init(&b.st_full[i], 1); mbar_init(&b.st_empty[i], 4); }
-    mbar_init(&b.v_ask, 1);
-    mbar_init(&b.v_ok, 2);
-    mbar_init(&b.q_full, 2);
-    mbar_init(&b.q_empty, 1);
+    mbar_init(&b.v_ask, 2);
+    mbar_init(&b.v_ok, C::kQueryWarps);
+    mbar_init(&b.q_full, C::kQueryWarps);
+    mbar_init(&b.q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.s_full[i], 1);
-      mbar_init(&b.p_full[i], 4);
+      mbar_init(&b.p_full[i][0], 4);
+      mbar_init(&b.p_full[i][1], 4);
       mbar_init(&b.pv_done[i], 1);
       mbar_init(&b.o_full[i], 1);
+      mbar_init(&b.drain[i], 1);
     }
-    // a job is read by the product thread, the two query warps, the eight softmax warps and the converters
-    for (int i = 0; i < kJobs; ++i) { mbar_init(&b.job_full[i], 1); mbar_init(&b.job_empty[i], kE4m3 ? 15 : 11); }
-    mbar_init(&b.drain, 1);
+    // a job is read by the two product warps, the query warps, the eight softmax warps and the converters
+    for (int i = 0; i < kJobs; ++i) {
+      mbar_init(&b.job_full[i], 1);
+      mbar_init(&b.job_empty[i], 10 + C::kQueryWarps + (kE4m3 ? 4 : 0));
+    }
     fence_mbar_init();
     p.s.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
   }
   pdl_launch_dependents();
   if (warp == 8) {
-    tmem_alloc(&b.tmem, 512);
+    tmem_alloc(&b.tmem, 512);  // all of it, so its addresses begin at 0
     tmem_relinquish();
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  // registers: 168 a thread at launch of 384 (504 of each group's thread), 128 of 512 (512)
+  // registers: 128 a thread at launch, 512 over the four groups
   if (warp < 8) {
-    if constexpr (kE4m3) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n" ::: "memory");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 208;\n" ::: "memory");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 176;\n" ::: "memory");
     softmax_group<kE4m3>(p, sm, b, warp >> 2, tid & 127);
   } else {
-    if constexpr (kE4m3) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;\n" ::: "memory");
-    if (warp == 8) {
-      if (elect_one_sync()) mma_thread<kE4m3>(p, sm, b);
-      __syncwarp();
-    } else if (warp == 9) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
+    if (warp < 10) {
+      mma_warp<kE4m3>(p, sm, b, warp - 8);
+    } else if (warp == 10) {
       load_warp<kE4m3>(p, sm, b, tid & 31);
-    } else if (warp < 12) {
-      query_warps<kE4m3>(p, sm, b, tid - 320);
-    } else {
+    } else if (kE4m3 && warp == 11) {
+      query_warps<kE4m3>(p, sm, b, tid & 31);
+    } else if (warp >= 12) {
       if constexpr (kE4m3) convert_group(p, sm, b, tid - 384);
+      else query_warps<kE4m3>(p, sm, b, tid - 384);
     }
   }
   tc_fence_before();
@@ -700,7 +794,7 @@ cudaError_t launch_chunk(const ChunkParams& p) {
   auto kern = attn_chunk_kernel<kE4m3>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
   if (e != cudaSuccess) return e;
-  kern<<<p.s.grid, Cfg<kE4m3>::kThreads, bytes, p.a.stream>>>(p);
+  kern<<<p.s.grid, kThreads, bytes, p.a.stream>>>(p);
   return cudaGetLastError();
 }
 

@@ -45,18 +45,13 @@ __device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wai
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// Wait for a barrier's phase, given up after two seconds (false): then the caller reports
-// KDA_ERR_TIMEOUT, stops waiting and leaves in order.
+// Wait for a barrier's phase, given up after 2^20 polls (false), each of which the hardware
+// holds for microseconds: then the caller reports KDA_ERR_TIMEOUT, stops waiting and leaves in
+// order.  Kept small: where it stands in a rarely fetched loop, its code is what it costs.
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
-  for (int i = 0; i < 64; ++i)
+#pragma unroll 1
+  for (uint32_t i = 0; i < (1u << 20); ++i)
     if (mbar_try_wait(bar, parity)) return true;
-  uint64_t t0, t1;
-  asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t0));
-  do {
-    for (int i = 0; i < 16; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    asm volatile("mov.u64 %0, %globaltimer;" : "=l"(t1));
-  } while (t1 - t0 < 2000000000ull);
   return false;
 }
 

@@ -317,6 +317,26 @@ def test_extreme_value_scales():
     check(o.flatten(0, 1), lse.flatten(0, 1), reference(c, q, [2, 2], [200, 130], 0, 0, D ** -0.5))
 
 
+@pytest.mark.parametrize("where", ["k", "v", "kv"])
+@pytest.mark.parametrize("spread", [3, 15, 16, 38])
+def test_prefill_scales_far_apart(where, spread):
+    """Rows whose scales lie just within and beyond what one f16 tile can hold, all-zero rows among them."""
+    g = gen(spread)
+
+    def values(n, i, x):
+        if n in where:
+            x *= torch.where(torch.rand(x.shape[0], 1, 1, generator=g) < 0.1, 2.0 ** -spread, 1.0).to(x.dtype) * 2.0 ** (spread // 2)
+        x[5::17] = 0
+        return x
+
+    new, lens = [150, 70], [400, 70]
+    c = Cache(lens, 2, 32, True, g, values=values)
+    q = (torch.randn(220, 4, D, generator=g) * 2.0 ** -(spread // 2 if "k" in where else 0)).to(torch.bfloat16)
+    for window, sink in ((0, 0), (90, 3)):
+        o, lse = run_prefill(c, q.cuda(), new, lens, window, sink)
+        check(o, lse, reference(c, torch.split(q, new), new, lens, window, sink, D ** -0.5))
+
+
 def test_scores_of_any_size():
     """Rows whose scores spread over hundreds, all very negative or very positive."""
     g = gen(14)
