@@ -7,7 +7,7 @@
 // r % G of the head's group, so 8 tokens of a group of 12 fill 96 rows and no tile is padded
 // by the group -- as two 128-row tiles A and B, and visits key tiles of 128:
 //     S = Q K^T    tcgen05, both operands in shared memory, S (fp32) in TMEM
-//     P = 2^(S c - m c), rounded to the values' type, over S's first 64 columns
+//     P = 2^(S c - m), rounded to the values' type, over S's columns
 //     O += P V     tcgen05, P from TMEM, V from shared memory (MN-major)
 // TMEM: S_A, S_B, O_A, O_B, 128 columns each: all 512.
 //
@@ -271,16 +271,16 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
       step();
       const bool more = i + 1 < end;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {  // the weights come in two halves of 64 keys
+      for (int h = 1; h >= 0; --h) {  // the weights come in two halves of 64 keys, the later keys first
         wait(&b.p_full[t][h], tiles);
-        if (h == 0 && edge) wait(&b.v_ok, edges++);
+        if (h == 1 && edge) wait(&b.v_ok, edges++);
         __syncwarp();
         tc_fence_after();
         const uint64_t db = dv + sv * (kSlot >> 4) + h * (4 * 2048 >> 4);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          mma_f16_ta_if(leader, 256 + 128 * t, 128 * t + 32 * h + 8 * kk, db + kk * (2048 >> 4), id_pv,
-                        kk > 0 || h > 0 || i > begin);
+          mma_f16_ta_if(leader, 256 + 128 * t, 128 * t + 64 * h + 8 * kk, db + kk * (2048 >> 4), id_pv,
+                        kk > 0 || h == 0 || i > begin);
       }
       mma_commit_if(leader, &b.pv_done[t]);
       mma_commit_if(leader, &b.empty[sv]);
@@ -426,18 +426,15 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
         const uint32_t st = n % C::kStages, s = n % C::kSlots;
         if (!dead && !bar_wait(&b.st_full[st], (n / C::kStages) & 1)) dead = true;
         const uint8_t* src = sm + C::kSmStage + st * kStage;
-        uint4 c[8];
         uint32_t any = 0, nan = 0;
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < 8; ++k) {
-          c[k] = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
-          any |= (c[k].x | c[k].y | c[k].z | c[k].w) & 0x7f7f7f7fu;
+          const uint4 c = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
+          any |= (c.x | c.y | c.z | c.w) & 0x7f7f7f7fu;
           auto has = [](uint32_t u) { return ((u & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };  // a byte 0x7f or 0xff
-          nan |= has(c[k].x) | has(c[k].y) | has(c[k].z) | has(c[k].w);
+          nan |= has(c.x) | has(c.y) | has(c.z) | has(c.w);
         }
         const uint32_t byte = src[sc_at];
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b.st_empty[st]);
         const bool bad = (nan || byte == 255) && !past;
         const bool counts = any && !past && !bad;
         const int e = static_cast<int>(byte) - 127;
@@ -477,26 +474,23 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
         // the row's factor as an f16 pair; NaN for a key row that holds one
         const int r = wide || !counts ? 0 : max(e - top, -24);
         __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>(r >= -14 ? (15 + r) << 10 : 1 << (24 + r))));
-        if (past || (bad && kv)) {
-#pragma unroll
-          for (int k = 0; k < 8; ++k) c[k] = make_uint4(0, 0, 0, 0);
-        } else if (bad) {
-          f = __half2half2(__ushort_as_half(0x7fff));
-        }
+        if (bad && !kv) f = __half2half2(__ushort_as_half(0x7fff));
+        const uint32_t keep = past || (bad && kv) ? 0u : 0xffffffffu;
         auto out = [&](uint32_t pair) {
-          const uint32_t h = e4m3_half2(pair);
+          const uint32_t h = e4m3_half2(pair & keep);
           const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h), f);
           return *reinterpret_cast<const uint32_t*>(&y);
         };
         uint8_t* dst = sm + C::kSmKV + s * kSlot;
-#pragma unroll
+#pragma unroll 2
         for (int k = 0; k < 8; ++k) {
+          const uint4 c = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
           uint8_t* row = dst + (k >> 2) * kPanel;
-          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3))) =
-              make_uint4(out(c[k].x), out(c[k].x >> 16), out(c[k].y), out(c[k].y >> 16));
-          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3) + 16)) =
-              make_uint4(out(c[k].z), out(c[k].z >> 16), out(c[k].w), out(c[k].w >> 16));
+          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3))) = make_uint4(out(c.x), out(c.x >> 16), out(c.y), out(c.y >> 16));
+          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3) + 16)) = make_uint4(out(c.z), out(c.z >> 16), out(c.w), out(c.w >> 16));
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.st_empty[st]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.full[s]);
@@ -558,9 +552,6 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       wait(&b.s_full[t], tiles);
       ++tiles;
       tc_fence_after();
-      float s[4][32];
-#pragma unroll
-      for (int g = 0; g < 4; ++g) tmem_ld32_async(ts + 32 * g, s[g]);
       float u = crow, off = 0.f;
       int wide = 0, bad = edge;
       if constexpr (kE4m3) {
@@ -571,31 +562,8 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
         off = sc.v;
         wide = sc.wide;
         bad = sc.bad;
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) tmem_wait_ld32(s[g]);
-      if (kE4m3 && wide) {  // y of the codes, key by key; then u = 1, off = 0
-        const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) s[g][e] = fmaf(s[g][e] * vec[32 * g + e], u, vec[128 + 32 * g + e] + off);
-        u = 1.f;
-        off = 0.f;
-      }
-      if (edge) {
-        const int first = kt * kTile;
-        const int hi = pos - first;                                                                  // columns past it are hidden
-        const int lo = a.window > 0 && pos >= a.window ? max(pos - a.window + 1 - first, 0) : 0;  // those before it too, but for
-        const int sink = a.n_sink - first;                                                           // the first tokens
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const int col = 32 * g + e;
-            if (col > hi || (col < lo && col >= sink)) s[g][e] = -INFINITY;
-          }
-        if constexpr (!kE4m3) wait(&b.v_ok, edges++);
+      } else if (edge) {
+        wait(&b.v_ok, edges++);
       }
       if (bad) {
         // 0 * NaN must not reach a row that does not see the key: such value rows were cleared,
@@ -603,39 +571,58 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
 #pragma unroll 1
         for (int g = 0; g < 4; ++g) {
           const uint32_t keys = b.bad[sv][g];
+#pragma unroll 1
           for (int e = 0; keys >> e && e < 32; ++e)
             if (((keys >> e) & 1) && sees(pos, kt * kTile + 32 * g + e, a.window, a.n_sink)) l = __uint_as_float(0x7fffffffu);
         }
       }
-      // a quarter's weights, packed, and their sum
-      uint64_t u2 = f32x2(u, u), nb2;
-      auto quarter = [&](const float (&x)[32], float (&pk)[16], uint64_t& sum) {
+      // 32 scores from column c on; wide tiles: y of the codes, key by key, then u = 1 and off = 0; hidden ones -inf
+      const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
+      auto fix = [&](float (&x)[32], int c) {
+        if (kE4m3 && wide) {
 #pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 y = unpack_f32x2(fma_f32x2(f32x2(x[e], x[e + 1]), u2, nb2));
-          const float p0 = exp2_fast(y.x), p1 = exp2_fast(y.y);
-          sum = e == 0 ? f32x2(p0, p1) : add_f32x2(sum, f32x2(p0, p1));
-          // rounded once, to the values' type: f16 2^-11, bf16 2^-8; the sum keeps 32 bits
-          pk[e >> 1] = __uint_as_float(kE4m3 ? pack_half2(p0, p1) : pack_bf162(p0, p1));
+          for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e] * vec[c + e], u, vec[128 + c + e] + off);
+        }
+        if (edge) {
+          const int first = kt * kTile + c;
+          const int hi = pos - first;                                                                  // columns past it are hidden
+          const int lo = a.window > 0 && pos >= a.window ? max(pos - a.window + 1 - first, 0) : 0;  // those before it too, but for
+          const int sink = a.n_sink - first;                                                           // the first tokens
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (e > hi || (e < lo && e >= sink)) x[e] = -INFINITY;
         }
       };
-      auto base = [&] {
-        const float nb = off - (m == -INFINITY ? 0.f : m);
-        nb2 = f32x2(nb, nb);
+      const bool special = edge || (kE4m3 && wide);
+      // ---- the row's maximum, 64 columns at a time; the last 64 stay in registers
+      float x[2][32];
+      auto load = [&](int c) {
+        tmem_ld32_async(ts + c, x[0]);
+        tmem_ld32_async(ts + c + 32, x[1]);
+        tmem_wait_ld32(x[0]);
+        tmem_wait_ld32(x[1]);
+        if (special) {
+          fix(x[0], c);
+          fix(x[1], c + 32);
+        }
       };
-      // The first quarter against the present reference, while the maximum is found: mostly it stays.
-      float pk[16];
-      uint64_t sum0, sum1, sum2, sum3;
-      base();
-      quarter(s[0], pk, sum0);
-      float mx[4];
+      float mx = -INFINITY;
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        load(64 * h);
+        float m0 = fmaxf(x[0][0], x[0][1]), m1 = fmaxf(x[1][0], x[1][1]);
+        float m2 = fmaxf(x[0][2], x[0][3]), m3 = fmaxf(x[1][2], x[1][3]);
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        mx[g] = fmaxf(s[g][0], s[g][1]);
-#pragma unroll
-        for (int e = 2; e < 32; e += 2) mx[g] = fmaxf(mx[g], fmaxf(s[g][e], s[g][e + 1]));
+        for (int e = 4; e < 32; e += 4) {
+          m0 = fmaxf(m0, fmaxf(x[0][e], x[0][e + 1]));
+          m1 = fmaxf(m1, fmaxf(x[1][e], x[1][e + 1]));
+          m2 = fmaxf(m2, fmaxf(x[0][e + 2], x[0][e + 3]));
+          m3 = fmaxf(m3, fmaxf(x[1][e + 2], x[1][e + 3]));
+        }
+        mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
       }
-      const float top = fmaf(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])), u, off);
+      if (kE4m3 && wide) { u = 1.f; off = 0.f; }
+      const float top = fmaf(mx, u, off);
       const bool grow = top - m > kLazy;  // also from -inf to anything; never for nothing visible
       if (__any_sync(0xffffffffu, grow)) {
         const float f = grow ? exp2_fast(m - top) : 1.f;
@@ -652,35 +639,46 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
             tmem_st16(to + 16 * g, o);
           }
         }
-        base();
-        quarter(s[0], pk, sum0);
       }
-      auto give = [&](int h) {
+      // ---- weights and their sum: keys 64 .. 127 from the registers, over their own scores' first
+      // 32 columns, then keys 0 .. 63
+      const float ref = m == -INFINITY ? 0.f : m;
+      const uint64_t u2 = f32x2(u, u), nb2 = f32x2(off - ref, off - ref);
+      uint64_t sum = f32x2(0.f, 0.f), sum1 = sum;
+#pragma unroll 1
+      for (int h = 1; h >= 0; --h) {
+        if (h == 0) {
+          if (kE4m3 && wide) { u = crow * b.tile[(n >> 1) & 1].k; off = b.tile[(n >> 1) & 1].v; }
+          load(0);
+        }
+        if (kE4m3 && wide) {  // the sum of 2^(y - ev - m), key by key
+          const float v = b.tile[(n >> 1) & 1].v;
+          float w0 = 0.f;
+#pragma unroll
+          for (int e = 0; e < 64; ++e) w0 += exp2_fast(x[e >> 5][e & 31] - vec[128 + 64 * h + e] - v - ref);
+          l += w0;
+        }
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = unpack_f32x2(fma_f32x2(f32x2(x[q][e], x[q][e + 1]), u2, nb2));
+            const float p0 = exp2_fast(y.x), p1 = exp2_fast(y.y);
+            if (e & 2) sum = add_f32x2(sum, f32x2(p0, p1)); else sum1 = add_f32x2(sum1, f32x2(p0, p1));
+            // rounded once, to the values' type: f16 2^-11, bf16 2^-8; the sum keeps 32 bits
+            pk[e >> 1] = __uint_as_float(kE4m3 ? pack_half2(p0, p1) : pack_bf162(p0, p1));
+          }
+          tmem_st16(ts + 64 * h + 16 * q, pk);
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.p_full[t][h]);
-      };
-      tmem_st16(ts, pk);
-      quarter(s[1], pk, sum1);
-      tmem_st16(ts + 16, pk);
-      give(0);
-      quarter(s[2], pk, sum2);
-      tmem_st16(ts + 32, pk);
-      quarter(s[3], pk, sum3);
-      tmem_st16(ts + 48, pk);
-      float2 sum = unpack_f32x2(add_f32x2(add_f32x2(sum0, sum1), add_f32x2(sum2, sum3)));
-      if (kE4m3 && wide) {  // the sum of 2^(y - ev - m), key by key
-        const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
-        const float v = b.tile[(n >> 1) & 1].v, nb = m == -INFINITY ? 0.f : m;
-        sum.x = sum.y = 0.f;
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-#pragma unroll
-          for (int e = 0; e < 32; ++e) sum.x += exp2_fast(s[g][e] - vec[128 + 32 * g + e] - v - nb);
       }
-      give(1);
-      l = fmaf(sum.x + sum.y, kE4m3 && !wide ? exp2_fast(-off) : 1.f, l);
+      const float2 sums = unpack_f32x2(add_f32x2(sum, sum1));
+      if (!kE4m3) l += sums.x + sums.y;
+      else if (!wide) l = fmaf(sums.x + sums.y, exp2_fast(-off), l);
     }
     // ---- the item's (or part's) rows
     wait(&b.o_full[t], items);
