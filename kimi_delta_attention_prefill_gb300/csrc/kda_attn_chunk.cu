@@ -78,7 +78,6 @@ struct TileScale {
   float k;        // 2^E of the keys
   float v;        // E of the values
   int wide;       // the scales of the keys (1), the values (2) lie too far apart: code tiles, per-key scales
-  int bad;        // some value row holds a NaN: look at bad[]
 };
 
 struct Bars {
@@ -90,9 +89,8 @@ struct Bars {
   uint64_t job_full[kJobs], job_empty[kJobs];
   uint64_t drain[2];
   Job job[kJobs];
-  uint32_t bad[5][4];              // edge tiles, by slot: keys with a non-finite value row
+  alignas(16) uint32_t bad[5][4];  // by slot, of bf16 edge tiles only: keys with a non-finite value row
   TileScale tile[2];               // e4m3, by tile parity
-  int reduce[2][4];
   uint32_t tmem;
 };
 
@@ -407,6 +405,7 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
 // scale lies further below (all-zero rows aside) the tile is "wide": its rows stay plain codes and
 // the softmax takes every key's scale by itself.  Rows past the last position, which may hold
 // anything, become zeros; so do value rows that hold a NaN, noted in bad[].
+constexpr int kLeast = 127 - 40;  // the least scale byte that is written
 __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
   using C = Cfg<true>;
   const AttnArgs& a = p.a;
@@ -420,59 +419,82 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
     const Job& w = *jp;
     const int begin = w.begin, end = w.end;
     for (int i = begin; i < end; ++i) {
-      const bool past = w.tile(i) * kTile + tid > w.p_last;
+      const int keys = w.p_last + 1 - w.tile(i) * kTile;  // those of the tile that are not past the last position
+      const bool past = tid >= keys;
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const uint32_t st = n % C::kStages, s = n % C::kSlots;
         if (!dead && !bar_wait(&b.st_full[st], (n / C::kStages) & 1)) dead = true;
         const uint8_t* src = sm + C::kSmStage + st * kStage;
-        uint32_t any = 0, nan = 0;
-#pragma unroll 2
-        for (int k = 0; k < 8; ++k) {
-          const uint4 c = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
-          any |= (c.x | c.y | c.z | c.w) & 0x7f7f7f7fu;
-          auto has = [](uint32_t u) { return ((u & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };  // a byte 0x7f or 0xff
-          nan |= has(c.x) | has(c.y) | has(c.z) | has(c.w);
-        }
-        const uint32_t byte = src[sc_at];
-        const bool bad = (nan || byte == 255) && !past;
-        const bool counts = any && !past && !bad;
-        const int e = static_cast<int>(byte) - 127;
-        const uint32_t bad_keys = __ballot_sync(0xffffffffu, bad);
-        const int hi = __reduce_max_sync(0xffffffffu, counts ? e : -1000), lo = __reduce_min_sync(0xffffffffu, counts ? e : 1000);
-        if (n >= C::kSlots && !dead && !bar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) dead = true;
-        if (lane == 0) {
-          b.reduce[kv][warp] = (hi + 1000) | ((lo + 1000) << 12) | (bad_keys ? 1 << 24 : 0);
-          if (kv) b.bad[s][warp] = bad_keys;
-        }
-        named_bar_sync(2, 128);
-        int top = -1000, low = 1000, bads = 0;
+        uint4 c[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int r = b.reduce[kv][k];
-          top = max(top, (r & 4095) - 1000);
-          low = min(low, ((r >> 12) & 4095) - 1000);
-          bads |= r >> 24;
+        for (int k = 0; k < 8; ++k) c[k] = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
+        const uint32_t byte = src[sc_at];
+        uint32_t nan = 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          auto has = [](uint32_t u) { return (u & 0x7f7f7f7fu) + 0x01010101u; };  // bit 7 of a byte: it is 0x7f or 0xff
+          nan |= (has(c[k].x) | has(c[k].y) | has(c[k].z) | has(c[k].w)) & 0x80808080u;
         }
-        if (top < -500) top = low = 0;
+        // Every warp finds E and the lowest exponent of all 128 rows by itself, four scale bytes a lane.
+        // NaN rows and rows past the last position do not count, nor do rows of zeros (they have the
+        // least scale): those of the least scale are looked into where that decides.
+        int top, low;
+        {
+          const int key = 4 * lane;
+          uint32_t four = *reinterpret_cast<const uint32_t*>(src + kTile * 128 + (key >> p_log) * 128 + (key & ((1 << p_log) - 1)));
+          int hi4 = 0, lo4 = 1000;
+          uint32_t least = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q, four >>= 8) {
+            const int v = four & 255u;
+            const bool in = v != 255 && key + q < keys;
+            hi4 = in ? max(hi4, v) : hi4;
+            if (in && v > kLeast) lo4 = min(lo4, v);
+            least |= in && v <= kLeast ? 1u << q : 0u;
+          }
+          top = __reduce_max_sync(0xffffffffu, hi4);
+          low = __reduce_min_sync(0xffffffffu, lo4);
+          if (top - 15 > kLeast) {
+            uint32_t lanes = __ballot_sync(0xffffffffu, least != 0);
+            while (lanes) {  // a warp's work on four keys at a time
+              const int from = __ffs(lanes) - 1;
+              lanes &= lanes - 1;
+              const uint32_t which = __shfl_sync(0xffffffffu, least, from);
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t part = *reinterpret_cast<const uint32_t*>(src + (4 * from + q) * 128 + 4 * lane);
+                if ((which >> q) & 1 && __any_sync(0xffffffffu, (part & 0x7f7f7f7fu) != 0)) low = kLeast;
+              }
+            }
+          }
+          top -= 127;
+          low = min(low - 127, top);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&b.st_empty[st]);
+        const bool bad = (nan || byte == 255) && !past;
+        const uint32_t bad_keys = __ballot_sync(0xffffffffu, bad);
+        if (n >= C::kSlots && !dead && !bar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) dead = true;
+        if (kv && lane == 0) b.bad[s][warp] = bad_keys;
         const bool wide = low < top - 15;
         TileScale& ts = b.tile[(n >> 1) & 1];
         if (tid == 0) {
           if (kv) {
             ts.v = wide ? 0.f : static_cast<float>(top);
             ts.wide |= wide ? 2 : 0;
-            ts.bad = bads;
           } else {
             ts.k = wide ? 1.f : pow2i(top);
             ts.wide = wide ? 1 : 0;
           }
         }
         float* vec = reinterpret_cast<float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
+        const int e = static_cast<int>(byte) - 127;
+        const bool counts = !past && byte != 255 && e >= low;
         // per-key scales, for a tile that is wide in either way: those of the side that is not are in the tile
         if (kv) vec[128 + tid] = wide ? static_cast<float>(counts ? e : low) : 0.f;  // a zero row must not raise m
         else vec[tid] = wide && counts ? pow2i(e) : 1.f;
         // the row's factor as an f16 pair; NaN for a key row that holds one
-        const int r = wide || !counts ? 0 : max(e - top, -24);
+        const int r = wide || !counts ? 0 : e - top;
         __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>(r >= -14 ? (15 + r) << 10 : 1 << (24 + r))));
         if (bad && !kv) f = __half2half2(__ushort_as_half(0x7fff));
         const uint32_t keep = past || (bad && kv) ? 0u : 0xffffffffu;
@@ -482,15 +504,14 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
           return *reinterpret_cast<const uint32_t*>(&y);
         };
         uint8_t* dst = sm + C::kSmKV + s * kSlot;
-#pragma unroll 2
+#pragma unroll
         for (int k = 0; k < 8; ++k) {
-          const uint4 c = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
           uint8_t* row = dst + (k >> 2) * kPanel;
-          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3))) = make_uint4(out(c.x), out(c.x >> 16), out(c.y), out(c.y >> 16));
-          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3) + 16)) = make_uint4(out(c.z), out(c.z >> 16), out(c.w), out(c.w >> 16));
+          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3))) =
+              make_uint4(out(c[k].x), out(c[k].x >> 16), out(c[k].y), out(c[k].y >> 16));
+          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3) + 16)) =
+              make_uint4(out(c[k].z), out(c[k].z >> 16), out(c[k].w), out(c[k].w >> 16));
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b.st_empty[st]);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.full[s]);
@@ -561,7 +582,8 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
         u = crow * sc.k;
         off = sc.v;
         wide = sc.wide;
-        bad = sc.bad;
+        const uint4 keys = *reinterpret_cast<const uint4*>(b.bad[sv]);
+        bad = (keys.x | keys.y | keys.z | keys.w) != 0;
       } else if (edge) {
         wait(&b.v_ok, edges++);
       }
