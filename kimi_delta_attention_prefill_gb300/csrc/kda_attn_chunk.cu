@@ -87,6 +87,7 @@ struct Bars {
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2][2], pv_done[2], o_full[2];
   uint64_t job_full[kJobs], job_empty[kJobs];
+  uint64_t turn[2];                // the product warps' turns
   uint64_t drain[2];
   Job job[kJobs];
   alignas(16) uint32_t bad[5][4];  // by slot, of bf16 edge tiles only: keys with a non-finite value row
@@ -191,8 +192,7 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
 }
 
 // -------------------------------------------------------------------------- products
-// One warp issues tile A's products, another tile B's: what a warp spends between its products
-// (barriers, its own instruction fetch) passes behind the other's.  The whole warp walks, so that
+// One warp issues tile A's products, another tile B's.  The whole warp walks, so that
 // addresses and descriptors stay in uniform registers; one lane issues.
 template <bool kE4m3>
 __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
@@ -208,7 +208,7 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
     if (!dead && !bar_wait(bar, parity & 1)) dead = true;
   };
   auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
-  uint32_t items = 0, edges = 0, tiles = 0;
+  uint32_t items = 0, edges = 0, tiles = 0, turns = 0;
   uint32_t sk = 0, pk = 0;  // the ring's slot and phase of the next tile to be used
   auto step = [&] {
     if (++sk == C::kSlots) { sk = 0; pk ^= 1; }
@@ -217,7 +217,8 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
   while (const Job* jp = feed.next()) {
     const int begin = uniform(jp->begin), end = uniform(jp->end), sink = uniform(jp->sink), lo = uniform(jp->lo);
     const int p_first = uniform(jp->p_first), p_last = uniform(jp->p_last);
-    const bool mine = uniform(jp->last_row) - uniform(jp->row0) >= 128 * t;  // the item has rows of this tile
+    const int last_row = uniform(jp->last_row) - uniform(jp->row0);
+    const bool mine = last_row >= 128 * t, both = last_row >= 128;  // the item has rows of this tile, of both
     __syncwarp();
     if (leader) feed.done();
     ++feed.k;
@@ -268,6 +269,9 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
       const uint32_t sv = sk;
       step();
       const bool more = i + 1 < end;
+      // A and B take turns of one P V and the next Q K^T each.  Left alone their products mix and
+      // end together, and then both tiles are in their softmax while the tensor core has nothing.
+      if (both && (t == 1 || turns > 0)) wait(&b.turn[t], t == 1 ? turns : turns - 1);
 #pragma unroll
       for (int h = 1; h >= 0; --h) {  // the weights come in two halves of 64 keys, the later keys first
         wait(&b.p_full[t][h], tiles);
@@ -287,13 +291,16 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
         // P lies over S: the next scores may be written once this product has read it
         wait(&b.pv_done[t], tiles);
         qk(sk, i + 2 == end);
+        if (both && leader) mbar_arrive(&b.turn[t ^ 1]);
         step();
         values(i + 1, sk, pk);
       } else {
         mma_commit_if(leader, &b.o_full[t]);
+        if (both && leader) mbar_arrive(&b.turn[t ^ 1]);
         wait(&b.pv_done[t], tiles);
       }
       ++tiles;
+      turns += both;
     }
   }
   // nothing of this block's may be in flight when it ends
@@ -767,6 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       mbar_init(&b.p_full[i][1], 4);
       mbar_init(&b.pv_done[i], 1);
       mbar_init(&b.o_full[i], 1);
+      mbar_init(&b.turn[i], 1);
       mbar_init(&b.drain[i], 1);
     }
     // a job is read by the two product warps, the query warps, the eight softmax warps and the converters
