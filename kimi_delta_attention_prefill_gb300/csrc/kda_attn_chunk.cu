@@ -60,19 +60,6 @@ struct Cfg {
   static constexpr int kSmBytes = kSmExp + (kE4m3 ? 2048 : 0) + 1024;
 };
 
-// One item (or part) of the block's share, as the copy warp hands it to the others.
-struct Job {
-  int head, row0, rows, last_row, len, n_tok;
-  int sink, lo;         // its key tiles
-  int begin, end;       // the visits that are this block's; none: the share is done
-  int p_first, p_last;  // positions of its first and last row
-  int slot;             // of the workspace, -1: whole
-  int seq;
-  int64_t base;
-  __device__ int tile(int i) const { return i < sink ? i : lo + (i - sink); }
-};
-constexpr int kJobs = 4;
-
 // E4M3: what the f16 tiles of a key tile were scaled by (see convert_group).
 struct TileScale {
   float k;        // 2^E of the keys
@@ -86,10 +73,9 @@ struct Bars {
   uint64_t st_full[3], st_empty[3];  // stages of codes
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2][2], pv_done[2], o_full[2];
-  uint64_t job_full[kJobs], job_empty[kJobs];
   uint64_t turn[2];                // the product warps' turns
   uint64_t drain[2];
-  Job job[kJobs];
+  JobRing jobs;
   alignas(16) uint32_t bad[5][4];  // by slot, of bf16 edge tiles only: keys with a non-finite value row
   TileScale tile[2];               // e4m3, by tile parity
   uint32_t tmem;
@@ -103,19 +89,6 @@ struct ChunkParams {
 
 using Walk = ItemWalk<kRows, kTile>;
 
-// The jobs in order, for one warp (or its one thread at work): next() waits for the next.
-struct JobFeed {
-  Bars& b;
-  bool& dead;
-  uint32_t k = 0;
-  __device__ const Job* next() {
-    if (!dead && !bar_wait(&b.job_full[k % kJobs], (k / kJobs) & 1)) dead = true;
-    const Job* j = &b.job[k % kJobs];
-    return dead || j->begin == j->end ? nullptr : j;
-  }
-  // By one thread, when its warp needs nothing of the job any more.
-  __device__ void done() { mbar_arrive(&b.job_empty[k % kJobs]); }
-};
 // Whether some row of the item does not see some key of key tile t.
 __device__ __forceinline__ bool edge_tile(const AttnArgs& a, int t, int p_first, int p_last) {
   const int first = t * kTile, last = first + kTile - 1;
@@ -137,18 +110,8 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
   Walk walk(p.a, p.s);
   bool more = walk.start_plan();
   for (;; ++k) {
-    if (k >= kJobs && !bar_wait(&b.job_empty[k % kJobs], (k / kJobs - 1) & 1)) break;
+    if (!b.jobs.put(k, walk, more, lane)) break;
     const Item& w = walk.item;
-    if (lane == 0) {
-      Job& j = b.job[k % kJobs];
-      j.begin = j.end = 0;
-      if (more) {
-        j.head = w.head; j.row0 = w.row0; j.rows = w.rows; j.last_row = w.last_row; j.len = w.len; j.n_tok = w.n_tok;
-        j.sink = w.tiles.sink; j.lo = w.tiles.lo; j.begin = walk.begin; j.end = walk.end;
-        j.p_first = w.p_first(); j.p_last = w.p_last(); j.slot = walk.part_slot(true); j.seq = w.seq; j.base = w.base;
-      }
-      mbar_arrive(&b.job_full[k % kJobs]);
-    }
     if (!more) return;
     const int p_first = w.p_first(), p_last = w.p_last(), begin = walk.begin, end = walk.end, head = w.head;
     const int32_t* table = a.page_table + static_cast<int64_t>(w.seq) * a.max_pages;
@@ -213,15 +176,13 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
   auto step = [&] {
     if (++sk == C::kSlots) { sk = 0; pk ^= 1; }
   };
-  JobFeed feed{b, dead};
+  JobFeed feed{b.jobs, dead};
   while (const Job* jp = feed.next()) {
     const int begin = uniform(jp->begin), end = uniform(jp->end), sink = uniform(jp->sink), lo = uniform(jp->lo);
     const int p_first = uniform(jp->p_first), p_last = uniform(jp->p_last);
     const int last_row = uniform(jp->last_row) - uniform(jp->row0);
     const bool mine = last_row >= 128 * t, both = last_row >= 128;  // the item has rows of this tile, of both
-    __syncwarp();
-    if (leader) feed.done();
-    ++feed.k;
+    feed.done(threadIdx.x & 31);
     wait(&b.q_full, items);
     ++items;
     // An edge tile's values are looked through by other warps before they are used.  Edge tiles
@@ -326,7 +287,7 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
   float* qexp = reinterpret_cast<float*>(sm + C::kSmExp);
   uint32_t n = 0, items = 0, edges = 0;
   bool dead = false;
-  JobFeed feed{b, dead};
+  JobFeed feed{b.jobs, dead};
   while (const Job* jp = feed.next()) {
     const Job& w = *jp;
     if (items > 0 && !dead && !bar_wait(&b.q_empty, (items - 1) & 1)) dead = true;
@@ -334,7 +295,7 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
     {
       const int first = w.row0 + grp;
       int tok = first / G, g = first - tok * G;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (w.base + tok) * a.q_stride[1] +
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + w.q_base + tok * a.q_stride[1] +
                             (static_cast<int64_t>(w.head) * G + g) * a.q_stride[2] + 8 * sub;
       const int n_rows = w.rows - w.row0;
 #pragma unroll 4
@@ -398,9 +359,7 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
         if (lane == 0) mbar_arrive(&b.v_ok);
       }
     }
-    __syncwarp();
-    if (lane == 0) feed.done();
-    ++feed.k;
+    feed.done(lane);
   }
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
@@ -421,7 +380,7 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
   const int sc_at = kTile * 128 + (tid >> p_log) * 128 + (tid & ((1 << p_log) - 1));
   uint32_t n = 0;
   bool dead = false;
-  JobFeed feed{b, dead};
+  JobFeed feed{b.jobs, dead};
   while (const Job* jp = feed.next()) {
     const Job& w = *jp;
     const int begin = w.begin, end = w.end;
@@ -524,9 +483,7 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
         if (lane == 0) mbar_arrive(&b.full[s]);
       }
     }
-    __syncwarp();
-    if (lane == 0) feed.done();
-    ++feed.k;
+    feed.done(lane);
   }
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
@@ -551,7 +508,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
     if (!dead && !bar_wait(bar, parity & 1)) dead = true;
   };
   const float scale = a.scale_log2 == 0.f ? 1.f : fabsf(a.scale_log2);  // the queries have its sign (0: are 0)
-  JobFeed feed{b, dead};
+  JobFeed feed{b.jobs, dead};
   while (const Job* jp = feed.next()) {
     const Job& w = *jp;
     const int begin = w.begin, end = w.end;
@@ -563,9 +520,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       }
       n += 2 * (end - begin);
       ++seen;
-      __syncwarp();
-      if (lane == 0) feed.done();
-      ++feed.k;
+      feed.done(lane);
       continue;
     }
     const bool live = row < w.rows;
@@ -744,9 +699,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       if (live && a.lse) a.lse[orow] = lse_of(m, l);
     }
     tc_fence_before();
-    __syncwarp();
-    if (lane == 0) feed.done();
-    ++feed.k;
+    feed.done(lane);
   }
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
@@ -778,10 +731,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       mbar_init(&b.drain[i], 1);
     }
     // a job is read by the two product warps, the query warps, the eight softmax warps and the converters
-    for (int i = 0; i < kJobs; ++i) {
-      mbar_init(&b.job_full[i], 1);
-      mbar_init(&b.job_empty[i], 10 + C::kQueryWarps + (kE4m3 ? 4 : 0));
-    }
+    b.jobs.init(10 + C::kQueryWarps + (kE4m3 ? 4 : 0));
     fence_mbar_init();
     p.s.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
   }

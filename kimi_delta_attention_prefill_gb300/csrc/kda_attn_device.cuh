@@ -98,11 +98,6 @@ struct Item {
   __device__ int p_of_row(int row) const { return len - n_tok + row / G; }
   __device__ int p_first() const { return p_of_row(row0); }
   __device__ int p_last() const { return p_of_row(last_row); }
-  __device__ int64_t q_offset(const AttnArgs& a, int row) const {
-    const int t = row / G, g = row - t * G;
-    const int64_t s = a.cu ? (base + t) * a.q_stride[1] : static_cast<int64_t>(seq) * a.q_stride[0] + t * a.q_stride[1];
-    return s + (static_cast<int64_t>(head) * G + g) * a.q_stride[2];
-  }
   __device__ int64_t o_row(const AttnArgs& a, int row) const {
     const int t = row / G, g = row - t * G;
     return (base + t) * a.H + static_cast<int64_t>(head) * G + g;
@@ -309,6 +304,61 @@ struct ItemWalk {
       s.desc[blockIdx.x] = make_int4(item.seq, item.head, item.row0, static_cast<int>((e * blocks + total - 1) / total - 1));
     }
     return 2 * blockIdx.x + 1;
+  }
+};
+
+// One item (or part) of a block's share, as the copy warp, which walks, hands it to the others.
+struct Job {
+  int head, row0, rows, last_row, len, n_tok;
+  int sink, lo;         // its key tiles
+  int begin, end;       // the visits that are this block's; none: the share is done
+  int p_first, p_last;  // positions of its first and last row
+  int slot;             // of the workspace, -1: whole
+  int64_t base;         // packed row of the sequence's first token
+  int64_t q_base;       // its queries' element offset
+  __device__ int tile(int i) const { return i < sink ? i : lo + (i - sink); }
+};
+constexpr int kJobs = 4;
+struct JobRing {
+  uint64_t full[kJobs], empty[kJobs];
+  Job job[kJobs];
+  __device__ void init(int readers) {
+    for (int i = 0; i < kJobs; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], readers); }
+  }
+  // The k-th job from the walk, or (more = false) the end.  By a whole warp; false: a wait ran out.
+  template <class Walk>
+  __device__ bool put(uint32_t k, const Walk& walk, bool more, int lane) {
+    if (k >= kJobs && !bar_wait(&empty[k % kJobs], (k / kJobs - 1) & 1)) return false;
+    if (lane == 0) {
+      Job& j = job[k % kJobs];
+      j.begin = j.end = 0;
+      if (more) {
+        const Item& w = walk.item;
+        j.head = w.head; j.row0 = w.row0; j.rows = w.rows; j.last_row = w.last_row; j.len = w.len; j.n_tok = w.n_tok;
+        j.sink = w.tiles.sink; j.lo = w.tiles.lo; j.begin = walk.begin; j.end = walk.end;
+        j.p_first = w.p_first(); j.p_last = w.p_last(); j.slot = walk.part_slot(true); j.base = w.base;
+        j.q_base = walk.a.cu ? w.base * walk.a.q_stride[1] : static_cast<int64_t>(w.seq) * walk.a.q_stride[0];
+      }
+      mbar_arrive(&full[k % kJobs]);
+    }
+    return true;
+  }
+};
+// The jobs in order, for one warp: next() waits for the next.
+struct JobFeed {
+  JobRing& r;
+  bool& dead;
+  uint32_t k = 0;
+  __device__ const Job* next() {
+    if (!dead && !bar_wait(&r.full[k % kJobs], (k / kJobs) & 1)) dead = true;
+    const Job* j = &r.job[k % kJobs];
+    return dead || j->begin == j->end ? nullptr : j;
+  }
+  // The warp needs nothing of the job any more.
+  __device__ void done(int lane) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&r.empty[k % kJobs]);
+    ++k;
   }
 };
 

@@ -15,10 +15,12 @@
 // the warp-level tensor rate (16 padded rows: 8 KFLOP per key against 512 bytes), so tcgen05's
 // 128-row tiles would add latency and win nothing.
 //
-// Blocks: 4 warps compute, 1 warp issues the copies (TMA, one box per page and tile of 64
-// keys, 128-byte swizzle) into a ring of stages.  With up to 16 rows the 4 warps split the
-// keys of a tile (each with its own m, l, O, joined once at the end), with up to 32 rows two
-// and two, with more each warp has 16 rows and all keys.
+// Blocks: 4 warps compute, 1 warp walks the block's share and issues the copies (TMA, one box
+// per page and tile of keys, 128-byte swizzle) into a ring of stages.  With up to 16 rows the 4
+// warps split the keys of a tile (each with its own m, l, O, joined once at the end), with up to
+// 32 rows two and two, with more each warp has 16 rows and all keys.  A tile is 64 keys of a
+// bf16 cache, 128 of an E4M3 cache: as many bytes, and twice the independent work for a warp,
+// whose conversions and products are then what bounds it.
 //
 // Work: the (sequence, head, row tile) items lie one after the other on a line of key tiles,
 // and every block takes an equal share of that line, whole items or parts of them: ragged
@@ -41,21 +43,21 @@ namespace kda {
 
 namespace {
 
-constexpr int kTile = 64;  // keys a stage
 constexpr int kWarps = 4;
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTileRows = 16;
 constexpr int kMaxRows = kWarps * kTileRows;
-constexpr int kMinTiles = 4;  // fewest key tiles of a block's share: below that the joining costs more than it spreads
-constexpr int kItemCost = 1;
 
 template <bool kE4m3>
 struct Stage {
-  static constexpr int kBytes = kE4m3 ? kTile * 128 : kTile * 256;  // one of K, V
-  static constexpr int kScales = kE4m3 ? 4 * 128 : 0;               // a 128-byte slot per page of the tile
+  static constexpr int kTile = kE4m3 ? 128 : 64;  // keys
+  static constexpr int kMinTiles = kE4m3 ? 2 : 4;  // a block's least share: below that the joining costs more than it spreads
+  static constexpr int kBytes = kTile * (kE4m3 ? 128 : 256);  // one of K, V
+  static constexpr int kScales = kE4m3 ? 8 * 128 : 0;         // a 128-byte slot per page of the tile
   static constexpr int kTotal = 2 * kBytes + 2 * kScales;
-  static constexpr int kCount = kE4m3 ? 5 : 3;
+  static constexpr int kCount = 3;
 };
+constexpr int kItemCost = 1;
 constexpr int kJoinBytes = 32 * 64 * 4 + 32 * 4 * 4;  // one warp's O and its (m, l) pairs
 template <bool kE4m3>
 constexpr int smem_bytes() {
@@ -82,14 +84,16 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Bits 0 / 1: the low / high half of a pair is NaN or infinite; such halves are cleared.
-template <bool kHalf>
-__device__ __forceinline__ uint32_t take_nonfinite(uint32_t& w) {
-  constexpr uint32_t e = kHalf ? 0x7c00u : 0x7f80u;
-  uint32_t f = 0;
-  if ((w & e) == e) { f |= 1; w &= 0xffff0000u; }
-  if ((w & (e << 16)) == (e << 16)) { f |= 2; w &= 0x0000ffffu; }
-  return f;
+// Address of the c-th 16-byte piece of a key's value row; whether a word holds a non-finite value.
+template <bool kE4m3>
+__device__ __forceinline__ uint32_t value_piece(uint32_t vb, uint32_t key, int c, int P, int p_log) {
+  if constexpr (kE4m3) return vb + sw128(key, 16 * c);
+  return vb + (key >> p_log) * (P * 256) + (c >> 3) * (P * 128) + sw128(key & (P - 1), 16 * (c & 7));
+}
+template <bool kE4m3>
+__device__ __forceinline__ bool nonfinite(uint32_t w) {
+  if constexpr (kE4m3) return (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0;
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
 struct ShortParams {
@@ -101,44 +105,52 @@ struct ShortParams {
 template <bool kE4m3, int kRG>
 __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_constant__ ShortParams p) {
   using St = Stage<kE4m3>;
+  constexpr int kTile = St::kTile;
   constexpr int kKG = kWarps / kRG;            // warps that split a tile's keys
   constexpr int kKeys = kTile / kKG;           // keys of a warp
-  constexpr int kNT = kKeys / 8;               // its 8-key column tiles
+  constexpr int kStep = kKeys < 32 ? kKeys : 32;  // of which so many at a time
+  constexpr int kNT = kStep / 8;               // 8-key column tiles
   constexpr int kRT = kRG * kTileRows;         // rows of an item
   extern __shared__ uint8_t smem_raw[];
   __shared__ alignas(8) uint64_t full[St::kCount], empty[St::kCount];
+  __shared__ JobRing jobs;
   uint8_t* sm = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < St::kCount; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], kWarps); }
+    jobs.init(kWarps);
     fence_mbar_init();
   }
   pdl_launch_dependents();
+  const int P = min(a.cache.page_size, kTile), n_blk = kTile / P;
   ItemWalk<kRT, kTile> walk(p.a, p.s);
   const bool any = walk.template start<kThreads>(tid);  // has the barriers that publish the mbarriers
   if (!any) return;
-  const int P = min(a.cache.page_size, kTile), n_blk = kTile / P;
 
   if (warp == kWarps) {  // ------------------------------------------------------ copies
-    int it = 0;
+    uint32_t it = 0;
     const int blk = lane;
-    do {
+    bool more = true;
+    for (uint32_t k = 0;; ++k) {
+      if (!jobs.put(k, walk, more, lane)) break;
+      if (!more) return;
       const Item& w = walk.item;
       const KeyTiles kt = w.tiles;
       const int p_first = w.p_first(), p_last = w.p_last();
+      const int32_t* table = a.page_table + static_cast<int64_t>(w.seq) * a.max_pages;
       for (int i = walk.begin; i < walk.end; ++i, ++it) {
         const int j0 = kt.at(i) * kTile + blk * P;  // first key of this lane's page block
         int page = -1;
         if (blk < n_blk && j0 <= p_last) {
-          page = a.page_table[static_cast<int64_t>(w.seq) * a.max_pages + (j0 >> a.cache.page_log2)];
+          page = table[j0 >> a.cache.page_log2];
           if (page < 0 || page >= a.cache.n_pages) {
             const bool needed = a.window == 0 || j0 + P - 1 > p_first - a.window || j0 < a.n_sink;
             if (needed) report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
             page = -1;  // out of the tensor map's range: the copy fills with zeros
           }
         }
-        const int s = it % St::kCount;
+        const uint32_t s = it % St::kCount;
         if (it >= St::kCount && !bar_wait(&empty[s], ((it / St::kCount) - 1) & 1)) {
           report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
           return;
@@ -159,7 +171,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           }
         }
       }
-    } while (walk.next());
+      more = walk.next();
+    }
+    report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
     return;
   }
 
@@ -168,11 +182,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
   const int rg = warp / kKG, kg = warp % kKG;
   float* join = reinterpret_cast<float*>(sm + St::kTotal * St::kCount);
   const int p_log = 31 - __clz(P);
-  int it = 0;
+  const int G = a.H / a.cache.heads;
+  uint32_t it = 0;
   bool dead = false;
-  do {
-    const Item& w = walk.item;
-    const KeyTiles kt = w.tiles;
+  JobFeed feed{jobs, dead};
+  while (const Job* jp = feed.next()) {
+    const Job& w = *jp;
     // this thread's rows g and g + 8 of the warp's 16: position, query fragments
     int pos[2];
     float cs[2];  // scale in log2 units (times the query row's own power of two)
@@ -181,8 +196,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
     for (int r = 0; r < 2; ++r) {
       const int row = w.row0 + rg * kTileRows + g + 8 * r;
       const bool live = row < w.rows;
-      pos[r] = live ? w.p_of_row(row) : -1;
-      const uint16_t* q = static_cast<const uint16_t*>(a.q) + w.q_offset(a, live ? row : 0);
+      const int tok = live ? row / G : 0, gh = live ? row - tok * G : 0;
+      pos[r] = live ? w.len - w.n_tok + tok : -1;
+      const uint16_t* q = static_cast<const uint16_t*>(a.q) + w.q_base + tok * a.q_stride[1] +
+                          (static_cast<int64_t>(w.head) * G + gh) * a.q_stride[2];
       cs[r] = a.scale_log2;
       if constexpr (kE4m3) {
         // channel order of the codes' 16-byte loads: this thread's chunks t and t + 4, 4 channels a step
@@ -217,14 +234,54 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-    const int p_first = w.p_first(), p_last = w.p_last();
-
-    for (int i = walk.begin; i < walk.end; ++i, ++it) {
-      const int s = it % St::kCount;
+    const int begin = w.begin, end = w.end;
+    for (int i = begin; i < end; ++i, ++it) {
+      const uint32_t s = it % St::kCount;
       // after a wait that ran out the loop goes on without waiting, so that every barrier is still met
       if (!dead && !bar_wait(&full[s], (it / St::kCount) & 1)) dead = true;
       const uint32_t kb = smem_u32(sm + s * St::kTotal), vb = kb + St::kBytes;
-      const int key0 = kt.at(i) * kTile + kg * kKeys;  // first key of this warp
+      const int t_first = w.tile(i) * kTile, t_last = t_first + kTile - 1;
+      const bool edge = t_last > w.p_first || (a.window > 0 && t_first <= w.p_last - a.window && t_last >= a.n_sink);
+      if (edge) {
+        // 0 * NaN must not reach a row that does not see the key: value rows with a non-finite
+        // value are cleared, and the rows that do see one become NaN here.
+        uint32_t bad[(kKeys + 31) / 32];
+#pragma unroll
+        for (int q = 0; q < (kKeys + 31) / 32; ++q) {
+          const uint32_t key = kg * kKeys + 32 * q + lane;
+          bool has = false;
+          if (32 * q + lane < kKeys) {
+#pragma unroll 1
+            for (int c = 0; c < (kE4m3 ? 8 : 16); ++c) {
+              const uint4 v = lds128(value_piece<kE4m3>(vb, key, c, P, p_log));
+              has |= nonfinite<kE4m3>(v.x) | nonfinite<kE4m3>(v.y) | nonfinite<kE4m3>(v.z) | nonfinite<kE4m3>(v.w);
+            }
+          }
+          bad[q] = __ballot_sync(0xffffffffu, has);
+        }
+        if constexpr (kRG > 1) named_bar_sync(2 + kg, 32 * kRG);  // the warps that share these keys have all looked
+#pragma unroll
+        for (int q = 0; q < (kKeys + 31) / 32; ++q) {
+          if (!bad[q]) continue;
+          if ((bad[q] >> lane) & 1) {
+#pragma unroll 1
+            for (int c = 0; c < (kE4m3 ? 8 : 16); ++c)
+              sts128(value_piece<kE4m3>(vb, kg * kKeys + 32 * q + lane, c, P, p_log), make_uint4(0, 0, 0, 0));
+          }
+          for (uint32_t m = bad[q]; m; m &= m - 1) {
+            const int key = t_first + kg * kKeys + 32 * q + __ffs(m) - 1;
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (sees(pos[r], key, a.window, a.n_sink)) l[r] = __uint_as_float(0x7fffffffu);
+          }
+        }
+        fence_proxy_async_smem();
+        if constexpr (kRG > 1) named_bar_sync(2 + kg, 32 * kRG);
+        else __syncwarp();
+      }
+#pragma unroll 1
+      for (int k0 = kg * kKeys; k0 < (kg + 1) * kKeys; k0 += kStep) {
+      const int key0 = t_first + k0;  // first key of this step
       float x[kNT][4];
 #pragma unroll
       for (int n = 0; n < kNT; ++n)
@@ -234,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
       if constexpr (kE4m3) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n) {
-          const uint32_t row = kg * kKeys + n * 8 + g;
+          const uint32_t row = k0 + n * 8 + g;
           const uint4 u0 = lds128(kb + sw128(row, 16 * t)), u1 = lds128(kb + sw128(row, 64 + 16 * t));
           const uint32_t c[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
@@ -244,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
       } else {
 #pragma unroll
         for (int n = 0; n < kNT; n += 2) {
-          const uint32_t row = kg * kKeys + n * 8 + (lane & 7) + ((lane >> 4) << 3);
+          const uint32_t row = k0 + n * 8 + (lane & 7) + ((lane >> 4) << 3);
           const uint32_t base = kb + (row >> p_log) * (P * 256), rr = row & (P - 1);
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -261,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
         if constexpr (kE4m3) {
-          const uint32_t key = kg * kKeys + n * 8 + 2 * t;
+          const uint32_t key = k0 + n * 8 + 2 * t;
           const uint8_t* sc = sm + s * St::kTotal + 2 * St::kBytes + (key >> p_log) * 128 + (key & (P - 1));
           const uint32_t k2 = *reinterpret_cast<const uint16_t*>(sc), v2 = *reinterpret_cast<const uint16_t*>(sc + St::kScales);
 #pragma unroll
@@ -277,8 +334,6 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           for (int e = 0; e < 4; ++e) x[n][e] *= cs[e >> 1];
         }
       }
-      const int t_first = kt.at(i) * kTile, t_last = t_first + kTile - 1;
-      const bool edge = t_last > p_first || (a.window > 0 && t_first <= p_last - a.window && t_last >= a.n_sink);
       if (edge) {
 #pragma unroll
         for (int n = 0; n < kNT; ++n)
@@ -331,9 +386,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
 #pragma unroll
       for (int n = 0; n < kNT; n += 2) {  // 16 keys
         const uint32_t pa[4] = {pf[n][0], pf[n][1], pf[n + 1][0], pf[n + 1][1]};
-        uint32_t bad = 0;  // bits: keys 2t, 2t + 1, 2t + 8, 2t + 9 have a non-finite value
         if constexpr (kE4m3) {
-          const uint32_t row = kg * kKeys + n * 8 + 2 * t;
+          const uint32_t row = k0 + n * 8 + 2 * t;
           uint32_t c[4][4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
@@ -347,43 +401,20 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
             uint32_t ba[4] = {e4m3_half2(a0), e4m3_half2(a0 >> 16), e4m3_half2(a1), e4m3_half2(a1 >> 16)};
             uint32_t bb[4] = {e4m3_half2(b0), e4m3_half2(b0 >> 16), e4m3_half2(b1), e4m3_half2(b1 >> 16)};
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              if (edge) bad |= take_nonfinite<true>(ba[q]) | (take_nonfinite<true>(bb[q]) << 2);
-              mma16816<true>(o[4 * e + q], pa, ba[q], bb[q]);
-            }
+            for (int q = 0; q < 4; ++q) mma16816<true>(o[4 * e + q], pa, ba[q], bb[q]);
           }
         } else {
-          const uint32_t row = kg * kKeys + n * 8 + (lane & 15);
+          const uint32_t row = k0 + n * 8 + (lane & 15);
           const uint32_t base_v = vb + (row >> p_log) * (P * 256), rr = row & (P - 1);
 #pragma unroll
           for (int c = 0; c < 16; c += 2) {
             uint32_t b[4];
             ldsm4t(base_v + (c >> 3) * (P * 128) + sw128(rr, 16 * ((c & 7) + (lane >> 4))), b);
-            if (edge) {
-              bad |= take_nonfinite<false>(b[0]) | (take_nonfinite<false>(b[1]) << 2);
-              bad |= take_nonfinite<false>(b[2]) | (take_nonfinite<false>(b[3]) << 2);
-            }
             mma16816<false>(o[c], pa, b[0], b[1]);
             mma16816<false>(o[c + 1], pa, b[2], b[3]);
           }
         }
-        if (edge) {
-          // 0 * NaN must not reach a row that does not see the key: the values were cleared, and
-          // the rows that do see it become NaN here.
-          bad |= __shfl_xor_sync(0xffffffffu, bad, 4);
-          bad |= __shfl_xor_sync(0xffffffffu, bad, 8);
-          bad |= __shfl_xor_sync(0xffffffffu, bad, 16);
-          if (bad) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if ((bad >> e) & 1) {
-                const int key = key0 + n * 8 + 2 * t + (e & 1) + 8 * (e >> 1);
-#pragma unroll
-                for (int r = 0; r < 2; ++r)
-                  if (sees(pos[r], key, a.window, a.n_sink)) l[r] = __uint_as_float(0x7fffffffu);
-              }
-          }
-        }
+      }
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
@@ -428,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
       }
     }
     if (kg == 0) {
-      const int slot = walk.part_slot(tid == 0);
+      const int slot = w.slot;
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const int lr = rg * kTileRows + g + 8 * r, row = w.row0 + lr;
@@ -450,7 +481,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           if (t == 0) p.s.part_ml[static_cast<int64_t>(slot) * p.s.part_rows + lr] = make_float2(m[r], l[r]);
         } else {
           const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
-          const int64_t orow = w.o_row(a, row);
+          const int64_t orow = (w.base + row / G) * a.H + static_cast<int64_t>(w.head) * G + row % G;
           uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.o) + orow * 128);
           if constexpr (kE4m3) {
 #pragma unroll
@@ -470,7 +501,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
         }
       }
     }
-  } while (walk.next());
+    feed.done(lane);
+  }
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
@@ -499,9 +531,10 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms) {
   p.a = a;
   const int grid = 2 * num_sms;
   attn_split_layout(&p.s, a.workspace, grid, kTileRows * rg, 0);
-  p.s.min_tiles = kMinTiles;
+  const int tile = a.cache.e4m3 ? Stage<true>::kTile : Stage<false>::kTile;
+  p.s.min_tiles = a.cache.e4m3 ? Stage<true>::kMinTiles : Stage<false>::kMinTiles;
   p.s.item_cost = kItemCost;
-  if (!make_cache_maps(a.cache, kTile, 2, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
+  if (!make_cache_maps(a.cache, tile, 2, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
   cudaError_t e;
   if (a.cache.e4m3)
     e = rg == 1 ? launch_short<true, 1>(p, grid) : rg == 2 ? launch_short<true, 2>(p, grid) : launch_short<true, 4>(p, grid);
@@ -529,10 +562,11 @@ cudaError_t launch_attn_prefill(const AttnArgs& a, int num_sms) {
   p.a = a;
   const int grid = 2 * num_sms;
   attn_split_layout(&p.s, a.workspace, grid, kMaxRows, attn_max_items(a.n_seq, a.tokens, G, kMaxRows));
-  p.s.min_tiles = kMinTiles;
+  const int tile = a.cache.e4m3 ? Stage<true>::kTile : Stage<false>::kTile;
+  p.s.min_tiles = a.cache.e4m3 ? Stage<true>::kMinTiles : Stage<false>::kMinTiles;
   p.s.item_cost = kItemCost;
-  if (!make_cache_maps(a.cache, kTile, 2, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
-  cudaError_t e = launch_attn_plan(a, p.s, kMaxRows, kTile);
+  if (!make_cache_maps(a.cache, tile, 2, &p.tk, &p.tv, &p.tks, &p.tvs)) return cudaErrorInvalidValue;
+  cudaError_t e = launch_attn_plan(a, p.s, kMaxRows, tile);
   if (e != cudaSuccess) return e;
   e = a.cache.e4m3 ? launch_short<true, 4>(p, grid) : launch_short<false, 4>(p, grid);
   if (e != cudaSuccess) return e;
