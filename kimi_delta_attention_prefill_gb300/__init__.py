@@ -21,6 +21,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -35,12 +36,6 @@ _lib = None
 _lock = threading.Lock()
 
 _c_int, _c_i64, _c_sz, _vp = ctypes.c_int, ctypes.c_int64, ctypes.c_size_t, ctypes.c_void_p
-
-
-class _KvCache(ctypes.Structure):  # kda_kv_cache
-    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("k_stride", _c_i64 * 3),
-                ("v_stride", _c_i64 * 3), ("k_scale_stride", _c_i64 * 2), ("v_scale_stride", _c_i64 * 2),
-                ("n_pages", _c_i64), ("n_kv_heads", _c_int), ("page_size", _c_int), ("dtype", _c_int)]
 
 
 class KdaLibraryError(RuntimeError):
@@ -111,8 +106,7 @@ def library():
             lib.kda_prefill_noalloc.restype = _c_int
             lib.kda_prefill_noalloc.argtypes = ([_vp] * 7 + [_c_int, _c_i64] + [_vp, _vp, _c_i64] + [_vp] * 3 +
                                                 [_c_int, _c_int, _c_int, _vp, _vp])
-            cache = ctypes.POINTER(_KvCache)
-            strides = ctypes.POINTER(_c_i64)
+            cache = strides = _vp  # a kda_kv_cache, int64 arrays
             lib.kda_kv_append.restype = _c_int
             lib.kda_kv_append.argtypes = [cache, _vp, strides, _vp, strides, _vp, _c_int, _c_int, _vp, _vp, _c_i64,
                                           _c_int, _vp, _vp]
@@ -585,8 +579,23 @@ def combine_pairs(M, S_tilde, S_in=None, entry=None, stream=None):
 
 
 # ------------------------------------------------------------------------ attention cache
-def _rows_of(t, name, dtype, lead):
-    """A tensor ``lead + [128]`` whose last dimension is contiguous; the others may be strided."""
+# A decode step makes a few of these calls a layer and each runs for microseconds, so what is
+# checked for every call is checked in as few steps as Python allows; the functions that say what
+# is wrong run only when something is.
+_BF16, _E4M3, _I32 = torch.bfloat16, torch.float8_e4m3fn, torch.int32
+_pack_cache = struct.Struct("4q 3q 3q 2q 2q q 3i 4x").pack  # kda_kv_cache
+_pack2, _pack3 = struct.Struct("2q").pack, struct.Struct("3q").pack
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream_of(stream):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return _stream_handle(stream)
+
+
+def _say_rows(t, name, dtype, lead):
+    """Why ``t`` is not a tensor ``lead + [128]`` of rows; None: it is."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -598,55 +607,113 @@ def _rows_of(t, name, dtype, lead):
         raise ValueError(f"{name} must have shape {shape}, got {tuple(t.shape)}")
     if t.numel() and t.stride(-1) != 1:
         raise ValueError(f"{name} must be contiguous in its last dimension")
-    return t
 
 
-def _row_strides(t):
-    # torch gives dimensions of extent 1 any stride; the library wants a sound one
-    packed = [1] * t.dim()
-    for i in range(t.dim() - 2, -1, -1):
-        packed[i] = packed[i + 1] * max(t.shape[i + 1], 1)
-    s = [t.stride(i) if t.shape[i] > 1 else packed[i] for i in range(t.dim() - 1)]
-    return (_c_i64 * len(s))(*s)
+def _sound(shape, strides):
+    """Strides of all dimensions but the last.  torch gives dimensions of extent 1 (and those of
+    empty tensors) any stride; the library wants a sound one."""
+    lead = shape[:-1]
+    if 1 not in lead and 0 not in lead:
+        return strides[:-1]
+    packed = [1] * len(shape)
+    for i in range(len(shape) - 2, -1, -1):
+        packed[i] = packed[i + 1] * max(shape[i + 1], 1)
+    empty = 0 in lead
+    return tuple(p if empty or n == 1 else s for p, s, n in zip(packed, strides, lead))
+
+
+def _rows_of(t, name, lead):
+    """Strides of bf16 rows ``lead + [128]``; all dimensions but the last may be strided."""
+    try:
+        shape, strides = t.shape, t.stride()
+        good = shape == lead + (HEAD_DIM,) and t.dtype is _BF16 and t.is_cuda and strides[-1] == 1
+    except AttributeError:
+        good = False
+    if not good:
+        _say_rows(t, name, _BF16, lead)
+        shape, strides = t.shape, t.stride()
+    return _sound(shape, strides)
+
+
+def _say_cache(k_pool, v_pool, k_scale, v_scale):
+    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
+        raise ValueError("k_pool must be a tensor [n_pages, n_kv_heads, page_size, 128]")
+    if k_pool.dtype not in (_BF16, _E4M3):
+        raise TypeError(f"k_pool must be torch.bfloat16 or torch.float8_e4m3fn, got {k_pool.dtype}")
+    lead = tuple(k_pool.shape[:3])
+    _say_rows(k_pool, "k_pool", k_pool.dtype, lead)
+    _say_rows(v_pool, "v_pool", k_pool.dtype, lead)
+    if k_pool.dtype == _BF16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale / v_scale belong to a float8_e4m3fn cache")
+        return
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if t is None:
+            raise ValueError(f"{name} is required for a float8_e4m3fn cache")
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype != torch.uint8:
+            raise TypeError(f"{name} must be torch.uint8, got {t.dtype}")
+        if tuple(t.shape) != lead:
+            raise ValueError(f"{name} must have shape {lead}, got {tuple(t.shape)}")
+        if t.numel() and t.stride(-1) != 1:
+            raise ValueError(f"{name} must be contiguous in its last dimension")
 
 
 def _kv_cache(k_pool, v_pool, k_scale, v_scale):
-    if not isinstance(k_pool, torch.Tensor) or k_pool.dim() != 4:
-        raise ValueError("k_pool must be a tensor [n_pages, n_kv_heads, page_size, 128]")
-    if k_pool.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise TypeError(f"k_pool must be torch.bfloat16 or torch.float8_e4m3fn, got {k_pool.dtype}")
-    lead = tuple(k_pool.shape[:3])
-    _rows_of(k_pool, "k_pool", k_pool.dtype, lead)
-    _rows_of(v_pool, "v_pool", k_pool.dtype, lead)
-    c = _KvCache(k=_ptr(k_pool), v=_ptr(v_pool), k_stride=_row_strides(k_pool), v_stride=_row_strides(v_pool),
-                 n_pages=lead[0], n_kv_heads=lead[1], page_size=lead[2], dtype=0)
-    if k_pool.dtype == torch.float8_e4m3fn:
-        c.dtype = 1
-        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-            if t is None:
-                raise ValueError(f"{name} is required for a float8_e4m3fn cache")
-            if not isinstance(t, torch.Tensor):
-                raise TypeError(f"{name} must be a torch.Tensor")
-            if not t.is_cuda:
-                raise ValueError(f"{name} must be a CUDA tensor")
-            if t.dtype != torch.uint8:
-                raise TypeError(f"{name} must be torch.uint8, got {t.dtype}")
-            if tuple(t.shape) != lead:
-                raise ValueError(f"{name} must have shape {lead}, got {tuple(t.shape)}")
-            if t.numel() and t.stride(-1) != 1:
-                raise ValueError(f"{name} must be contiguous in its last dimension")
-            setattr(c, name, _ptr(t))
-            setattr(c, name + "_stride", _row_strides(t))
-    elif k_scale is not None or v_scale is not None:
-        raise ValueError("k_scale / v_scale belong to a float8_e4m3fn cache")
-    return c
+    """The cache as the library takes it (the bytes of a kda_kv_cache), and its heads."""
+    try:
+        shape, dtype, ks, vs = k_pool.shape, k_pool.dtype, k_pool.stride(), v_pool.stride()
+        good = (len(shape) == 4 and shape[3] == HEAD_DIM and v_pool.shape == shape and v_pool.dtype is dtype
+                and k_pool.is_cuda and v_pool.is_cuda and ks[3] == 1 and vs[3] == 1)
+        if dtype is _E4M3:
+            lead = shape[:3]
+            good = (good and k_scale.shape == lead and v_scale.shape == lead and k_scale.dtype is torch.uint8
+                    and v_scale.dtype is torch.uint8 and k_scale.is_cuda and v_scale.is_cuda)
+            kss, vss = k_scale.stride(), v_scale.stride()
+            good = good and kss[2] == 1 and vss[2] == 1
+        else:
+            good = good and dtype is _BF16 and k_scale is None and v_scale is None
+    except (AttributeError, IndexError):
+        good = False
+    if not good:
+        _say_cache(k_pool, v_pool, k_scale, v_scale)
+        shape, dtype, ks, vs = k_pool.shape, k_pool.dtype, k_pool.stride(), v_pool.stride()
+        if dtype is _E4M3:
+            kss, vss = k_scale.stride(), v_scale.stride()
+    ks, vs = _sound(shape, ks), _sound(shape, vs)
+    n, heads, page, _ = shape
+    if dtype is _E4M3:
+        three = shape[:3]
+        c = _pack_cache(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *ks, *vs,
+                        *_sound(three, kss), *_sound(three, vss), n, heads, page, 1)
+    else:
+        c = _pack_cache(k_pool.data_ptr(), v_pool.data_ptr(), 0, 0, *ks, *vs, 0, 0, 0, 0, n, heads, page, 0)
+    return c, heads
+
+
+def _index(t, name, shape):
+    """Address of a contiguous int32 CUDA tensor of that shape."""
+    try:
+        if t.dtype is _I32 and t.shape == shape and t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _need(t, name, _I32, shape)
+    return t.data_ptr()
 
 
 def _page_table(page_table):
-    _need(page_table, "page_table", torch.int32)
+    _need(page_table, "page_table", _I32)
     if page_table.dim() != 2:
         raise ValueError(f"page_table must have shape [sequences, pages], got {tuple(page_table.shape)}")
-    return tuple(page_table.shape)
+    return page_table.shape
+
+
+def _status_ptr(dev_status):
+    return None if dev_status is None else _need(dev_status, "dev_status", _I32).data_ptr()
 
 
 def kv_append(k, v, k_pool, v_pool, page_table, cu_seqlens, kv_start, k_scale=None, v_scale=None, dev_status=None,
@@ -662,18 +729,14 @@ def kv_append(k, v, k_pool, v_pool, page_table, cu_seqlens, kv_start, k_scale=No
     row ``cu[i] + t`` becomes token ``kv_start[i] + t`` of sequence i.  Updates the pools (and
     scales) in place.
     """
-    c = _kv_cache(k_pool, v_pool, k_scale, v_scale)
+    c, heads = _kv_cache(k_pool, v_pool, k_scale, v_scale)
     n_seq, max_pages = _page_table(page_table)
     T = k.shape[0] if isinstance(k, torch.Tensor) and k.dim() == 3 else 0
-    _rows_of(k, "k", torch.bfloat16, (T, c.n_kv_heads))
-    _rows_of(v, "v", torch.bfloat16, (T, c.n_kv_heads))
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (n_seq + 1,))
-    _need(kv_start, "kv_start", torch.int32, (n_seq,))
-    if dev_status is not None:
-        _need(dev_status, "dev_status", torch.int32)
-    st = library().kda_kv_append(ctypes.byref(c), _ptr(k), _row_strides(k), _ptr(v), _row_strides(v),
-                                 _ptr(page_table), n_seq, max_pages, _ptr(cu_seqlens), _ptr(kv_start), T, HEAD_DIM,
-                                 _ptr(dev_status), _stream_handle(stream))
+    ks, vs = _rows_of(k, "k", (T, heads)), _rows_of(v, "v", (T, heads))
+    st = (_lib or library()).kda_kv_append(
+        c, k.data_ptr(), _pack2(*ks), v.data_ptr(), _pack2(*vs), page_table.data_ptr(), n_seq, max_pages,
+        _index(cu_seqlens, "cu_seqlens", (n_seq + 1,)), _index(kv_start, "kv_start", (n_seq,)), T, HEAD_DIM,
+        _status_ptr(dev_status), _stream_of(stream))
     if st != 0:
         raise KdaError(st, "kda_kv_append")
 
@@ -686,22 +749,16 @@ def kv_read(k_pool, v_pool, page_table, cu_seqlens, kv_start, total_tokens, k_sc
     ``total_tokens`` is ``cu[N]``.  The cache's arguments are those of :func:`kv_append`.
     Returns ``(k, v)``, each ``[total_tokens, Hkv, 128]`` bf16 (float8 values are exact in bf16).
     """
-    c = _kv_cache(k_pool, v_pool, k_scale, v_scale)
+    c, heads = _kv_cache(k_pool, v_pool, k_scale, v_scale)
     n_seq, max_pages = _page_table(page_table)
     T = int(total_tokens)
-    shape = (T, c.n_kv_heads, HEAD_DIM)
-    if k is None:
-        k = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device)
-    if v is None:
-        v = torch.empty(shape, dtype=torch.bfloat16, device=k_pool.device)
-    _need(k, "k", torch.bfloat16, shape)
-    _need(v, "v", torch.bfloat16, shape)
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (n_seq + 1,))
-    _need(kv_start, "kv_start", torch.int32, (n_seq,))
-    if dev_status is not None:
-        _need(dev_status, "dev_status", torch.int32)
-    st = library().kda_kv_read(ctypes.byref(c), _ptr(k), _ptr(v), _ptr(page_table), n_seq, max_pages, _ptr(cu_seqlens),
-                               _ptr(kv_start), T, HEAD_DIM, _ptr(dev_status), _stream_handle(stream))
+    shape = (T, heads, HEAD_DIM)
+    k = torch.empty(shape, dtype=_BF16, device=k_pool.device) if k is None else _need(k, "k", _BF16, shape)
+    v = torch.empty(shape, dtype=_BF16, device=k_pool.device) if v is None else _need(v, "v", _BF16, shape)
+    st = (_lib or library()).kda_kv_read(
+        c, k.data_ptr(), v.data_ptr(), page_table.data_ptr(), n_seq, max_pages,
+        _index(cu_seqlens, "cu_seqlens", (n_seq + 1,)), _index(kv_start, "kv_start", (n_seq,)), T, HEAD_DIM,
+        _status_ptr(dev_status), _stream_of(stream))
     if st != 0:
         raise KdaError(st, "kda_kv_read")
     return k, v
@@ -715,14 +772,12 @@ def attn_decode_workspace_size(B, n_tok, H, n_kv_heads, d=HEAD_DIM) -> int:
     return int(library().kda_attn_decode_workspace_size(int(B), int(n_tok), int(H), int(n_kv_heads), int(d)))
 
 
-def _attn_outputs(q, o, lse, return_lse):
-    if o is None:
-        o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
-    _need(o, "o", torch.bfloat16, q.shape)
-    if lse is None and return_lse:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+def _attn_outputs(q, shape, o, lse, return_lse):
+    o = torch.empty(shape, dtype=_BF16, device=q.device) if o is None else _need(o, "o", _BF16, shape)
     if lse is not None:
-        _need(lse, "lse", torch.float32, q.shape[:-1])
+        _need(lse, "lse", torch.float32, shape[:-1])
+    elif return_lse:
+        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
     return o, lse
 
 
@@ -738,26 +793,24 @@ def attn_prefill_paged(q, k_pool, v_pool, page_table, cu_seqlens, kv_len, k_scal
     ``window`` keys up to itself and the first ``n_sink`` of the sequence.  Returns o
     ``[T, H, 128]`` bf16, or ``(o, lse)`` with ``return_lse`` or ``lse`` given (``[T, H]`` fp32).
     """
-    c = _kv_cache(k_pool, v_pool, k_scale, v_scale)
+    c, heads = _kv_cache(k_pool, v_pool, k_scale, v_scale)
     n_seq, max_pages = _page_table(page_table)
     if not isinstance(q, torch.Tensor) or q.dim() != 3:
         raise ValueError("q must be a tensor [T, H, 128]")
-    T, H, _ = q.shape
-    _rows_of(q, "q", torch.bfloat16, (T, H))
-    _need(cu_seqlens, "cu_seqlens", torch.int32, (n_seq + 1,))
-    _need(kv_len, "kv_len", torch.int32, (n_seq,))
-    o, lse = _attn_outputs(q, o, lse, return_lse)
+    shape = q.shape
+    T, H, _ = shape
+    qs = _rows_of(q, "q", (T, H))
+    o, lse = _attn_outputs(q, shape, o, lse, return_lse)
+    lib = _lib or library()
     if workspace is None:
-        workspace = torch.empty(attn_prefill_workspace_size(n_seq, T, H, c.n_kv_heads), dtype=torch.uint8,
+        workspace = torch.empty(lib.kda_attn_prefill_workspace_size(n_seq, T, H, heads, HEAD_DIM), dtype=torch.uint8,
                                 device=q.device)
-    if dev_status is not None:
-        _need(dev_status, "dev_status", torch.int32)
-    st = library().kda_attn_prefill_paged(_ptr(q), _row_strides(q), ctypes.byref(c), _ptr(page_table), n_seq, max_pages,
-                                          _ptr(cu_seqlens), _ptr(kv_len), T, H, HEAD_DIM,
-                                          HEAD_DIM ** -0.5 if scale is None else float(scale), int(window), int(n_sink),
-                                          _ptr(o), _ptr(lse), _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _ptr(dev_status),
-                                          _stream_handle(stream))
+    st = lib.kda_attn_prefill_paged(
+        q.data_ptr(), _pack2(*qs), c, page_table.data_ptr(), n_seq, max_pages,
+        _index(cu_seqlens, "cu_seqlens", (n_seq + 1,)), _index(kv_len, "kv_len", (n_seq,)), T, H, HEAD_DIM,
+        HEAD_DIM ** -0.5 if scale is None else scale, window, n_sink, o.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _status_ptr(dev_status), _stream_of(stream))
     if st != 0:
         raise KdaError(st, "kda_attn_prefill_paged")
     return o if lse is None else (o, lse)
@@ -770,26 +823,25 @@ def attn_decode_paged(q, k_pool, v_pool, page_table, kv_len, k_scale=None, v_sca
     ``[B]`` int32 includes them (0: an idle slot, o = 0).  Returns o ``[B, n_tok, H, 128]``
     bf16, or ``(o, lse)`` with lse ``[B, n_tok, H]`` fp32.
     """
-    c = _kv_cache(k_pool, v_pool, k_scale, v_scale)
+    c, heads = _kv_cache(k_pool, v_pool, k_scale, v_scale)
     n_seq, max_pages = _page_table(page_table)
     if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be a tensor [B, n_tok, H, 128]")
-    B, n_tok, H, _ = q.shape
-    _rows_of(q, "q", torch.bfloat16, (B, n_tok, H))
+    shape = q.shape
+    B, n_tok, H, _ = shape
+    qs = _rows_of(q, "q", (B, n_tok, H))
     if B != n_seq:
         raise ValueError(f"page_table must have {B} rows, got {n_seq}")
-    _need(kv_len, "kv_len", torch.int32, (B,))
-    o, lse = _attn_outputs(q, o, lse, return_lse)
+    o, lse = _attn_outputs(q, shape, o, lse, return_lse)
+    lib = _lib or library()
     if workspace is None:
-        workspace = torch.empty(attn_decode_workspace_size(B, n_tok, H, c.n_kv_heads), dtype=torch.uint8,
+        workspace = torch.empty(lib.kda_attn_decode_workspace_size(B, n_tok, H, heads, HEAD_DIM), dtype=torch.uint8,
                                 device=q.device)
-    if dev_status is not None:
-        _need(dev_status, "dev_status", torch.int32)
-    st = library().kda_attn_decode_paged(_ptr(q), _row_strides(q), ctypes.byref(c), _ptr(page_table), B, n_tok, max_pages,
-                                         _ptr(kv_len), H, HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else float(scale),
-                                         int(window), int(n_sink), _ptr(o), _ptr(lse), _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(), _ptr(dev_status),
-                                         _stream_handle(stream))
+    st = lib.kda_attn_decode_paged(
+        q.data_ptr(), _pack3(*qs), c, page_table.data_ptr(), B, n_tok, max_pages, _index(kv_len, "kv_len", (B,)), H,
+        HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else scale, window, n_sink, o.data_ptr(),
+        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        _status_ptr(dev_status), _stream_of(stream))
     if st != 0:
         raise KdaError(st, "kda_attn_decode_paged")
     return o if lse is None else (o, lse)

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 
@@ -74,6 +75,21 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms);
 // Many rows a sequence: kda_attn_chunk.cu.
 size_t attn_chunk_workspace(int n_seq, int64_t tokens, int group, int num_sms);
 cudaError_t launch_attn_chunk(const AttnArgs& a, int num_sms);
+
+// A kernel's dynamic shared memory limit, raised once per device (the call costs a microsecond).
+struct SmemOptIn {
+  std::atomic<uint64_t> done{0};
+  cudaError_t operator()(const void* kernel, int bytes) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = dev < 64 ? uint64_t{1} << dev : 0;
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+  }
+};
 
 // The split of the work over blocks, and the workspace that joins it (kda_attn_common.cu).
 // The items -- (sequence, row tile) x kv head -- lie one after the other on a line of key

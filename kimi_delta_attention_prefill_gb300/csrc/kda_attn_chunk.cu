@@ -770,7 +770,8 @@ template <bool kE4m3>
 cudaError_t launch_chunk(const ChunkParams& p) {
   constexpr int bytes = Cfg<kE4m3>::kSmBytes;
   auto kern = attn_chunk_kernel<kE4m3>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(reinterpret_cast<const void*>(kern), bytes);
   if (e != cudaSuccess) return e;
   kern<<<p.s.grid, kThreads, bytes, p.a.stream>>>(p);
   return cudaGetLastError();

@@ -510,7 +510,8 @@ template <bool kE4m3, int kRG>
 cudaError_t launch_short(const ShortParams& p, int grid) {
   constexpr int bytes = smem_bytes<kE4m3>();
   auto kern = attn_short_kernel<kE4m3, kRG>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  static SmemOptIn opt_in;
+  const cudaError_t e = opt_in(reinterpret_cast<const void*>(kern), bytes);
   if (e != cudaSuccess) return e;
   kern<<<grid, kThreads, bytes, p.a.stream>>>(p);
   return cudaGetLastError();

@@ -13,6 +13,13 @@ HAS_GPU = torch.cuda.is_available()
 P = ctypes.c_void_p
 
 
+class KvCache(ctypes.Structure):  # kda_kv_cache
+    _fields_ = [("k", P), ("v", P), ("k_scale", P), ("v_scale", P), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("k_scale_stride", ctypes.c_int64 * 2),
+                ("v_scale_stride", ctypes.c_int64 * 2), ("n_pages", ctypes.c_int64), ("n_kv_heads", ctypes.c_int),
+                ("page_size", ctypes.c_int), ("dtype", ctypes.c_int)]
+
+
 @pytest.fixture(scope="module")
 def lib():
     build.build()
@@ -25,7 +32,7 @@ def strides(*s):
 
 def cache(e4m3=False, heads=2, page=16, n_pages=8, **kw):
     row = [heads * page * 128, page * 128, 128]
-    c = kda._KvCache(k=0x100000, v=0x200000, k_stride=strides(*row), v_stride=strides(*row), n_pages=n_pages,
+    c = KvCache(k=0x100000, v=0x200000, k_stride=strides(*row), v_stride=strides(*row), n_pages=n_pages,
                      n_kv_heads=heads, page_size=page, dtype=int(e4m3))
     if e4m3:
         c.k_scale, c.v_scale = 0x300000, 0x400000
