@@ -76,6 +76,23 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms);
 size_t attn_chunk_workspace(int n_seq, int64_t tokens, int group, int num_sms);
 cudaError_t launch_attn_chunk(const AttnArgs& a, int num_sms);
 
+// Launches a kernel that may begin before the one ahead of it in the stream has ended
+// (programmatic dependent launch); it waits for that one's writes itself.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // A kernel's dynamic shared memory limit, raised once per device (the call costs a microsecond).
 struct SmemOptIn {
   std::atomic<uint64_t> done{0};
@@ -96,9 +113,16 @@ struct SmemOptIn {
 // tiles; block c of the first C takes [c W / C, (c + 1) W / C) of its W tiles.  Parts of items
 // that two or more blocks share go to slots of the workspace: block c's first part, of an item
 // begun by an earlier block, to slot 2c, its last part, of an item that a later block goes on
-// with, to slot 2c + 1, and desc[c] = {sequence, head, first row, last block} names the latter.
+// with, to slot 2c + 1, and desc[c] says where the latter's rows belong.
+struct PartDesc {
+  int64_t base;  // packed row of the sequence's first token
+  int head;
+  int row0;      // the item's first row
+  int rows;      // the sequence's
+  int last;      // the block that has the item's last part; -1: there is no such part
+};
 struct AttnSplit {
-  int4* desc = nullptr;        // [grid], .w = -1: none
+  PartDesc* desc = nullptr;    // [grid]
   float2* part_ml = nullptr;   // [2 grid][part_rows] (maximum, sum)
   float* part_o = nullptr;     // [2 grid][part_rows][128] unnormalised
   int64_t* plan_total = nullptr;   // prefill: tiles of all items of one kv head

@@ -45,7 +45,7 @@ constexpr int kRows = 256;
 constexpr int kPanel = kTile * 128;     // 64 channels of 128 rows, 16-bit
 constexpr int kSlot = 2 * kPanel;       // one tile of K or V (or 128 rows of Q) as 16-bit values
 constexpr int kStage = kTile * 128 + 8 * 128;  // a tile of codes and a 128-byte slot of scale bytes per page
-constexpr int kMinTiles = 4, kItemCost = 3;
+constexpr int kMinTiles = 2, kItemCost = 3;
 
 template <bool kE4m3>
 struct Cfg {
@@ -106,8 +106,13 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
   constexpr int kRing = kE4m3 ? C::kStages : C::kSlots;
   uint64_t* full = kE4m3 ? b.st_full : b.full;
   uint64_t* empty = kE4m3 ? b.st_empty : b.empty;
+  if (lane == 0) {
+    tma_prefetch_desc(&p.tk);
+    tma_prefetch_desc(&p.tv);
+  }
   uint32_t n = 0, k = 0;
   Walk walk(p.a, p.s);
+  pdl_wait();  // for the plan; everything else was there before it began
   bool more = walk.start_plan();
   for (;; ++k) {
     if (!b.jobs.put(k, walk, more, lane)) break;
@@ -733,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     // a job is read by the two product warps, the query warps, the eight softmax warps and the converters
     b.jobs.init(10 + C::kQueryWarps + (kE4m3 ? 4 : 0));
     fence_mbar_init();
-    p.s.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
+    p.s.desc[blockIdx.x].last = -1;
   }
   pdl_launch_dependents();
   if (warp == 8) {
@@ -773,8 +778,7 @@ cudaError_t launch_chunk(const ChunkParams& p) {
   static SmemOptIn opt_in;
   const cudaError_t e = opt_in(reinterpret_cast<const void*>(kern), bytes);
   if (e != cudaSuccess) return e;
-  kern<<<p.s.grid, kThreads, bytes, p.a.stream>>>(p);
-  return cudaGetLastError();
+  return launch_after(kern, dim3(static_cast<unsigned>(p.s.grid)), dim3(kThreads), bytes, p.a.stream, p);
 }
 
 }  // namespace

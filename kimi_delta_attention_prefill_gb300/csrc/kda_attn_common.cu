@@ -65,29 +65,32 @@ bool scale_map(CUtensorMap* m, const void* base, const int64_t* stride, const Kv
 // at a time.  Offsets or lengths that cannot be are reported and leave their sequence out.
 constexpr int kPlanThreads = 1024;
 
-__device__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* total) {  // exclusive
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  int64_t incl = v;
+__device__ int64_t warp_scan(int64_t v, int lane) {  // inclusive
 #pragma unroll
   for (int off = 1; off < 32; off <<= 1) {
-    const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
-    if (lane >= off) incl += up;
+    const int64_t up = __shfl_up_sync(0xffffffffu, v, off);
+    if (lane >= off) v += up;
   }
+  return v;
+}
+__device__ int64_t block_scan(int64_t v, int64_t* sh, int64_t* total) {  // exclusive
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t incl = warp_scan(v, lane);
   __syncthreads();
   if (lane == 31) sh[warp] = incl;
   __syncthreads();
-  int64_t before = 0, all = 0;
-  for (int k = 0; k < kPlanThreads / 32; ++k) {
-    if (k < warp) before += sh[k];
-    all += sh[k];
-  }
-  *total = all;
-  return before + incl - v;
+  const int64_t upto = warp_scan(sh[lane], lane);  // every warp, of the 32 warps' sums
+  *total = __shfl_sync(0xffffffffu, upto, 31);
+  const int64_t before = __shfl_sync(0xffffffffu, upto, warp > 0 ? warp - 1 : 0);
+  return (warp > 0 ? before : 0) + incl - v;
 }
 
-__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs a, const AttnSplit s, int rows, int tile) {
+__global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_constant__ AttnArgs a,
+                                                                 const __grid_constant__ AttnSplit s, int rows, int tile) {
   __shared__ int64_t sh[kPlanThreads / 32];
   __shared__ int64_t first_item[kPlanThreads];
+  __shared__ int sh_len[kPlanThreads], sh_tok[kPlanThreads];
+  pdl_launch_dependents();
   const int tid = threadIdx.x;
   int64_t items = 0, line = 0;
   for (int b = 0; b < a.n_seq; b += kPlanThreads) {
@@ -99,6 +102,8 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
       else if (seq_bad(a, w.len, w.base, w.base + w.n_tok))
         report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
     }
+    sh_len[tid] = w.len;
+    sh_tok[tid] = w.n_tok;
     int64_t all;
     first_item[tid] = block_scan(n, sh, &all);
     __syncthreads();
@@ -117,8 +122,11 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
           const int mid = (lo + hi) >> 1;
           if (first_item[mid] <= k) lo = mid; else hi = mid;
         }
-        item_sequence(a, b + lo, &w);
         d = make_int2(b + lo, static_cast<int>(k - first_item[lo]) * rows);
+        w.len = sh_len[lo];
+        w.n_tok = sh_tok[lo];
+        w.G = a.H / a.cache.heads;
+        w.rows = w.n_tok * w.G;
         item_tiles(a, d.y, rows, tile, &w);
         count = w.tiles.count() + s.item_cost;
       }
@@ -140,37 +148,48 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const AttnArgs 
   }
 }
 
-// One block per (block of the attention kernel, row): the row's parts, weighted to a common
-// maximum, added in block order.
-__global__ void __launch_bounds__(128) attn_join_kernel(const __grid_constant__ AttnArgs a,
-                                                        const __grid_constant__ AttnSplit s) {
+// A warp a row, four channels a lane: the row's parts, weighted to a common maximum, added in
+// block order.  Blocks wait on the attention kernel from early on (programmatic launch), so what
+// counts is the chain of loads after its end: desc, the parts' (m, l) -- a part a lane --, the parts.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a,
+                                                                 const __grid_constant__ AttnSplit s) {
   pdl_wait();
-  const int c0 = blockIdx.x;
-  const int4 d = s.desc[c0];
-  if (d.w < 0) return;
-  Item w;
-  item_sequence(a, d.x, &w);
-  w.head = d.y;
-  const int lr = blockIdx.y, row = d.z + lr;
-  if (row >= w.rows) return;
-  const int t = threadIdx.x;
-  const int64_t R = s.part_rows;
-  float m = -INFINITY;
-  for (int c = c0; c <= d.w; ++c) m = fmaxf(m, s.part_ml[(2 * c + (c == c0)) * R + lr].x);
-  const float b = m == -INFINITY ? 0.f : m;
-  float l = 0.f, o = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= d.w; ++c) {
-    const int64_t i = (2 * c + (c == c0)) * R + lr;
-    const float2 ml = s.part_ml[i];
-    const float f = exp2_fast(ml.x - b);
-    l += ml.y * f;
-    o += s.part_o[i * 128 + t] * f;
+  const int c0 = blockIdx.x, lane = threadIdx.x & 31;
+  const PartDesc d = s.desc[c0];
+  if (d.last < 0) return;
+  const int G = a.H / a.cache.heads, R = s.part_rows, n = d.last - c0 + 1;
+  for (int lr = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5); lr < R; lr += gridDim.y * (kJoinThreads / 32)) {
+    const int row = d.row0 + lr;
+    if (row >= d.rows) return;
+    const int64_t at = (2 * static_cast<int64_t>(c0) + 1) * R + lr;  // part i > 0 lies at block c0 + i's first slot
+    auto slot = [&](int i) { return at + (i == 0 ? 0 : (2 * static_cast<int64_t>(i) - 1) * R); };
+    float m = -INFINITY;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, s.part_ml[slot(i)].x);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+    const float b = m == -INFINITY ? 0.f : m;
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+      const float2 ml = i0 + lane < n ? s.part_ml[slot(i0 + lane)] : make_float2(-INFINITY, 0.f);
+      const float f = exp2_fast(ml.x - b);
+      const int k = min(n - i0, 32);
+#pragma unroll 8
+      for (int i = 0; i < k; ++i) {
+        const float fi = __shfl_sync(0xffffffffu, f, i);
+        const float4 v = reinterpret_cast<const float4*>(s.part_o + slot(i0 + i) * 128)[lane];
+        l += __shfl_sync(0xffffffffu, ml.y, i) * fi;
+        o.x += v.x * fi; o.y += v.y * fi; o.z += v.z * fi; o.w += v.w * fi;
+      }
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const int t = row / G;
+    const int64_t orow = (d.base + t) * a.H + static_cast<int64_t>(d.head) * G + (row - t * G);
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + orow * 128)[lane] =
+        make_uint2(pack_bf162(o.x * inv, o.y * inv), pack_bf162(o.z * inv, o.w * inv));
+    if (a.lse && lane == 0) a.lse[orow] = lse_of(m, l);
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  const int64_t orow = w.o_row(a, row);
-  static_cast<__nv_bfloat16*>(a.o)[orow * 128 + t] = __float2bfloat16_rn(o * inv);
-  if (a.lse && t == 0) a.lse[orow] = lse_of(m, l);
 }
 
 size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
@@ -186,7 +205,7 @@ bool make_cache_maps(const KvCache& c, int tile, int panels, CUtensorMap* k, CUt
 
 size_t attn_split_bytes(int grid, int part_rows, int64_t max_items) {
   const size_t parts = 2 * static_cast<size_t>(grid) * part_rows;
-  return up256(16 * static_cast<size_t>(grid)) + up256(8 * parts) + up256(512 * parts) +
+  return up256(sizeof(PartDesc) * static_cast<size_t>(grid)) + up256(8 * parts) + up256(512 * parts) +
          (max_items > 0 ? 256 + up256(8 * static_cast<size_t>(max_items + 1)) + up256(8 * static_cast<size_t>(max_items)) : 0);
 }
 
@@ -194,7 +213,7 @@ void attn_split_layout(AttnSplit* s, void* workspace, int grid, int part_rows, i
   const size_t parts = 2 * static_cast<size_t>(grid) * part_rows;
   uint8_t* w = static_cast<uint8_t*>(workspace);
   s->grid = grid; s->part_rows = part_rows; s->max_items = max_items;
-  s->desc = reinterpret_cast<int4*>(w); w += up256(16 * static_cast<size_t>(grid));
+  s->desc = reinterpret_cast<PartDesc*>(w); w += up256(sizeof(PartDesc) * static_cast<size_t>(grid));
   s->part_ml = reinterpret_cast<float2*>(w); w += up256(8 * parts);
   s->part_o = reinterpret_cast<float*>(w); w += up256(512 * parts);
   if (max_items <= 0) return;
@@ -210,16 +229,10 @@ cudaError_t launch_attn_plan(const AttnArgs& a, const AttnSplit& s, int rows, in
 }
 
 cudaError_t launch_attn_join(const AttnArgs& a, const AttnSplit& s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(s.grid), static_cast<unsigned>(s.part_rows));
-  cfg.blockDim = dim3(128);
-  cfg.stream = a.stream;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attn_join_kernel, a, s);
+  const int per = kJoinThreads / 32, most = 8;  // blocks a part: enough to have every row at once up to 64 rows
+  const int y = (s.part_rows + per - 1) / per;
+  return launch_after(attn_join_kernel, dim3(static_cast<unsigned>(s.grid), static_cast<unsigned>(y < most ? y : most)),
+                      dim3(kJoinThreads), 0, a.stream, a, s);
 }
 
 }  // namespace kda

@@ -98,10 +98,6 @@ struct Item {
   __device__ int p_of_row(int row) const { return len - n_tok + row / G; }
   __device__ int p_first() const { return p_of_row(row0); }
   __device__ int p_last() const { return p_of_row(last_row); }
-  __device__ int64_t o_row(const AttnArgs& a, int row) const {
-    const int t = row / G, g = row - t * G;
-    return (base + t) * a.H + static_cast<int64_t>(head) * G + g;
-  }
 };
 
 // A kv_len that the table cannot hold, or offsets that run backwards.
@@ -142,7 +138,8 @@ struct ItemWalk {
   Item item;
   int begin = 0, end = 0;   // key tile visits of the item that are this block's
   int64_t pos = 0, stop = 0, at = 0;  // on the line: where we are, the share's end, where the item begins
-  int64_t blocks = 1, total = 0;
+  int blocks = 1;
+  int64_t total = 0;
   int idx = 0;      // prefill: the plan's item
   int unit = 0, n_units = 1;  // decode: head and row tile within the sequence
 
@@ -159,6 +156,10 @@ struct ItemWalk {
     return (n > 0 ? n : 1) + s.item_cost;
   }
 
+  // a / b of non-negative numbers, without the long division where 32 bits will do
+  __device__ static int64_t div(int64_t a, int64_t b) {
+    return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
+  }
   // Prefill, by any one thread or warp: the block's share from the plan.
   __device__ bool start_plan() {
     n_units = a.cache.heads;
@@ -166,15 +167,15 @@ struct ItemWalk {
     return total > 0 && take_share() && find_plan();
   }
   __device__ bool take_share() {
-    blocks = total / s.min_tiles;
-    blocks = blocks < 1 ? 1 : blocks > gridDim.x ? gridDim.x : blocks;
+    blocks = total < int64_t{s.min_tiles} * gridDim.x ? static_cast<int>(total) / s.min_tiles : gridDim.x;
+    if (blocks < 1) blocks = 1;
     if (blockIdx.x >= blocks) return false;
-    pos = blockIdx.x * total / blocks;
-    stop = (blockIdx.x + 1) * total / blocks;
+    pos = div(blockIdx.x * total, blocks);
+    stop = div((blockIdx.x + 1) * total, blocks);
     return true;
   }
   __device__ bool find_plan() {
-    const int64_t target = pos / n_units;
+    const int64_t target = div(pos, n_units);
     int lo = 0, hi = *s.plan_items;  // plan_start[lo] <= target < plan_start[hi]
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -194,9 +195,10 @@ struct ItemWalk {
     const int warp = tid >> 5, lane = tid & 31;
     const int rows = a.n_tok * (a.H / a.cache.heads);
     n_units = a.cu ? a.cache.heads : a.cache.heads * ((rows + kRows - 1) / kRows);
-    if (tid == 0) s.desc[blockIdx.x] = make_int4(0, 0, 0, -1);
+    if (tid == 0) s.desc[blockIdx.x].last = -1;
     int64_t sum = 0;
     if (a.cu) {
+      pdl_wait();  // for the plan
       sum = *s.plan_total;
       __syncthreads();
     } else {
@@ -212,7 +214,7 @@ struct ItemWalk {
     }
     total = sum * n_units;
     if (total == 0 || !take_share()) return false;
-    const int64_t target = pos / n_units;
+    const int64_t target = div(pos, n_units);
     if (a.cu) {
       return find_plan();
     } else {
@@ -243,7 +245,7 @@ struct ItemWalk {
       item_sequence(a, sh_seq, &item);
       item_tiles(a, 0, rows, kTileKeys, &item);
       at = sh_at * n_units;
-      unit = static_cast<int>((pos - at) / length());
+      unit = static_cast<int>(div(pos - at, length()));
       at += static_cast<int64_t>(unit) * length();
       set_unit();
     }
@@ -261,7 +263,7 @@ struct ItemWalk {
     item_sequence(a, d.x, &item);
     item_tiles(a, d.y, kRows, kTileKeys, &item);
     at = s.plan_start[idx] * n_units;
-    item.head = pos > at ? static_cast<int>((pos - at) / length()) : 0;
+    item.head = pos > at ? static_cast<int>(div(pos - at, length())) : 0;
     at += static_cast<int64_t>(item.head) * length();
   }
   __device__ bool clip() {  // false: nothing of the item's tiles is in the share
@@ -301,7 +303,7 @@ struct ItemWalk {
     if (names) {
       // the block that has the item's last tile: c1 = ceil(E C / W) - 1
       const int64_t e = at + length();
-      s.desc[blockIdx.x] = make_int4(item.seq, item.head, item.row0, static_cast<int>((e * blocks + total - 1) / total - 1));
+      s.desc[blockIdx.x] = PartDesc{item.base, item.head, item.row0, item.rows, static_cast<int>(div(e * blocks + total - 1, total) - 1)};
     }
     return 2 * blockIdx.x + 1;
   }

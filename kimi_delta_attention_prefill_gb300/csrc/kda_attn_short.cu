@@ -123,6 +123,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
     fence_mbar_init();
   }
   pdl_launch_dependents();
+  if (tid == kWarps * 32) {
+    tma_prefetch_desc(&p.tk);
+    tma_prefetch_desc(&p.tv);
+  }
   const int P = min(a.cache.page_size, kTile), n_blk = kTile / P;
   ItemWalk<kRT, kTile> walk(p.a, p.s);
   const bool any = walk.template start<kThreads>(tid);  // has the barriers that publish the mbarriers
@@ -513,6 +517,7 @@ cudaError_t launch_short(const ShortParams& p, int grid) {
   static SmemOptIn opt_in;
   const cudaError_t e = opt_in(reinterpret_cast<const void*>(kern), bytes);
   if (e != cudaSuccess) return e;
+  if (p.a.cu) return launch_after(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), bytes, p.a.stream, p);
   kern<<<grid, kThreads, bytes, p.a.stream>>>(p);
   return cudaGetLastError();
 }
