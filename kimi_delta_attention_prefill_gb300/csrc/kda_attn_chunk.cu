@@ -112,8 +112,7 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
   }
   uint32_t n = 0, k = 0;
   Walk walk(p.a, p.s);
-  pdl_wait();  // for the plan; everything else was there before it began
-  bool more = walk.start_plan();
+  bool more = walk.start(lane);
   for (;; ++k) {
     if (!b.jobs.put(k, walk, more, lane)) break;
     const Item& w = walk.item;

@@ -149,9 +149,10 @@ __global__ void __launch_bounds__(kPlanThreads) attn_plan_kernel(const __grid_co
 }
 
 // A warp a row, four channels a lane: the row's parts, weighted to a common maximum, added in
-// block order.  Blocks wait on the attention kernel from early on (programmatic launch), so what
-// counts is the chain of loads after its end: desc, the parts' (m, l) -- a part a lane --, the parts.
-constexpr int kJoinThreads = 256;
+// block order.  The parts were written by other SMs and a dependent load of them costs most of a
+// microsecond, so a row is one chain of three -- desc, all of (up to eight) parts with their
+// (m, l) at once, the output -- and rows are spread over as many warps as there are.
+constexpr int kJoinThreads = 128, kJoinParts = 8;
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ AttnArgs a,
                                                                  const __grid_constant__ AttnSplit s) {
   pdl_wait();
@@ -163,24 +164,30 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_co
     const int row = d.row0 + lr;
     if (row >= d.rows) return;
     const int64_t at = (2 * static_cast<int64_t>(c0) + 1) * R + lr;  // part i > 0 lies at block c0 + i's first slot
-    auto slot = [&](int i) { return at + (i == 0 ? 0 : (2 * static_cast<int64_t>(i) - 1) * R); };
-    float m = -INFINITY;
-    for (int i = lane; i < n; i += 32) m = fmaxf(m, s.part_ml[slot(i)].x);
-#pragma unroll
-    for (int off = 16; off; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-    const float b = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
+    float m = -INFINITY, l = 0.f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int i0 = 0; i0 < n; i0 += 32) {
-      const float2 ml = i0 + lane < n ? s.part_ml[slot(i0 + lane)] : make_float2(-INFINITY, 0.f);
-      const float f = exp2_fast(ml.x - b);
-      const int k = min(n - i0, 32);
-#pragma unroll 8
-      for (int i = 0; i < k; ++i) {
-        const float fi = __shfl_sync(0xffffffffu, f, i);
-        const float4 v = reinterpret_cast<const float4*>(s.part_o + slot(i0 + i) * 128)[lane];
-        l += __shfl_sync(0xffffffffu, ml.y, i) * fi;
-        o.x += v.x * fi; o.y += v.y * fi; o.z += v.z * fi; o.w += v.w * fi;
+    for (int i0 = 0; i0 < n; i0 += kJoinParts) {
+      float2 ml[kJoinParts];
+      float4 v[kJoinParts];
+#pragma unroll
+      for (int i = 0; i < kJoinParts; ++i) {
+        const int k = i0 + i;
+        const int64_t slot = at + (k == 0 ? 0 : (2 * static_cast<int64_t>(k) - 1) * R);
+        ml[i] = k < n ? s.part_ml[slot] : make_float2(-INFINITY, 0.f);
+        v[i] = k < n ? reinterpret_cast<const float4*>(s.part_o + slot * 128)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      float top = m;
+#pragma unroll
+      for (int i = 0; i < kJoinParts; ++i) top = fmaxf(top, ml[i].x);
+      const float b = top == -INFINITY ? 0.f : top, f0 = exp2_fast(m - b);
+      m = top;
+      l *= f0;
+      o.x *= f0; o.y *= f0; o.z *= f0; o.w *= f0;
+#pragma unroll
+      for (int i = 0; i < kJoinParts; ++i) {
+        const float f = exp2_fast(ml[i].x - b);
+        l += ml[i].y * f;
+        o.x += v[i].x * f; o.y += v[i].y * f; o.z += v[i].z * f; o.w += v[i].w * f;
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -229,9 +236,8 @@ cudaError_t launch_attn_plan(const AttnArgs& a, const AttnSplit& s, int rows, in
 }
 
 cudaError_t launch_attn_join(const AttnArgs& a, const AttnSplit& s) {
-  const int per = kJoinThreads / 32, most = 8;  // blocks a part: enough to have every row at once up to 64 rows
-  const int y = (s.part_rows + per - 1) / per;
-  return launch_after(attn_join_kernel, dim3(static_cast<unsigned>(s.grid), static_cast<unsigned>(y < most ? y : most)),
+  const int y = s.part_rows <= 64 ? s.part_rows / (kJoinThreads / 32) : 32;  // a row a warp; of 256 rows two
+  return launch_after(attn_join_kernel, dim3(static_cast<unsigned>(s.grid), static_cast<unsigned>(y)),
                       dim3(kJoinThreads), 0, a.stream, a, s);
 }
 

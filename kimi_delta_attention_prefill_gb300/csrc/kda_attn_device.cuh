@@ -160,7 +160,7 @@ struct ItemWalk {
   __device__ static int64_t div(int64_t a, int64_t b) {
     return (a | b) >> 32 ? a / b : static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b));
   }
-  // Prefill, by any one thread or warp: the block's share from the plan.
+  // Prefill: from the plan.
   __device__ bool start_plan() {
     n_units = a.cache.heads;
     total = *s.plan_total * n_units;
@@ -186,69 +186,46 @@ struct ItemWalk {
     return clip();
   }
 
-  // Takes this block's share; false: there is none.  Called by all kThreads threads.
-  template <int kThreads>
-  __device__ bool start(int tid) {
-    __shared__ int64_t sh_sum[kThreads / 32 + 1];
-    __shared__ int64_t sh_at;
-    __shared__ int sh_seq;
-    const int warp = tid >> 5, lane = tid & 31;
-    const int rows = a.n_tok * (a.H / a.cache.heads);
-    n_units = a.cu ? a.cache.heads : a.cache.heads * ((rows + kRows - 1) / kRows);
-    if (tid == 0) s.desc[blockIdx.x].last = -1;
-    int64_t sum = 0;
+  // Takes this block's share; false: there is none.  By a whole warp.
+  __device__ bool start(int lane) {
     if (a.cu) {
-      pdl_wait();  // for the plan
-      sum = *s.plan_total;
-      __syncthreads();
-    } else {
-      for (int i = tid; i < a.n_seq; i += kThreads) sum += decode_length(i);
-#pragma unroll
-      for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-      if (lane == 0) sh_sum[warp] = sum;
-      __syncthreads();
-      sum = 0;
-#pragma unroll
-      for (int i = 0; i < kThreads / 32; ++i) sum += sh_sum[i];
-      __syncthreads();
+      pdl_wait();  // for the plan; everything else was there before it began
+      return start_plan();
     }
+    const int rows = a.n_tok * (a.H / a.cache.heads);
+    n_units = a.cache.heads * ((rows + kRows - 1) / kRows);
+    int64_t sum = 0;
+    for (int i = lane; i < a.n_seq; i += 32) sum += decode_length(i);
+#pragma unroll
+    for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     total = sum * n_units;
     if (total == 0 || !take_share()) return false;
     const int64_t target = div(pos, n_units);
-    if (a.cu) {
-      return find_plan();
-    } else {
-      int64_t run = 0;
-      for (int b = 0; b < a.n_seq; b += kThreads) {
-        const int i = b + tid;
-        const int64_t c = i < a.n_seq ? decode_length(i) : 0;
-        int64_t incl = c;
+    int64_t run = 0;  // 32 sequences at a time up to the one that holds the share's begin
+    int seq = 0;
+    for (int b = 0;; b += 32) {
+      const int i = b + lane;
+      const int64_t c = i < a.n_seq ? decode_length(i) : 0;
+      int64_t incl = c;
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-          const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
-          if (lane >= off) incl += up;
-        }
-        if (lane == 31) sh_sum[warp] = incl;
-        __syncthreads();
-        int64_t before = run, all = run;
-#pragma unroll
-        for (int k = 0; k < kThreads / 32; ++k) {
-          if (k < warp) before += sh_sum[k];
-          all += sh_sum[k];
-        }
-        incl += before;
-        if (incl - c <= target && target < incl) { sh_seq = i; sh_at = incl - c; }
-        __syncthreads();
-        run = all;
-        if (run > target) break;
+      for (int off = 1; off < 32; off <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += up;
       }
-      item_sequence(a, sh_seq, &item);
-      item_tiles(a, 0, rows, kTileKeys, &item);
-      at = sh_at * n_units;
-      unit = static_cast<int>(div(pos - at, length()));
-      at += static_cast<int64_t>(unit) * length();
-      set_unit();
+      const uint32_t past = __ballot_sync(0xffffffffu, run + incl > target);
+      if (past) {
+        const int k = __ffs(past) - 1;
+        seq = b + k;
+        at = (run + __shfl_sync(0xffffffffu, incl - c, k)) * n_units;
+        break;
+      }
+      run += __shfl_sync(0xffffffffu, incl, 31);
     }
+    item_sequence(a, seq, &item);
+    item_tiles(a, 0, rows, kTileKeys, &item);
+    unit = static_cast<int>(div(pos - at, length()));
+    at += static_cast<int64_t>(unit) * length();
+    set_unit();
     return clip();
   }
 

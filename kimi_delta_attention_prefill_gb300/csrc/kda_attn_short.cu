@@ -121,6 +121,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
     for (int i = 0; i < St::kCount; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], kWarps); }
     jobs.init(kWarps);
     fence_mbar_init();
+    p.s.desc[blockIdx.x].last = -1;
   }
   pdl_launch_dependents();
   if (tid == kWarps * 32) {
@@ -128,14 +129,13 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
     tma_prefetch_desc(&p.tv);
   }
   const int P = min(a.cache.page_size, kTile), n_blk = kTile / P;
-  ItemWalk<kRT, kTile> walk(p.a, p.s);
-  const bool any = walk.template start<kThreads>(tid);  // has the barriers that publish the mbarriers
-  if (!any) return;
+  __syncthreads();
 
   if (warp == kWarps) {  // ------------------------------------------------------ copies
+    ItemWalk<kRT, kTile> walk(p.a, p.s);
+    bool more = walk.start(lane);
     uint32_t it = 0;
     const int blk = lane;
-    bool more = true;
     for (uint32_t k = 0;; ++k) {
       if (!jobs.put(k, walk, more, lane)) break;
       if (!more) return;
@@ -550,19 +550,28 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms) {
   return launch_attn_join(p.a, p.s);
 }
 
+// Which kernel takes a chunk.  This one for up to 64 rows (tokens x shared heads) a sequence on
+// average, where it reads the keys once, and for little work altogether, where the other's longer
+// way to its first product counts: 77 tokens of 3 sequences over 1500 keys, 16 heads on 2: 25 us
+// here, 37 us there; but 128 tokens of 8 sequences over 8000 keys, 96 heads on 8: 96 us here,
+// 63 us there.  The work is bounded by the page table's width, the lengths being on the device.
 namespace {
-// Chunks of up to 64 rows (tokens x shared heads) a sequence on average stay with this kernel.
-bool short_chunks(int n_seq, int64_t tokens, int group) { return tokens * group <= static_cast<int64_t>(kMaxRows) * n_seq; }
+bool short_chunks(const AttnArgs& a) {
+  const int group = a.H / a.cache.heads;
+  if (a.tokens * group <= static_cast<int64_t>(kMaxRows) * a.n_seq) return true;
+  return 512.0 * a.tokens * a.H * (static_cast<double>(a.max_pages) * a.cache.page_size) <= 2.5e9;
+}
 }  // namespace
 
 size_t attn_prefill_workspace(int n_seq, int64_t tokens, int H, int kv_heads, int num_sms) {
-  if (!short_chunks(n_seq, tokens, H / kv_heads)) return attn_chunk_workspace(n_seq, tokens, H / kv_heads, num_sms);
-  return attn_split_bytes(2 * num_sms, kMaxRows, attn_max_items(n_seq, tokens, H / kv_heads, kMaxRows));
+  const size_t here = attn_split_bytes(2 * num_sms, kMaxRows, attn_max_items(n_seq, tokens, H / kv_heads, kMaxRows));
+  const size_t there = attn_chunk_workspace(n_seq, tokens, H / kv_heads, num_sms);
+  return here > there ? here : there;
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, int num_sms) {
+  if (!short_chunks(a)) return launch_attn_chunk(a, num_sms);
   const int G = a.H / a.cache.heads;
-  if (!short_chunks(a.n_seq, a.tokens, G)) return launch_attn_chunk(a, num_sms);
   ShortParams p;
   memset(&p, 0, sizeof(p));
   p.a = a;
