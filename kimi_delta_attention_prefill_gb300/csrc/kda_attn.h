@@ -58,6 +58,8 @@ struct AttnArgs {
   int max_pages = 0;
   int64_t tokens = 0;
   int H = 0;
+  uint64_t g_magic = 0;    // row / (H / kv heads) = row * g_magic >> g_shift (rows below 2^31)
+  int g_shift = 0;
   float scale_log2 = 0.f;  // softmax scale in log2 units
   int window = 0;
   int n_sink = 0;

@@ -78,7 +78,14 @@ kda_status check_attn(const void* q, const int64_t* qs, int n_strides, const kda
       !aligned(kv_len, 4) || !aligned(lse, 4) || !aligned(status, 4) || !aligned(workspace, 256))
     return KDA_ERR_ALIGNMENT;
   a->q = q; a->page_table = page_table; a->kv_len = kv_len; a->n_seq = n_seq; a->max_pages = max_pages;
-  a->tokens = tokens; a->H = H; a->scale_log2 = scale * 1.4426950408889634f;
+  a->tokens = tokens; a->H = H;
+  // ceil(2^(31 + b) / G) with 2^b >= G: exact for 31-bit rows, and the product fits 64 bits
+  const uint64_t G = static_cast<uint64_t>(H / cache->n_kv_heads);
+  int bits = 0;
+  while ((uint64_t{1} << bits) < G) ++bits;
+  a->g_shift = 31 + bits;
+  a->g_magic = ((uint64_t{1} << a->g_shift) + G - 1) / G;
+  a->scale_log2 = scale * 1.4426950408889634f;
   // a window no sequence can outgrow is none, and the kernels' 32-bit positions need no more first tokens than fit
   const int64_t most = static_cast<int64_t>(max_pages) * cache->page_size;
   a->window = window >= most ? 0 : window;

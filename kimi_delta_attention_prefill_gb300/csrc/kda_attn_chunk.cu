@@ -211,61 +211,57 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
       }
       continue;
     }
-    auto qk = [&](uint32_t slot, bool last) {
-      __syncwarp();
-      tc_fence_after();
-      const uint64_t db = dk + slot * (kSlot >> 4);
-#pragma unroll
-      for (int kk = 0; kk < 8; ++kk) {
-        const uint32_t off = ((kk >> 2) * kPanel + 32 * (kk & 3)) >> 4;
-        mma_f16_if(leader, 128 * t, dq + off, db + off, id_qk, kk > 0);
-      }
-      mma_commit_if(leader, &b.s_full[t]);
-      mma_commit_if(leader, &b.empty[slot]);
-      if (last) mma_commit_if(leader, &b.q_empty);
-    };
-    wait(&b.full[sk], pk);
-    qk(sk, end - begin == 1);  // S is free: the last P V over it is done (below)
-    step();
-    values(begin, sk, pk);
     // The tensor core has products queued while this warp waits: what can be waited for early is
-    // waited for behind a product, so that nothing but the softmax comes before P V.
-    for (int i = begin; i < end; ++i) {
-      const uint32_t sv = sk;
-      step();
-      const bool more = i + 1 < end;
-      // A and B take turns of one P V and the next Q K^T each.  Left alone their products mix and
-      // end together, and then both tiles are in their softmax while the tensor core has nothing.
-      if (both && (t == 1 || turns > 0)) wait(&b.turn[t], t == 1 ? turns : turns - 1);
+    // waited for behind a product, so that nothing but the softmax comes before P V.  (One loop
+    // with one place for each product: this warp's code is fetched anew every time round.)
+    uint32_t sv = 0;
+#pragma unroll 1
+    for (int i = begin - 1; i < end; ++i) {
+      const bool pv = i >= begin, more = i + 1 < end;
+      if (pv) {
+        // A and B take turns of one P V and the next Q K^T each.  Left alone their products mix and
+        // end together, and then both tiles are in their softmax while the tensor core has nothing.
+        if (both && (t == 1 || turns > 0)) wait(&b.turn[t], t == 1 ? turns : turns - 1);
+        turns += both;
 #pragma unroll
-      for (int h = 1; h >= 0; --h) {  // the weights come in two halves of 64 keys, the later keys first
-        wait(&b.p_full[t][h], tiles);
-        if (h == 1 && edge) wait(&b.v_ok, edges++);
+        for (int h = 1; h >= 0; --h) {  // the weights come in two halves of 64 keys, the later keys first
+          wait(&b.p_full[t][h], tiles);
+          if (h == 1 && edge) wait(&b.v_ok, edges++);
+          __syncwarp();
+          tc_fence_after();
+          const uint64_t db = dv + sv * (kSlot >> 4) + h * (4 * 2048 >> 4);
+#pragma unroll
+          for (int kk = 0; kk < 4; ++kk)
+            mma_f16_ta_if(leader, 256 + 128 * t, 128 * t + 64 * h + 8 * kk, db + kk * (2048 >> 4), id_pv,
+                          kk > 0 || h == 0 || i > begin);
+        }
+        mma_commit_if(leader, &b.pv_done[t]);
+        mma_commit_if(leader, &b.empty[sv]);
+        if (!more) {
+          mma_commit_if(leader, &b.o_full[t]);
+          if (both && leader) mbar_arrive(&b.turn[t ^ 1]);
+        }
+      }
+      if (more) wait(&b.full[sk], pk);
+      if (pv) wait(&b.pv_done[t], tiles++);  // P lies over S: the next scores may be written once it has been read
+      if (more) {
         __syncwarp();
         tc_fence_after();
-        const uint64_t db = dv + sv * (kSlot >> 4) + h * (4 * 2048 >> 4);
+        const uint64_t db = dk + sk * (kSlot >> 4);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          mma_f16_ta_if(leader, 256 + 128 * t, 128 * t + 64 * h + 8 * kk, db + kk * (2048 >> 4), id_pv,
-                        kk > 0 || h == 0 || i > begin);
-      }
-      mma_commit_if(leader, &b.pv_done[t]);
-      mma_commit_if(leader, &b.empty[sv]);
-      if (more) {
-        wait(&b.full[sk], pk);
-        // P lies over S: the next scores may be written once this product has read it
-        wait(&b.pv_done[t], tiles);
-        qk(sk, i + 2 == end);
-        if (both && leader) mbar_arrive(&b.turn[t ^ 1]);
+        for (int kk = 0; kk < 8; ++kk) {
+          const uint32_t off = ((kk >> 2) * kPanel + 32 * (kk & 3)) >> 4;
+          mma_f16_if(leader, 128 * t, dq + off, db + off, id_qk, kk > 0);
+        }
+        mma_commit_if(leader, &b.s_full[t]);
+        mma_commit_if(leader, &b.empty[sk]);
+        if (i + 2 == end) mma_commit_if(leader, &b.q_empty);
+        if (pv && both && leader) mbar_arrive(&b.turn[t ^ 1]);
         step();
+        sv = sk;
         values(i + 1, sk, pk);
-      } else {
-        mma_commit_if(leader, &b.o_full[t]);
-        if (both && leader) mbar_arrive(&b.turn[t ^ 1]);
-        wait(&b.pv_done[t], tiles);
+        step();
       }
-      ++tiles;
-      turns += both;
     }
   }
   // nothing of this block's may be in flight when it ends
@@ -284,7 +280,7 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
   const int lane = tid & 31, sub = tid & 15, grp = tid >> 4;
-  constexpr int kGroups = 2 * C::kQueryWarps;  // of 16 lanes
+  constexpr int kGroups = 2 * C::kQueryWarps, kGroupRows = kRows / kGroups;  // of 16 lanes
   const int G = a.H / a.cache.heads;
   const uint32_t q_at = smem_u32(sm + C::kSmQ) + (sub >> 3) * kPanel;
   auto q_piece = [&](int r) { return q_at + (r >> 7) * kSlot + sw128(r & 127, 16 * (sub & 7)); };  // this lane's 8 channels
@@ -294,25 +290,34 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
   JobFeed feed{b.jobs, dead};
   while (const Job* jp = feed.next()) {
     const Job& w = *jp;
+    const int n_rows = w.rows - w.row0;
+    const uint16_t* q0 = static_cast<const uint16_t*>(a.q) + w.q_base + static_cast<int64_t>(w.head) * G * a.q_stride[2];
+    // while the last item still uses the tiles, the rows' lines into L2: a few rows a lane
+    for (int r = tid; r < min(kRows, n_rows); r += 16 * kGroups) {
+      const int tok = row_token(a, w.row0 + r), g = w.row0 + r - tok * G;
+      const uint16_t* src = q0 + tok * a.q_stride[1] + g * a.q_stride[2];
+      prefetch_l2(src);
+      prefetch_l2(src + 64);
+    }
     if (items > 0 && !dead && !bar_wait(&b.q_empty, (items - 1) & 1)) dead = true;
     // every piece is on its way before any is waited for; zeros past the last row
     {
-      const int first = w.row0 + grp;
-      int tok = first / G, g = first - tok * G;
-      const uint16_t* src = static_cast<const uint16_t*>(a.q) + w.q_base + tok * a.q_stride[1] +
-                            (static_cast<int64_t>(w.head) * G + g) * a.q_stride[2] + 8 * sub;
-      const int n_rows = w.rows - w.row0;
+      const int first = grp * kGroupRows, tok = row_token(a, w.row0 + first);
+      int g = w.row0 + first - tok * G;
+      const uint16_t* src = q0 + tok * a.q_stride[1] + g * a.q_stride[2] + 8 * sub;
+      const int64_t wrap = a.q_stride[1] - (G - 1) * a.q_stride[2];
 #pragma unroll 4
-      for (int r = grp; r < kRows; r += kGroups) {
+      for (int r = first; r < first + kGroupRows; ++r) {
         cp_async16(q_piece(r), src, r < n_rows);
-        src += kGroups * a.q_stride[2];
-        for (g += kGroups; g >= G; g -= G) src += a.q_stride[1] - G * a.q_stride[2];
+        const bool end = ++g == G;
+        src += end ? wrap : a.q_stride[2];
+        g = end ? 0 : g;
       }
     }
     cp_async_wait_all();
     if (kE4m3 || a.scale_log2 <= 0.f) {  // in place: each thread its own pieces
 #pragma unroll 4
-      for (int r = grp; r < kRows; r += kGroups) {
+      for (int r = grp * kGroupRows; r < (grp + 1) * kGroupRows; ++r) {
         uint4 x = lds128(q_piece(r));
         if (a.scale_log2 == 0.f) x = make_uint4(0, 0, 0, 0);
         if constexpr (kE4m3) {
@@ -345,14 +350,14 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
         // thread = key: a row of 128 values with a NaN or an infinity is cleared and noted
         uint8_t* v = sm + C::kSmKV + s * kSlot;
         bool bad = false;
-#pragma unroll
+#pragma unroll 8
         for (int c = 0; c < 16; ++c) {
           const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * kPanel + sw128(tid, 16 * (c & 7)));
           auto has = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
           bad |= has(x.x) | has(x.y) | has(x.z) | has(x.w);
         }
         if (bad) {
-#pragma unroll 4
+#pragma unroll 1
           for (int c = 0; c < 16; ++c)
             *reinterpret_cast<uint4*>(v + (c >> 3) * kPanel + sw128(tid, 16 * (c & 7))) = make_uint4(0, 0, 0, 0);
         }
@@ -529,7 +534,8 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
     }
     const bool live = row < w.rows;
     const int G = a.H / a.cache.heads;
-    const int pos = live ? w.len - w.n_tok + row / G : -1;
+    const int tok = row_token(a, row);
+    const int pos = live ? w.len - w.n_tok + tok : -1;
     float crow = scale;
     float m = -INFINITY, l = 0.f;
     for (int i = begin; i < end; ++i, n += 2) {
@@ -564,24 +570,35 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
             if (((keys >> e) & 1) && sees(pos, kt * kTile + 32 * g + e, a.window, a.n_sink)) l = __uint_as_float(0x7fffffffu);
         }
       }
-      // 32 scores from column c on; wide tiles: y of the codes, key by key, then u = 1 and off = 0; hidden ones -inf
+      // ---- in edge and wide tiles, the scores in place first: y of the codes, key by key, after which
+      // u = 1 and off = 0; hidden ones -inf.  Rolled: the code is cold whenever it runs.
       const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
-      auto fix = [&](float (&x)[32], int c) {
-        if (kE4m3 && wide) {
+      const float v_off = off;
+      if (edge || (kE4m3 && wide)) {
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 16) {
+          float x[16];
+          tmem_ld16(ts + c, x);
+          if (kE4m3 && wide) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) x[e] = fmaf(x[e] * vec[c + e], u, vec[128 + c + e] + off);
-        }
-        if (edge) {
-          const int first = kt * kTile + c;
-          const int hi = pos - first;                                                                  // columns past it are hidden
-          const int lo = a.window > 0 && pos >= a.window ? max(pos - a.window + 1 - first, 0) : 0;  // those before it too, but for
-          const int sink = a.n_sink - first;                                                           // the first tokens
+            for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e] * vec[c + e], u, vec[128 + c + e] + off);
+          }
+          if (edge) {
+            const int first = kt * kTile + c;
+            // columns before `end`, from `from` on or before `sink`
+            auto below = [](int k) { return k <= 0 ? 0u : k >= 32 ? ~0u : (1u << k) - 1; };
+            const uint32_t end = below(pos + 1 - first), sink = below(a.n_sink - first);
+            const uint32_t from = a.window > 0 && pos >= a.window ? ~below(pos - a.window + 1 - first) : ~0u;
+            const uint32_t see = end & (from | sink);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e > hi || (e < lo && e >= sink)) x[e] = -INFINITY;
+            for (int e = 0; e < 16; ++e)
+              if (!((see >> e) & 1)) x[e] = -INFINITY;
+          }
+          tmem_st16(ts + c, x);
         }
-      };
-      const bool special = edge || (kE4m3 && wide);
+        tmem_wait_st();
+        if (kE4m3 && wide) { u = 1.f; off = 0.f; }
+      }
       // ---- the row's maximum, 64 columns at a time; the last 64 stay in registers
       float x[2][32];
       auto load = [&](int c) {
@@ -589,10 +606,6 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
         tmem_ld32_async(ts + c + 32, x[1]);
         tmem_wait_ld32(x[0]);
         tmem_wait_ld32(x[1]);
-        if (special) {
-          fix(x[0], c);
-          fix(x[1], c + 32);
-        }
       };
       float mx = -INFINITY;
 #pragma unroll 1
@@ -609,7 +622,6 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
         }
         mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
       }
-      if (kE4m3 && wide) { u = 1.f; off = 0.f; }
       const float top = fmaf(mx, u, off);
       const bool grow = top - m > kLazy;  // also from -inf to anything; never for nothing visible
       if (__any_sync(0xffffffffu, grow)) {
@@ -631,21 +643,20 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       // ---- weights and their sum: keys 64 .. 127 from the registers, over their own scores' first
       // 32 columns, then keys 0 .. 63
       const float ref = m == -INFINITY ? 0.f : m;
+      if (kE4m3 && wide) {  // the sum of 2^(y - ev - m), key by key
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 16) {
+          float y[16];
+          tmem_ld16(ts + c, y);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) l += exp2_fast(y[e] - vec[128 + c + e] - v_off - ref);
+        }
+      }
       const uint64_t u2 = f32x2(u, u), nb2 = f32x2(off - ref, off - ref);
       uint64_t sum = f32x2(0.f, 0.f), sum1 = sum;
 #pragma unroll 1
       for (int h = 1; h >= 0; --h) {
-        if (h == 0) {
-          if (kE4m3 && wide) { u = crow * b.tile[(n >> 1) & 1].k; off = b.tile[(n >> 1) & 1].v; }
-          load(0);
-        }
-        if (kE4m3 && wide) {  // the sum of 2^(y - ev - m), key by key
-          const float v = b.tile[(n >> 1) & 1].v;
-          float w0 = 0.f;
-#pragma unroll
-          for (int e = 0; e < 64; ++e) w0 += exp2_fast(x[e >> 5][e & 31] - vec[128 + 64 * h + e] - v - ref);
-          l += w0;
-        }
+        if (h == 0) load(0);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
           float pk[16];
@@ -673,35 +684,30 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
     ++items;
     ++seen;
     tc_fence_after();
-    const int slot = w.slot;
-    if (slot >= 0) {
-      const int64_t at = static_cast<int64_t>(slot) * p.s.part_rows + 128 * t + tid;
+    const bool part = w.slot >= 0;
+    const int64_t at = static_cast<int64_t>(w.slot) * p.s.part_rows + 128 * t + tid;
+    const int64_t orow = (w.base + tok) * a.H + static_cast<int64_t>(w.head) * G + (row - tok * G);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint8_t* dst = part ? reinterpret_cast<uint8_t*>(p.s.part_o + at * 128) : static_cast<uint8_t*>(a.o) + orow * 256;
 #pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
-        float o[32];
-        tmem_ld32(to + 32 * g, o);
-        float4* dst = reinterpret_cast<float4*>(p.s.part_o + at * 128 + 32 * g);
-        if (live)
+    for (int g = 0; g < 8; ++g) {
+      float o[16];
+      tmem_ld16(to + 16 * g, o);
+      if (!live) continue;
+      if (part) {
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) dst[e >> 2] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-      }
-      if (live) p.s.part_ml[at] = make_float2(m, l);
-    } else {
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      const int64_t orow = live ? (w.base + row / G) * a.H + static_cast<int64_t>(w.head) * G + row % G : 0;
-#pragma unroll 1
-      for (int g = 0; g < 4; ++g) {
-        float o[32];
-        tmem_ld32(to + 32 * g, o);
-        uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + orow * 128 + 32 * g);
-        if (live)
+        for (int e = 0; e < 4; ++e)
+          reinterpret_cast<float4*>(dst)[4 * g + e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+      } else {
 #pragma unroll
-          for (int e = 0; e < 32; e += 8)
-            dst[e >> 3] = make_uint4(pack_bf162(o[e] * inv, o[e + 1] * inv), pack_bf162(o[e + 2] * inv, o[e + 3] * inv),
-                                     pack_bf162(o[e + 4] * inv, o[e + 5] * inv), pack_bf162(o[e + 6] * inv, o[e + 7] * inv));
+        for (int e = 0; e < 2; ++e)
+          reinterpret_cast<uint4*>(dst)[2 * g + e] =
+              make_uint4(pack_bf162(o[8 * e] * inv, o[8 * e + 1] * inv), pack_bf162(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                         pack_bf162(o[8 * e + 4] * inv, o[8 * e + 5] * inv), pack_bf162(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
       }
-      if (live && a.lse) a.lse[orow] = lse_of(m, l);
     }
+    if (live && part) p.s.part_ml[at] = make_float2(m, l);
+    if (live && !part && a.lse) a.lse[orow] = lse_of(m, l);
     tc_fence_before();
     feed.done(lane);
   }

@@ -87,6 +87,11 @@ __device__ __forceinline__ float lse_of(float m, float l) {  // m in log2 units
   return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
+// The token of a row, row / (H / kv heads).
+__device__ __forceinline__ int row_token(const AttnArgs& a, int row) {
+  return static_cast<int>((static_cast<uint64_t>(static_cast<uint32_t>(row)) * a.g_magic) >> a.g_shift);
+}
+
 // One (sequence, kv head, row tile): rows [row0, row0 + tile rows) of the sequence's
 // rows = n_tok G rows, row r = token r / G, query head head * G + r % G.
 struct Item {
