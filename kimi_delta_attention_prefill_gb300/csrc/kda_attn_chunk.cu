@@ -218,6 +218,7 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
 #pragma unroll 1
     for (int i = begin - 1; i < end; ++i) {
       const bool pv = i >= begin, more = i + 1 < end;
+      if (more) wait(&b.full[sk], pk);
       if (pv) {
         // A and B take turns of one P V and the next Q K^T each.  Left alone their products mix and
         // end together, and then both tiles are in their softmax while the tensor core has nothing.
@@ -236,14 +237,15 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
                           kk > 0 || h == 0 || i > begin);
         }
         mma_commit_if(leader, &b.pv_done[t]);
-        mma_commit_if(leader, &b.empty[sv]);
-        if (!more) {
-          mma_commit_if(leader, &b.o_full[t]);
-          if (both && leader) mbar_arrive(&b.turn[t ^ 1]);
+        if (!more) mma_commit_if(leader, &b.o_full[t]);
+        wait(&b.pv_done[t], tiles++);  // P lies over S: the next scores may be written once it has been read
+        // The turn goes on before this tile's Q K^T is issued: the other warp takes as long to its
+        // first product as this one to issue its eight.
+        if (leader) {
+          if (both) mbar_arrive(&b.turn[t ^ 1]);
+          mbar_arrive(&b.empty[sv]);
         }
       }
-      if (more) wait(&b.full[sk], pk);
-      if (pv) wait(&b.pv_done[t], tiles++);  // P lies over S: the next scores may be written once it has been read
       if (more) {
         __syncwarp();
         tc_fence_after();
@@ -256,7 +258,6 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
         mma_commit_if(leader, &b.s_full[t]);
         mma_commit_if(leader, &b.empty[sk]);
         if (i + 2 == end) mma_commit_if(leader, &b.q_empty);
-        if (pv && both && leader) mbar_arrive(&b.turn[t ^ 1]);
         step();
         sv = sk;
         values(i + 1, sk, pk);
