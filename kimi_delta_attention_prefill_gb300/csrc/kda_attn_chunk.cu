@@ -45,11 +45,10 @@ constexpr int kRows = 256;
 constexpr int kPanel = kTile * 128;     // 64 channels of 128 rows, 16-bit
 constexpr int kSlot = 2 * kPanel;       // one tile of K or V (or 128 rows of Q) as 16-bit values
 constexpr int kStage = kTile * 128 + 8 * 128;  // a tile of codes and a 128-byte slot of scale bytes per page
-constexpr int kMinTiles = 2, kItemCost = 3;
+constexpr int kMinTiles = 2, kItemCost = 5;
 
 template <bool kE4m3>
 struct Cfg {
-  static constexpr int kQueryWarps = kE4m3 ? 1 : 4;
   static constexpr int kSlots = kE4m3 ? 3 : 5;
   static constexpr int kStages = kE4m3 ? 3 : 0;
   static constexpr int kSmQ = 0;
@@ -64,7 +63,7 @@ struct Cfg {
 struct TileScale {
   float k;        // 2^E of the keys
   float v;        // E of the values
-  int wide;       // the scales of the keys (1), the values (2) lie too far apart: code tiles, per-key scales
+  int wide_k, wide_v;  // their scales lie too far apart: tiles of codes, scales key by key
 };
 
 struct Bars {
@@ -134,24 +133,24 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
       const int slot = j0 & (a.cache.page_size - 1);
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++n) {
-        const uint32_t s = n % kRing;
-        if (n >= kRing && !bar_wait(&empty[s], (n / kRing - 1) & 1)) {
-          report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
-          return;
-        }
-        if (lane == 0) mbar_arrive_expect_tx(&full[s], kE4m3 ? kTile * 128 + kTile : kSlot);
-        __syncwarp();
-        if (blk < n_blk) {
-          if constexpr (kE4m3) {
-            uint8_t* st = sm + C::kSmStage + s * kStage;
-            tma_load_4d(st + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, head, page);
-            tma_load_3d(st + kTile * 128 + blk * 128, kv ? &p.tvs : &p.tks, &full[s], slot, head, page);
-          } else {
-            uint8_t* st = sm + C::kSmKV + s * kSlot;
-            tma_load_5d(st + panel * kPanel + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, panel, head, page);
+          const uint32_t s = n % kRing;
+          if (n >= kRing && !bar_wait(&empty[s], (n / kRing - 1) & 1)) {
+            report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+            return;
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&full[s], kE4m3 ? kTile * 128 + kTile : kSlot);
+          __syncwarp();
+          if (blk < n_blk) {
+            if constexpr (kE4m3) {
+              uint8_t* st = sm + C::kSmStage + s * kStage;
+              tma_load_4d(st + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, head, page);
+              tma_load_3d(st + kTile * 128 + blk * 128, kv ? &p.tvs : &p.tks, &full[s], slot, head, page);
+            } else {
+              uint8_t* st = sm + C::kSmKV + s * kSlot;
+              tma_load_5d(st + panel * kPanel + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, panel, head, page);
+            }
           }
         }
-      }
     }
     more = walk.next();
   }
@@ -194,22 +193,22 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
     // warps need not follow the ring.
     bool edge = false;
     auto values = [&](int i, uint32_t slot, uint32_t phase) {
-      wait(&b.full[slot], phase);
-      edge = !kE4m3 && edge_tile(a, i < sink ? i : lo + (i - sink), p_first, p_last);
-      if (edge && leader) mbar_arrive(&b.v_ask);
+        wait(&b.full[slot], phase);
+        edge = !kE4m3 && edge_tile(a, i < sink ? i : lo + (i - sink), p_first, p_last);
+        if (edge && leader) mbar_arrive(&b.v_ask);
     };
     if (!mine) {  // only keeps the other warps' counts
-      if (leader) mbar_arrive(&b.q_empty);
-      for (int i = begin; i < end; ++i) {
-        wait(&b.full[sk], pk);
-        if (leader) mbar_arrive(&b.empty[sk]);
-        step();
-        values(i, sk, pk);
-        if (edge) wait(&b.v_ok, edges++);
-        if (leader) mbar_arrive(&b.empty[sk]);
-        step();
-      }
-      continue;
+        if (leader) mbar_arrive(&b.q_empty);
+        for (int i = begin; i < end; ++i) {
+          wait(&b.full[sk], pk);
+          if (leader) mbar_arrive(&b.empty[sk]);
+          step();
+          values(i, sk, pk);
+          if (edge) wait(&b.v_ok, edges++);
+          if (leader) mbar_arrive(&b.empty[sk]);
+          step();
+        }
+        continue;
     }
     // The tensor core has products queued while this warp waits: what can be waited for early is
     // waited for behind a product, so that nothing but the softmax comes before P V.  (One loop
@@ -217,52 +216,52 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
     uint32_t sv = 0;
 #pragma unroll 1
     for (int i = begin - 1; i < end; ++i) {
-      const bool pv = i >= begin, more = i + 1 < end;
-      if (more) wait(&b.full[sk], pk);
-      if (pv) {
-        // A and B take turns of one P V and the next Q K^T each.  Left alone their products mix and
-        // end together, and then both tiles are in their softmax while the tensor core has nothing.
-        if (both && (t == 1 || turns > 0)) wait(&b.turn[t], t == 1 ? turns : turns - 1);
-        turns += both;
+        const bool pv = i >= begin, more = i + 1 < end;
+        if (more) wait(&b.full[sk], pk);
+        if (pv) {
+          // A and B take turns of one P V and the next Q K^T each.  Left alone their products mix and
+          // end together, and then both tiles are in their softmax while the tensor core has nothing.
+          if (both && (t == 1 || turns > 0)) wait(&b.turn[t], t == 1 ? turns : turns - 1);
+          turns += both;
 #pragma unroll
-        for (int h = 1; h >= 0; --h) {  // the weights come in two halves of 64 keys, the later keys first
-          wait(&b.p_full[t][h], tiles);
-          if (h == 1 && edge) wait(&b.v_ok, edges++);
-          __syncwarp();
+          for (int h = 1; h >= 0; --h) {  // the weights come in two halves of 64 keys, the later keys first
+            wait(&b.p_full[t][h], tiles);
+            if (h == 1 && edge) wait(&b.v_ok, edges++);
+            __syncwarp();
+            tc_fence_after();
+            const uint64_t db = dv + sv * (kSlot >> 4) + h * (4 * 2048 >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_f16_ta_if(leader, 256 + 128 * t, 128 * t + 64 * h + 8 * kk, db + kk * (2048 >> 4), id_pv,
+                            kk > 0 || h == 0 || i > begin);
+          }
+          mma_commit_if(leader, &b.pv_done[t]);
+          if (!more) mma_commit_if(leader, &b.o_full[t]);
+          wait(&b.pv_done[t], tiles++);  // P lies over S: the next scores may be written once it has been read
+          // The turn goes on before this tile's Q K^T is issued: the other warp takes as long to its
+          // first product as this one to issue its eight.
+          if (leader) {
+            if (both) mbar_arrive(&b.turn[t ^ 1]);
+            mbar_arrive(&b.empty[sv]);
+          }
+        }
+        if (more) {
+            __syncwarp();
           tc_fence_after();
-          const uint64_t db = dv + sv * (kSlot >> 4) + h * (4 * 2048 >> 4);
+          const uint64_t db = dk + sk * (kSlot >> 4);
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk)
-            mma_f16_ta_if(leader, 256 + 128 * t, 128 * t + 64 * h + 8 * kk, db + kk * (2048 >> 4), id_pv,
-                          kk > 0 || h == 0 || i > begin);
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = ((kk >> 2) * kPanel + 32 * (kk & 3)) >> 4;
+            mma_f16_if(leader, 128 * t, dq + off, db + off, id_qk, kk > 0);
+          }
+          mma_commit_if(leader, &b.s_full[t]);
+          mma_commit_if(leader, &b.empty[sk]);
+          if (i + 2 == end) mma_commit_if(leader, &b.q_empty);
+          step();
+          sv = sk;
+          values(i + 1, sk, pk);
+          step();
         }
-        mma_commit_if(leader, &b.pv_done[t]);
-        if (!more) mma_commit_if(leader, &b.o_full[t]);
-        wait(&b.pv_done[t], tiles++);  // P lies over S: the next scores may be written once it has been read
-        // The turn goes on before this tile's Q K^T is issued: the other warp takes as long to its
-        // first product as this one to issue its eight.
-        if (leader) {
-          if (both) mbar_arrive(&b.turn[t ^ 1]);
-          mbar_arrive(&b.empty[sv]);
-        }
-      }
-      if (more) {
-        __syncwarp();
-        tc_fence_after();
-        const uint64_t db = dk + sk * (kSlot >> 4);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          const uint32_t off = ((kk >> 2) * kPanel + 32 * (kk & 3)) >> 4;
-          mma_f16_if(leader, 128 * t, dq + off, db + off, id_qk, kk > 0);
-        }
-        mma_commit_if(leader, &b.s_full[t]);
-        mma_commit_if(leader, &b.empty[sk]);
-        if (i + 2 == end) mma_commit_if(leader, &b.q_empty);
-        step();
-        sv = sk;
-        values(i + 1, sk, pk);
-        step();
-      }
     }
   }
   // nothing of this block's may be in flight when it ends
@@ -272,53 +271,45 @@ __device__ void mma_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int t) {
 }
 
 // --------------------------------------------------------------------------- queries
-// One warp (bf16: four) brings an item's 256 query rows, 16 lanes a row, zero past the last, and in a bf16
-// cache's edge tiles look the values through (see the softmax).  A negative scale is the same
-// as negated queries and a scale of 0 as zero queries with any scale, so the softmax's scale c
-// is positive.
+// Four warps bring an item's 256 query rows, 16 lanes a row, zero past the last.  A negative
+// scale is the same as negated queries and a scale of 0 as zero queries with any scale, so the
+// softmax's scale is positive.
 template <bool kE4m3>
-__device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
+__device__ void load_queries(const AttnArgs& a, const Job& w, uint8_t* sm, Bars& b, int tid, uint32_t items, bool& dead) {
   using C = Cfg<kE4m3>;
-  const AttnArgs& a = p.a;
   const int lane = tid & 31, sub = tid & 15, grp = tid >> 4;
-  constexpr int kGroups = 2 * C::kQueryWarps, kGroupRows = kRows / kGroups;  // of 16 lanes
+  constexpr int kGroups = 8, kGroupRows = kRows / kGroups;  // of 16 lanes
   const int G = a.H / a.cache.heads;
   const uint32_t q_at = smem_u32(sm + C::kSmQ) + (sub >> 3) * kPanel;
   auto q_piece = [&](int r) { return q_at + (r >> 7) * kSlot + sw128(r & 127, 16 * (sub & 7)); };  // this lane's 8 channels
-  float* qexp = reinterpret_cast<float*>(sm + C::kSmExp);
-  uint32_t n = 0, items = 0, edges = 0;
-  bool dead = false;
-  JobFeed feed{b.jobs, dead};
-  while (const Job* jp = feed.next()) {
-    const Job& w = *jp;
-    const int n_rows = w.rows - w.row0;
-    const uint16_t* q0 = static_cast<const uint16_t*>(a.q) + w.q_base + static_cast<int64_t>(w.head) * G * a.q_stride[2];
-    // while the last item still uses the tiles, the rows' lines into L2: a few rows a lane
-    for (int r = tid; r < min(kRows, n_rows); r += 16 * kGroups) {
-      const int tok = row_token(a, w.row0 + r), g = w.row0 + r - tok * G;
-      const uint16_t* src = q0 + tok * a.q_stride[1] + g * a.q_stride[2];
-      prefetch_l2(src);
-      prefetch_l2(src + 64);
-    }
-    if (items > 0 && !dead && !bar_wait(&b.q_empty, (items - 1) & 1)) dead = true;
-    // every piece is on its way before any is waited for; zeros past the last row
-    {
-      const int first = grp * kGroupRows, tok = row_token(a, w.row0 + first);
-      int g = w.row0 + first - tok * G;
-      const uint16_t* src = q0 + tok * a.q_stride[1] + g * a.q_stride[2] + 8 * sub;
-      const int64_t wrap = a.q_stride[1] - (G - 1) * a.q_stride[2];
+  const int n_rows = w.rows - w.row0;
+  const uint16_t* q0 = static_cast<const uint16_t*>(a.q) + w.q_base + static_cast<int64_t>(w.head) * G * a.q_stride[2];
+  // while the last item still uses the tiles, the rows' lines into L2: a few rows a lane
+  for (int r = tid; r < min(kRows, n_rows); r += 16 * kGroups) {
+    const int tok = row_token(a, w.row0 + r), g = w.row0 + r - tok * G;
+    const uint16_t* src = q0 + tok * a.q_stride[1] + g * a.q_stride[2];
+    prefetch_l2(src);
+    prefetch_l2(src + 64);
+  }
+  if (items > 0 && !dead && !bar_wait(&b.q_empty, (items - 1) & 1)) dead = true;
+  // every piece is on its way before any is waited for; zeros past the last row
+  {
+    const int first = grp * kGroupRows, tok = row_token(a, w.row0 + first);
+    int g = w.row0 + first - tok * G;
+    const uint16_t* src = q0 + tok * a.q_stride[1] + g * a.q_stride[2] + 8 * sub;
+    const int64_t wrap = a.q_stride[1] - (G - 1) * a.q_stride[2];
 #pragma unroll 4
-      for (int r = first; r < first + kGroupRows; ++r) {
+    for (int r = first; r < first + kGroupRows; ++r) {
         cp_async16(q_piece(r), src, r < n_rows);
         const bool end = ++g == G;
         src += end ? wrap : a.q_stride[2];
         g = end ? 0 : g;
-      }
     }
-    cp_async_wait_all();
-    if (kE4m3 || a.scale_log2 <= 0.f) {  // in place: each thread its own pieces
+  }
+  cp_async_wait_all();
+  if (kE4m3 || a.scale_log2 <= 0.f) {  // in place: each thread its own pieces
 #pragma unroll 4
-      for (int r = grp * kGroupRows; r < (grp + 1) * kGroupRows; ++r) {
+    for (int r = grp * kGroupRows; r < (grp + 1) * kGroupRows; ++r) {
         uint4 x = lds128(q_piece(r));
         if (a.scale_log2 == 0.f) x = make_uint4(0, 0, 0, 0);
         if constexpr (kE4m3) {
@@ -328,7 +319,7 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
           for (int off = 8; off; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
           const int e = query_exponent(top);
           const float inv = a.scale_log2 < 0.f ? -pow2i(-e) : pow2i(-e);
-          if (sub == 0) qexp[(items & 1) * kRows + r] = pow2i(e);
+          if (sub == 0) reinterpret_cast<float*>(sm + C::kSmExp)[(items & 1) * kRows + r] = pow2i(e);
           auto half = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv); };
           x = make_uint4(half(x.x), half(x.y), half(x.z), half(x.w));
         } else if (a.scale_log2 < 0.f) {
@@ -336,38 +327,51 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
           x = make_uint4(x.x ^ flip, x.y ^ flip, x.z ^ flip, x.w ^ flip);
         }
         sts128(q_piece(r), x);
-      }
     }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&b.q_full);
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) mbar_arrive(&b.q_full);
+}
+
+// bf16 cache: four warps for the queries, which also look the edge tiles' values through (see the softmax).
+__device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
+  using C = Cfg<false>;
+  const AttnArgs& a = p.a;
+  const int lane = tid & 31;
+  uint32_t n = 0, items = 0, edges = 0;
+  bool dead = false;
+  JobFeed feed{b.jobs, dead};
+  while (const Job* jp = feed.next()) {
+    const Job& w = *jp;
+    load_queries<false>(a, w, sm, b, tid, items, dead);
     ++items;
-    if constexpr (!kE4m3) {
-      const int begin = w.begin, end = w.end;
-      for (int i = begin; i < end; ++i, n += 2) {
-        if (!edge_tile(a, w.tile(i), w.p_first, w.p_last)) continue;
-        const uint32_t s = (n + 1) % C::kSlots;
-        if (!dead && !bar_wait(&b.v_ask, edges++ & 1)) dead = true;
-        // thread = key: a row of 128 values with a NaN or an infinity is cleared and noted
-        uint8_t* v = sm + C::kSmKV + s * kSlot;
-        bool bad = false;
+    {
+        const int begin = w.begin, end = w.end;
+        for (int i = begin; i < end; ++i, n += 2) {
+          if (!edge_tile(a, w.tile(i), w.p_first, w.p_last)) continue;
+          const uint32_t s = (n + 1) % C::kSlots;
+          if (!dead && !bar_wait(&b.v_ask, edges++ & 1)) dead = true;
+          // thread = key: a row of 128 values with a NaN or an infinity is cleared and noted
+          uint8_t* v = sm + C::kSmKV + s * kSlot;
+          bool bad = false;
 #pragma unroll 8
-        for (int c = 0; c < 16; ++c) {
-          const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * kPanel + sw128(tid, 16 * (c & 7)));
-          auto has = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
-          bad |= has(x.x) | has(x.y) | has(x.z) | has(x.w);
-        }
-        if (bad) {
+          for (int c = 0; c < 16; ++c) {
+            const uint4 x = *reinterpret_cast<const uint4*>(v + (c >> 3) * kPanel + sw128(tid, 16 * (c & 7)));
+            auto has = [](uint32_t u) { return (u & 0x7f80u) == 0x7f80u || (u & 0x7f800000u) == 0x7f800000u; };
+            bad |= has(x.x) | has(x.y) | has(x.z) | has(x.w);
+          }
+          if (bad) {
 #pragma unroll 1
-          for (int c = 0; c < 16; ++c)
-            *reinterpret_cast<uint4*>(v + (c >> 3) * kPanel + sw128(tid, 16 * (c & 7))) = make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < 16; ++c)
+              *reinterpret_cast<uint4*>(v + (c >> 3) * kPanel + sw128(tid, 16 * (c & 7))) = make_uint4(0, 0, 0, 0);
+          }
+          const uint32_t m = __ballot_sync(0xffffffffu, bad);
+          if (lane == 0) b.bad[s][tid >> 5] = m;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&b.v_ok);
         }
-        const uint32_t m = __ballot_sync(0xffffffffu, bad);
-        if (lane == 0) b.bad[s][tid >> 5] = m;
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&b.v_ok);
-      }
     }
     feed.done(lane);
   }
@@ -375,12 +379,13 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
 }
 
 // ------------------------------------------------------------------- codes to f16 tiles
-// Four warps, thread = key.  With E the largest scale exponent of the tile's keys (values), a row
-// becomes code * 2^(e - E) in f16: exact for e >= E - 15 (codes go down to 2^-9, f16 to 2^-24),
-// so that one factor 2^E serves the whole tile and the softmax has no per-key work.  Where a row's
-// scale lies further below (all-zero rows aside) the tile is "wide": its rows stay plain codes and
-// the softmax takes every key's scale by itself.  Rows past the last position, which may hold
-// anything, become zeros; so do value rows that hold a NaN, noted in bad[].
+// Four warps, which also bring the queries; thread = key.  (Eight, four for the keys and four for
+// the values, were slower: 3.0 against 2.7 ms for 2048 tokens over 30 K keys, 96 heads on 8.)  With E the largest scale exponent of the tile's keys (values), a row becomes code * 2^(e - E) in
+// f16: exact for e >= E - 15 (codes go down to 2^-9, f16 to 2^-24), so that one factor 2^E serves
+// the whole tile and the softmax has no per-key work.  Where a row's scale lies further below
+// (all-zero rows aside) the tile is "wide": its rows stay plain codes and the softmax takes every
+// key's scale by itself.  Rows past the last position, which may hold anything, become zeros; so
+// do value rows that hold a NaN, noted in bad[].
 constexpr int kLeast = 127 - 40;  // the least scale byte that is written
 __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
   using C = Cfg<true>;
@@ -388,17 +393,18 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
   const int lane = tid & 31, warp = tid >> 5;
   const int p_log = min(a.cache.page_log2, 7);
   const int sc_at = kTile * 128 + (tid >> p_log) * 128 + (tid & ((1 << p_log) - 1));
-  uint32_t n = 0;
+  uint32_t n = 0, items = 0;
   bool dead = false;
   JobFeed feed{b.jobs, dead};
   while (const Job* jp = feed.next()) {
     const Job& w = *jp;
+    load_queries<true>(a, w, sm, b, tid, items++, dead);
     const int begin = w.begin, end = w.end;
     for (int i = begin; i < end; ++i) {
-      const int keys = w.p_last + 1 - w.tile(i) * kTile;  // those of the tile that are not past the last position
-      const bool past = tid >= keys;
+        const int keys = w.p_last + 1 - w.tile(i) * kTile;  // those of the tile that are not past the last position
+        const bool past = tid >= keys, edge = edge_tile(a, w.tile(i), w.p_first, w.p_last);
 #pragma unroll 1
-      for (int kv = 0; kv < 2; ++kv, ++n) {
+        for (int kv = 0; kv < 2; ++kv, ++n) {
         const uint32_t st = n % C::kStages, s = n % C::kSlots;
         if (!dead && !bar_wait(&b.st_full[st], (n / C::kStages) & 1)) dead = true;
         const uint8_t* src = sm + C::kSmStage + st * kStage;
@@ -406,11 +412,14 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
 #pragma unroll
         for (int k = 0; k < 8; ++k) c[k] = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
         const uint32_t byte = src[sc_at];
+        // A code of NaN matters here where some row does not see the key; elsewhere it makes its own way.
         uint32_t nan = 0;
+        if (edge) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          auto has = [](uint32_t u) { return (u & 0x7f7f7f7fu) + 0x01010101u; };  // bit 7 of a byte: it is 0x7f or 0xff
-          nan |= (has(c[k].x) | has(c[k].y) | has(c[k].z) | has(c[k].w)) & 0x80808080u;
+          for (int k = 0; k < 8; ++k) {
+            auto has = [](uint32_t u) { return (u & 0x7f7f7f7fu) + 0x01010101u; };  // bit 7 of a byte: it is 0x7f or 0xff
+            nan |= (has(c[k].x) | has(c[k].y) | has(c[k].z) | has(c[k].w)) & 0x80808080u;
+          }
         }
         // Every warp finds E and the lowest exponent of all 128 rows by itself, four scale bytes a lane.
         // NaN rows and rows past the last position do not count, nor do rows of zeros (they have the
@@ -457,10 +466,10 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
         if (tid == 0) {
           if (kv) {
             ts.v = wide ? 0.f : static_cast<float>(top);
-            ts.wide |= wide ? 2 : 0;
+            ts.wide_v = wide;
           } else {
             ts.k = wide ? 1.f : pow2i(top);
-            ts.wide = wide ? 1 : 0;
+            ts.wide_k = wide;
           }
         }
         float* vec = reinterpret_cast<float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
@@ -474,19 +483,24 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
         __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>(r >= -14 ? (15 + r) << 10 : 1 << (24 + r))));
         if (bad && !kv) f = __half2half2(__ushort_as_half(0x7fff));
         const uint32_t keep = past || (bad && kv) ? 0u : 0xffffffffu;
-        auto out = [&](uint32_t pair) {
-          const uint32_t h = e4m3_half2(pair & keep);
-          const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&h), f);
-          return *reinterpret_cast<const uint32_t*>(&y);
+        auto out = [&](uint32_t codes, uint32_t& lo, uint32_t& hi) {
+          uint32_t l, h;
+          e4m3_half4(codes & keep, l, h);
+          const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&l), f), y = __hmul2(*reinterpret_cast<const __half2*>(&h), f);
+          lo = *reinterpret_cast<const uint32_t*>(&x);
+          hi = *reinterpret_cast<const uint32_t*>(&y);
         };
         uint8_t* dst = sm + C::kSmKV + s * kSlot;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           uint8_t* row = dst + (k >> 2) * kPanel;
-          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3))) =
-              make_uint4(out(c[k].x), out(c[k].x >> 16), out(c[k].y), out(c[k].y >> 16));
-          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3) + 16)) =
-              make_uint4(out(c[k].z), out(c[k].z >> 16), out(c[k].w), out(c[k].w >> 16));
+          uint4 x, y;
+          out(c[k].x, x.x, x.y);
+          out(c[k].y, x.z, x.w);
+          out(c[k].z, y.x, y.y);
+          out(c[k].w, y.z, y.w);
+          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3))) = x;
+          *reinterpret_cast<uint4*>(row + sw128(tid, 32 * (k & 3) + 16)) = y;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -546,30 +560,26 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       wait(&b.s_full[t], tiles);
       ++tiles;
       tc_fence_after();
+      // 0 * NaN must not reach a row that does not see the key: value rows with a non-finite value
+      // were cleared, and the rows that do see one become NaN here.
+      auto poison = [&] {
+        const uint4 any = *reinterpret_cast<const uint4*>(b.bad[sv]);
+        if ((any.x | any.y | any.z | any.w) == 0) return;
+#pragma unroll 1
+        for (int k = 0; k < kTile; ++k)
+          if (((b.bad[sv][k >> 5] >> (k & 31)) & 1) && sees(pos, kt * kTile + k, a.window, a.n_sink))
+            l = __uint_as_float(0x7fffffffu);
+      };
       float u = crow, off = 0.f;
-      int wide = 0, bad = edge;
+      int wide = 0;
       if constexpr (kE4m3) {
         if (i == begin) crow = scale * reinterpret_cast<const float*>(sm + C::kSmExp)[(seen & 1) * kRows + 128 * t + tid];
         wait(&b.full[sv], (n + 1) / C::kSlots);  // the value scales come with the values
         const TileScale& sc = b.tile[(n >> 1) & 1];
         u = crow * sc.k;
         off = sc.v;
-        wide = sc.wide;
-        const uint4 keys = *reinterpret_cast<const uint4*>(b.bad[sv]);
-        bad = (keys.x | keys.y | keys.z | keys.w) != 0;
-      } else if (edge) {
-        wait(&b.v_ok, edges++);
-      }
-      if (bad) {
-        // 0 * NaN must not reach a row that does not see the key: such value rows were cleared,
-        // and the rows that do see one become NaN here.
-#pragma unroll 1
-        for (int g = 0; g < 4; ++g) {
-          const uint32_t keys = b.bad[sv][g];
-#pragma unroll 1
-          for (int e = 0; keys >> e && e < 32; ++e)
-            if (((keys >> e) & 1) && sees(pos, kt * kTile + 32 * g + e, a.window, a.n_sink)) l = __uint_as_float(0x7fffffffu);
-        }
+        wide = sc.wide_k | sc.wide_v;
+        poison();
       }
       // ---- in edge and wide tiles, the scores in place first: y of the codes, key by key, after which
       // u = 1 and off = 0; hidden ones -inf.  Rolled: the code is cold whenever it runs.
@@ -676,6 +686,10 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.p_full[t][h]);
       }
+      if (!kE4m3 && edge) {  // P V waits for this too: the slot is not used again before
+        wait(&b.v_ok, edges++);
+        poison();
+      }
       const float2 sums = unpack_f32x2(add_f32x2(sum, sum1));
       if (!kE4m3) l += sums.x + sums.y;
       else if (!wide) l = fmaf(sums.x + sums.y, exp2_fast(-off), l);
@@ -729,8 +743,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     }
     for (int i = 0; i < 3; ++i) { mbar_init(&b.st_full[i], 1); mbar_init(&b.st_empty[i], 4); }
     mbar_init(&b.v_ask, 2);
-    mbar_init(&b.v_ok, C::kQueryWarps);
-    mbar_init(&b.q_full, C::kQueryWarps);
+    mbar_init(&b.v_ok, 4);
+    mbar_init(&b.q_full, 4);
     mbar_init(&b.q_empty, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&b.s_full[i], 1);
@@ -742,7 +756,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       mbar_init(&b.drain[i], 1);
     }
     // a job is read by the two product warps, the query warps, the eight softmax warps and the converters
-    b.jobs.init(10 + C::kQueryWarps + (kE4m3 ? 4 : 0));
+    b.jobs.init(10 + 4);
     fence_mbar_init();
     p.s.desc[blockIdx.x].last = -1;
   }
@@ -760,15 +774,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
     softmax_group<kE4m3>(p, sm, b, warp >> 2, tid & 127);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 80;\n" ::: "memory");
-    if (warp < 10) {
-      mma_warp<kE4m3>(p, sm, b, warp - 8);
-    } else if (warp == 10) {
-      load_warp<kE4m3>(p, sm, b, tid & 31);
-    } else if (kE4m3 && warp == 11) {
-      query_warps<kE4m3>(p, sm, b, tid & 31);
-    } else if (warp >= 12) {
+    if (warp < 10) mma_warp<kE4m3>(p, sm, b, warp - 8);
+    else if (warp == 10) load_warp<kE4m3>(p, sm, b, tid & 31);
+    else if (warp >= 12) {
       if constexpr (kE4m3) convert_group(p, sm, b, tid - 384);
-      else query_warps<kE4m3>(p, sm, b, tid - 384);
+      else query_warps(p, sm, b, tid - 384);
     }
   }
   tc_fence_before();

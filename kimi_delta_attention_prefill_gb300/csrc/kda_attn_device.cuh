@@ -55,11 +55,14 @@ __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
   return false;
 }
 
-// Two e4m3 codes (low 16 bits) as two f16 values, exactly.
-__device__ __forceinline__ uint32_t e4m3_half2(uint32_t pair) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(static_cast<uint16_t>(pair)));
-  return r;
+// Four e4m3 codes as two pairs of f16 values, exactly.
+__device__ __forceinline__ void e4m3_half4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\t"
+      "mov.b32 {l, h}, %2;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(codes));
 }
 
 // Scale bytes of E4M3 rows: 2^(b - 127), NaN for 255 (what is written lies in [87, 167]; other

@@ -300,7 +300,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           const uint32_t c[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
 #pragma unroll
           for (int e = 0; e < 8; ++e)
-            mma16816<true>(x[n], qf[e], e4m3_half2(c[e]), e4m3_half2(c[e] >> 16));
+          {
+            uint32_t lo, hi;
+            e4m3_half4(c[e], lo, hi);
+            mma16816<true>(x[n], qf[e], lo, hi);
+          }
         }
       } else {
 #pragma unroll
@@ -402,8 +406,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           for (int e = 0; e < 4; ++e) {  // 4 channels: column tiles 4e .. 4e + 3
             const uint32_t a0 = __byte_perm(c[0][e], c[1][e], 0x5140), a1 = __byte_perm(c[0][e], c[1][e], 0x7362);
             const uint32_t b0 = __byte_perm(c[2][e], c[3][e], 0x5140), b1 = __byte_perm(c[2][e], c[3][e], 0x7362);
-            uint32_t ba[4] = {e4m3_half2(a0), e4m3_half2(a0 >> 16), e4m3_half2(a1), e4m3_half2(a1 >> 16)};
-            uint32_t bb[4] = {e4m3_half2(b0), e4m3_half2(b0 >> 16), e4m3_half2(b1), e4m3_half2(b1 >> 16)};
+            uint32_t ba[4], bb[4];
+            e4m3_half4(a0, ba[0], ba[1]);
+            e4m3_half4(a1, ba[2], ba[3]);
+            e4m3_half4(b0, bb[0], bb[1]);
+            e4m3_half4(b1, bb[2], bb[3]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) mma16816<true>(o[4 * e + q], pa, ba[q], bb[q]);
           }
