@@ -49,7 +49,7 @@ kda_status check_rows(const kda_kv_cache* cache, const void* k, const int64_t* k
   if (n_seq < 0 || max_pages < 0 || tokens < 0 || tokens > 0x7fffffffLL) return KDA_ERR_INVALID_ARG;
   if (n_seq == 0 && tokens > 0) return KDA_ERR_INVALID_ARG;
   if (tokens == 0) return KDA_OK;
-  if (tokens * cache->n_kv_heads >= (int64_t{1} << 35)) return KDA_ERR_UNSUPPORTED;  // 32 rows a block
+  if ((tokens + 31) / 32 * cache->n_kv_heads > 0x7fffffffLL) return KDA_ERR_UNSUPPORTED;  // a block a head and 32 tokens
   if (!k || !v || !ks || !vs || !cu || !start || (max_pages > 0 && !page_table)) return KDA_ERR_INVALID_ARG;
   if (!aligned(k, 16) || !aligned(v, 16) || !strides_ok(ks, 2, 2) || !strides_ok(vs, 2, 2) || !aligned(page_table, 4) ||
       !aligned(cu, 4) || !aligned(start, 4) || !aligned(status, 4))

@@ -65,16 +65,13 @@ __device__ __forceinline__ void e4m3_half4(uint32_t codes, uint32_t& lo, uint32_
       : "r"(codes));
 }
 
-// Scale bytes of E4M3 rows: 2^(b - 127), NaN for 255 (what is written lies in [87, 167]; other
-// bytes keep their meaning as far as 32 bits go).
-__device__ __forceinline__ float scale_value(uint32_t b) {
-  return __uint_as_float(b == 255 ? 0x7fffffffu : b == 0 ? 0x00400000u : b << 23);
-}
-__device__ __forceinline__ float scale_inverse(uint32_t b) {
-  return __uint_as_float(b == 255 ? 0x7fffffffu : b == 254 ? 0x00400000u : (254u - b) << 23);
-}
+// Scale bytes of E4M3 rows, in the low 8 bits of b: 2^(b - 127), 2^(127 - b) and b - 127.  Of a row of
+// NaN (255, codes 0) they make infinity, by which a score of 0 becomes NaN, -infinity, which
+// makes a sum negative, and 128: no instruction is spent on it.
+__device__ __forceinline__ float scale_value(uint32_t b) { return __uint_as_float((b << 23) & 0x7f800000u); }
+__device__ __forceinline__ float scale_inverse(uint32_t b) { return __uint_as_float(0x7f000000u - ((b << 23) & 0x7f800000u)); }
 __device__ __forceinline__ float scale_exponent(uint32_t b) {
-  return b == 255 ? __uint_as_float(0x7fffffffu) : static_cast<float>(static_cast<int>(b) - 127);
+  return __uint_as_float(0x4b000000u | (b & 255u)) - (8388608.f + 127.f);
 }
 
 __device__ __forceinline__ float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(127 + e) << 23); }

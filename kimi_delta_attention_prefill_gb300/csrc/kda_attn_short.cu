@@ -331,9 +331,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           const uint32_t k2 = *reinterpret_cast<const uint16_t*>(sc), v2 = *reinterpret_cast<const uint16_t*>(sc + St::kScales);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t kbyte = (k2 >> (8 * h)) & 255u, vbyte = (v2 >> (8 * h)) & 255u;
-            const float ks = scale_value(kbyte), ev = scale_exponent(vbyte);
-            rv[n][h] = scale_inverse(vbyte);
+            const float ks = scale_value(k2 >> (8 * h)), ev = scale_exponent(v2 >> (8 * h));
+            rv[n][h] = scale_inverse(v2 >> (8 * h));
             x[n][h] = fmaf(x[n][h] * ks, cs[0], ev);
             x[n][h + 2] = fmaf(x[n][h + 2] * ks, cs[1], ev);
           }
@@ -374,8 +373,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           const float p0 = exp2_fast(x[n][2 * r] - base[r]), p1 = exp2_fast(x[n][2 * r + 1] - base[r]);
           // weights rounded once, to the values' type: f16 2^-11, bf16 2^-8 at most; l keeps 32 bits
           if constexpr (kE4m3) {
-            // a hidden key's scale may be NaN, its weight is 0 whatever the scale says
-            l[r] += (p0 == 0.f ? 0.f : p0 * rv[n][0]) + (p1 == 0.f ? 0.f : p1 * rv[n][1]);
+            float r0 = rv[n][0], r1 = rv[n][1];
+            if (edge) {  // a hidden key's scale may be that of a NaN row; its weight is 0 whatever it says
+              r0 = p0 == 0.f ? 0.f : r0;
+              r1 = p1 == 0.f ? 0.f : r1;
+            }
+            l[r] = fmaf(p0, r0, fmaf(p1, r1, l[r]));
             pf[n][r] = pack_half2(p0, p1);
           } else {
             l[r] += p0 + p1;
@@ -431,9 +434,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
       if (lane == 0) mbar_arrive(&empty[s]);
     }
 
-    // ---- one row's sum lies over the 4 lanes that share it
+    // ---- a NaN value row left -inf (see scale_inverse); one row's sum lies over the 4 lanes that share it
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
+      if (kE4m3 && l[r] < 0.f) l[r] = __uint_as_float(0x7fffffffu);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
       l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
     }

@@ -8,9 +8,10 @@
 //
 // Bound by memory: each row is read once and written once.  16 lanes hold a row, 16 bytes
 // (8 bf16 values) a lane, so a load instruction of a warp covers two whole rows; the row's
-// maximum is four shuffles.  A block takes kRowsPerBlock consecutive (token, head) rows of
-// both k and v.  Their loads are issued before the block looks up which sequence and page
-// each token belongs to, so the two latencies overlap.
+// maximum is four shuffles.  A block takes one head's rows of 32 or 64 consecutive tokens, k and v:
+// whole stretches of a page (4 or 8 KB of codes), while the blocks of the other heads, next to it in
+// the grid, fill in the packed rows between.  Its source loads are issued before it looks up
+// which sequence and page each token belongs to, so the two latencies overlap.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -23,10 +24,13 @@ namespace kda {
 namespace {
 
 constexpr int kKvThreads = 256;
-constexpr int kLanes = 16;                        // lanes a row
-constexpr int kGroups = kKvThreads / kLanes;      // rows at a time
-constexpr int kRowsPerGroup = 2;
-constexpr int kRowsPerBlock = kGroups * kRowsPerGroup;
+constexpr int kLanes = 16;                    // lanes a row
+constexpr int kGroups = kKvThreads / kLanes;  // rows at a time
+// Rows that a group of lanes has in flight.  208873 tokens of 8 heads read: 2 rows 230 us, 4 rows
+// 192 us (6.7 TB/s, the copy rate); 130049 tokens appended, e4m3: 1 row 159 us, 2 rows 148 us
+// (5.4 TB/s), 4 rows 189 us, whose registers leave fewer blocks.
+template <bool kRead>
+constexpr int kInFlightRows = kRead ? 4 : 2;
 
 // Where token t (packed) lives: its page, or -1 when nothing may be touched there.
 // `strict`: a table entry -1 is an error (read); otherwise it only means "not here".
@@ -121,85 +125,78 @@ __device__ __forceinline__ uint4 load_e4m3(uint2 c, uint32_t byte) {
 
 template <bool kE4m3, bool kRead>
 __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(const __grid_constant__ KvRows a) {
-  __shared__ Slot slots[kRowsPerBlock];
-  const int64_t rows = a.tokens * a.cache.heads;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kRowsPerBlock;
+  constexpr int kInFlight = kInFlightRows<kRead>, kBlockTokens = kGroups * kInFlight;
+  __shared__ Slot slots[kBlockTokens];
   const int tid = threadIdx.x, lane = tid & (kLanes - 1), grp = tid / kLanes;
-  const int64_t t0 = row0 / a.cache.heads;
-  int64_t tok[kRowsPerGroup];
-  int head[kRowsPerGroup];
-  bool live[kRowsPerGroup];
-  uint4 x[kRowsPerGroup][2];
+  const unsigned heads = a.cache.heads, tile = blockIdx.x / heads, head = blockIdx.x - tile * heads;
+  const int64_t t0 = static_cast<int64_t>(tile) * kBlockTokens;
+  const int n_tok = a.tokens - t0 < kBlockTokens ? static_cast<int>(a.tokens - t0) : kBlockTokens;
+  uint16_t* k = static_cast<uint16_t*>(a.k) + head * a.k_stride[1] + 8 * lane;
+  uint16_t* v = static_cast<uint16_t*>(a.v) + head * a.v_stride[1] + 8 * lane;
+  bool live[kInFlight];
+  uint4 x[kInFlight][2];
 #pragma unroll
-  for (int r = 0; r < kRowsPerGroup; ++r) {
-    const int64_t row = row0 + r * kGroups + grp;
-    live[r] = row < rows;
-    tok[r] = live[r] ? row / a.cache.heads : t0;
-    head[r] = live[r] ? static_cast<int>(row - tok[r] * a.cache.heads) : 0;
+  for (int r = 0; r < kInFlight; ++r) {
+    const int t = r * kGroups + grp;
+    live[r] = t < n_tok;
     if constexpr (!kRead) {
       x[r][0] = x[r][1] = make_uint4(0, 0, 0, 0);
       if (live[r]) {
-        const uint16_t* k = static_cast<const uint16_t*>(a.k) + tok[r] * a.k_stride[0] + head[r] * a.k_stride[1];
-        const uint16_t* v = static_cast<const uint16_t*>(a.v) + tok[r] * a.v_stride[0] + head[r] * a.v_stride[1];
-        x[r][0] = __ldcs(reinterpret_cast<const uint4*>(k) + lane);
-        x[r][1] = __ldcs(reinterpret_cast<const uint4*>(v) + lane);
+        x[r][0] = __ldcs(reinterpret_cast<const uint4*>(k + (t0 + t) * a.k_stride[0]));
+        x[r][1] = __ldcs(reinterpret_cast<const uint4*>(v + (t0 + t) * a.v_stride[0]));
       }
     }
   }
-  const int64_t last = row0 + kRowsPerBlock < rows ? row0 + kRowsPerBlock : rows;
-  const int n_tok = static_cast<int>((last - 1) / a.cache.heads - t0) + 1;
   if (tid < n_tok) slots[tid] = find_slot(a, t0 + tid, kRead);
   __syncthreads();
-  const int64_t ks[3] = {a.cache.k_stride[0], a.cache.k_stride[1], a.cache.k_stride[2]};
-  const int64_t vs[3] = {a.cache.v_stride[0], a.cache.v_stride[1], a.cache.v_stride[2]};
-  if constexpr (kRead) {
-    uint2 c[kRowsPerGroup][2];
-    uint32_t sb[kRowsPerGroup][2];
+  // the rows' places in the pools, in elements and (scales) bytes
+  int64_t ko[kInFlight], vo[kInFlight], kso[kInFlight], vso[kInFlight];
 #pragma unroll
-    for (int r = 0; r < kRowsPerGroup; ++r) {
-      const Slot s = slots[tok[r] - t0];
-      live[r] = live[r] && s.page >= 0;
+  for (int r = 0; r < kInFlight; ++r) {
+    const Slot s = slots[live[r] ? r * kGroups + grp : 0];
+    live[r] = live[r] && s.page >= 0;
+    const int64_t page = live[r] ? s.page : 0;
+    ko[r] = page * a.cache.k_stride[0] + head * a.cache.k_stride[1] + s.slot * a.cache.k_stride[2];
+    vo[r] = page * a.cache.v_stride[0] + head * a.cache.v_stride[1] + s.slot * a.cache.v_stride[2];
+    kso[r] = page * a.cache.ks_stride[0] + head * a.cache.ks_stride[1] + s.slot;
+    vso[r] = page * a.cache.vs_stride[0] + head * a.cache.vs_stride[1] + s.slot;
+  }
+  if constexpr (kRead) {
+    uint2 c[kInFlight][2];
+    uint32_t sb[kInFlight][2];
+#pragma unroll
+    for (int r = 0; r < kInFlight; ++r) {
       if (!live[r]) continue;
-      const int64_t ko = s.page * ks[0] + head[r] * ks[1] + s.slot * ks[2];
-      const int64_t vo = s.page * vs[0] + head[r] * vs[1] + s.slot * vs[2];
       if constexpr (kE4m3) {
-        c[r][0] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.cache.k) + ko) + lane);
-        c[r][1] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.cache.v) + vo) + lane);
-        sb[r][0] = a.cache.ks[s.page * a.cache.ks_stride[0] + head[r] * a.cache.ks_stride[1] + s.slot];
-        sb[r][1] = a.cache.vs[s.page * a.cache.vs_stride[0] + head[r] * a.cache.vs_stride[1] + s.slot];
+        c[r][0] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.cache.k) + ko[r]) + lane);
+        c[r][1] = __ldcs(reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(a.cache.v) + vo[r]) + lane);
+        sb[r][0] = a.cache.ks[kso[r]];
+        sb[r][1] = a.cache.vs[vso[r]];
       } else {
-        x[r][0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.cache.k) + ko) + lane);
-        x[r][1] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.cache.v) + vo) + lane);
+        x[r][0] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.cache.k) + ko[r]) + lane);
+        x[r][1] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.cache.v) + vo[r]) + lane);
       }
     }
 #pragma unroll
-    for (int r = 0; r < kRowsPerGroup; ++r) {
+    for (int r = 0; r < kInFlight; ++r) {
       if (!live[r]) continue;
-      uint16_t* k = static_cast<uint16_t*>(a.k) + tok[r] * a.k_stride[0] + head[r] * a.k_stride[1];
-      uint16_t* v = static_cast<uint16_t*>(a.v) + tok[r] * a.v_stride[0] + head[r] * a.v_stride[1];
       if constexpr (kE4m3) {
         x[r][0] = load_e4m3(c[r][0], sb[r][0]);
         x[r][1] = load_e4m3(c[r][1], sb[r][1]);
       }
-      __stcs(reinterpret_cast<uint4*>(k) + lane, x[r][0]);
-      __stcs(reinterpret_cast<uint4*>(v) + lane, x[r][1]);
+      const int64_t t = t0 + r * kGroups + grp;
+      __stcs(reinterpret_cast<uint4*>(k + t * a.k_stride[0]), x[r][0]);
+      __stcs(reinterpret_cast<uint4*>(v + t * a.v_stride[0]), x[r][1]);
     }
   } else {
 #pragma unroll
-    for (int r = 0; r < kRowsPerGroup; ++r) {
-      const Slot s = slots[tok[r] - t0];
-      live[r] = live[r] && s.page >= 0;
-      const int64_t page = live[r] ? s.page : 0;
-      const int64_t ko = page * ks[0] + head[r] * ks[1] + s.slot * ks[2];
-      const int64_t vo = page * vs[0] + head[r] * vs[1] + s.slot * vs[2];
+    for (int r = 0; r < kInFlight; ++r) {
       if constexpr (kE4m3) {
-        store_e4m3(x[r][0], static_cast<uint8_t*>(a.cache.k) + ko,
-                   a.cache.ks + page * a.cache.ks_stride[0] + head[r] * a.cache.ks_stride[1] + s.slot, lane, live[r]);
-        store_e4m3(x[r][1], static_cast<uint8_t*>(a.cache.v) + vo,
-                   a.cache.vs + page * a.cache.vs_stride[0] + head[r] * a.cache.vs_stride[1] + s.slot, lane, live[r]);
+        store_e4m3(x[r][0], static_cast<uint8_t*>(a.cache.k) + ko[r], a.cache.ks + kso[r], lane, live[r]);
+        store_e4m3(x[r][1], static_cast<uint8_t*>(a.cache.v) + vo[r], a.cache.vs + vso[r], lane, live[r]);
       } else if (live[r]) {
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.cache.k) + ko)[lane] = x[r][0];
-        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.cache.v) + vo)[lane] = x[r][1];
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.cache.k) + ko[r])[lane] = x[r][0];
+        reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.cache.v) + vo[r])[lane] = x[r][1];
       }
     }
   }
@@ -207,8 +204,8 @@ __global__ void __launch_bounds__(kKvThreads) kv_rows_kernel(const __grid_consta
 
 template <bool kRead>
 cudaError_t launch_rows(const KvRows& a) {
-  const int64_t rows = a.tokens * a.cache.heads;
-  const unsigned grid = static_cast<unsigned>((rows + kRowsPerBlock - 1) / kRowsPerBlock);
+  constexpr int kBlockTokens = kGroups * kInFlightRows<kRead>;
+  const unsigned grid = static_cast<unsigned>((a.tokens + kBlockTokens - 1) / kBlockTokens * a.cache.heads);
   if (a.cache.e4m3)
     kv_rows_kernel<true, kRead><<<grid, kKvThreads, 0, a.stream>>>(a);
   else
