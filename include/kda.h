@@ -350,7 +350,8 @@ kda_status kda_combine_pairs(const float* M, const float* S_tilde, int n_pairs, 
  *   page_size     16, 32, 64 or 128 tokens
  *   dtype         KDA_KV_BF16: the rows as they are, no scales.
  *                 KDA_KV_E4M3: 8-bit floats with one power-of-two scale per row (token and
- *                 head): the row's values are code * 2^(byte - 127); byte 255 marks a row of NaN.
+ *                 head): the row's values are code * 2^(byte - 127); byte 255, with codes of 0,
+ *                 marks a row of NaN.
  *   k_scale, v_scale  E4M3 only: scale bytes, logically [n_pages][n_kv_heads][page_size], with
  *                 strides *_scale_stride of the first two dimensions (positive multiples of
  *                 16; the last contiguous), bases 16-byte aligned.
