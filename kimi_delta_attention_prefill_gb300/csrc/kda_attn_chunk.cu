@@ -44,19 +44,22 @@ constexpr int kTile = 128;
 constexpr int kRows = 256;
 constexpr int kPanel = kTile * 128;     // 64 channels of 128 rows, 16-bit
 constexpr int kSlot = 2 * kPanel;       // one tile of K or V (or 128 rows of Q) as 16-bit values
-constexpr int kStage = kTile * 128 + 8 * 128;  // a tile of codes and a 128-byte slot of scale bytes per page
+constexpr int kStage = kTile * 128;     // a tile of codes
 constexpr int kMinTiles = 2, kItemCost = 5;
 
 template <bool kE4m3>
 struct Cfg {
-  static constexpr int kSlots = kE4m3 ? 3 : 5;
-  static constexpr int kStages = kE4m3 ? 3 : 0;
+  // Four slots are as good as five; with three the next keys' slot is free only once the last P V
+  // has read it, and both wait (2.0 ms against 2.7 ms over 30 K keys).
+  static constexpr int kSlots = kE4m3 ? 4 : 5;
+  static constexpr int kStages = kE4m3 ? 2 : 0;
   static constexpr int kSmQ = 0;
   static constexpr int kSmKV = 2 * kSlot;
   static constexpr int kSmStage = kSmKV + kSlots * kSlot;
-  static constexpr int kSmVec = kSmStage + kStages * kStage;          // [2 tiles][2^ek, ev][128] floats (wide tiles)
-  static constexpr int kSmExp = kSmVec + (kE4m3 ? 2 * 2 * 512 : 0);   // [2 items][256] query row scales
-  static constexpr int kSmBytes = kSmExp + (kE4m3 ? 2048 : 0) + 1024;
+  static constexpr int kSmScale = kSmStage + kStages * kStage;         // [stages][128] scale bytes
+  static constexpr int kSmVec = kSmScale + kStages * kTile;            // [2 tiles][keys, values][128] scale bytes (wide tiles)
+  static constexpr int kSmExp = kSmVec + (kE4m3 ? 2 * 2 * kTile : 0);  // [2 items][256] query rows' exponents (int8)
+  static constexpr int kSmBytes = kSmExp + (kE4m3 ? 2 * kRows : 0) + 1024;
 };
 
 // E4M3: what the f16 tiles of a key tile were scaled by (see convert_group).
@@ -69,7 +72,7 @@ struct TileScale {
 struct Bars {
   uint64_t full[5], empty[5];      // slots of K / V tiles
   uint64_t v_ask, v_ok;            // bf16: an edge tile's values are there / have been looked through
-  uint64_t st_full[3], st_empty[3];  // stages of codes
+  uint64_t st_full[2], st_empty[2];  // stages of codes
   uint64_t q_full, q_empty;
   uint64_t s_full[2], p_full[2][2], pv_done[2], o_full[2];
   uint64_t turn[2];                // the product warps' turns
@@ -131,26 +134,37 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
         }
       }
       const int slot = j0 & (a.cache.page_size - 1);
+      const int pages = __popc(__ballot_sync(0xffffffffu, page >= 0));
 #pragma unroll
       for (int kv = 0; kv < 2; ++kv, ++n) {
-          const uint32_t s = n % kRing;
-          if (n >= kRing && !bar_wait(&empty[s], (n / kRing - 1) & 1)) {
-            report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
-            return;
+        const uint32_t s = n % kRing;
+        if (n >= kRing && !bar_wait(&empty[s], (n / kRing - 1) & 1)) {
+          report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+          return;
+        }
+        if constexpr (kE4m3) {
+          if (blk < n_blk && page < 0) {  // no page: scale bytes of 0
+            uint32_t* sc = reinterpret_cast<uint32_t*>(sm + C::kSmScale + s * kTile + blk * P);
+            for (int e = 0; e < P / 4; ++e) sc[e] = 0;
+            fence_proxy_async_smem();
           }
-          if (lane == 0) mbar_arrive_expect_tx(&full[s], kE4m3 ? kTile * 128 + kTile : kSlot);
           __syncwarp();
-          if (blk < n_blk) {
-            if constexpr (kE4m3) {
-              uint8_t* st = sm + C::kSmStage + s * kStage;
-              tma_load_4d(st + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, head, page);
-              tma_load_3d(st + kTile * 128 + blk * 128, kv ? &p.tvs : &p.tks, &full[s], slot, head, page);
-            } else {
-              uint8_t* st = sm + C::kSmKV + s * kSlot;
-              tma_load_5d(st + panel * kPanel + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, panel, head, page);
-            }
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&full[s], kE4m3 ? kStage + pages * P : kSlot);
+        __syncwarp();
+        if (blk < n_blk) {
+          if constexpr (kE4m3) {
+            tma_load_4d(sm + C::kSmStage + s * kStage + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, head, page);
+            const int64_t* st = kv ? a.cache.vs_stride : a.cache.ks_stride;
+            if (page >= 0)
+              bulk_load(sm + C::kSmScale + s * kTile + blk * P, (kv ? a.cache.vs : a.cache.ks) + page * st[0] + head * st[1] + slot,
+                        P, &full[s]);
+          } else {
+            uint8_t* st = sm + C::kSmKV + s * kSlot;
+            tma_load_5d(st + panel * kPanel + blk * P * 128, kv ? &p.tv : &p.tk, &full[s], 0, slot, panel, head, page);
           }
         }
+      }
     }
     more = walk.next();
   }
@@ -319,7 +333,7 @@ __device__ void load_queries(const AttnArgs& a, const Job& w, uint8_t* sm, Bars&
           for (int off = 8; off; off >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
           const int e = query_exponent(top);
           const float inv = a.scale_log2 < 0.f ? -pow2i(-e) : pow2i(-e);
-          if (sub == 0) reinterpret_cast<float*>(sm + C::kSmExp)[(items & 1) * kRows + r] = pow2i(e);
+          if (sub == 0) reinterpret_cast<int8_t*>(sm + C::kSmExp)[(items & 1) * kRows + r] = static_cast<int8_t>(e);
           auto half = [&](uint32_t v) { return pack_half2(__uint_as_float(v << 16) * inv, __uint_as_float(v & 0xffff0000u) * inv); };
           x = make_uint4(half(x.x), half(x.y), half(x.z), half(x.w));
         } else if (a.scale_log2 < 0.f) {
@@ -391,8 +405,6 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
   using C = Cfg<true>;
   const AttnArgs& a = p.a;
   const int lane = tid & 31, warp = tid >> 5;
-  const int p_log = min(a.cache.page_log2, 7);
-  const int sc_at = kTile * 128 + (tid >> p_log) * 128 + (tid & ((1 << p_log) - 1));
   uint32_t n = 0, items = 0;
   bool dead = false;
   JobFeed feed{b.jobs, dead};
@@ -401,17 +413,20 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
     load_queries<true>(a, w, sm, b, tid, items++, dead);
     const int begin = w.begin, end = w.end;
     for (int i = begin; i < end; ++i) {
-        const int keys = w.p_last + 1 - w.tile(i) * kTile;  // those of the tile that are not past the last position
-        const bool past = tid >= keys, edge = edge_tile(a, w.tile(i), w.p_first, w.p_last);
+      const int keys = w.p_last + 1 - w.tile(i) * kTile;  // those of the tile that are not past the last position
+      const bool past = tid >= keys, edge = edge_tile(a, w.tile(i), w.p_first, w.p_last);
+      float k_scale = 1.f;
+      int k_wide = 0, k_byte = 127;
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++n) {
+      for (int kv = 0; kv < 2; ++kv, ++n) {
         const uint32_t st = n % C::kStages, s = n % C::kSlots;
         if (!dead && !bar_wait(&b.st_full[st], (n / C::kStages) & 1)) dead = true;
         const uint8_t* src = sm + C::kSmStage + st * kStage;
         uint4 c[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) c[k] = *reinterpret_cast<const uint4*>(src + sw128(tid, 16 * k));
-        const uint32_t byte = src[sc_at];
+        const uint8_t* scales = sm + C::kSmScale + st * kTile;
+        const uint32_t byte = scales[tid];
         // A code of NaN matters here where some row does not see the key; elsewhere it makes its own way.
         uint32_t nan = 0;
         if (edge) {
@@ -422,12 +437,12 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
           }
         }
         // Every warp finds E and the lowest exponent of all 128 rows by itself, four scale bytes a lane.
-        // NaN rows and rows past the last position do not count, nor do rows of zeros (they have the
-        // least scale): those of the least scale are looked into where that decides.
+        // NaN rows and rows past the last position do not count, nor need rows of zeros, which have the
+        // least scale: rows of that scale are looked into where they decide whether the tile is wide.
         int top, low;
         {
           const int key = 4 * lane;
-          uint32_t four = *reinterpret_cast<const uint32_t*>(src + kTile * 128 + (key >> p_log) * 128 + (key & ((1 << p_log) - 1)));
+          uint32_t four = *reinterpret_cast<const uint32_t*>(scales + key);
           int hi4 = 0, lo4 = 1000;
           uint32_t least = 0;
 #pragma unroll
@@ -440,7 +455,9 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
           }
           top = __reduce_max_sync(0xffffffffu, hi4);
           low = __reduce_min_sync(0xffffffffu, lo4);
-          if (top - 15 > kLeast) {
+          if (top - 15 <= kLeast) {
+            if (__any_sync(0xffffffffu, least != 0)) low = kLeast;
+          } else {
             uint32_t lanes = __ballot_sync(0xffffffffu, least != 0);
             while (lanes) {  // a warp's work on four keys at a time
               const int from = __ffs(lanes) - 1;
@@ -462,22 +479,22 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
         if (n >= C::kSlots && !dead && !bar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) dead = true;
         if (kv && lane == 0) b.bad[s][warp] = bad_keys;
         const bool wide = low < top - 15;
-        TileScale& ts = b.tile[(n >> 1) & 1];
-        if (tid == 0) {
-          if (kv) {
-            ts.v = wide ? 0.f : static_cast<float>(top);
-            ts.wide_v = wide;
-          } else {
-            ts.k = wide ? 1.f : pow2i(top);
-            ts.wide_k = wide;
-          }
-        }
-        float* vec = reinterpret_cast<float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
         const int e = static_cast<int>(byte) - 127;
         const bool counts = !past && byte != 255 && e >= low;
-        // per-key scales, for a tile that is wide in either way: those of the side that is not are in the tile
-        if (kv) vec[128 + tid] = wide ? static_cast<float>(counts ? e : low) : 0.f;  // a zero row must not raise m
-        else vec[tid] = wide && counts ? pow2i(e) : 1.f;
+        // What the softmax needs of both is written with the values, for whose slot P V of the
+        // tile before last has been waited: until then it may still read the words' last tile.
+        // Per-key scales, for a tile that is wide in either way: those of the side that is not are in
+        // the tile (127: 1), and a zero row's must not raise m.
+        if (kv) {
+          if (tid == 0) b.tile[(n >> 1) & 1] = TileScale{k_scale, wide ? 0.f : static_cast<float>(top), k_wide, wide};
+          uint8_t* vec = sm + C::kSmVec + ((n >> 1) & 1) * 256;
+          vec[tid] = k_byte;
+          vec[128 + tid] = wide ? (counts ? byte : low + 127) : 127;
+        } else {
+          k_scale = wide ? 1.f : pow2i(top);
+          k_wide = wide;
+          k_byte = wide && counts ? byte : 127;
+        }
         // the row's factor as an f16 pair; NaN for a key row that holds one
         const int r = wide || !counts ? 0 : e - top;
         __half2 f = __half2half2(__ushort_as_half(static_cast<unsigned short>(r >= -14 ? (15 + r) << 10 : 1 << (24 + r))));
@@ -573,7 +590,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       float u = crow, off = 0.f;
       int wide = 0;
       if constexpr (kE4m3) {
-        if (i == begin) crow = scale * reinterpret_cast<const float*>(sm + C::kSmExp)[(seen & 1) * kRows + 128 * t + tid];
+        if (i == begin) crow = scale * pow2i(reinterpret_cast<const int8_t*>(sm + C::kSmExp)[(seen & 1) * kRows + 128 * t + tid]);
         wait(&b.full[sv], (n + 1) / C::kSlots);  // the value scales come with the values
         const TileScale& sc = b.tile[(n >> 1) & 1];
         u = crow * sc.k;
@@ -583,7 +600,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       }
       // ---- in edge and wide tiles, the scores in place first: y of the codes, key by key, after which
       // u = 1 and off = 0; hidden ones -inf.  Rolled: the code is cold whenever it runs.
-      const float* vec = reinterpret_cast<const float*>(sm + C::kSmVec) + ((n >> 1) & 1) * 256;
+      const uint8_t* vec = sm + C::kSmVec + ((n >> 1) & 1) * 256;
       const float v_off = off;
       if (edge || (kE4m3 && wide)) {
 #pragma unroll 1
@@ -592,7 +609,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
           tmem_ld16(ts + c, x);
           if (kE4m3 && wide) {
 #pragma unroll
-            for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e] * vec[c + e], u, vec[128 + c + e] + off);
+            for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e] * scale_value(vec[c + e]), u, scale_exponent(vec[128 + c + e]) + off);
           }
           if (edge) {
             const int first = kt * kTile + c;
@@ -660,7 +677,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
           float y[16];
           tmem_ld16(ts + c, y);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) l += exp2_fast(y[e] - vec[128 + c + e] - v_off - ref);
+          for (int e = 0; e < 16; ++e) l += exp2_fast(y[e] - scale_exponent(vec[128 + c + e]) - v_off - ref);
         }
       }
       const uint64_t u2 = f32x2(u, u), nb2 = f32x2(off - ref, off - ref);
@@ -741,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_chunk_kernel(const __grid_co
       mbar_init(&b.full[i], kE4m3 ? 4 : 1);
       mbar_init(&b.empty[i], 2);
     }
-    for (int i = 0; i < 3; ++i) { mbar_init(&b.st_full[i], 1); mbar_init(&b.st_empty[i], 4); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&b.st_full[i], 1); mbar_init(&b.st_empty[i], 4); }
     mbar_init(&b.v_ask, 2);
     mbar_init(&b.v_ok, 4);
     mbar_init(&b.q_full, 4);

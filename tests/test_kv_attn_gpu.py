@@ -337,6 +337,26 @@ def test_prefill_scales_far_apart(where, spread):
         check(o, lse, reference(c, torch.split(q, new), new, lens, window, sink, D ** -0.5))
 
 
+@pytest.mark.parametrize("decode", [False, True])
+def test_rows_at_the_least_scale(decode):
+    """Keys and values so small that their scales are the least one, or a few steps above it."""
+    g = gen(41)
+
+    def values(n, i, x):
+        return x * torch.where(torch.rand(x.shape[0], 1, 1, generator=g) < 0.3, 2.0 ** -30, 2.0 ** -37).to(x.dtype)
+
+    lens = [333, 70]
+    c = Cache(lens, 2, 64, True, g, values=values)
+    n = [1, 1] if decode else [150, 70]
+    q = (torch.randn(sum(n), 4, D, generator=g) * 2.0 ** 30).to(torch.bfloat16)
+    if decode:
+        o, lse = run_decode(c, q.cuda()[:, None], lens)
+        o, lse = o[:, 0], lse[:, 0]
+    else:
+        o, lse = run_prefill(c, q.cuda(), n, lens)
+    check(o, lse, reference(c, torch.split(q, n), n, lens, 0, 0, D ** -0.5))
+
+
 def test_scores_of_any_size():
     """Rows whose scores spread over hundreds, all very negative or very positive."""
     g = gen(14)
