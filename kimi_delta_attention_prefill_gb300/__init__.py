@@ -586,11 +586,12 @@ _BF16, _E4M3, _I32 = torch.bfloat16, torch.float8_e4m3fn, torch.int32
 _pack_cache = struct.Struct("4q 3q 3q 2q 2q q 3i 4x").pack  # kda_kv_cache
 _pack2, _pack3 = struct.Struct("2q").pack, struct.Struct("3q").pack
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_of(stream):
     if stream is None and _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_current_device())
     return _stream_handle(stream)
 
 
@@ -613,8 +614,13 @@ def _sound(shape, strides):
     """Strides of all dimensions but the last.  torch gives dimensions of extent 1 (and those of
     empty tensors) any stride; the library wants a sound one."""
     lead = shape[:-1]
-    if 1 not in lead and 0 not in lead:
+    for s in strides[:-1]:
+        if s <= 0 or s & 15:
+            break
+    else:
         return strides[:-1]
+    if 1 not in lead and 0 not in lead:
+        return strides[:-1]  # the library says what is wrong with them
     packed = [1] * len(shape)
     for i in range(len(shape) - 2, -1, -1):
         packed[i] = packed[i + 1] * max(shape[i + 1], 1)
@@ -682,16 +688,13 @@ def _kv_cache(k_pool, v_pool, k_scale, v_scale):
         _say_cache(k_pool, v_pool, k_scale, v_scale)
         shape, dtype, ks, vs = k_pool.shape, k_pool.dtype, k_pool.stride(), v_pool.stride()
         if dtype is _E4M3:
-            kss, vss = k_scale.stride(), v_scale.stride()
+            lead, kss, vss = shape[:3], k_scale.stride(), v_scale.stride()
     ks, vs = _sound(shape, ks), _sound(shape, vs)
     n, heads, page, _ = shape
     if dtype is _E4M3:
-        three = shape[:3]
-        c = _pack_cache(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *ks, *vs,
-                        *_sound(three, kss), *_sound(three, vss), n, heads, page, 1)
-    else:
-        c = _pack_cache(k_pool.data_ptr(), v_pool.data_ptr(), 0, 0, *ks, *vs, 0, 0, 0, 0, n, heads, page, 0)
-    return c, heads
+        return _pack_cache(k_pool.data_ptr(), v_pool.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), *ks, *vs,
+                           *_sound(lead, kss), *_sound(lead, vss), n, heads, page, 1), heads
+    return _pack_cache(k_pool.data_ptr(), v_pool.data_ptr(), 0, 0, *ks, *vs, 0, 0, 0, 0, n, heads, page, 0), heads
 
 
 def _index(t, name, shape):
@@ -706,6 +709,12 @@ def _index(t, name, shape):
 
 
 def _page_table(page_table):
+    try:
+        shape = page_table.shape
+        if len(shape) == 2 and page_table.dtype is _I32 and page_table.is_cuda and page_table.is_contiguous():
+            return shape
+    except AttributeError:
+        pass
     _need(page_table, "page_table", _I32)
     if page_table.dim() != 2:
         raise ValueError(f"page_table must have shape [sequences, pages], got {tuple(page_table.shape)}")
