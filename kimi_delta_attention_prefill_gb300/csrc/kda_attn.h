@@ -147,8 +147,9 @@ cudaError_t launch_attn_plan(const AttnArgs& a, const AttnSplit& s, int rows, in
 cudaError_t launch_attn_join(const AttnArgs& a, const AttnSplit& s);
 // Tensor maps of the cache, one box per (page, kv head): min(page_size, tile) tokens, bf16 rows
 // in `panels` (1 or 2) panels of 64 channels.
-bool make_cache_maps(const KvCache& c, int tile, int panels, struct CUtensorMap_st* k, struct CUtensorMap_st* v,
-                     struct CUtensorMap_st* ks, struct CUtensorMap_st* vs);
+bool make_cache_maps(const KvCache& c, int tile, int panels, struct CUtensorMap_st* k, struct CUtensorMap_st* v);
+// The same of an e4m3 cache's scale bytes.
+bool make_scale_maps(const KvCache& c, int tile, struct CUtensorMap_st* ks, struct CUtensorMap_st* vs);
 
 // The key tiles (of `tile` keys) that rows at positions p_first .. p_last have to visit: the
 // tiles [0, sink) of the first tokens, then [lo, hi) up to the last visible key.

@@ -203,11 +203,12 @@ size_t up256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
-bool make_cache_maps(const KvCache& c, int tile, int panels, CUtensorMap* k, CUtensorMap* v, CUtensorMap* ks,
-                     CUtensorMap* vs) {
-  if (!encode_fn()) return false;
-  if (!rows_map(k, c.k, c.k_stride, c, tile, panels) || !rows_map(v, c.v, c.v_stride, c, tile, panels)) return false;
-  return !c.e4m3 || (scale_map(ks, c.ks, c.ks_stride, c, tile) && scale_map(vs, c.vs, c.vs_stride, c, tile));
+bool make_cache_maps(const KvCache& c, int tile, int panels, CUtensorMap* k, CUtensorMap* v) {
+  return encode_fn() && rows_map(k, c.k, c.k_stride, c, tile, panels) && rows_map(v, c.v, c.v_stride, c, tile, panels);
+}
+
+bool make_scale_maps(const KvCache& c, int tile, CUtensorMap* ks, CUtensorMap* vs) {
+  return encode_fn() && scale_map(ks, c.ks, c.ks_stride, c, tile) && scale_map(vs, c.vs, c.vs_stride, c, tile);
 }
 
 size_t attn_split_bytes(int grid, int part_rows, int64_t max_items) {
