@@ -60,7 +60,11 @@ struct Stage {
   static constexpr int kTotal = 2 * kBytes + 2 * kScales;
   static constexpr int kCount = 3;
 };
-constexpr int kItemCost = 1;
+// What an item costs besides its keys (queries, joining the warps, output), in tiles.  For 1 / 2 / 4 /
+// 6 / 8 / 12: 256 sequences of up to 8191 keys, 96 heads on 8, e4m3 389 / 369 / 343 / 346 / 352 /
+// 362 us; 64 sequences of 4 tokens, window 4096, bf16 173 / 165 / 163-165 / 159 / 163 / 163 us;
+// 37 sequences of up to 2000 keys, e4m3 - / - / 26.0 / 26.9 / 29.5 / 29.6 us.
+constexpr int kItemCost = 4;
 constexpr int kJoinBytes = 32 * 64 * 4 + 32 * 4 * 4;  // one warp's O and its (m, l) pairs
 template <bool kE4m3>
 constexpr int smem_bytes() {
