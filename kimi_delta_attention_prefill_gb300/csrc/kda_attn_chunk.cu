@@ -707,13 +707,16 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
           tmem_st16(ts + 64 * h + 16 * q, pk);
         }
         tmem_wait_st();
+        // The look through an edge tile's values must have been seen, and its words read, before the
+        // last weights are handed over: P V waits for them, and what follows it asks for the next edge
+        // tile's look, whose end is the next phase of the same barrier.
+        if (!kE4m3 && h == 0 && edge) {
+          wait(&b.v_ok, edges++);
+          poison();
+        }
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&b.p_full[t][h]);
-      }
-      if (!kE4m3 && edge) {  // P V waits for this too: the slot is not used again before
-        wait(&b.v_ok, edges++);
-        poison();
       }
       const float2 sums = unpack_f32x2(add_f32x2(sum, sum1));
       if (!kE4m3) l += sums.x + sums.y;
