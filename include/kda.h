@@ -469,6 +469,16 @@ kda_status kda_attn_decode_paged(const kda_bf16* q, const int64_t* q_stride, con
 void kda_debug_stall_next_prefill(int chunk);
 
 /*
+ * kda_debug_stall_next_attention -- the same for the attention cache's kernels (no counterpart
+ * on the pages): in the next kda_attn_prefill_paged or kda_attn_decode_paged call of this process
+ * each block leaves out the copy numbered `copy` of its share of the keys.  The waits for it run out
+ * after some seconds; the block's warps then leave in order, its other copies and products land, the
+ * tensor memory is released, and KDA_ERR_TIMEOUT is written to dev_status; that call's outputs
+ * are undefined.  Nothing faults or traps and the CUDA context stays usable.  One-shot.
+ */
+void kda_debug_stall_next_attention(int copy);
+
+/*
  * kda_prefill_noalloc -- kda_prefill for callers that cannot allocate device memory.
  *
  * This entry point has no counterpart on the pages; it exists for the library's users.

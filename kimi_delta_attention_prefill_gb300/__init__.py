@@ -99,6 +99,9 @@ def library():
             if hasattr(lib, "kda_debug_stall_next_prefill"):  # diagnostic hook (tests)
                 lib.kda_debug_stall_next_prefill.restype = None
                 lib.kda_debug_stall_next_prefill.argtypes = [_c_int]
+            if hasattr(lib, "kda_debug_stall_next_attention"):  # diagnostic hook (tests)
+                lib.kda_debug_stall_next_attention.restype = None
+                lib.kda_debug_stall_next_attention.argtypes = [_c_int]
             lib.kda_prefill_pairs.restype = _c_int
             lib.kda_prefill_pairs.argtypes = [_vp] * 6 + [_c_int, _c_i64, _vp, _vp, _c_int, _c_int, _vp, _vp]
             lib.kda_combine_pairs.restype = _c_int
@@ -481,6 +484,13 @@ def debug_stall_next_prefill(chunk):
     hand-off at ``chunk`` and gives up its waits after 4096 polls, so it reports
     KDA_ERR_TIMEOUT in ``dev_status`` without any fault."""
     library().kda_debug_stall_next_prefill(int(chunk))
+
+
+def debug_stall_next_attention(copy):
+    """Test hook (``kda_debug_stall_next_attention``): in the next attention call each block leaves
+    out one copy of its keys; the call reports KDA_ERR_TIMEOUT in ``dev_status`` after some
+    seconds, without any fault."""
+    library().kda_debug_stall_next_attention(int(copy))
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

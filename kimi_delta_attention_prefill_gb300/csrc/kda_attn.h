@@ -67,6 +67,7 @@ struct AttnArgs {
   float* lse = nullptr;
   void* workspace = nullptr;
   int* status = nullptr;
+  int stall = -1;  // test hook: the copy that each block leaves out
   cudaStream_t stream = nullptr;
 };
 size_t attn_prefill_workspace(int n_seq, int64_t tokens, int H, int kv_heads, int num_sms);

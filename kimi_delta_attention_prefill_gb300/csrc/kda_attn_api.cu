@@ -1,6 +1,7 @@
 // kda_attn_api.cu -- the attention cache's C entry points (include/kda.h): host-side
 // validation and launch.  Nothing here allocates or keeps anything between calls.
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -8,6 +9,8 @@
 #include "kda_attn.h"
 
 namespace {
+
+std::atomic<int> g_stall_copy{-1};  // kda_debug_stall_next_attention: consumed by the next attention launch
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -91,6 +94,7 @@ kda_status check_attn(const void* q, const int64_t* qs, int n_strides, const kda
   a->window = window >= most ? 0 : window;
   a->n_sink = static_cast<int>(n_sink < most ? n_sink : most);
   a->o = const_cast<void*>(o); a->lse = const_cast<float*>(lse); a->workspace = const_cast<void*>(workspace);
+  if (g_stall_copy.load(std::memory_order_relaxed) >= 0) a->stall = g_stall_copy.exchange(-1);
   return KDA_OK;
 }
 
@@ -181,5 +185,7 @@ kda_status kda_attn_decode_paged(const kda_bf16* q, const int64_t* q_stride, con
   a.status = dev_status; a.stream = stream;
   return kda::launch_attn_decode(a, sms) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
+
+void kda_debug_stall_next_attention(int copy) { g_stall_copy.store(copy < 0 ? -1 : copy); }
 
 }  // extern "C"

@@ -119,15 +119,18 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
   }
   uint32_t n = 0, k = 0;
   Walk walk(p.a, p.s);
-  bool more = walk.start(lane);
-  for (;; ++k) {
-    if (!b.jobs.put(k, walk, more, lane)) break;
+  bool more = walk.start(lane), ok = true;
+  for (; ok; ++k) {
+    if (!b.jobs.put(k, walk, more, lane)) {
+      ok = false;
+      break;
+    }
     const Item& w = walk.item;
-    if (!more) return;
+    if (!more) break;
     const int p_first = w.p_first(), p_last = w.p_last(), begin = walk.begin, end = walk.end, head = w.head;
     const int32_t* table = a.page_table + static_cast<int64_t>(w.seq) * a.max_pages;
     const KeyTiles kt = w.tiles;
-    for (int i = begin; i < end; ++i) {
+    for (int i = begin; ok && i < end; ++i) {
       const int j0 = kt.at(i) * kTile + blk * P;
       int page = -1;
       if (blk < n_blk && j0 <= p_last) {
@@ -144,9 +147,10 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const uint32_t s = n % kRing;
         if (n >= kRing && !bar_wait(&empty[s], (n / kRing - 1) & 1)) {
-          report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
-          return;
+          ok = false;
+          break;
         }
+        if (n == static_cast<uint32_t>(a.stall)) continue;
         if constexpr (kE4m3) {
           if (blk < n_blk && page < 0) {  // no page: scale bytes of 0
             uint32_t* sc = reinterpret_cast<uint32_t*>(sm + C::kSmScale + s * kTile + blk * P);
@@ -171,9 +175,10 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
         }
       }
     }
-    more = walk.next();
+    more = ok && walk.next();
   }
-  report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+  if (!ok) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+  drain_ring(full, kRing, n);
 }
 
 // -------------------------------------------------------------------------- products

@@ -142,10 +142,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
     ItemWalk<kRT, kTile> walk(p.a, p.s);
     bool more = walk.start(lane);
     uint32_t it = 0;
+    bool ok = true;
     const int blk = lane;
-    for (uint32_t k = 0;; ++k) {
-      if (!jobs.put(k, walk, more, lane)) break;
-      if (!more) return;
+    for (uint32_t k = 0; ok; ++k) {
+      if (!jobs.put(k, walk, more, lane)) {
+        ok = false;
+        break;
+      }
+      if (!more) break;
       const Item& w = walk.item;
       const KeyTiles kt = w.tiles;
       const int p_first = w.p_first(), p_last = w.p_last();
@@ -163,9 +167,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
         }
         const uint32_t s = it % St::kCount;
         if (it >= St::kCount && !bar_wait(&empty[s], ((it / St::kCount) - 1) & 1)) {
-          report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
-          return;
+          ok = false;
+          break;
         }
+        if (it == static_cast<uint32_t>(a.stall)) continue;
         if (lane == 0) mbar_arrive_expect_tx(&full[s], 2 * St::kBytes + (kE4m3 ? 2 * kTile : 0));
         __syncwarp();
         if (blk < n_blk) {
@@ -182,9 +187,10 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           }
         }
       }
-      more = walk.next();
+      more = ok && walk.next();
     }
-    report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+    if (!ok) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+    drain_ring(full, St::kCount, it);
     return;
   }
 
@@ -197,7 +203,11 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
   uint32_t it = 0;
   bool dead = false;
   JobFeed feed{jobs, dead};
-  while (const Job* jp = feed.next()) {
+  for (;;) {
+    const Job* jp = feed.next();
+    // The four warps leave together: one alone would be missing at the barriers among them.
+    dead = named_bar_any(1, kWarps * 32, dead);
+    if (dead || !jp) break;
     const Job& w = *jp;
     // this thread's rows g and g + 8 of the warp's 16: position, query fragments
     int pos[2];
