@@ -15,7 +15,8 @@ Functions mirror the C entry points: :func:`prefill` (``kda_prefill``, or
 :func:`attn_decode_paged` (``kda_attn_decode_paged``), the workspace-size queries, and
 :func:`status_string` (``kda_status_string``).  The cross-device split's exchange is in :mod:`.kcp`.  Tensors are torch CUDA tensors (pinned
 host tensors for :func:`prefill_host`); the launch goes to the current torch stream
-unless ``stream`` is given.
+unless ``stream`` is given.  Tensors that a call makes, outputs and workspaces, are made on the
+stream that it runs on.
 """
 from __future__ import annotations
 
@@ -147,6 +148,25 @@ def _stream_handle(stream):
     return s.cuda_stream
 
 
+def _scratch(n_bytes, device, stream):
+    """A workspace for one call, made on the stream that the call runs on: the allocator must not give
+    memory that another stream's work still uses, nor take it back before the call's kernels are done."""
+    if stream is None:
+        return torch.empty(n_bytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n_bytes, dtype=torch.uint8, device=device)
+
+
+def _output(shape, dtype, device, stream):
+    """A call's output, made as :func:`_scratch`; the caller's stream may use it as well."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
 def _need(t, name, dtype, shape=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -178,7 +198,7 @@ def decode(q, k, v, g, beta, S_state, n_commit=None, o=None, dev_status=None, st
     if n_commit is not None:
         _need(n_commit, "n_commit", torch.int32, (B,))
     if o is None:
-        o = torch.empty((B, n_tok, H, d), dtype=torch.float32, device=q.device)
+        o = _output((B, n_tok, H, d), torch.float32, q.device, stream)
     _need(o, "o", torch.float32, (B, n_tok, H, d))
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
@@ -218,7 +238,7 @@ def decode_fused(qp, kp, vp, conv_w, conv_cache, z, a_log, b, S_state, n_commit=
         if norm_weight is not None:
             _need(norm_weight, "norm_weight", torch.float32, (d,))
     if o is None:
-        o = torch.empty((B, n_tok, H, d), dtype=torch.float32, device=qp.device)
+        o = _output((B, n_tok, H, d), torch.float32, qp.device, stream)
     _need(o, "o", torch.float32, (B, n_tok, H, d))
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
@@ -267,17 +287,17 @@ def prefill(q, k, v, g, beta, cu_seqlens, S_in=None, ckpt_off=None, ckpt_pos=Non
         _need(ckpt_pos, "ckpt_pos", torch.int32)
         n_ckpt = ckpt_pos.shape[0]
         if ckpts is None:
-            ckpts = torch.empty((n_ckpt, H, d, d), dtype=torch.float32, device=q.device)
+            ckpts = _output((n_ckpt, H, d, d), torch.float32, q.device, stream)
         _need(ckpts, "ckpts", torch.float32, (n_ckpt, H, d, d))
     if o is None:
-        o = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        o = _output((T, H, d), torch.bfloat16, q.device, stream)
     _need(o, "o", torch.bfloat16, (T, H, d))
     if S_out is None:
-        S_out = torch.empty((n_seq, H, d, d), dtype=torch.float32, device=q.device)
+        S_out = _output((n_seq, H, d, d), torch.float32, q.device, stream)
     _need(S_out, "S_out", torch.float32, (n_seq, H, d, d))
     ws_need = prefill_workspace_size(n_seq, H, T, n_segments, d)
     if workspace is None and ws_need > 0:
-        workspace = torch.empty(ws_need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(ws_need, q.device, stream)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
@@ -349,7 +369,7 @@ def prefill_paged(q, k, v, g, beta, cu_seqlens, state_pool, s_in_page=None, s_ou
         n_ckpt = ckpt_pos.shape[0]
         _table(ckpt_page, "ckpt_page", n_ckpt * H)
     if o is None:
-        o = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        o = _output((T, H, d), torch.bfloat16, q.device, stream)
     _need(o, "o", torch.bfloat16, (T, H, d))
     if gate is not None:
         _need(gate, "gate", torch.bfloat16, q.shape)
@@ -357,7 +377,7 @@ def prefill_paged(q, k, v, g, beta, cu_seqlens, state_pool, s_in_page=None, s_ou
             _need(norm_weight, "norm_weight", torch.float32, (d,))
     if workspace is None:
         need = prefill_paged_workspace_size(n_seq, H, T, n_pages, n_segments, d)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _scratch(need, q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
@@ -395,10 +415,10 @@ def decode_paged(q, k, v, g, beta, state_pool, s_in_page, s_out_page=None, n_com
     if n_commit is not None:
         _need(n_commit, "n_commit", torch.int32, (B,))
     if o is None:
-        o = torch.empty((B, n_tok, H, d), dtype=torch.float32, device=q.device)
+        o = _output((B, n_tok, H, d), torch.float32, q.device, stream)
     _need(o, "o", torch.float32, (B, n_tok, H, d))
     if workspace is None:
-        workspace = torch.empty(decode_paged_workspace_size(n_pages), dtype=torch.uint8, device=q.device)
+        workspace = _scratch(decode_paged_workspace_size(n_pages), q.device, stream)
     ws_bytes = workspace.numel() * workspace.element_size()
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
@@ -466,8 +486,7 @@ def prefill_host(q, k, v, g, beta, cu_seqlens, S_in=None, o=None, S_out=None, bl
     _host(S_out, "S_out", torch.float32, (n_seq, H, d, d))
     dev = torch.device("cuda", torch.cuda.current_device()) if stream is None else stream.device
     if workspace is None:
-        workspace = torch.empty(prefill_host_workspace_size(n_seq, H, T, block_tokens, d), dtype=torch.uint8,
-                                device=dev)
+        workspace = _scratch(prefill_host_workspace_size(n_seq, H, T, block_tokens, d), dev, stream)
     _need(workspace, "workspace", torch.uint8)
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
@@ -521,13 +540,13 @@ def prefill_noalloc(q, k, v, g, beta, cu_seqlens, S_in=None, ckpt_off=None, ckpt
         _need(ckpt_pos, "ckpt_pos", torch.int32)
         n_ckpt = ckpt_pos.shape[0]
         if ckpts is None:
-            ckpts = torch.empty((n_ckpt, H, d, d), dtype=torch.float32, device=q.device)
+            ckpts = _output((n_ckpt, H, d, d), torch.float32, q.device, stream)
         _need(ckpts, "ckpts", torch.float32, (n_ckpt, H, d, d))
     if o is None:
-        o = torch.empty((T, H, d), dtype=torch.bfloat16, device=q.device)
+        o = _output((T, H, d), torch.bfloat16, q.device, stream)
     _need(o, "o", torch.bfloat16, (T, H, d))
     if S_out is None:
-        S_out = torch.empty((n_seq, H, d, d), dtype=torch.float32, device=q.device)
+        S_out = _output((n_seq, H, d, d), torch.float32, q.device, stream)
     _need(S_out, "S_out", torch.float32, (n_seq, H, d, d))
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
@@ -553,9 +572,9 @@ def prefill_pairs(q, k, v, g, beta, cu_seqlens, M=None, S_tilde=None, dev_status
     _need(cu_seqlens, "cu_seqlens", torch.int32)
     n_seq = cu_seqlens.shape[0] - 1
     if M is None:
-        M = torch.empty((n_seq, H, d, d), dtype=torch.float32, device=q.device)
+        M = _output((n_seq, H, d, d), torch.float32, q.device, stream)
     if S_tilde is None:
-        S_tilde = torch.empty((n_seq, H, d, d), dtype=torch.float32, device=q.device)
+        S_tilde = _output((n_seq, H, d, d), torch.float32, q.device, stream)
     _need(M, "M", torch.float32, (n_seq, H, d, d))
     _need(S_tilde, "S_tilde", torch.float32, (n_seq, H, d, d))
     if dev_status is not None:
@@ -579,7 +598,7 @@ def combine_pairs(M, S_tilde, S_in=None, entry=None, stream=None):
     if S_in is not None:
         _need(S_in, "S_in", torch.float32, (n_seq, H, d, d))
     if entry is None:
-        entry = torch.empty((n_seq, H, d, d), dtype=torch.float32, device=M.device)
+        entry = _output((n_seq, H, d, d), torch.float32, M.device, stream)
     _need(entry, "entry", torch.float32, (n_seq, H, d, d))
     st = library().kda_combine_pairs(_ptr(M) if R else None, _ptr(S_tilde) if R else None, R, _ptr(S_in),
                                      _ptr(entry), n_seq, H, d, _stream_handle(stream))
@@ -772,8 +791,8 @@ def kv_read(k_pool, v_pool, page_table, cu_seqlens, kv_start, total_tokens, k_sc
     n_seq, max_pages = _page_table(page_table)
     T = int(total_tokens)
     shape = (T, heads, HEAD_DIM)
-    k = torch.empty(shape, dtype=_BF16, device=k_pool.device) if k is None else _need(k, "k", _BF16, shape)
-    v = torch.empty(shape, dtype=_BF16, device=k_pool.device) if v is None else _need(v, "v", _BF16, shape)
+    k = _output(shape, _BF16, k_pool.device, stream) if k is None else _need(k, "k", _BF16, shape)
+    v = _output(shape, _BF16, k_pool.device, stream) if v is None else _need(v, "v", _BF16, shape)
     st = (_lib or library()).kda_kv_read(
         c, k.data_ptr(), v.data_ptr(), page_table.data_ptr(), n_seq, max_pages,
         _index(cu_seqlens, "cu_seqlens", (n_seq + 1,)), _index(kv_start, "kv_start", (n_seq,)), T, HEAD_DIM,
@@ -791,12 +810,12 @@ def attn_decode_workspace_size(B, n_tok, H, n_kv_heads, d=HEAD_DIM) -> int:
     return int(library().kda_attn_decode_workspace_size(int(B), int(n_tok), int(H), int(n_kv_heads), int(d)))
 
 
-def _attn_outputs(q, shape, o, lse, return_lse):
-    o = torch.empty(shape, dtype=_BF16, device=q.device) if o is None else _need(o, "o", _BF16, shape)
+def _attn_outputs(q, shape, o, lse, return_lse, stream):
+    o = _output(shape, _BF16, q.device, stream) if o is None else _need(o, "o", _BF16, shape)
     if lse is not None:
         _need(lse, "lse", torch.float32, shape[:-1])
     elif return_lse:
-        lse = torch.empty(shape[:-1], dtype=torch.float32, device=q.device)
+        lse = _output(shape[:-1], torch.float32, q.device, stream)
     return o, lse
 
 
@@ -819,11 +838,10 @@ def attn_prefill_paged(q, k_pool, v_pool, page_table, cu_seqlens, kv_len, k_scal
     shape = q.shape
     T, H, _ = shape
     qs = _rows_of(q, "q", (T, H))
-    o, lse = _attn_outputs(q, shape, o, lse, return_lse)
+    o, lse = _attn_outputs(q, shape, o, lse, return_lse, stream)
     lib = _lib or library()
     if workspace is None:
-        workspace = torch.empty(lib.kda_attn_prefill_workspace_size(n_seq, T, H, heads, HEAD_DIM), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _scratch(lib.kda_attn_prefill_workspace_size(n_seq, T, H, heads, HEAD_DIM), q.device, stream)
     st = lib.kda_attn_prefill_paged(
         q.data_ptr(), _pack2(*qs), c, page_table.data_ptr(), n_seq, max_pages,
         _index(cu_seqlens, "cu_seqlens", (n_seq + 1,)), _index(kv_len, "kv_len", (n_seq,)), T, H, HEAD_DIM,
@@ -851,11 +869,10 @@ def attn_decode_paged(q, k_pool, v_pool, page_table, kv_len, k_scale=None, v_sca
     qs = _rows_of(q, "q", (B, n_tok, H))
     if B != n_seq:
         raise ValueError(f"page_table must have {B} rows, got {n_seq}")
-    o, lse = _attn_outputs(q, shape, o, lse, return_lse)
+    o, lse = _attn_outputs(q, shape, o, lse, return_lse, stream)
     lib = _lib or library()
     if workspace is None:
-        workspace = torch.empty(lib.kda_attn_decode_workspace_size(B, n_tok, H, heads, HEAD_DIM), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _scratch(lib.kda_attn_decode_workspace_size(B, n_tok, H, heads, HEAD_DIM), q.device, stream)
     st = lib.kda_attn_decode_paged(
         q.data_ptr(), _pack3(*qs), c, page_table.data_ptr(), B, n_tok, max_pages, _index(kv_len, "kv_len", (B,)), H,
         HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else scale, window, n_sink, o.data_ptr(),
