@@ -58,7 +58,7 @@ __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;"
 // order.  Kept small: where it stands in a rarely fetched loop, its code is what it costs.
 // By a whole warp, whose lanes decide together: a wait that runs out while the barrier flips must
 // not send some lanes on and some away, warp-wide instructions coming after it.  (On one GPU with
-// and without the vote: a prompt of 8192 1205 and 1210 us, 2048 tokens over 30 K e4m3 keys 2545 and
+// and without the vote: a prompt of 8192 1197 and 1210 us, 2048 tokens over 30 K e4m3 keys 2544 and
 // 2499 us.  A vote only where a warp's way is decided: 1226 and 2515 us.)
 __device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
