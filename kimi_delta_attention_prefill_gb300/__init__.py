@@ -157,6 +157,19 @@ def _scratch(n_bytes, device, stream):
         return torch.empty(n_bytes, dtype=torch.uint8, device=device)
 
 
+def _workspace(t):
+    """Address and bytes of a workspace given by the caller (None: none)."""
+    if t is None:
+        return None, 0
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("workspace must be a CUDA tensor")
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _output(shape, dtype, device, stream):
     """A call's output, made as :func:`_scratch`; the caller's stream may use it as well."""
     if stream is None:
@@ -298,13 +311,13 @@ def prefill(q, k, v, g, beta, cu_seqlens, S_in=None, ckpt_off=None, ckpt_pos=Non
     ws_need = prefill_workspace_size(n_seq, H, T, n_segments, d)
     if workspace is None and ws_need > 0:
         workspace = _scratch(ws_need, q.device, stream)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    ws, ws_bytes = _workspace(workspace)
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
     if gate is None:
         st = library().kda_prefill(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(S_in), _ptr(cu_seqlens),
                                    n_seq, T, _ptr(ckpt_off), _ptr(ckpt_pos), n_ckpt, _ptr(o), _ptr(S_out),
-                                   _ptr(ckpts), H, d, int(n_segments), _ptr(workspace), ws_bytes, _ptr(dev_status),
+                                   _ptr(ckpts), H, d, int(n_segments), ws, ws_bytes, _ptr(dev_status),
                                    _stream_handle(stream))
         if st != 0:
             raise KdaError(st, "kda_prefill")
@@ -315,7 +328,7 @@ def prefill(q, k, v, g, beta, cu_seqlens, S_in=None, ckpt_off=None, ckpt_pos=Non
     st = library().kda_prefill_gated(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(gate), _ptr(norm_weight),
                                      float(eps), _ptr(S_in), _ptr(cu_seqlens), n_seq, T, _ptr(ckpt_off),
                                      _ptr(ckpt_pos), n_ckpt, _ptr(o), _ptr(S_out), _ptr(ckpts), H, d,
-                                     int(n_segments), _ptr(workspace), ws_bytes, _ptr(dev_status),
+                                     int(n_segments), ws, ws_bytes, _ptr(dev_status),
                                      _stream_handle(stream))
     if st != 0:
         raise KdaError(st, "kda_prefill_gated")
@@ -378,13 +391,13 @@ def prefill_paged(q, k, v, g, beta, cu_seqlens, state_pool, s_in_page=None, s_ou
     if workspace is None:
         need = prefill_paged_workspace_size(n_seq, H, T, n_pages, n_segments, d)
         workspace = _scratch(need, q.device, stream)
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws, ws_bytes = _workspace(workspace)
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
     st = library().kda_prefill_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(gate), _ptr(norm_weight),
                                      float(eps), _ptr(state_pool), n_pages, _ptr(s_in_page), _ptr(s_out_page),
                                      _ptr(cu_seqlens), n_seq, T, _ptr(ckpt_off), _ptr(ckpt_pos), n_ckpt,
-                                     _ptr(ckpt_page), _ptr(o), H, d, int(n_segments), _ptr(workspace), ws_bytes,
+                                     _ptr(ckpt_page), _ptr(o), H, d, int(n_segments), ws, ws_bytes,
                                      _ptr(dev_status), _stream_handle(stream))
     if st != 0:
         raise KdaError(st, "kda_prefill_paged")
@@ -419,12 +432,12 @@ def decode_paged(q, k, v, g, beta, state_pool, s_in_page, s_out_page=None, n_com
     _need(o, "o", torch.float32, (B, n_tok, H, d))
     if workspace is None:
         workspace = _scratch(decode_paged_workspace_size(n_pages), q.device, stream)
-    ws_bytes = workspace.numel() * workspace.element_size()
+    ws, ws_bytes = _workspace(workspace)
     if dev_status is not None:
         _need(dev_status, "dev_status", torch.int32)
     st = library().kda_decode_paged(_ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(state_pool), n_pages,
                                     _ptr(s_in_page), _ptr(s_out_page), _ptr(n_commit), _ptr(o), B, n_tok, H, d,
-                                    _ptr(workspace), ws_bytes, _ptr(dev_status), _stream_handle(stream))
+                                    ws, ws_bytes, _ptr(dev_status), _stream_handle(stream))
     if st != 0:
         raise KdaError(st, "kda_decode_paged")
     return o
@@ -846,7 +859,7 @@ def attn_prefill_paged(q, k_pool, v_pool, page_table, cu_seqlens, kv_len, k_scal
         q.data_ptr(), _pack2(*qs), c, page_table.data_ptr(), n_seq, max_pages,
         _index(cu_seqlens, "cu_seqlens", (n_seq + 1,)), _index(kv_len, "kv_len", (n_seq,)), T, H, HEAD_DIM,
         HEAD_DIM ** -0.5 if scale is None else scale, window, n_sink, o.data_ptr(),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        None if lse is None else lse.data_ptr(), *_workspace(workspace),
         _status_ptr(dev_status), _stream_of(stream))
     if st != 0:
         raise KdaError(st, "kda_attn_prefill_paged")
@@ -876,7 +889,7 @@ def attn_decode_paged(q, k_pool, v_pool, page_table, kv_len, k_scale=None, v_sca
     st = lib.kda_attn_decode_paged(
         q.data_ptr(), _pack3(*qs), c, page_table.data_ptr(), B, n_tok, max_pages, _index(kv_len, "kv_len", (B,)), H,
         HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else scale, window, n_sink, o.data_ptr(),
-        None if lse is None else lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        None if lse is None else lse.data_ptr(), *_workspace(workspace),
         _status_ptr(dev_status), _stream_of(stream))
     if st != 0:
         raise KdaError(st, "kda_attn_decode_paged")

@@ -1,0 +1,35 @@
+"""Arguments that the binding must not pass on to the library as they are (no GPU needed): the library
+and the tensors' device are test_streams.py's stand-ins."""
+import pytest
+import torch
+
+import kimi_delta_attention_prefill_gb300 as kda
+from test_streams import F32, I32, dev, fakes  # noqa: F401 (fixture)
+
+
+def with_workspace():
+    rows, gates = [dev(5, 2, 128) for _ in range(3)], [dev(5, 2, 128, dtype=F32), dev(5, 2, dtype=F32)]
+    step = [t.unsqueeze(0)[:, :4] for t in rows + gates]
+    cu, table, one = dev(2, dtype=I32), dev(1, 4, dtype=I32), dev(1, dtype=I32)
+    pool, state = dev(8, 2, 16, 128), dev(2, 128, 128, dtype=F32)
+    return {
+        "prefill": lambda w: kda.prefill(*rows, *gates, cu, workspace=w),
+        "prefill_paged": lambda w: kda.prefill_paged(*rows, *gates, cu, state, workspace=w),
+        "decode_paged": lambda w: kda.decode_paged(*step, state, dev(2, dtype=I32), workspace=w),
+        "attn_prefill_paged": lambda w: kda.attn_prefill_paged(rows[0], pool, pool, table, cu, one, workspace=w),
+        "attn_decode_paged": lambda w: kda.attn_decode_paged(step[0], pool, pool, table, one, workspace=w),
+    }
+
+
+@pytest.mark.parametrize("name", sorted(with_workspace()))
+def test_workspace_on_the_host_or_in_pieces_is_refused(fakes, name):  # noqa: F811
+    """The kernels would write through a host address, or past the end of a strided tensor."""
+    call = with_workspace()[name]
+    call(dev(512, dtype=torch.uint8))
+    call(dev(64, dtype=torch.float64))  # any type, as bytes
+    with pytest.raises(ValueError, match="workspace must be a CUDA tensor"):
+        call(torch.zeros(512, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="workspace must be contiguous"):
+        call(dev(1024, dtype=torch.uint8)[::2])
+    with pytest.raises(TypeError, match="workspace"):
+        call(bytearray(512))
