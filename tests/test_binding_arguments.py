@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import kimi_delta_attention_prefill_gb300 as kda
-from test_streams import F32, I32, dev, fakes  # noqa: F401 (fixture)
+from test_streams import F32, I32, Stream, dev, fakes  # noqa: F401 (fixture)
 
 
 def with_workspace():
@@ -13,11 +13,11 @@ def with_workspace():
     cu, table, one = dev(2, dtype=I32), dev(1, 4, dtype=I32), dev(1, dtype=I32)
     pool, state = dev(8, 2, 16, 128), dev(2, 128, 128, dtype=F32)
     return {
-        "prefill": lambda w: kda.prefill(*rows, *gates, cu, workspace=w),
-        "prefill_paged": lambda w: kda.prefill_paged(*rows, *gates, cu, state, workspace=w),
-        "decode_paged": lambda w: kda.decode_paged(*step, state, dev(2, dtype=I32), workspace=w),
-        "attn_prefill_paged": lambda w: kda.attn_prefill_paged(rows[0], pool, pool, table, cu, one, workspace=w),
-        "attn_decode_paged": lambda w: kda.attn_decode_paged(step[0], pool, pool, table, one, workspace=w),
+        "prefill": lambda w: kda.prefill(*rows, *gates, cu, workspace=w, stream=Stream()),
+        "prefill_paged": lambda w: kda.prefill_paged(*rows, *gates, cu, state, workspace=w, stream=Stream()),
+        "decode_paged": lambda w: kda.decode_paged(*step, state, dev(2, dtype=I32), workspace=w, stream=Stream()),
+        "attn_prefill_paged": lambda w: kda.attn_prefill_paged(rows[0], pool, pool, table, cu, one, workspace=w, stream=Stream()),
+        "attn_decode_paged": lambda w: kda.attn_decode_paged(step[0], pool, pool, table, one, workspace=w, stream=Stream()),
     }
 
 
