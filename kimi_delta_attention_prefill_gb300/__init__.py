@@ -823,6 +823,12 @@ def attn_decode_workspace_size(B, n_tok, H, n_kv_heads, d=HEAD_DIM) -> int:
     return int(library().kda_attn_decode_workspace_size(int(B), int(n_tok), int(H), int(n_kv_heads), int(d)))
 
 
+def _c_count(n):
+    """A window or a number of tokens as the library's 32-bit int: more than fits is more than any
+    sequence has, and what is negative stays so."""
+    return max(-1, min(n, 0x7fffffff))
+
+
 def _attn_outputs(q, shape, o, lse, return_lse, stream):
     o = _output(shape, _BF16, q.device, stream) if o is None else _need(o, "o", _BF16, shape)
     if lse is not None:
@@ -858,7 +864,7 @@ def attn_prefill_paged(q, k_pool, v_pool, page_table, cu_seqlens, kv_len, k_scal
     st = lib.kda_attn_prefill_paged(
         q.data_ptr(), _pack2(*qs), c, page_table.data_ptr(), n_seq, max_pages,
         _index(cu_seqlens, "cu_seqlens", (n_seq + 1,)), _index(kv_len, "kv_len", (n_seq,)), T, H, HEAD_DIM,
-        HEAD_DIM ** -0.5 if scale is None else scale, window, n_sink, o.data_ptr(),
+        HEAD_DIM ** -0.5 if scale is None else scale, _c_count(window), _c_count(n_sink), o.data_ptr(),
         None if lse is None else lse.data_ptr(), *_workspace(workspace),
         _status_ptr(dev_status), _stream_of(stream))
     if st != 0:
@@ -888,7 +894,7 @@ def attn_decode_paged(q, k_pool, v_pool, page_table, kv_len, k_scale=None, v_sca
         workspace = _scratch(lib.kda_attn_decode_workspace_size(B, n_tok, H, heads, HEAD_DIM), q.device, stream)
     st = lib.kda_attn_decode_paged(
         q.data_ptr(), _pack3(*qs), c, page_table.data_ptr(), B, n_tok, max_pages, _index(kv_len, "kv_len", (B,)), H,
-        HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else scale, window, n_sink, o.data_ptr(),
+        HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else scale, _c_count(window), _c_count(n_sink), o.data_ptr(),
         None if lse is None else lse.data_ptr(), *_workspace(workspace),
         _status_ptr(dev_status), _stream_of(stream))
     if st != 0:

@@ -33,3 +33,19 @@ def test_workspace_on_the_host_or_in_pieces_is_refused(fakes, name):  # noqa: F8
         call(dev(1024, dtype=torch.uint8)[::2])
     with pytest.raises(TypeError, match="workspace"):
         call(bytearray(512))
+
+
+@pytest.mark.parametrize("name", ["attn_prefill_paged", "attn_decode_paged"])
+def test_window_and_first_tokens_past_32_bits(fakes, monkeypatch, name):  # noqa: F811
+    """A window wider than any sequence is no window, not what is left of its low 32 bits."""
+    got = []
+    entry = getattr(kda.library(), "kda_" + name)
+    lib = kda.library()
+    monkeypatch.setattr(type(lib), "kda_" + name, lambda self, *a: (got.append(a), entry(*a))[1], raising=False)
+    rows, table, one = dev(4, 2, 128), dev(1, 4, dtype=I32), dev(1, dtype=I32)
+    pool = dev(8, 2, 16, 128)
+    q, more = (rows, (dev(2, dtype=I32), one)) if "prefill" in name else (rows[None], (one,))
+    at = 12 if "prefill" in name else 11  # window, n_sink
+    for value, want in ((2 ** 31 - 1, 2 ** 31 - 1), (2 ** 32 + 5, 2 ** 31 - 1), (2 ** 40, 2 ** 31 - 1), (-1, -1), (-2 ** 32 + 5, -1), (7, 7)):
+        getattr(kda, name)(q, pool, pool, table, *more, window=value, n_sink=value, stream=Stream())
+        assert got[-1][at:at + 2] == (want, want)
