@@ -479,7 +479,7 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
               }
             }
           }
-          top -= 127;
+          top = top == 0 ? 0 : top - 127;  // none counts: any factor, but not 0 (hidden scores are -inf)
           low = min(low - 127, top);
         }
         __syncwarp();
@@ -606,7 +606,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
         if (i == begin) crow = scale * pow2i(reinterpret_cast<const int8_t*>(sm + C::kSmExp)[(seen & 1) * kRows + 128 * t + tid]);
         wait(&b.full[sv], (n + 1) / C::kSlots);  // the value scales come with the values
         const TileScale& sc = b.tile[(n >> 1) & 1];
-        u = crow * sc.k;
+        u = fminf(fmaxf(crow * sc.k, 0x1p-126f), 0x1.fp127f);  // hidden scores are -inf, zero keys' 0: neither may meet the other
         off = sc.v;
         wide = sc.wide_k | sc.wide_v;
         poison();
