@@ -351,7 +351,10 @@ kda_status kda_combine_pairs(const float* M, const float* S_tilde, int n_pairs, 
  *   dtype         KDA_KV_BF16: the rows as they are, no scales.
  *                 KDA_KV_E4M3: 8-bit floats with one power-of-two scale per row (token and
  *                 head): the row's values are code * 2^(byte - 127); byte 255, with codes of 0,
- *                 marks a row of NaN.
+ *                 marks a row of NaN.  kda_kv_append writes bytes 127 - 40 to 127 + 40.  A cache
+ *                 filled by others may hold bytes 127 - 80 to 127 + 80, rows of zeros too, with
+ *                 value scales within 2^100 of each other among the keys that a query sees
+ *                 (the sums are of 32 bits); kda_kv_read takes every byte.
  *   k_scale, v_scale  E4M3 only: scale bytes, logically [n_pages][n_kv_heads][page_size], with
  *                 strides *_scale_stride of the first two dimensions (positive multiples of
  *                 16; the last contiguous), bases 16-byte aligned.

@@ -775,7 +775,8 @@ def kv_append(k, v, k_pool, v_pool, page_table, cu_seqlens, kv_start, k_scale=No
     strided); k_pool, v_pool ``[n_pages, Hkv, page_size, 128]`` bf16 or float8_e4m3fn (any
     strides over the first three dimensions; page_size 16, 32, 64 or 128), with k_scale,
     v_scale ``[n_pages, Hkv, page_size]`` uint8 for float8_e4m3fn: a row's values are
-    ``code * 2**(scale - 127)``, scale 255 marks a row of NaN.  page_table ``[N, max_pages]``
+    ``code * 2**(scale - 127)``, scale 255 marks a row of NaN (a cache filled by others: scales
+    47 to 207, see ``kda.h``).  page_table ``[N, max_pages]``
     int32 (-1: tokens there are not written); cu_seqlens ``[N + 1]``, kv_start ``[N]`` int32:
     row ``cu[i] + t`` becomes token ``kv_start[i] + t`` of sequence i.  Updates the pools (and
     scales) in place.

@@ -67,6 +67,8 @@ struct Cfg {
   static constexpr int kSmBytes = kSmExp + (kE4m3 ? 2 * kRows : 0) + 1024;
 };
 
+constexpr uint32_t kLeast = 127 - 40;  // the least scale byte that kda_kv_append writes; rows of zeros have it
+
 // E4M3: what the f16 tiles of a key tile were scaled by (see convert_group).
 struct TileScale {
   float k;        // 2^E of the keys
@@ -152,9 +154,9 @@ __device__ void load_warp(const ChunkParams& p, uint8_t* sm, Bars& b, int lane) 
         }
         if (n == static_cast<uint32_t>(a.stall)) continue;
         if constexpr (kE4m3) {
-          if (blk < n_blk && page < 0) {  // no page: scale bytes of 0
+          if (blk < n_blk && page < 0) {  // no page: rows of zeros, as they are kept
             uint32_t* sc = reinterpret_cast<uint32_t*>(sm + C::kSmScale + s * kTile + blk * P);
-            for (int e = 0; e < P / 4; ++e) sc[e] = 0;
+            for (int e = 0; e < P / 4; ++e) sc[e] = kLeast * 0x01010101u;
             fence_proxy_async_smem();
           }
           __syncwarp();
@@ -410,7 +412,6 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
 // (all-zero rows aside) the tile is "wide": its rows stay plain codes and the softmax takes every
 // key's scale by itself.  Rows past the last position, which may hold anything, become zeros; so
 // do value rows that hold a NaN, noted in bad[].
-constexpr int kLeast = 127 - 40;  // the least scale byte that is written
 __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
   using C = Cfg<true>;
   const AttnArgs& a = p.a;
@@ -448,25 +449,27 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
         }
         // Every warp finds E and the lowest exponent of all 128 rows by itself, four scale bytes a lane.
         // NaN rows and rows past the last position do not count, nor need rows of zeros, which have the
-        // least scale: rows of that scale are looked into where they decide whether the tile is wide.
+        // least scale: rows of that scale or below (others than kda_kv_append may have filled the
+        // cache) are looked into where they decide whether the tile is wide.
         int top, low;
         {
           const int key = 4 * lane;
           uint32_t four = *reinterpret_cast<const uint32_t*>(scales + key);
-          int hi4 = 0, lo4 = 1000;
+          int hi4 = 0, lo4 = 1000, few4 = 1000;
           uint32_t least = 0;
 #pragma unroll
           for (int q = 0; q < 4; ++q, four >>= 8) {
             const int v = four & 255u;
-            const bool in = v != 255 && key + q < keys;
+            const bool in = v != 255 && key + q < keys, few = v <= static_cast<int>(kLeast);
             hi4 = in ? max(hi4, v) : hi4;
-            if (in && v > kLeast) lo4 = min(lo4, v);
-            least |= in && v <= kLeast ? 1u << q : 0u;
+            if (in && !few) lo4 = min(lo4, v);
+            if (in && few) few4 = min(few4, v);
+            least |= in && few ? 1u << q : 0u;
           }
           top = __reduce_max_sync(0xffffffffu, hi4);
           low = __reduce_min_sync(0xffffffffu, lo4);
-          if (top - 15 <= kLeast) {
-            if (__any_sync(0xffffffffu, least != 0)) low = kLeast;
+          if (top - 15 <= static_cast<int>(kLeast)) {
+            low = min(low, __reduce_min_sync(0xffffffffu, few4));
           } else {
             uint32_t lanes = __ballot_sync(0xffffffffu, least != 0);
             while (lanes) {  // a warp's work on four keys at a time
@@ -475,7 +478,8 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
               const uint32_t which = __shfl_sync(0xffffffffu, least, from);
               for (int q = 0; q < 4; ++q) {
                 const uint32_t part = *reinterpret_cast<const uint32_t*>(src + (4 * from + q) * 128 + 4 * lane);
-                if ((which >> q) & 1 && __any_sync(0xffffffffu, (part & 0x7f7f7f7fu) != 0)) low = kLeast;
+                if ((which >> q) & 1 && __any_sync(0xffffffffu, (part & 0x7f7f7f7fu) != 0))
+                  low = min(low, static_cast<int>(scales[4 * from + q]));
               }
             }
           }

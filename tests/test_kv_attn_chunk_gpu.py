@@ -8,7 +8,7 @@ import pytest
 import torch
 
 from kv_attn_util import D, Cache, attention, check
-from test_kv_attn_gpu import gen, reference, run_prefill
+from test_kv_attn_gpu import gen, reference, run_decode, run_prefill
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +82,39 @@ def test_scores_too_small_to_tell_apart(fp8):
     q = (torch.randn(200, 8, D, generator=g) * 2.0 ** -100).to(torch.bfloat16)
     o, lse = run_prefill(c, q.cuda(), new, lens, scale=2.0 ** -120)
     check(o, lse, reference(c, [q], new, lens, 0, 0, 2.0 ** -120))
+
+
+@pytest.mark.parametrize("kernel", ["many rows", "few rows", "decode"])
+@pytest.mark.parametrize("k_down,v_down", [([50], [50]), ([0, 47], [0]), ([0], [0, 45, 62]), ([40, 47, 50, 57], [40, 41]), ([-55], [-55, -20])])
+def test_scales_that_others_write(kernel, k_down, v_down):
+    """Scale bytes below and above those that kda_kv_append writes, alone and next to ordinary ones, rows of zeros among them."""
+    g = gen(len(k_down) + 10 * len(v_down))
+    new = [150, 130]
+    lens = [400, 130]
+
+    def values(n, i, x):
+        x[3::11] = 0
+        return x
+
+    c = Cache(lens, 2, 32, True, g, values=values, max_pages=wide(32) if kernel == "many rows" else None)
+    for n, down in (("k", k_down), ("v", v_down)):
+        byte = c.scales[n + "_scale"].cpu()
+        for i, t in enumerate(lens):  # the rows' scales go down, a choice by row and head
+            by = torch.tensor(down)[torch.randint(len(down), (t, 2), generator=g)]
+            j = torch.arange(t)
+            page, slot = c.table[i].cpu().long()[j // 32], j % 32
+            byte[page, :, slot] = (byte[page, :, slot].long() - by).to(torch.uint8)
+            c.value[n][i] = c.value[n][i] * torch.exp2(-by.double())[..., None]
+        c.scales[n + "_scale"].copy_(byte)
+    q = (torch.randn(sum(new), 8, D, generator=g) * 2.0 ** (sum(k_down) / len(k_down))).to(torch.bfloat16)
+    if kernel == "decode":
+        q = q[:4]
+        o, lse = run_decode(c, q.view(2, 2, 8, D).cuda(), lens)
+        o, lse, new = o.flatten(0, 1), lse.flatten(0, 1), [2, 2]
+    elif kernel == "few rows":
+        new = [10, 5]
+        q = q[:15]
+        o, lse = run_prefill(c, q.cuda(), new, lens)
+    else:
+        o, lse = run_prefill(c, q.cuda(), new, lens)
+    check(o, lse, reference(c, torch.split(q, new), new, lens, 0, 0, D ** -0.5))
