@@ -17,9 +17,8 @@
 // into f16 tiles (exact).  The tensor core runs P V and the next Q K^T of one tile while the
 // other tile is in its softmax.
 //
-// The maximum is lazy: O is rescaled only when a row's maximum has grown by more than 2^32
-// (bf16 weights) or 2^8 (f16 weights) since the last time, which random rows do in their first
-// tiles only.
+// The maximum is lazy: O is rescaled only when a row's maximum has grown by more than 2^8 since
+// the last time, which random rows do in their first tiles only.
 //
 // Work is split as in kda_attn_short.cu: equal shares of the line of key tiles, at most two
 // partial items a block, joined by attn_join_kernel.
@@ -551,12 +550,14 @@ template <bool kE4m3>
 __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t, int tid) {
   using C = Cfg<kE4m3>;
   const AttnArgs& a = p.a;
-  // A row's reference m follows its maximum only when that has grown by this much (log2): bf16
-  // weights have fp32's range and may grow far, f16 weights end at 2^16.  With 8 for bf16 as well a
-  // prompt of 8192 takes 1230 us instead of 1162, 2048 tokens over 30 K keys 2069 instead of 2017;
-  // the price is that a dominating key's weight is then rarely a power of two, so it is rounded
-  // (2^-8): error against 64 bits 2.29e-3 instead of 2.07e-3 (norm), o's own rounding included.
-  constexpr float kLazy = kE4m3 ? 8.f : 32.f;
+  // A row's reference m moves only when a score stands more than kMost (log2) above it, and then so
+  // that this score's weight is 2^kFresh.  No bf16 weight is above 1: the sums of values are no larger
+  // than with the maximum itself.  The price of moving late is that a dominating key's weight is then
+  // rarely a power of two, so it is rounded (2^-8).  bf16, kFresh -2 / -8 / -32: 8192 tokens 1395 /
+  // 1264 / 1198 us, under a window of 1024 695 / 690 / 633 us, 2048 tokens over 30 K keys 2218 / 2118 /
+  // 2055 us; error of 8192 tokens against 64 bits in the norm 1.80e-3 / 2.07e-3 / 2.29e-3 (with weights
+  // of 32 bits 1.66e-3, most of it o's own rounding).
+  constexpr float kFresh = kE4m3 ? 0.f : -8.f, kMost = kE4m3 ? 8.f : 0.f;
   const int lane = tid & 31;
   const uint32_t tl = static_cast<uint32_t>(tid & 96) << 16;
   const uint32_t ts = tl + 128 * t, to = tl + 256 + 128 * t;
@@ -668,10 +669,10 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
         mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
       }
       const float top = fmaf(mx, u, off);
-      const bool grow = top - m > kLazy;  // also from -inf to anything; never for nothing visible
+      const bool grow = top - m > kMost;  // also from -inf to anything; never for nothing visible
       if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? exp2_fast(m - top) : 1.f;
-        m = grow ? top : m;
+        const float f = grow ? exp2_fast(m - (top - kFresh)) : 1.f;
+        m = grow ? top - kFresh : m;
         l *= f;
         if (i > begin) {
           // The scores' barrier stands for every product issued before them, the last P V among them.

@@ -118,3 +118,25 @@ def test_scales_that_others_write(kernel, k_down, v_down):
     else:
         o, lse = run_prefill(c, q.cuda(), new, lens)
     check(o, lse, reference(c, torch.split(q, new), new, lens, 0, 0, D ** -0.5))
+
+
+@pytest.mark.parametrize("exponent", [119, 100, 0, -110])
+@pytest.mark.parametrize("rise", [5.0, 12.0, 40.0])
+def test_rising_scores_and_values_of_any_size(exponent, rise):
+    """Scores that rise along the keys, by tiles, with values near the ends of bf16's range."""
+    g = gen(exponent + 200)
+    new, lens = [140, 60], [1100, 700]
+
+    def values(n, i, x):
+        if n == "v":
+            return (x.clamp(-4, 4).float() * 2.0 ** exponent).to(torch.bfloat16)
+        x = x * 0.1
+        x[..., 0] = torch.linspace(-0.5, 0.5, x.shape[0])[:, None] * rise  # times the queries' first channel
+        return x
+
+    c = Cache(lens, 2, 64, False, g, values=values, max_pages=wide(64))
+    q = torch.randn(sum(new), 8, D, generator=g)
+    q[..., 0] = D ** 0.5
+    q = q.to(torch.bfloat16)
+    o, lse = run_prefill(c, q.cuda(), new, lens)
+    check(o, lse, reference(c, torch.split(q, new), new, lens, 0, 0, D ** -0.5))
