@@ -669,6 +669,24 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
         mx = fmaxf(mx, fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)));
       }
       const float top = fmaf(mx, u, off);
+      // Scores past 2^20: what a fused y - m keeps of the product beyond y's own 24 bits would grow to
+      // whole powers of two, beyond the weights' type.  There y is rounded first, in place, as m is.
+      // (The vote and its cold code cost 1 to 2 % of a prompt; remembering it from tile to tile instead
+      // cost as much.)
+      if (__any_sync(0xffffffffu, fabsf(top) > 0x1p20f && fabsf(top) < INFINITY)) {
+#pragma unroll 1
+        for (int c = 0; c < kTile; c += 16) {
+          float y[16];
+          tmem_ld16(ts + c, y);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) y[e] = fmaf(y[e], u, off);
+          tmem_st16(ts + c, y);
+        }
+        tmem_wait_st();
+        u = 1.f;
+        off = 0.f;
+        load(64);
+      }
       const bool grow = top - m > kMost;  // also from -inf to anything; never for nothing visible
       if (__any_sync(0xffffffffu, grow)) {
         const float f = grow ? exp2_fast(m - (top - kFresh)) : 1.f;
@@ -730,7 +748,7 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       }
       const float2 sums = unpack_f32x2(add_f32x2(sum, sum1));
       if (!kE4m3) l += sums.x + sums.y;
-      else if (!wide) l = fmaf(sums.x + sums.y, exp2_fast(-off), l);
+      else if (!wide) l = fmaf(sums.x + sums.y, exp2_fast(-v_off), l);
     }
     // ---- the item's (or part's) rows
     wait(&b.o_full[t], items);

@@ -140,3 +140,24 @@ def test_rising_scores_and_values_of_any_size(exponent, rise):
     q = q.to(torch.bfloat16)
     o, lse = run_prefill(c, q.cuda(), new, lens)
     check(o, lse, reference(c, torch.split(q, new), new, lens, 0, 0, D ** -0.5))
+
+
+@pytest.mark.parametrize("kernel", ["many rows", "few rows", "decode"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("exponent", [18, 23, 26, 28, 30, 34, 50])
+def test_scores_far_beyond_what_32_bits_tell_apart(kernel, fp8, exponent):
+    """Scores of 2^20 to 2^53: whichever key wins, every result is finite and a mean of values."""
+    g = gen(exponent)
+    new, lens = [150, 70], [700, 70]
+    c = Cache(lens, 2, 64, fp8, g, max_pages=wide(64) if kernel == "many rows" else None)
+    q = (torch.randn(sum(new), 8, D, generator=g) * 2.0 ** exponent).to(torch.bfloat16)
+    if kernel == "decode":
+        q, new = q[:4], [2, 2]
+        o, lse = run_decode(c, q.view(2, 2, 8, D).cuda(), lens)
+        o, lse = o.flatten(0, 1), lse.flatten(0, 1)
+    elif kernel == "few rows":
+        q, new = q[:15], [10, 5]
+        o, lse = run_prefill(c, q.cuda(), new, lens)
+    else:
+        o, lse = run_prefill(c, q.cuda(), new, lens)
+    check(o, lse, reference(c, torch.split(q, new), new, lens, 0, 0, D ** -0.5))
