@@ -20,6 +20,11 @@
 // The maximum is lazy: O is rescaled only when a row's maximum has grown by more than 2^8 since
 // the last time, which random rows do in their first tiles only.
 //
+// What f16 weights (E4M3) lose: 2^-11 of themselves or, below 2^-14, 2^-25.  A new maximum of the scores
+// times the tile's largest value scale weighs 2^7, that scale being at most 2^8 above the one of
+// the row that has the maximum: 2^-25 is at most 2^-24 of the largest weight times value scale that a
+// query row sees.
+//
 // Work is split as in kda_attn_short.cu: equal shares of the line of key tiles, at most two
 // partial items a block, joined by attn_join_kernel.
 #include <cuda_runtime.h>
@@ -66,6 +71,7 @@ struct Cfg {
   static constexpr int kSmBytes = kSmExp + (kE4m3 ? 2 * kRows : 0) + 1024;
 };
 
+constexpr int kReach = 8;
 constexpr uint32_t kLeast = 127 - 40;  // the least scale byte that kda_kv_append writes; rows of zeros have it
 
 // E4M3: what the f16 tiles of a key tile were scaled by (see convert_group).
@@ -405,11 +411,15 @@ __device__ void query_warps(const ChunkParams& p, uint8_t* sm, Bars& b, int tid)
 
 // ------------------------------------------------------------------- codes to f16 tiles
 // Four warps, which also bring the queries; thread = key.  (Eight, four for the keys and four for
-// the values, were slower: 3.0 against 2.7 ms for 2048 tokens over 30 K keys, 96 heads on 8.)  With E the largest scale exponent of the tile's keys (values), a row becomes code * 2^(e - E) in
-// f16: exact for e >= E - 15 (codes go down to 2^-9, f16 to 2^-24), so that one factor 2^E serves
-// the whole tile and the softmax has no per-key work.  Where a row's scale lies further below
-// (all-zero rows aside) the tile is "wide": its rows stay plain codes and the softmax takes every
-// key's scale by itself.  Rows past the last position, which may hold anything, become zeros; so
+// the values, were slower: 3.0 against 2.7 ms for 2048 tokens over 30 K keys, 96 heads on 8.)  With E
+// the largest scale exponent of the tile's keys (values), a row becomes code * 2^(e - E) in f16: exact
+// for e >= E - 15 (codes go down to 2^-9, f16 to 2^-24), so that one factor 2^E serves the whole tile
+// and the softmax has no per-key work.  Where a row's scale lies below E - kReach (all-zero rows
+// aside) the tile is "wide": its rows stay plain codes and the softmax takes every key's scale by
+// itself.  kReach is less than 15 for the values' sake: their E stands in the reference of the f16
+// weights, whoever sees the row that has it.  (15 for the keys and 8 for the values, a register
+// more: 2698 us instead of 2600 for 2048 tokens over 30 K keys.)  Rows past the last position, which
+// may hold anything, become zeros; so
 // do value rows that hold a NaN, noted in bad[].
 __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int tid) {
   using C = Cfg<true>;
@@ -467,7 +477,7 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
           }
           top = __reduce_max_sync(0xffffffffu, hi4);
           low = __reduce_min_sync(0xffffffffu, lo4);
-          if (top - 15 <= static_cast<int>(kLeast)) {
+          if (top - kReach <= static_cast<int>(kLeast)) {
             low = min(low, __reduce_min_sync(0xffffffffu, few4));
           } else {
             uint32_t lanes = __ballot_sync(0xffffffffu, least != 0);
@@ -491,7 +501,7 @@ __device__ void convert_group(const ChunkParams& p, uint8_t* sm, Bars& b, int ti
         const uint32_t bad_keys = __ballot_sync(0xffffffffu, bad);
         if (n >= C::kSlots && !dead && !bar_wait(&b.empty[s], (n / C::kSlots - 1) & 1)) dead = true;
         if (kv && lane == 0) b.bad[s][warp] = bad_keys;
-        const bool wide = low < top - 15;
+        const bool wide = low < top - kReach;
         const int e = static_cast<int>(byte) - 127;
         const bool counts = !past && byte != 255 && e >= low;
         // What the softmax needs of both is written with the values, for whose slot P V of the
@@ -552,12 +562,13 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
   const AttnArgs& a = p.a;
   // A row's reference m moves only when a score stands more than kMost (log2) above it, and then so
   // that this score's weight is 2^kFresh.  No bf16 weight is above 1: the sums of values are no larger
-  // than with the maximum itself.  The price of moving late is that a dominating key's weight is then
+  // than with the maximum itself.  f16 weights end at 2^16 and lose bits below 2^-14, so they go up to
+  // 2^15: see the kernel's head for what is lost.  The price of moving late is that a dominating key's weight is then
   // rarely a power of two, so it is rounded (2^-8).  bf16, kFresh -2 / -8 / -32: 8192 tokens 1395 /
   // 1264 / 1198 us, under a window of 1024 695 / 690 / 633 us, 2048 tokens over 30 K keys 2218 / 2118 /
   // 2055 us; error of 8192 tokens against 64 bits in the norm 1.80e-3 / 2.07e-3 / 2.29e-3 (with weights
   // of 32 bits 1.66e-3, most of it o's own rounding).
-  constexpr float kFresh = kE4m3 ? 0.f : -8.f, kMost = kE4m3 ? 8.f : 0.f;
+  constexpr float kFresh = kE4m3 ? 7.f : -8.f, kMost = kE4m3 ? 15.f : 0.f;
   const int lane = tid & 31;
   const uint32_t tl = static_cast<uint32_t>(tid & 96) << 16;
   const uint32_t ts = tl + 128 * t, to = tl + 256 + 128 * t;
@@ -689,8 +700,9 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       }
       const bool grow = top - m > kMost;  // also from -inf to anything; never for nothing visible
       if (__any_sync(0xffffffffu, grow)) {
-        const float f = grow ? exp2_fast(m - (top - kFresh)) : 1.f;
-        m = grow ? top - kFresh : m;
+        const float to_m = kE4m3 ? __fadd_ru(top, -kFresh) : top - kFresh;  // never further below, however large
+        const float f = grow ? exp2_fast(m - to_m) : 1.f;
+        m = grow ? to_m : m;
         l *= f;
         if (i > begin) {
           // The scores' barrier stands for every product issued before them, the last P V among them.

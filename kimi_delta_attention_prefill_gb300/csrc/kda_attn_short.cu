@@ -4,9 +4,11 @@
 //     x_j = scale log2(e) q . k_j,   m' = max(m, max_j x_j),   l <- l 2^(m-m') + sum_j 2^(x_j-m'),
 //     O <- O 2^(m-m') + sum_j 2^(x_j-m') v_j,                  o = O / l,  lse = ln 2 (m + log2 l).
 // E4M3 rows stand for code * 2^e.  The key's scale multiplies x_j; the value's joins the
-// exponent, y_j = x_j + ev_j with m the maximum of the y_j, so P_j = 2^(y_j - m) <= 1 is
-// already the weight of the codes (exact in f16) and l sums P_j 2^-ev_j.  A large value row
-// therefore costs the others no precision, and nothing is rescaled tile by tile.
+// exponent, y_j = x_j + ev_j with m 14 below the maximum of the y_j, so P_j = 2^(y_j - m) <= 2^14 is
+// already the weight of the codes (exact in f16) and l sums P_j 2^-ev_j; nothing is rescaled tile
+// by tile.  P_j is rounded to f16: by 2^-11 of itself or, below 2^-14, by 2^-25, which is 2^-39 of the
+// largest weight times value scale that the row sees.  (With m the maximum itself that was 2^-25: next
+// to a value row 2^20 larger, however little attended, the others' weights had few bits left.)
 //
 // Bound by the cache's bytes: every key and value row is read once per (sequence, kv head),
 // whatever the number of query heads that share it.  The H / kv_heads query heads of a kv
@@ -65,6 +67,7 @@ struct Stage {
 // 362 us; 64 sequences of 4 tokens, window 4096, bf16 173 / 165 / 163-165 / 159 / 163 / 163 us;
 // 37 sequences of up to 2000 keys, e4m3 - / - / 26.0 / 26.9 / 29.5 / 29.6 us.
 constexpr int kItemCost = 4;
+constexpr float kAbove = 14.f;  // e4m3: log2 of the largest weight
 constexpr int kJoinBytes = 32 * 64 * 4 + 32 * 4 * 4;  // one warp's O and its (m, l) pairs
 template <bool kE4m3>
 constexpr int smem_bytes() {
@@ -375,6 +378,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
         for (int n = 0; n < kNT; ++n) mx = fmaxf(mx, fmaxf(x[n][2 * r], x[n][2 * r + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if constexpr (kE4m3) mx = __fadd_ru(mx, -kAbove);  // never further below, however large
         const float mn = fmaxf(m[r], mx);
         base[r] = mn == -INFINITY ? 0.f : mn;
         corr[r] = exp2_fast(m[r] - base[r]);

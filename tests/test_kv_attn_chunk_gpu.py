@@ -7,7 +7,7 @@ import math
 import pytest
 import torch
 
-from kv_attn_util import D, Cache, attention, check
+from kv_attn_util import D, Cache, attention, check, visible
 from test_kv_attn_gpu import gen, reference, run_decode, run_prefill
 
 pytestmark = pytest.mark.gpu
@@ -161,3 +161,64 @@ def test_scores_far_beyond_what_32_bits_tell_apart(kernel, fp8, exponent):
     else:
         o, lse = run_prefill(c, q.cuda(), new, lens)
     check(o, lse, reference(c, torch.split(q, new), new, lens, 0, 0, D ** -0.5))
+
+
+def e4m3_bounds(c, i, q, see, loss):
+    """The bounds of kv_attn_util.attention with the f16 weights' own term: a weight times 2^ev is off by
+    2^-11 of itself or by `loss` of the largest that the row sees."""
+    k, v = c.value["k"][i], c.value["v"][i]
+    total, Hkv = k.shape[:2]
+    ro, rl, bo, bl = attention(q, k, v, see, D ** -0.5, True)
+    j = torch.arange(total)
+    byte = c.scales["v_scale"].cpu()[c.table[i].cpu().long()[j // c.page], :, j % c.page].long()
+    size = torch.exp2(byte.double() - 127)  # [total, Hkv]
+    for h in range(q.shape[1]):
+        kh, vh, ev = k[:, h * Hkv // q.shape[1]], v[:, h * Hkv // q.shape[1]], size[:, h * Hkv // q.shape[1]]
+        qh = q[:, h].double()
+        x = torch.where(see, qh @ kh.T * D ** -0.5, -math.inf)
+        w = torch.exp(x - torch.logsumexp(x, 1)[:, None])
+        dx = 136 * 2.0 ** -24 * (qh.abs() @ kh.abs().T * D ** -0.5).amax(1) + 8 * 2.0 ** -24 * x.masked_fill(~see, 0).abs().amax(1)
+        rel = 2 * dx + 2.0 ** -20 + 2 * total * 2.0 ** -24 + 2.0 ** -11
+        codes = torch.where(see[:, :, None], (vh / ev[:, None]).abs(), 0.0).sum(1)
+        bo[:, h] = 2.0 ** -8 * ro[:, h].abs() + 1.01 * rel[:, None] * (w @ vh.abs()) + loss * (w * ev).amax(1)[:, None] * codes
+    return ro, rl, bo, bl
+
+
+@pytest.mark.parametrize("kernel", ["many rows", "few rows", "decode"])
+@pytest.mark.parametrize("above,score", [(7, -12), (8, -12), (9, -12), (12, -12), (14, -12), (15, -12), (16, -12), (24, -12), (24, -1)])
+def test_one_large_value_row(kernel, above, score):
+    """A value row 2^above times the others', in one channel, that hardly any row attends to, and one
+    that stands behind the queries of its tile.  A key that takes most of the weight is zero in half of
+    the channels, which are then those of 1500 ordinary keys with some 2^-13 of its weight each."""
+    g = gen(above)
+    new, lens = [300], [1500]
+
+    def values(n, i, x):
+        x = x / x.abs().amax(-1, keepdim=True)  # a scale for all
+        if n == "k":
+            x[:, :, 0] = 0
+            for j, s in ((3, 9.0), (70, score), (1390, 0.0)):
+                x[j] = 0
+                x[j, :, 0] = s  # times the queries' first channel
+        else:
+            x[3, :, 64:] = 0
+            for j in (70, 1390):
+                x[j] = 0
+                x[j, :, 3] = 2.0 ** above
+        return x
+
+    c = Cache(lens, 2, 64, True, g, values=values, max_pages=wide(64) if kernel == "many rows" else None)
+    q = torch.randn(300, 4, D, generator=g)
+    q[..., 0] = D ** 0.5
+    q = q.to(torch.bfloat16)
+    if kernel == "decode":
+        q, new = q[:3], [3]
+        o, lse = run_decode(c, q[None].cuda(), lens)
+        o, lse = o[0], lse[0]
+    elif kernel == "few rows":
+        q, new = q[:20], [20]
+        o, lse = run_prefill(c, q.cuda(), new, lens)
+    else:
+        o, lse = run_prefill(c, q.cuda(), new, lens)
+    see = visible(new[0], lens[0], 0, 0)
+    check(o, lse, e4m3_bounds(c, 0, q, see, 2.0 ** -24 if kernel == "many rows" else 2.0 ** -39))
