@@ -395,9 +395,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_short_kernel(const __grid_co
           // weights rounded once, to the values' type: f16 2^-11, bf16 2^-8 at most; l keeps 32 bits
           if constexpr (kE4m3) {
             float r0 = rv[n][0], r1 = rv[n][1];
-            if (edge) {  // a hidden key's scale may be that of a NaN row; its weight is 0 whatever it says
-              r0 = p0 == 0.f ? 0.f : r0;
-              r1 = p1 == 0.f ? 0.f : r1;
+            if (edge) {  // a hidden key's scale may be that of a NaN row; that of a visible one counts, however small its weight
+              r0 = x[n][2 * r] == -INFINITY ? 0.f : r0;
+              r1 = x[n][2 * r + 1] == -INFINITY ? 0.f : r1;
             }
             l[r] = fmaf(p0, r0, fmaf(p1, r1, l[r]));
             pf[n][r] = pack_half2(p0, p1);

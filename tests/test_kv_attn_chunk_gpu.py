@@ -222,3 +222,43 @@ def test_one_large_value_row(kernel, above, score):
         o, lse = run_prefill(c, q.cuda(), new, lens)
     see = visible(new[0], lens[0], 0, 0)
     check(o, lse, e4m3_bounds(c, 0, q, see, 2.0 ** -24 if kernel == "many rows" else 2.0 ** -39))
+
+
+@pytest.mark.parametrize("kernel", ["many rows", "few rows", "decode"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("score", [-10.0, -150.0, -400.0])
+@pytest.mark.parametrize("at", [40, 995])
+def test_nan_values_of_keys_without_weight(kernel, fp8, score, at):
+    """A NaN value row makes the rows that see it NaN, however small its weight; in a tile that all rows
+    see and in the last one."""
+    g = gen(at)
+    new, lens = [130], [1000]
+
+    def values(n, i, x):
+        if n == "k":
+            x[:, :, 0] = 0
+            x[at] = 0
+            x[at, :, 0] = score  # times the queries' first channel
+        else:
+            x[at, :, 9] = math.nan
+        return x
+
+    c = Cache(lens, 2, 64, fp8, g, values=values, max_pages=wide(64) if kernel == "many rows" else None)
+    q = torch.randn(130, 8, D, generator=g)
+    q[..., 0] = D ** 0.5
+    q = q.to(torch.bfloat16)
+    if kernel == "decode":
+        q, new = q[:4], [4]
+        o, lse = run_decode(c, q[None].cuda(), lens)
+        o, lse = o[0], lse[0]
+    elif kernel == "few rows":
+        q, new = q[:12], [12]
+        o, lse = run_prefill(c, q.cuda(), new, lens)
+    else:
+        o, lse = run_prefill(c, q.cuda(), new, lens)
+    ro, rl, bo, bl = reference(c, torch.split(q, new), new, lens, 0, 0, D ** -0.5)
+    bad = torch.isnan(ro).any(-1)
+    assert bad.any() and (at == 40 or kernel == "decode" or not bad.all())
+    lse[bad.cuda()] = 0
+    rl[bad] = 0
+    check(o, lse, (ro, rl, bo, bl))
