@@ -482,6 +482,13 @@ void kda_debug_stall_next_prefill(int chunk);
 void kda_debug_stall_next_attention(int copy);
 
 /*
+ * kda_debug_attention_kernel -- which kernel a kda_attn_prefill_paged call takes (no counterpart on
+ * the pages), for tests that are written for one of them: 1 the tensor-core kernel, 0 the
+ * warp-level one, -1 bad sizes.  most_keys is max_pages * page_size.
+ */
+int kda_debug_attention_kernel(int n_seq, int64_t total_tokens, int H, int n_kv_heads, int64_t most_keys);
+
+/*
  * kda_prefill_noalloc -- kda_prefill for callers that cannot allocate device memory.
  *
  * This entry point has no counterpart on the pages; it exists for the library's users.

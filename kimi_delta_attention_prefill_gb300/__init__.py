@@ -103,6 +103,8 @@ def library():
             if hasattr(lib, "kda_debug_stall_next_attention"):  # diagnostic hook (tests)
                 lib.kda_debug_stall_next_attention.restype = None
                 lib.kda_debug_stall_next_attention.argtypes = [_c_int]
+                lib.kda_debug_attention_kernel.restype = _c_int
+                lib.kda_debug_attention_kernel.argtypes = [_c_int, _c_i64, _c_int, _c_int, _c_i64]
             lib.kda_prefill_pairs.restype = _c_int
             lib.kda_prefill_pairs.argtypes = [_vp] * 6 + [_c_int, _c_i64, _vp, _vp, _c_int, _c_int, _vp, _vp]
             lib.kda_combine_pairs.restype = _c_int
@@ -523,6 +525,12 @@ def debug_stall_next_attention(copy):
     out one copy of its keys; the call reports KDA_ERR_TIMEOUT in ``dev_status`` after some
     seconds, without any fault."""
     library().kda_debug_stall_next_attention(int(copy))
+
+
+def debug_attention_kernel(n_seq, total_tokens, H, n_kv_heads, most_keys) -> int:
+    """Which kernel an :func:`attn_prefill_paged` call takes (``kda_debug_attention_kernel``): 1 the
+    tensor-core kernel, 0 the warp-level one.  ``most_keys`` is the page table's width in tokens."""
+    return int(library().kda_debug_attention_kernel(int(n_seq), int(total_tokens), int(H), int(n_kv_heads), int(most_keys)))
 
 
 NOALLOC_SCRATCH_BYTES = 32 << 20

@@ -74,6 +74,8 @@ size_t attn_prefill_workspace(int n_seq, int64_t tokens, int H, int kv_heads, in
 size_t attn_decode_workspace(int n_seq, int n_tok, int H, int kv_heads, int num_sms);
 cudaError_t launch_attn_prefill(const AttnArgs& a, int num_sms);
 cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms);
+// Whether a chunk of so many tokens, over tables with room for most_keys, is the short kernel's.
+bool attn_short_chunks(int n_seq, int64_t tokens, int H, int kv_heads, int64_t most_keys);
 
 // Many rows a sequence: kda_attn_chunk.cu.
 size_t attn_chunk_workspace(int n_seq, int64_t tokens, int group, int num_sms);

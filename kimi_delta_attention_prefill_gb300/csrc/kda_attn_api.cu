@@ -186,6 +186,11 @@ kda_status kda_attn_decode_paged(const kda_bf16* q, const int64_t* q_stride, con
   return kda::launch_attn_decode(a, sms) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
+int kda_debug_attention_kernel(int n_seq, int64_t total_tokens, int H, int n_kv_heads, int64_t most_keys) {
+  if (n_seq < 0 || total_tokens < 0 || H < 1 || n_kv_heads < 1 || H % n_kv_heads != 0 || most_keys < 0) return -1;
+  return kda::attn_short_chunks(n_seq, total_tokens, H, n_kv_heads, most_keys) ? 0 : 1;
+}
+
 void kda_debug_stall_next_attention(int copy) { g_stall_copy.store(copy < 0 ? -1 : copy); }
 
 }  // extern "C"

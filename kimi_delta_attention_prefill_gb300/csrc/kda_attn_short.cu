@@ -592,13 +592,10 @@ cudaError_t launch_attn_decode(const AttnArgs& a, int num_sms) {
 // way to its first product counts: 77 tokens of 3 sequences over 1500 keys, 16 heads on 2: 25 us
 // here, 37 us there; but 128 tokens of 8 sequences over 8000 keys, 96 heads on 8: 96 us here,
 // 63 us there.  The work is bounded by the page table's width, the lengths being on the device.
-namespace {
-bool short_chunks(const AttnArgs& a) {
-  const int group = a.H / a.cache.heads;
-  if (a.tokens * group <= static_cast<int64_t>(kMaxRows) * a.n_seq) return true;
-  return 512.0 * a.tokens * a.H * (static_cast<double>(a.max_pages) * a.cache.page_size) <= 2.5e9;
+bool attn_short_chunks(int n_seq, int64_t tokens, int H, int kv_heads, int64_t most_keys) {
+  if (tokens * (H / kv_heads) <= static_cast<int64_t>(kMaxRows) * n_seq) return true;
+  return 512.0 * tokens * H * static_cast<double>(most_keys) <= 2.5e9;
 }
-}  // namespace
 
 size_t attn_prefill_workspace(int n_seq, int64_t tokens, int H, int kv_heads, int num_sms) {
   const size_t here = attn_split_bytes(2 * num_sms, kMaxRows, attn_max_items(n_seq, tokens, H / kv_heads, kMaxRows));
@@ -607,7 +604,8 @@ size_t attn_prefill_workspace(int n_seq, int64_t tokens, int H, int kv_heads, in
 }
 
 cudaError_t launch_attn_prefill(const AttnArgs& a, int num_sms) {
-  if (!short_chunks(a)) return launch_attn_chunk(a, num_sms);
+  if (!attn_short_chunks(a.n_seq, a.tokens, a.H, a.cache.heads, static_cast<int64_t>(a.max_pages) * a.cache.page_size))
+    return launch_attn_chunk(a, num_sms);
   const int G = a.H / a.cache.heads;
   ShortParams p;
   memset(&p, 0, sizeof(p));

@@ -2,11 +2,15 @@
 
 Calls of little work go to the warp-level kernel; the work is bounded by the page table's width, so
 a table much wider than the sequences sends small inputs through the tensor-core kernel."""
+import functools
+import inspect
 import math
 
 import pytest
 import torch
 
+import kimi_delta_attention_prefill_gb300 as kda
+import test_kv_attn_gpu as base
 from kv_attn_util import D, Cache, attention, check, visible
 from test_kv_attn_gpu import gen, reference, run_decode, run_prefill
 
@@ -17,6 +21,92 @@ WIDE = 1 << 17  # tokens that the page tables have room for
 
 def wide(page):
     return WIDE // page
+
+
+@pytest.fixture(autouse=True)
+def kernel_is_named(request, monkeypatch):
+    """Every prefill call here is of the kernel that the test says: its "kernel" parameter, or the
+    tensor-core kernel."""
+    params = getattr(getattr(request.node, "callspec", None), "params", {})
+    want = 0 if params.get("kernel") == "few rows" else 1
+    call = kda.attn_prefill_paged
+
+    def attn_prefill_paged(q, k_pool, v_pool, page_table, *a, **kw):
+        got = kda.debug_attention_kernel(page_table.shape[0], q.shape[0], q.shape[1], k_pool.shape[1],
+                                         page_table.shape[1] * k_pool.shape[2])
+        assert got == want, "the call goes to the other kernel"
+        return call(q, k_pool, v_pool, page_table, *a, **kw)
+
+    monkeypatch.setattr(kda, "attn_prefill_paged", attn_prefill_paged)
+
+
+# ---------------------------------------------- the tests of small prefill calls, on this kernel
+def again(test):
+    """A test of test_kv_attn_gpu.py, with its parameters, over wide tables."""
+    @functools.wraps(test)
+    def run(monkeypatch, **kw):
+        monkeypatch.setattr(base, "Cache", lambda lens, Hkv, page, *a, **k: Cache(lens, Hkv, page, *a, max_pages=wide(page), **k))
+        test(**kw)
+
+    names = list(inspect.signature(test).parameters)
+    run.__signature__ = inspect.Signature([inspect.Parameter(n, inspect.Parameter.POSITIONAL_OR_KEYWORD) for n in names + ["monkeypatch"]])
+    return run
+
+
+test_prefill = again(base.test_prefill)
+test_prefill_edges_far_apart = again(base.test_prefill_edges_far_apart)
+test_prefill_rows_before_the_first_token = again(base.test_prefill_rows_before_the_first_token)
+test_strided_queries_scales_and_long_range = again(base.test_strided_queries_scales_and_long_range)
+test_nonfinite_rows_reach_only_rows_that_see_them = again(base.test_nonfinite_rows_reach_only_rows_that_see_them)
+test_prefill_scales_far_apart = again(base.test_prefill_scales_far_apart)
+test_same_bits_again_on_other_streams_and_in_graphs = again(base.test_same_bits_again_on_other_streams_and_in_graphs)
+
+
+def test_rows_at_the_least_scale(monkeypatch):
+    again(base.test_rows_at_the_least_scale)(monkeypatch, decode=False)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_pages_behind_the_window_are_not_needed(fp8, page):
+    g = gen(page)
+    new, lens = [200, 1], [900, 50]
+    c = Cache(lens, 2, page, fp8, g, max_pages=wide(page))
+    q = torch.randn(201, 8, D, generator=g).to(torch.bfloat16)
+    ref = reference(c, torch.split(q, new), new, lens, 100, 20, D ** -0.5)
+    c.table[0, -(-20 // page):601 // page] = -1  # visible: 0 .. 19 and 601 .. 899
+    o, lse = run_prefill(c, q.cuda(), new, lens, 100, 20)
+    check(o, lse, ref)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_bad_pages_and_lengths_report(fp8):
+    """Bad entries among visible pages, lengths and offsets are reported; other sequences keep their bits."""
+    g = gen(4)
+    new, lens = [120, 150, 90], [300, 400, 90]
+    c = Cache(lens, 2, 32, fp8, g, max_pages=wide(32))
+    q = torch.randn(360, 4, D, generator=g).to(torch.bfloat16).cuda()
+    good, _ = run_prefill(c, q, new, lens)
+    ends = torch.tensor(new).cumsum(0).tolist()
+    for entry in (-1, 9999, -5):
+        table = c.table.clone()
+        c.table[1, 3] = entry
+        o, _ = run_prefill(c, q, new, lens, status=base.DEVICE_CHECK)
+        c.table.copy_(table)
+        for a, b in ((0, ends[0]), (ends[1], ends[2])):
+            check_close(o[a:b], good[a:b])
+    for bad in (-1, WIDE + 1):
+        o = torch.full_like(good, 3.0)
+        run_prefill(c, q, new, [lens[0], bad, lens[2]], status=base.DEVICE_CHECK, o=o)
+        assert (o[ends[0]:ends[1]] == 3).all()
+        for a, b in ((0, ends[0]), (ends[1], ends[2])):
+            check_close(o[a:b], good[a:b])
+
+
+def check_close(a, b):
+    """Sequences of another batch: split elsewhere, so the sums' last bits and one rounding of o may
+    differ; 2^-8 of the largest is far above that."""
+    assert ((a.float() - b.float()).abs().max() <= 2.0 ** -8 * 2 * b.float().abs().max())
 
 
 @pytest.mark.parametrize("new,past,window,sink", [([900, 60], [0, 400], 20, 0), ([700], [500], 100, 5), ([60] * 12, [3 * i for i in range(12)], 0, 0),
