@@ -869,13 +869,16 @@ def attn_prefill_paged(q, k_pool, v_pool, page_table, cu_seqlens, kv_len, k_scal
     o, lse = _attn_outputs(q, shape, o, lse, return_lse, stream)
     lib = _lib or library()
     if workspace is None:
-        workspace = _scratch(lib.kda_attn_prefill_workspace_size(n_seq, T, H, heads, HEAD_DIM), q.device, stream)
+        ws_bytes = lib.kda_attn_prefill_workspace_size(n_seq, T, H, heads, HEAD_DIM)
+        workspace = _scratch(ws_bytes, q.device, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws, ws_bytes = _workspace(workspace)
     st = lib.kda_attn_prefill_paged(
         q.data_ptr(), _pack2(*qs), c, page_table.data_ptr(), n_seq, max_pages,
         _index(cu_seqlens, "cu_seqlens", (n_seq + 1,)), _index(kv_len, "kv_len", (n_seq,)), T, H, HEAD_DIM,
         HEAD_DIM ** -0.5 if scale is None else scale, _c_count(window), _c_count(n_sink), o.data_ptr(),
-        None if lse is None else lse.data_ptr(), *_workspace(workspace),
-        _status_ptr(dev_status), _stream_of(stream))
+        None if lse is None else lse.data_ptr(), ws, ws_bytes, _status_ptr(dev_status), _stream_of(stream))
     if st != 0:
         raise KdaError(st, "kda_attn_prefill_paged")
     return o if lse is None else (o, lse)
@@ -900,12 +903,15 @@ def attn_decode_paged(q, k_pool, v_pool, page_table, kv_len, k_scale=None, v_sca
     o, lse = _attn_outputs(q, shape, o, lse, return_lse, stream)
     lib = _lib or library()
     if workspace is None:
-        workspace = _scratch(lib.kda_attn_decode_workspace_size(B, n_tok, H, heads, HEAD_DIM), q.device, stream)
+        ws_bytes = lib.kda_attn_decode_workspace_size(B, n_tok, H, heads, HEAD_DIM)
+        workspace = _scratch(ws_bytes, q.device, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws, ws_bytes = _workspace(workspace)
     st = lib.kda_attn_decode_paged(
         q.data_ptr(), _pack3(*qs), c, page_table.data_ptr(), B, n_tok, max_pages, _index(kv_len, "kv_len", (B,)), H,
         HEAD_DIM, HEAD_DIM ** -0.5 if scale is None else scale, _c_count(window), _c_count(n_sink), o.data_ptr(),
-        None if lse is None else lse.data_ptr(), *_workspace(workspace),
-        _status_ptr(dev_status), _stream_of(stream))
+        None if lse is None else lse.data_ptr(), ws, ws_bytes, _status_ptr(dev_status), _stream_of(stream))
     if st != 0:
         raise KdaError(st, "kda_attn_decode_paged")
     return o if lse is None else (o, lse)
