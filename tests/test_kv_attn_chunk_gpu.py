@@ -352,3 +352,41 @@ def test_nan_values_of_keys_without_weight(kernel, fp8, score, at):
     lse[bad.cuda()] = 0
     rl[bad] = 0
     check(o, lse, (ro, rl, bo, bl))
+
+
+@pytest.mark.parametrize("kernel", ["many rows", "few rows"])
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("N", [1023, 1025, 2600])
+def test_more_sequences_than_a_plan_takes_at_a_time(kernel, fp8, N):
+    """The list of row tiles is made 1024 sequences, then 1024 tiles, at a time; some sequences are empty."""
+    g = gen(N)
+    H = 72 if kernel == "many rows" else 6
+    new = [(1, 0, 3, 1, 2)[i % 5] for i in range(N)]
+    new[N // 2] = 40
+    lens = [n + i % 7 for i, n in enumerate(new)]
+    c = Cache(lens, 1, 16, fp8, g, max_pages=wide(16) if kernel == "many rows" else None)
+    q = torch.randn(sum(new), H, D, generator=g).to(torch.bfloat16)
+    o, lse = run_prefill(c, q.cuda(), new, lens)
+    parts = torch.split(q, new)
+    some = [i for i in range(N) if new[i] and (i % 37 == 0 or abs(i - N // 2) < 3 or i > N - 8 or 1018 < i < 1030)]
+    at = torch.tensor([0] + new).cumsum(0).tolist()
+    for i in some:
+        see = visible(new[i], lens[i], 0, 0)
+        check(o[at[i]:at[i + 1]], lse[at[i]:at[i + 1]], attention(parts[i], c.value["k"][i], c.value["v"][i], see, D ** -0.5, fp8))
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("kernel", ["many rows", "few rows"])
+@pytest.mark.parametrize("cu", [[0, 50, 20, 70], [-5, 20, 40, 70], [0, 30, 50, 71], [0, 80, 60, 70]])
+def test_bad_offsets_report(kernel, cu):
+    """Offsets that run backwards, begin before the rows or end past them."""
+    g = gen(6)
+    c = Cache([60, 90, 80], 2, 32, False, g, max_pages=wide(32) if kernel == "many rows" else None)
+    H = 32 if kernel == "many rows" else 4
+    q = torch.randn(70, H, D, generator=g).to(torch.bfloat16).cuda()
+    st = base.i32(0)
+    around = torch.full((90, H, D), 5.0, dtype=torch.bfloat16, device="cuda")
+    kda.attn_prefill_paged(q, *c.args, base.i32(*cu), base.i32(60, 90, 80), o=around[10:80], dev_status=st)
+    torch.cuda.synchronize()
+    assert int(st) == base.DEVICE_CHECK
+    assert (around[:10] == 5).all() and (around[80:] == 5).all()
