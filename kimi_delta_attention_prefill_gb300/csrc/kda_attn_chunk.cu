@@ -52,8 +52,8 @@ constexpr int kStage = kTile * 128;     // a tile of codes
 // A block's least share: 1, 2 and 4 tiles took the same time (400 tokens of a prompt, 32 us).
 constexpr int kMinTiles = 2;
 // What an item costs besides its keys (queries, the pipeline's filling and draining, output), in
-// tiles.  A prompt of 8192, 96 heads on 8, bf16: 3 / 4 / 5 / 6 / 12 took 1298 / 1159 / 1157-1167 /
-// 1171 / 1239 us.
+// tiles.  A prompt of 8192, 96 heads on 8: 3 / 4 / 5 / 6 / 12 took 1279 / 1270 / 1285 / 1296 / 1373 us
+// (bf16), 4 / 5 1719 / 1594 us (e4m3).
 constexpr int kItemCost = 5;
 
 template <bool kE4m3>

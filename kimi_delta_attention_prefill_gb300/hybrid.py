@@ -21,7 +21,7 @@ D = kda.HEAD_DIM
 
 
 class Pages:
-    """Pages of one attention layer's cache, and the sequences' page tables (on the host)."""
+    """Pages of one attention layer's cache (the page table, on the device, is the stack's)."""
 
     def __init__(self, n_pages, n_kv_heads, page_size, fp8, device):
         shape = (n_pages, n_kv_heads, page_size, D)

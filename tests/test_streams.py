@@ -135,3 +135,24 @@ def test_workspaces_of_two_streams_are_apart(monkeypatch):
             assert seen[-1][0] != at
             torch.cuda.synchronize()
             assert torch.equal(o, want[i]) and torch.equal(o2, want[i])
+
+
+@pytest.mark.gpu
+def test_capture_with_the_stream_given():
+    """A call captured into a graph with its stream named makes its tensors in the graph's memory."""
+    g = torch.Generator(device="cuda").manual_seed(2)
+    rnd = lambda *s: torch.randn(s, generator=g, device="cuda", dtype=BF)
+    q, pool = rnd(300, 8, 128), rnd(2, 64, 2, 64, 128)
+    table = torch.arange(64, dtype=I32, device="cuda")[None]
+    cu, kv = torch.tensor([0, 300], dtype=I32, device="cuda"), torch.tensor([4000], dtype=I32, device="cuda")
+    want = kda.attn_prefill_paged(q, *pool, table, cu, kv)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        o = kda.attn_prefill_paged(q, *pool, table, cu, kv, stream=torch.cuda.current_stream())
+        k, v = kda.kv_read(*pool, table, cu, kv - 300, 300, stream=torch.cuda.current_stream())
+    for _ in range(2):
+        held = [torch.full((1 << 22,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want) and torch.equal(k, pool[0].transpose(1, 2).reshape(-1, 2, 128)[3700:4000])
+        del held
