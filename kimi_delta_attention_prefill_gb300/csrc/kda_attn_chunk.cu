@@ -719,13 +719,13 @@ __device__ void softmax_group(const ChunkParams& p, uint8_t* sm, Bars& b, int t,
       // ---- weights and their sum: keys 64 .. 127 from the registers, over their own scores' first
       // 32 columns, then keys 0 .. 63
       const float ref = m == -INFINITY ? 0.f : m;
-      if (kE4m3 && wide) {  // the sum of 2^(y - ev - m), key by key
+      if (kE4m3 && wide) {  // the sum of 2^((y - m) - ev), key by key: of the weights that P V gets, however large y
 #pragma unroll 1
         for (int c = 0; c < kTile; c += 16) {
           float y[16];
           tmem_ld16(ts + c, y);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) l += exp2_fast(y[e] - scale_exponent(vec[128 + c + e]) - v_off - ref);
+          for (int e = 0; e < 16; ++e) l += exp2_fast((y[e] - ref) - (scale_exponent(vec[128 + c + e]) + v_off));
         }
       }
       const uint64_t u2 = f32x2(u, u), nb2 = f32x2(off - ref, off - ref);

@@ -175,7 +175,8 @@ def test_scores_too_small_to_tell_apart(fp8):
 
 
 @pytest.mark.parametrize("kernel", ["many rows", "few rows", "decode"])
-@pytest.mark.parametrize("k_down,v_down", [([50], [50]), ([0, 47], [0]), ([0], [0, 45, 62]), ([40, 47, 50, 57], [40, 41]), ([-55], [-55, -20])])
+@pytest.mark.parametrize("k_down,v_down", [([50], [50]), ([0, 47], [0]), ([0], [0, 45, 62]), ([40, 47, 50, 57], [40, 41]), ([-55], [-55, -20]),
+                                           ([72], [72]), ([-84], [-84]), ([-30, 30], [-49, 49])])
 def test_scales_that_others_write(kernel, k_down, v_down):
     """Scale bytes below and above those that kda_kv_append writes, alone and next to ordinary ones, rows of zeros among them."""
     g = gen(len(k_down) + 10 * len(v_down))
