@@ -459,6 +459,90 @@ kda_status kda_attn_decode_paged(const kda_bf16* q, const int64_t* q_stride, con
                                  void* workspace, size_t workspace_bytes, int* dev_status, cudaStream_t stream);
 
 /*
+ * Linear attention with a decay a head.  No counterpart on the pages: a hybrid stack may hold layers
+ * whose 128 x 128 state a head only decays and adds, without the delta rule's correction:
+ *
+ *     S_t = exp(g_t) S_{t-1} + k_t v_t^T,        o_t = scale S_t^T q_t        (row of S = d_k channel)
+ *
+ * with one log-decay g_t in [-inf, 0] a (token, head); -inf forgets what is before the token (a state
+ * of finite values).
+ * H heads of v, g and o share qk_heads heads of q and k: head h reads head h / (H / qk_heads).
+ *
+ * Rows of q, k, v and gate are bf16; *_stride are host arrays with the element strides of their leading
+ * dimensions (the last is contiguous), positive multiples of 8, so rows of a fused projection may be
+ * passed as they lie.  g_stride likewise for g (fp32), any values >= 0: a token stride of 0 gives a
+ * decay a head that is the same for every token.
+ *
+ * With gate != NULL the layer's output stage is applied before o is written (kda_prefill_gated's):
+ *     sigmoid(gate) * norm_weight * o / sqrt(mean_c(o[c]^2) + eps)       (norm_weight NULL: ones)
+ *
+ * A value that is not finite in q, k, v or g makes non-finite only what depends on it: a token's q its
+ * own row; its k, v and g its own row and the later ones and the final state of its sequence and head.
+ * With g above 0 results may overflow.
+ *
+ * kda_lin_prefill -- packed sequences, chunk by chunk (128 tokens):
+ *   q, k        [total_tokens, qk_heads, d]      v, gate  [total_tokens, H, d]
+ *   g           [total_tokens, H]
+ *   S_in        [n_seq, H, d, d] fp32 entry states, or NULL for zeros
+ *   cu_seqlens  [n_seq + 1] int32: sequence i owns rows [cu[i], cu[i+1]); cu[0] = 0, non-decreasing,
+ *               cu[n_seq] = total_tokens (checked on the device: KDA_ERR_DEVICE_CHECK, the call's
+ *               outputs are then left as they were)
+ *   o           [total_tokens, H, d] bf16, contiguous
+ *   S_out       [n_seq, H, d, d] fp32 final states, or NULL; may be S_in (in place)
+ *   n_segments  0: a sequence is split over the SMs by the library's rule when there are few heads and
+ *               sequences; k >= 1: every sequence into min(k, its chunks) segments
+ *   workspace   kda_lin_prefill_workspace_size(...) bytes (never 0), 256-byte aligned; its contents need
+ *               no preparation and mean nothing between calls
+ * The same call gives the same bits; a split sequence's last bits may depend on what else is in the call.
+ * Products take bf16 operands: q, k, v as they are, the decayed weights of a chunk and the state in front
+ * of it rounded to bf16 for o only.  The states themselves are carried in fp32, from decayed keys of 16 bits.
+ */
+size_t kda_lin_prefill_workspace_size(int n_seq, int H, int d, int64_t total_tokens, int n_segments);
+kda_status kda_lin_prefill(const kda_bf16* q, const int64_t* q_stride, const kda_bf16* k, const int64_t* k_stride,
+                           const kda_bf16* v, const int64_t* v_stride, const float* g, const int64_t* g_stride, float scale,
+                           const kda_bf16* gate, const int64_t* gate_stride, const float* norm_weight, float eps,
+                           const float* S_in, const int32_t* cu_seqlens, int n_seq, int64_t total_tokens, kda_bf16* o,
+                           float* S_out, int qk_heads, int H, int d, int n_segments, void* workspace,
+                           size_t workspace_bytes, int* dev_status, cudaStream_t stream);
+
+/*
+ * kda_lin_decode -- a decode (n_tok = 1) or verify (n_tok <= 4) step, in fp32:
+ *   q, k        [B, n_tok, qk_heads, d]      v, gate  [B, n_tok, H, d]      g  [B, n_tok, H]
+ *               (strides of the first three dimensions)
+ *   S_state     [B, H, d, d] fp32, read, then overwritten in place with the state after n_commit[b]
+ *               tokens (left untouched when 0)
+ *   n_commit    [B] int32 in [0, n_tok], or NULL for n_tok; an entry out of range leaves that
+ *               sequence's state untouched and reports KDA_ERR_DEVICE_CHECK
+ *   o           [B, n_tok, H, d] fp32, contiguous: the outputs of all n_tok tokens
+ */
+kda_status kda_lin_decode(const kda_bf16* q, const int64_t* q_stride, const kda_bf16* k, const int64_t* k_stride,
+                          const kda_bf16* v, const int64_t* v_stride, const float* g, const int64_t* g_stride, float scale,
+                          const kda_bf16* gate, const int64_t* gate_stride, const float* norm_weight, float eps,
+                          float* S_state, const int32_t* n_commit, float* o, int B, int n_tok, int qk_heads, int H, int d,
+                          int* dev_status, cudaStream_t stream);
+
+/*
+ * kda_block_norm -- the step between two blocks over rows of a residual stream, in one pass:
+ *
+ *     x' = x + scale * sigmoid(gate) * post_weight * N(y),      h = weight * x' / sqrt(mean(x'^2) + eps)
+ *
+ * with N(y) = y / sqrt(mean(y^2) + eps) when post_norm is set, else y.
+ *   x            [rows, width] bf16 (KDA_ROWS_BF16) or fp32 (KDA_ROWS_F32), rows x_stride elements apart
+ *   y, gate      [rows, width] bf16, rows y_stride / gate_stride elements apart.  y NULL: x' = x (the norm
+ *                in front of the first block); gate NULL: no gate
+ *   weight, post_weight  [width] fp32, or NULL for ones
+ *   h            [rows, width] bf16, contiguous, or NULL
+ *   x_out        [rows, width] of x's type, contiguous, or NULL: x'; may be x itself.  NULL without y
+ * h is made from x' before x' is rounded to x's type.  Strides are positive whole 16-byte units; width is a
+ * multiple of 8, at most 32768 (KDA_ERR_UNSUPPORTED).  Sums of squares are of 32 bits.
+ */
+enum { KDA_ROWS_BF16 = 0, KDA_ROWS_F32 = 1 };
+kda_status kda_block_norm(const void* x, int x_dtype, int64_t x_stride, const float* weight, const kda_bf16* y,
+                          int64_t y_stride, int post_norm, const float* post_weight, const kda_bf16* gate,
+                          int64_t gate_stride, float scale, float eps, kda_bf16* h, void* x_out, int64_t rows, int width,
+                          cudaStream_t stream);
+
+/*
  * kda_debug_stall_next_prefill -- test hook for the bounded waits (no counterpart on the
  * pages).  The next prefill launch of this process runs a test instance of the kernel
  * whose prep warps withhold their first hand-off of chunk `chunk` (counted within each

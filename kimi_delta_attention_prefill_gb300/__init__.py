@@ -12,7 +12,9 @@ Functions mirror the C entry points: :func:`prefill` (``kda_prefill``, or
 :func:`combine_pairs` (``kda_combine_pairs``), :func:`prefill_noalloc`
 (``kda_prefill_noalloc``), the attention cache's :func:`kv_append` (``kda_kv_append``),
 :func:`kv_read` (``kda_kv_read``), :func:`attn_prefill_paged` (``kda_attn_prefill_paged``) and
-:func:`attn_decode_paged` (``kda_attn_decode_paged``), the workspace-size queries, and
+:func:`attn_decode_paged` (``kda_attn_decode_paged``), linear attention's :func:`lin_prefill`
+(``kda_lin_prefill``) and :func:`lin_decode` (``kda_lin_decode``), the step between blocks
+:func:`block_norm` (``kda_block_norm``), the workspace-size queries, and
 :func:`status_string` (``kda_status_string``).  The cross-device split's exchange is in :mod:`.kcp`.  Tensors are torch CUDA tensors (pinned
 host tensors for :func:`prefill_host`); the launch goes to the current torch stream
 unless ``stream`` is given.  Tensors that a call makes, outputs and workspaces, are made on the
@@ -129,6 +131,16 @@ def library():
             lib.kda_attn_decode_paged.restype = _c_int
             lib.kda_attn_decode_paged.argtypes = ([_vp, strides, cache, _vp, _c_int, _c_int, _c_int, _vp, _c_int, _c_int,
                                                    ctypes.c_float, _c_int, _c_int] + [_vp, _vp, _vp, _c_sz, _vp, _vp])
+            rows = [_vp, strides] * 4 + [ctypes.c_float, _vp, strides, _vp, ctypes.c_float]  # q, k, v, g; output stage
+            lib.kda_lin_prefill_workspace_size.restype = _c_sz
+            lib.kda_lin_prefill_workspace_size.argtypes = [_c_int, _c_int, _c_int, _c_i64, _c_int]
+            lib.kda_lin_prefill.restype = _c_int
+            lib.kda_lin_prefill.argtypes = rows + [_vp, _vp, _c_int, _c_i64, _vp, _vp] + [_c_int] * 4 + [_vp, _c_sz, _vp, _vp]
+            lib.kda_lin_decode.restype = _c_int
+            lib.kda_lin_decode.argtypes = rows + [_vp, _vp, _vp] + [_c_int] * 5 + [_vp, _vp]
+            lib.kda_block_norm.restype = _c_int
+            lib.kda_block_norm.argtypes = [_vp, _c_int, _c_i64, _vp, _vp, _c_i64, _c_int, _vp, _vp, _c_i64, ctypes.c_float,
+                                           ctypes.c_float, _vp, _vp, _c_i64, _c_int, _vp]
             _lib = lib
     return _lib
 
@@ -915,3 +927,173 @@ def attn_decode_paged(q, k_pool, v_pool, page_table, kv_len, k_scale=None, v_sca
     if st != 0:
         raise KdaError(st, "kda_attn_decode_paged")
     return o if lse is None else (o, lse)
+
+
+# ---------------------------------------------------- linear attention with a decay a head
+_F32 = torch.float32
+
+
+def _on(device, stream, *tensors):
+    """All tensors are on one device, and it is the one that the call runs on."""
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"all tensors must be on one device, got cuda:{device} and {t.device}")
+    if device >= 0 and device != (_current_device() if stream is None else stream.device.index):
+        raise ValueError(f"the tensors are on cuda:{device}, which is not the device that the call runs on")
+
+
+def _decays(g, lead, H):
+    """Strides of the log-decays: ``lead + [H]``, or ``[H]`` for every token alike."""
+    if not isinstance(g, torch.Tensor):
+        raise TypeError("g must be a torch.Tensor")
+    if not g.is_cuda:
+        raise ValueError("g must be a CUDA tensor")
+    if g.dtype is not _F32:
+        raise TypeError(f"g must be {_F32}, got {g.dtype}")
+    if g.shape == lead + (H,):
+        return g.stride()
+    if g.shape == (H,):
+        return (0,) * len(lead) + g.stride()
+    raise ValueError(f"g must have shape {lead + (H,)} or {(H,)}, got {tuple(g.shape)}")
+
+
+def _lin_rows(q, k, v, g, gate, norm_weight, n_lead, names, pack, pack_g):
+    """What the two calls share: sizes, and the rows' strides as the library takes them."""
+    if not isinstance(q, torch.Tensor) or q.dim() != n_lead + 2:
+        raise ValueError(f"q must be a tensor [{names}, heads, {HEAD_DIM}]")
+    if not isinstance(v, torch.Tensor) or v.dim() != n_lead + 2:
+        raise ValueError(f"v must be a tensor [{names}, heads, {HEAD_DIM}]")
+    shape = q.shape
+    lead, Hk, H = tuple(shape[:n_lead]), shape[n_lead], v.shape[n_lead]
+    if Hk < 1 or H < 1 or H % Hk:
+        raise ValueError(f"the heads of v must be a multiple of those of q and k, got {H} and {Hk}")
+    qs, ks = _rows_of(q, "q", lead + (Hk,)), _rows_of(k, "k", lead + (Hk,))
+    vs, gs = _rows_of(v, "v", lead + (H,)), _decays(g, lead, H)
+    gates = None
+    if gate is not None:
+        gates = pack(*_rows_of(gate, "gate", lead + (H,)))
+        if norm_weight is not None:
+            _need(norm_weight, "norm_weight", _F32, (HEAD_DIM,))
+    elif norm_weight is not None:
+        raise ValueError("norm_weight belongs to the output stage, which needs gate")
+    return lead, Hk, H, pack(*qs), pack(*ks), pack(*vs), pack_g(*gs), gates
+
+
+def lin_prefill_workspace_size(n_seq, H, total_tokens, n_segments=0, d=HEAD_DIM) -> int:
+    return int(library().kda_lin_prefill_workspace_size(int(n_seq), int(H), int(d), int(total_tokens), int(n_segments)))
+
+
+def lin_prefill(q, k, v, g, cu_seqlens, S_in=None, scale=1.0, gate=None, norm_weight=None, eps=1e-5, o=None, S_out=None,
+                n_segments=0, workspace=None, dev_status=None, stream=None):
+    """Linear attention with a decay a head over packed sequences (``kda_lin_prefill``):
+    ``S_t = exp(g_t) S_{t-1} + k_t v_t^T``, ``o_t = scale * S_t^T q_t``.
+
+    q, k ``[T, Hk, 128]``, v ``[T, H, 128]`` bf16 (token and head dimensions may be strided; H a
+    multiple of Hk); g ``[T, H]`` fp32 log-decays <= 0 (any strides), or ``[H]`` for every token
+    alike; cu_seqlens ``[N + 1]`` int32; S_in ``[N, H, 128, 128]`` fp32 or None (zeros).  With
+    ``gate`` (``[T, H, 128]`` bf16 logits, may be strided) the output stage is fused:
+    ``sigmoid(gate) * norm_weight * o / sqrt(mean(o^2) + eps)``.  S_out may be S_in.
+    Returns ``(o, S_out)``: ``[T, H, 128]`` bf16 and ``[N, H, 128, 128]`` fp32.
+    """
+    (T,), Hk, H, qs, ks, vs, gs, gates = _lin_rows(q, k, v, g, gate, norm_weight, 1, "T", _pack2, _pack2)
+    n_seq = cu_seqlens.shape[0] - 1 if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dim() == 1 else -1
+    if n_seq < 0:
+        raise ValueError("cu_seqlens must be a tensor [sequences + 1]")
+    _on(q.get_device(), stream, k, v, g, gate, norm_weight, S_in, cu_seqlens, o, S_out, workspace, dev_status)
+    shape, states = (T, H, HEAD_DIM), (n_seq, H, HEAD_DIM, HEAD_DIM)
+    cu = _index(cu_seqlens, "cu_seqlens", (n_seq + 1,))
+    if S_in is not None:
+        _need(S_in, "S_in", _F32, states)
+    o = _output(shape, _BF16, q.device, stream) if o is None else _need(o, "o", _BF16, shape)
+    S_out = _output(states, _F32, q.device, stream) if S_out is None else _need(S_out, "S_out", _F32, states)
+    lib = _lib or library()
+    if workspace is None:
+        ws_bytes = lib.kda_lin_prefill_workspace_size(n_seq, H, HEAD_DIM, T, n_segments)
+        workspace = _scratch(ws_bytes, q.device, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws, ws_bytes = _workspace(workspace)
+    st = lib.kda_lin_prefill(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs, scale, _ptr(gate), gates,
+        _ptr(norm_weight), eps, _ptr(S_in), cu, n_seq, T, o.data_ptr(), S_out.data_ptr(), Hk, H, HEAD_DIM, n_segments, ws,
+        ws_bytes, _status_ptr(dev_status), _stream_of(stream))
+    if st != 0:
+        raise KdaError(st, "kda_lin_prefill")
+    return o, S_out
+
+
+def lin_decode(q, k, v, g, S_state, n_commit=None, scale=1.0, gate=None, norm_weight=None, eps=1e-5, o=None,
+               dev_status=None, stream=None):
+    """:func:`lin_prefill` for a decode (n_tok = 1) or verify (n_tok <= 4) step in fp32
+    (``kda_lin_decode``); updates ``S_state`` ``[B, H, 128, 128]`` in place to the state after
+    ``n_commit`` ``[B]`` int32 tokens (None: all; 0 leaves it untouched).
+
+    q, k ``[B, n_tok, Hk, 128]``, v and gate ``[B, n_tok, H, 128]`` bf16 (leading dimensions may be
+    strided); g ``[B, n_tok, H]`` or ``[H]`` fp32.  Returns o ``[B, n_tok, H, 128]`` fp32.
+    """
+    (B, n_tok), Hk, H, qs, ks, vs, gs, gates = _lin_rows(q, k, v, g, gate, norm_weight, 2, "B, n_tok", _pack3, _pack3)
+    _on(q.get_device(), stream, k, v, g, gate, norm_weight, S_state, n_commit, o, dev_status)
+    _need(S_state, "S_state", _F32, (B, H, HEAD_DIM, HEAD_DIM))
+    commit = None if n_commit is None else _index(n_commit, "n_commit", (B,))
+    shape = (B, n_tok, H, HEAD_DIM)
+    o = _output(shape, _F32, q.device, stream) if o is None else _need(o, "o", _F32, shape)
+    st = (_lib or library()).kda_lin_decode(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs, scale, _ptr(gate), gates,
+        _ptr(norm_weight), eps, S_state.data_ptr(), commit, o.data_ptr(), B, n_tok, Hk, H, HEAD_DIM,
+        _status_ptr(dev_status), _stream_of(stream))
+    if st != 0:
+        raise KdaError(st, "kda_lin_decode")
+    return o
+
+
+def _wide_rows(t, name, dtypes, shape):
+    """Elements from one row to the next of ``t`` ``[rows, width]``; the rows may be strided."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in dtypes:
+        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and t.shape != shape):
+        raise ValueError(f"{name} must have shape {'[rows, width]' if shape is None else tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape[1] > 1 and t.shape[0] and t.stride(1) != 1:
+        raise ValueError(f"{name} must be contiguous in its last dimension")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def block_norm(x, weight=None, y=None, post_norm=False, post_weight=None, gate=None, scale=1.0, eps=1e-5, h=None,
+               x_out=None, stream=None):
+    """The step between two blocks, in one pass (``kda_block_norm``):
+    ``x' = x + scale * sigmoid(gate) * post_weight * N(y)`` and
+    ``h = weight * x' / sqrt(mean(x'^2) + eps)``, N the same norm with ``post_norm``, else nothing.
+
+    x ``[T, W]`` the residual stream, bf16 or fp32; y ``[T, W]`` bf16 the block's output, or None (the
+    norm in front of the first block); gate ``[T, W]`` bf16 logits or None; weight, post_weight ``[W]``
+    fp32 or None (ones).  Rows may be strided; W a multiple of 8.  Returns ``(h, x')``: h ``[T, W]``
+    bf16; x' of x's type, in ``x_out`` (which may be x) when given, and x itself without y.
+    """
+    xs = _wide_rows(x, "x", (_BF16, _F32), None)
+    shape = x.shape
+    T, W = shape
+    ys = gs = 0
+    if y is not None:
+        ys = _wide_rows(y, "y", (_BF16,), shape)
+        if gate is not None:
+            gs = _wide_rows(gate, "gate", (_BF16,), shape)
+        if post_weight is not None:
+            _need(post_weight, "post_weight", _F32, (W,))
+        x_out = _output(shape, x.dtype, x.device, stream) if x_out is None else _need(x_out, "x_out", x.dtype, shape)
+    elif gate is not None or post_norm or post_weight is not None:
+        raise ValueError("post_norm, post_weight and gate belong to a block's output y")
+    elif x_out is not None:
+        raise ValueError("x_out needs a block's output y")
+    if weight is not None:
+        _need(weight, "weight", _F32, (W,))
+    _on(x.get_device(), stream, y, gate, weight, post_weight, h, x_out)
+    h = _output(shape, _BF16, x.device, stream) if h is None else _need(h, "h", _BF16, shape)
+    st = (_lib or library()).kda_block_norm(
+        x.data_ptr(), 0 if x.dtype is _BF16 else 1, xs, _ptr(weight), _ptr(y), ys, post_norm, _ptr(post_weight), _ptr(gate),
+        gs, scale, eps, h.data_ptr(), _ptr(x_out), T, W, _stream_of(stream))
+    if st != 0:
+        raise KdaError(st, "kda_block_norm")
+    return h, x if x_out is None else x_out
