@@ -566,6 +566,13 @@ void kda_debug_stall_next_prefill(int chunk);
 void kda_debug_stall_next_attention(int copy);
 
 /*
+ * kda_debug_stall_next_linear -- the same for linear attention: in the next kda_lin_prefill call of this
+ * process each block leaves out the copy numbered `copy` of its tiles (the first pass of a split call
+ * too).  One-shot.
+ */
+void kda_debug_stall_next_linear(int copy);
+
+/*
  * kda_debug_attention_kernel -- which kernel a kda_attn_prefill_paged call takes (no counterpart on
  * the pages), for tests that are written for one of them: 1 the tensor-core kernel, 0 the
  * warp-level one, -1 bad sizes.  most_keys is max_pages * page_size.

@@ -107,6 +107,9 @@ def library():
                 lib.kda_debug_stall_next_attention.argtypes = [_c_int]
                 lib.kda_debug_attention_kernel.restype = _c_int
                 lib.kda_debug_attention_kernel.argtypes = [_c_int, _c_i64, _c_int, _c_int, _c_i64]
+            if hasattr(lib, "kda_debug_stall_next_linear"):  # diagnostic hook (tests)
+                lib.kda_debug_stall_next_linear.restype = None
+                lib.kda_debug_stall_next_linear.argtypes = [_c_int]
             lib.kda_prefill_pairs.restype = _c_int
             lib.kda_prefill_pairs.argtypes = [_vp] * 6 + [_c_int, _c_i64, _vp, _vp, _c_int, _c_int, _vp, _vp]
             lib.kda_combine_pairs.restype = _c_int
@@ -537,6 +540,12 @@ def debug_stall_next_attention(copy):
     out one copy of its keys; the call reports KDA_ERR_TIMEOUT in ``dev_status`` after some
     seconds, without any fault."""
     library().kda_debug_stall_next_attention(int(copy))
+
+
+def debug_stall_next_linear(copy):
+    """Test hook (``kda_debug_stall_next_linear``): in the next :func:`lin_prefill` call each block
+    leaves out one copy; the call reports KDA_ERR_TIMEOUT in ``dev_status``, without any fault."""
+    library().kda_debug_stall_next_linear(int(copy))
 
 
 def debug_attention_kernel(n_seq, total_tokens, H, n_kv_heads, most_keys) -> int:

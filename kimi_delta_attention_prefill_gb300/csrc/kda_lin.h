@@ -36,6 +36,7 @@ struct LinArgs {
   int H = 0;
   int group = 1;  // heads that share a q/k head
   int n_segments = 0;
+  int stall = -1;  // test hook: the copy that each block leaves out
   void* workspace = nullptr;
   int* status = nullptr;
   cudaStream_t stream = nullptr;

@@ -2,6 +2,7 @@
 // blocks (include/kda.h): host-side validation and launch.  Nothing here allocates or keeps anything
 // between calls.
 #include <cuda_runtime.h>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -9,6 +10,8 @@
 #include "kda_lin.h"
 
 namespace {
+
+std::atomic<int> g_stall_copy{-1};  // kda_debug_stall_next_linear: consumed by the next kda_lin_prefill
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -83,6 +86,7 @@ kda_status kda_lin_prefill(const kda_bf16* q, const int64_t* q_stride, const kda
   if (dev != KDA_OK) return dev;
   a.S_in = S_in; a.S_out = S_out; a.cu = cu_seqlens; a.n_segments = n_segments; a.workspace = workspace;
   a.status = dev_status; a.stream = stream;
+  if (g_stall_copy.load(std::memory_order_relaxed) >= 0) a.stall = g_stall_copy.exchange(-1);
   return kda::launch_lin_prefill(a, sms) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
 
@@ -131,5 +135,7 @@ kda_status kda_block_norm(const void* x, int x_dtype, int64_t x_stride, const fl
   a.x_f32 = f32; a.post_norm = post_norm != 0; a.scale = scale; a.eps = eps; a.stream = stream;
   return kda::launch_block_norm(a, sms) == cudaSuccess ? KDA_OK : KDA_ERR_CUDA;
 }
+
+void kda_debug_stall_next_linear(int copy) { g_stall_copy.store(copy < 0 ? -1 : copy); }
 
 }  // extern "C"
