@@ -6,18 +6,25 @@
 // All exponents are differences of sums of values <= 0, so nothing can grow whatever the decays are.
 //
 // One block walks the chunks of a (sequence, head) or of a segment of one; its warps:
-//     0       copies (TMA, a ring of five 32 KiB tiles: k, q, v, k, q, ..) and the line of work items
-//     1       products (tcgen05): Q K^T, Q S, K^T V, P V; 128 x 128 x 128 each, accumulators in tensor memory
-//     2       decays: sums in 64-bit fixed point (2^-32 of a factor of 2), so that no difference loses bits
-//     4 - 7   weights P = (Q K^T) o D to bf16 over their scores, then the outputs (thread = token)
-//     8 - 11  decayed keys, split into two bf16 parts (16 bits together): hi in place of k, lo beside it
-//     12 - 19 the state, in fp32 registers (thread = half a row); its bf16 copy for Q S in shared memory
+//     0        copies (TMA; two tiles each of q, k and v) and the line of work items
+//     1        products (tcgen05)
+//     2        decays (3: the output stage's gate, into q's tile when q is used): sums in 64-bit fixed point (2^-32 of a factor of 2), so that no difference loses bits
+//     4 - 7    weights P = (Q K^T) o D to bf16 over their scores; Q S times e^G in place, on which P V is then
+//              added; outputs (thread = token)
+//     8 - 15   decayed values, transposed into tensor memory as three bf16 parts (24 bits together)
+//     16 - 23  the state, in fp32 registers (thread = half a column); its bf16 copy for Q S in shared memory
 //
-// Rounded to bf16: P and the copy of S, for o only, which is bf16 itself.  The state sees 16-bit keys and
-// exact values: K^T V is two products.
+// Rounded to bf16: P and the copy of S, for o only, which is bf16 itself.  The state sees 24-bit products:
+// S^T gets three products, one for each part of the values, with K as it lies.  The decay is on the values'
+// side because they can then be an operand in tensor memory: shared memory, whose 128 bytes a cycle the
+// products of operands in it take in full, is the block's bottleneck.  The parts go through a ring of four
+// units (a part of 64 tokens), so that they are made while the products of the units before them run.
 //
-// A token's NaN or infinity must not reach earlier tokens, but 0 * NaN is NaN in P V: a row whose P V part is
-// not finite is computed once more from the weights and values of the tokens that it sees (cold).
+// The products of a chunk: Q K^T | Q S | units of tokens 0 - 63 | units of tokens 64 - 127 | P V.  Weights are made
+// during the three in the middle, outputs and the next state during P V and the next Q K^T.
+//
+// A token's NaN or infinity must not reach earlier tokens, but 0 * NaN is NaN in P V: values that are not
+// finite are cleared in the tile, and the rows that see one get NaN in its channel when they are written.
 //
 // Few heads: plan_segments' rule cuts a sequence into as many segments as its share of the work is worth
 // in SMs.  A first pass (the same kernel without q and o) leaves each segment's state from zeros, the second
@@ -39,13 +46,17 @@ namespace {
 
 constexpr int kD = kHeadDim;
 constexpr int kC = 128;  // tokens a chunk
-constexpr int kThreads = 640;
-constexpr int kRegs = 96;  // at launch
-constexpr int kSlots = 5;
+constexpr int kThreads = 768;
+constexpr int kRegs = 80;  // at launch
 constexpr uint32_t kTile = 32768, kPanel = 16384;
-constexpr uint32_t kSmLo = kSlots * kTile, kSmState = kSmLo + kTile, kSmSmall = kSmState + kTile;
-// tensor memory columns
-constexpr uint32_t kTS = 0, kTO = 128, kTI = 256, kTKV = 384;  // scores / weights; P V; Q S; K^T V
+constexpr uint32_t kSmState = 6 * kTile, kSmSmall = kSmState + kTile;
+// tensor memory columns: scores and weights; outputs; K^T V, transposed; four units of the values' parts
+constexpr uint32_t kTS = 0, kTO = 128, kTKV = 256, kTV = 384;
+// The first pass has neither scores nor outputs: K^T V in two places in turn, and twice as many units.
+template <bool kFull>
+__device__ __forceinline__ uint32_t kv_column(uint32_t n) { return kFull ? kTKV : 128 * (n & 1); }
+template <bool kFull>
+__device__ __forceinline__ uint32_t unit_column(uint32_t u) { return kFull ? kTV + 32 * (u & 3) : 256 + 32 * (u & 7); }
 constexpr int kMinSegment = 8;  // chunks
 
 // ------------------------------------------------------------------------------------ plan
@@ -57,10 +68,11 @@ struct Item {
 };
 
 struct Plan {
-  int* counts = nullptr;  // items of pass 2, of pass 1; next item of pass 2, of pass 1
+  int* counts = nullptr;  // items of pass 2, of pass 1; next item of pass 2, of pass 1; items without tokens, after pass 2's
   Item* items[2] = {nullptr, nullptr};
   float* decay = nullptr;  // [slots][H] factor of a segment's decay
   float* slots = nullptr;  // [slots][H][128][128]: slot base: the sequence's entry state; base + 1 + j: segment j's exit
+  uint32_t* bad = nullptr; // [blocks][4][128] values that are not finite, of a block's chunks (clear_bad)
   int64_t most[2] = {0, 0}, n_slots = 0;
 };
 
@@ -94,6 +106,9 @@ size_t plan_layout(Plan* p, void* ws, int n_seq, int64_t tokens, int H, int forc
     p->items[i] = reinterpret_cast<Item*>(b + at);
     at = up(at + sizeof(Item) * static_cast<size_t>(p->most[i]));
   }
+  p->bad = reinterpret_cast<uint32_t*>(b + at);
+  const int64_t blocks = p->most[0] * H < sms ? p->most[0] * H : sms;
+  at += sizeof(uint32_t) * 4 * kD * static_cast<size_t>(blocks);
   p->decay = reinterpret_cast<float*>(b + at);
   at = up(at + sizeof(float) * static_cast<size_t>(p->n_slots) * H);
   p->slots = reinterpret_cast<float*>(b + at);
@@ -115,7 +130,7 @@ __global__ void __launch_bounds__(1024) lin_plan_kernel(const int32_t* __restric
   if (__syncthreads_or(bad)) {
     if (tid == 0) {
       report_status(status, 7 /* KDA_ERR_DEVICE_CHECK */);
-      p.counts[0] = p.counts[1] = p.counts[2] = p.counts[3] = 0;
+      for (int i = 0; i < 5; ++i) p.counts[i] = 0;
     }
     return;
   }
@@ -124,13 +139,14 @@ __global__ void __launch_bounds__(1024) lin_plan_kernel(const int32_t* __restric
   auto length = [&](int s) { const int n = segments(s); return (chunks(s) + n - 1) / n; };
   for (int s = tid; s < n_seq; s += blockDim.x) atomicMax(&longest, length(s));
   __syncthreads();
-  auto bin = [&](int s) { return 255 - static_cast<int>(static_cast<int64_t>(length(s)) * 255 / longest); };
+  auto bin = [&](int s) { return cu[s + 1] == cu[s] ? 255 : 254 - static_cast<int>(static_cast<int64_t>(length(s)) * 254 / longest); };
   for (int s = tid; s < n_seq; s += blockDim.x) atomicAdd(&at[bin(s)], segments(s));
   __syncthreads();
   if (tid == 0) {
     int sum = 0;
     for (int i = 0; i < 256; ++i) { const int n = at[i]; at[i] = sum; sum += n; }
-    p.counts[0] = sum;
+    p.counts[0] = at[255];
+    p.counts[4] = sum - at[255];
     p.counts[2] = p.counts[3] = 0;
   }
   __syncthreads();
@@ -154,7 +170,7 @@ __global__ void __launch_bounds__(1024) lin_plan_kernel(const int32_t* __restric
 
 // ---------------------------------------------------------------------------------- kernel
 struct LinParams {
-  CUtensorMap tq, tk, tv;
+  CUtensorMap tq, tk, tv, tg, to;
   LinArgs a;
   Plan p;
 };
@@ -165,25 +181,65 @@ struct Job {
 };
 
 struct Decays {  // of a chunk, in units of log2
-  float G[kC];    // G_i
-  float cf[kC];   // 2^{G at the end of the token's block of 32 - G_i}
-  float wb[4];    // 2^{G_last - G at the end of block b}
-  float a;        // 2^{G_last}
-  float pad[3];
+  float G[kC];   // G_i
+  float cf[kC];  // 2^{G at the end of the token's block of 32 - G_i}
 };
 
+enum { kK, kV, kQ };  // tiles
+// Instances: outputs, outputs with the output stage, states only (the first pass of a split sequence).  The code
+// of a chunk has to stay in the instruction caches: what an instance does not need is not in it.
+enum { kPlain, kGated, kStates };
+// The full kernel has two buffers of each tile; the first pass, without q, three.
+template <bool kFull> constexpr int kKinds = kFull ? 3 : 2;
+template <bool kFull> constexpr uint32_t kBufs = kFull ? 2 : 3;
+
 struct Small {
-  Decays dec[2];
+  Decays dec;
+  float w[2][kC];            // 2^{G_last - G_t}, by the chunk's parity
+  float a[2];                // 2^{G_last}
+  float pad[2];
+  float weight[kD];          // the output stage's
   Job job[2];
-  uint64_t full[kSlots], empty[kSlots];
-  uint64_t job_full[2], job_empty[2], dec_full[2], dec_empty[2];
-  uint64_t scores, weights, keys, kv, state, out, out_free, drain;
+  uint64_t full[2][3];  // [k and q; v][buffer]
+  uint64_t free[3][3];  // [tile][buffer]; in the full kernel only q's: kv and out tell when k and v are free
+  uint64_t job_full[2], job_empty[2], dec_full, dec_empty, w_full[2], w_empty[2];
+  uint64_t scores, inter, ready, out[2], out_free, gate_full, half_full[2], half_free[2], kv[2], kv_read[2], state, drain;
+  uint32_t bad_chunk[4];  // chunk number + 1 with values that are not finite, by its last two bits
   uint32_t tmem;
 };
 constexpr int kSmBytes = kSmSmall + sizeof(Small);
 static_assert(kSmBytes <= 232448, "shared memory");
 
-constexpr int kReaders = 18;  // warps that read a job
+template <bool kFull>
+struct Tiles {  // of chunk n
+  uint32_t buf, phase;
+  __device__ explicit Tiles(uint32_t n) : buf(n % kBufs<kFull>), phase(n / kBufs<kFull>) {}
+  __device__ uint32_t at(int kind) const { return (kind * kBufs<kFull> + buf) * kTile; }
+};
+
+// As bar_wait, with few instructions a poll: most warps wait most of the time, and what their polls issue the
+// others cannot.  Given up after 2^19 polls, of 4 us at most.
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\t.reg .b32 i;\n\t"
+      "mov.b32 i, 0;\n"
+      "POLL%=:\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 P, [%1], %2, 4000;\n\t"
+      "vote.sync.all.pred P, P, 0xffffffff;\n\t"
+      "@P bra DONE%=;\n\t"
+      "add.u32 i, i, 1;\n\t"
+      "setp.lt.u32 P, i, 524288;\n\t"
+      "@P bra POLL%=;\n\t"
+      "setp.ne.u32 P, 0, 0;\n"
+      "DONE%=:\n\t"
+      "selp.b32 %0, 1, 0, P;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+#define LIN_WAIT(bar, parity) do { if (!dead && !wait_for(smem_u32(&(bar)), (parity) & 1)) dead = true; } while (0)
 
 // The jobs that warp 0 hands out, in every other warp.
 struct Jobs {
@@ -192,7 +248,8 @@ struct Jobs {
   bool& dead;
   __device__ Jobs(Small& s_, bool& d) : s(s_), dead(d) {}
   __device__ bool next(Job& j) {
-    if (dead || !bar_wait(&s.job_full[n & 1], (n >> 1) & 1)) { dead = true; return false; }
+    LIN_WAIT(s.job_full[n & 1], n >> 1);
+    if (dead) return false;
     j = s.job[n & 1];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) mbar_arrive(&s.job_empty[n & 1]);
@@ -201,20 +258,17 @@ struct Jobs {
   }
 };
 
-#define LIN_WAIT(bar, parity) do { if (!dead && !bar_wait(&(bar), (parity) & 1)) dead = true; } while (0)
-
 __device__ __forceinline__ int live_rows(const Item& it, int c) { return min(kC, it.len - c * kC); }
 
 template <bool kFull>
 __device__ void load_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
-  constexpr int kEach = kFull ? 3 : 2;  // tiles a chunk
   bool dead = false;
-  uint32_t u = 0, n = 0, left = 0;
+  uint32_t u = 0, n = 0, jobs = 0;
   const int pass = kFull ? 0 : 1;
   const int64_t total = static_cast<int64_t>(p.p.counts[pass]) * p.a.H;
   int64_t t = blockIdx.x;
-  for (;; ++n) {
-    LIN_WAIT(s.job_empty[n & 1], (n >> 1) + 1);
+  for (;; ++jobs) {
+    LIN_WAIT(s.job_empty[jobs & 1], (jobs >> 1) + 1);
     const bool more = t < total && !dead;
     Item it = {};
     int head = -1;
@@ -223,119 +277,123 @@ __device__ void load_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
       head = static_cast<int>(t % p.a.H);
     }
     if (lane == 0) {
-      s.job[n & 1].item = it;
-      s.job[n & 1].head = head;
-      mbar_arrive(&s.job_full[n & 1]);
+      s.job[jobs & 1].item = it;
+      s.job[jobs & 1].head = head;
+      mbar_arrive(&s.job_full[jobs & 1]);
     }
     if (!more) break;
     // the next item's number, known by the time that this one's copies are under way
     int next = 0;
     if (lane == 0) next = atomicAdd(&p.p.counts[2 + pass], 1);
-    for (int c = it.c0; c < it.c1; ++c) {
-      const int row = it.first + c * kC, hq = head / p.a.group;
+    const int hq = head / p.a.group;
+    for (int c = it.c0; c < it.c1; ++c, ++n) {
+      const int row = it.first + c * kC;
+      const Tiles<kFull> tile(n);
 #pragma unroll 1
-      for (int w = 0; w < kEach; ++w, ++u) {
-        const int which = kFull ? w : 2 * w;  // k, q, v
-        const uint32_t slot = u % kSlots;
-        LIN_WAIT(s.empty[slot], u / kSlots + 1);
-        if (static_cast<int>(u) == p.a.stall) { ++left; continue; }
-        if (dead) continue;
+      for (int w = 0; w < kKinds<kFull>; ++w, ++u) {
+        const int kind = w;
+        if (!kFull || kind == kQ) LIN_WAIT(s.free[kind][tile.buf], tile.phase + 1);
+        else if (n > 1) LIN_WAIT(kind == kK ? s.kv[n & 1] : s.out[n & 1], (n >> 1) - 1);
+        if (dead || static_cast<int>(u) == p.a.stall) continue;
         if (lane == 0) {
-          const CUtensorMap* m = which == 0 ? &p.tk : which == 1 ? &p.tq : &p.tv;
-          const int h = which == 2 ? head : hq;
-          uint8_t* dst = sm + slot * kTile;
-          mbar_arrive_expect_tx(&s.full[slot], kTile);
-          tma_load_3d(dst, m, &s.full[slot], 0, h, row);
-          tma_load_3d(dst + kPanel, m, &s.full[slot], 64, h, row);
+          const CUtensorMap* m = kind == kK ? &p.tk : kind == kQ ? &p.tq : &p.tv;
+          const int h = kind == kV ? head : hq;
+          uint8_t* dst = sm + tile.at(kind);
+          uint64_t* full = &s.full[kind == kV][tile.buf];
+          mbar_arrive_expect_tx(full, kTile);
+          tma_load_3d(dst, m, full, 0, h, row);
+          tma_load_3d(dst + kPanel, m, full, 64, h, row);
         }
         __syncwarp();
       }
     }
     t = gridDim.x + static_cast<int64_t>(__shfl_sync(0xffffffffu, next, 0));
   }
-  // the ring's last copies have landed before the block gives its shared memory back
-  if (dead || left) {
-    for (uint32_t i = 0; i < kSlots; ++i) { bar_wait(&s.full[i], 0); bar_wait(&s.full[i], 1); }
-  } else {
-    drain_ring(s.full, kSlots, u);
-  }
+  // the last copies have landed before the block gives its shared memory back; of a barrier without any
+  // (a copy left out) both phases are looked at, one of them for nothing
+  for (int k = 0; k < 2; ++k)
+    for (uint32_t i = 0; i < kBufs<kFull>; ++i) {
+      const uint32_t uses = (n + kBufs<kFull> - 1 - i) / kBufs<kFull>;
+      if (dead || p.a.stall >= 0) { wait_for(smem_u32(&s.full[k][i]), 0); wait_for(smem_u32(&s.full[k][i]), 1); }
+      else if (uses > 0) wait_for(smem_u32(&s.full[k][i]), (uses - 1) & 1);
+    }
   if (dead && lane == 0) report_status(p.a.status, 6 /* KDA_ERR_TIMEOUT */);
+}
+
+// D = A B^T, both K-major tiles of 128 columns.
+__device__ __forceinline__ void product_ss(uint32_t who, uint32_t d, uint64_t a, uint64_t b) {
+  constexpr uint32_t id = idesc_f16(128, 128, true, false, false);
+#pragma unroll
+  for (uint32_t kk = 0; kk < 8; ++kk) {
+    const uint64_t off = ((kk & 4) << 8) | ((kk & 3) << 1);  // 16-byte units: panels of 64 columns, 16 columns a step
+    mma_f16_if(who, d, a + off, b + off, id, kk);
+  }
+}
+// D (+)= A B, A in tensor memory, B rows of an N-major tile.
+template <uint32_t kSteps>
+__device__ __forceinline__ void product_ts(uint32_t who, uint32_t d, uint32_t a, uint64_t b, uint32_t more) {
+  constexpr uint32_t id = idesc_f16(128, 128, true, false, true);
+#pragma unroll
+  for (uint32_t kk = 0; kk < kSteps; ++kk) mma_f16_ta_if(who, d, a + 8 * kk, b + 128 * kk, id, more | kk);
 }
 
 template <bool kFull>
 __device__ void mma_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
-  constexpr int kEach = kFull ? 3 : 2;
-  constexpr uint32_t id_kk = idesc_f16(128, 128, true, false, false), id_km = idesc_f16(128, 128, true, false, true),
-                     id_mm = idesc_f16(128, 128, true, true, true);
   bool dead = false;
   Jobs jobs(s, dead);
   Job j;
-  uint32_t n = 0;
+  uint32_t n = 0, u = 0;
   const uint32_t who = elect_one_sync();
-  const uint64_t d_k = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);          // K-major tiles
-  const uint64_t d_m = smem_desc(smem_u32(sm), kPanel, 1024, kSwizzle128B);      // the same, M- or N-major
-  auto at = [](uint32_t slot) { return static_cast<uint64_t>(slot * kTile >> 4); };
+  const uint64_t d_k = smem_desc(smem_u32(sm), 16, 1024, kSwizzle128B);      // K-major tiles
+  const uint64_t d_m = smem_desc(smem_u32(sm), kPanel, 1024, kSwizzle128B);  // the same, N-major
   while (jobs.next(j)) {
     for (int c = j.item.c0; c < j.item.c1; ++c, ++n) {
-      const uint32_t uk = kEach * n, uq = uk + 1, uv = uk + kEach - 1;
-      const uint32_t sk = uk % kSlots, sq = uq % kSlots, sv = uv % kSlots;
-      LIN_WAIT(s.full[sk], uk / kSlots);
+      const Tiles<kFull> tile(n);
+      const uint64_t tk = tile.at(kK) >> 4, tq = tile.at(kQ) >> 4, tv = tile.at(kV) >> 4;
+      LIN_WAIT(s.full[0][tile.buf], tile.phase);
       if constexpr (kFull) {
-        LIN_WAIT(s.full[sq], uq / kSlots);
-        if (n > 0) {  // the last chunk's outputs are read: its scores, weights and values are free
-          LIN_WAIT(s.out_free, n - 1);
-          if (lane == 0) mbar_arrive(&s.empty[(uv - kEach) % kSlots]);
-        }
+        if (n > 0) LIN_WAIT(s.out[(n - 1) & 1], (n - 1) >> 1);  // the last weights, where the scores go, are used
         tc_fence_after();
-        if (!dead) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk) {
-            const uint64_t off = ((kk >> 2) * kPanel + 32 * (kk & 3)) >> 4;
-            mma_f16_if(who, kTS, d_k + at(sq) + off, d_k + at(sk) + off, id_kk, kk > 0);
-          }
-          mma_commit_if(who, &s.scores);
-        }
-      }
-      LIN_WAIT(s.state, n);  // the state in front of the chunk is in shared memory, the last K^T V is read
-      tc_fence_after();
-      if constexpr (kFull) {
-        if (!dead) {
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16_if(who, kTI, d_k + at(sq) + (((kk >> 2) * kPanel + 32 * (kk & 3)) >> 4),
-                       d_m + ((kSmState + kk * 2048) >> 4), id_km, kk > 0);
-          mma_commit_if(who, &s.empty[sq]);
-        }
-      }
-      LIN_WAIT(s.full[sv], uv / kSlots);
-      LIN_WAIT(s.keys, n);
-      tc_fence_after();
-      if (!dead) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_f16_if(who, kTKV, d_m + at(sk) + ((kk * 2048) >> 4), d_m + at(sv) + ((kk * 2048) >> 4), id_mm, kk > 0);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_f16_if(who, kTKV, d_m + ((kSmLo + kk * 2048) >> 4), d_m + at(sv) + ((kk * 2048) >> 4), id_mm, 1);
-        mma_commit_if(who, &s.kv);
-        mma_commit_if(who, &s.empty[sk]);
-        if constexpr (!kFull) mma_commit_if(who, &s.empty[sv]);
-      }
-      if constexpr (kFull) {
-        LIN_WAIT(s.weights, n);
+        if (dead) break;
+        product_ss(who, kTS, d_k + tq, d_k + tk);
+        mma_commit_if(who, &s.scores);
+        LIN_WAIT(s.state, n);  // the state in front of the chunk is in shared memory, the last K^T V is read
+        if (n > 0) LIN_WAIT(s.out_free, n - 1);
         tc_fence_after();
-        if (!dead) {
+        if (dead) break;
+        product_ss(who, kTO, d_k + tq, d_k + (kSmState >> 4));
+        mma_commit_if(who, &s.inter);
+      }
+      if (!kFull && n > 1) LIN_WAIT(s.kv_read[n & 1], (n >> 1) - 1);  // K^T V of the last chunk but one is read
+      // (the values' parts)^T K, 64 tokens at a time
+#pragma unroll 1
+      for (uint32_t h = 0; h < 2; ++h) {
+        if constexpr (kFull) LIN_WAIT(s.half_full[0], 2 * n + h);
+        else LIN_WAIT(s.half_full[h], n);
+        tc_fence_after();
+        if (dead) break;
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_f16_ta_if(who, kTO, kTS + 8 * kk, d_m + at(sv) + ((kk * 2048) >> 4), id_km, kk > 0);
-          mma_commit_if(who, &s.out);
+        for (uint32_t part = 0; part < 3; ++part, ++u) {
+          product_ts<4>(who, kv_column<kFull>(n), unit_column<kFull>(u), d_m + tk + 512 * h, h | part);
+          if (part == 1) mma_commit_if(who, &s.half_free[kFull ? 0 : h]);  // with the one before, room for the next three
         }
+      }
+      if (dead) break;
+      mma_commit_if(who, &s.kv[n & 1]);
+      if constexpr (!kFull) mma_commit_if(who, &s.free[kK][tile.buf]);
+      if constexpr (kFull) {
+        LIN_WAIT(s.ready, n);  // v has landed before its parts were made
+        tc_fence_after();
+        if (dead) break;
+        product_ts<8>(who, kTO, kTS, d_m + tv, 1);
+        mma_commit_if(who, &s.out[n & 1]);
       }
     }
+    if (dead) break;
   }
   // products in flight end before the tensor memory is given back
   mma_commit_if(who, &s.drain);
-  bar_wait(&s.drain, 0);
+  wait_for(smem_u32(&s.drain), 0);
   if (dead && lane == 0) report_status(p.a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
@@ -382,245 +440,385 @@ __device__ void decay_warp(const LinParams& p, Small& s, int lane) {
       const long long end = __shfl_sync(0xffffffffu, sum, lane | 7);  // of the block of 32 tokens
       auto real = [](long long d) { return static_cast<float>(d) * (1.f / kUnit); };
       const float none = __int_as_float(0x7fffffff);
-      float v[4], f[4];
+      float v[4], f[4], w[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         G[i] += sum - own;
         v[i] = 4 * lane + i >= nan_at ? none : real(G[i]);
         f[i] = exp2f(real(end - G[i]));
+        w[i] = exp2f(real(last - G[i]));
       }
-      LIN_WAIT(s.dec_empty[n & 1], (n >> 1) + 1);
-      Decays& d = s.dec[n & 1];
-      *reinterpret_cast<float4*>(&d.G[4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-      *reinterpret_cast<float4*>(&d.cf[4 * lane]) = make_float4(f[0], f[1], f[2], f[3]);
-      if ((lane & 7) == 7) d.wb[lane >> 3] = exp2f(real(last - end));
-      if (lane == 0) d.a = nan_at < kC ? none : exp2f(real(last));
+      LIN_WAIT(s.w_empty[n & 1], (n >> 1) + 1);
+      *reinterpret_cast<float4*>(&s.w[n & 1][4 * lane]) = make_float4(w[0], w[1], w[2], w[3]);
+      if (lane == 0) s.a[n & 1] = nan_at < kC ? none : exp2f(real(last));
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.dec_full[n & 1]);
+      if (lane == 0) mbar_arrive(&s.w_full[n & 1]);
+      if constexpr (kFull) {
+        LIN_WAIT(s.dec_empty, n + 1);
+        *reinterpret_cast<float4*>(&s.dec.G[4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
+        *reinterpret_cast<float4*>(&s.dec.cf[4 * lane]) = make_float4(f[0], f[1], f[2], f[3]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.dec_full);
+      }
     }
   }
   if (dead && lane == 0) report_status(p.a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
-// What is not finite in 32 columns of P V, once more from the weights and values of the tokens that a row
-// sees.  In place: the caller's registers stay out of memory.
-__device__ __noinline__ void seen_only(uint32_t v, uint32_t tl, int row, int block) {
-  float x[32], was[32];
-#pragma unroll
-  for (int e = 0; e < 32; ++e) x[e] = 0.f;
-  const uint32_t base = v + (block >> 1) * kPanel;
-#pragma unroll 1
-  for (int j = 0; j < kC; ++j) {
-    uint32_t pair;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;\n" : "=r"(pair) : "r"(tl + kTS + (j >> 1)));
-    const float w = __uint_as_float(j & 1 ? pair & 0xffff0000u : pair << 16);
-    if (j <= row) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint4 u = lds128(base + sw128(j, (block & 1) * 64 + 16 * q));
-        const uint32_t b[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          x[8 * q + 2 * e] = fmaf(w, __uint_as_float(b[e] << 16), x[8 * q + 2 * e]);
-          x[8 * q + 2 * e + 1] = fmaf(w, __uint_as_float(b[e] & 0xffff0000u), x[8 * q + 2 * e + 1]);
-        }
-      }
-    }
-    __syncwarp();
-  }
-  tmem_ld32(tl + kTO + 32 * block, was);
-#pragma unroll
-  for (int e = 0; e < 32; ++e) x[e] = fabsf(was[e]) < INFINITY ? was[e] : x[e];
-  tmem_st32(tl + kTO + 32 * block, x);
-  tmem_wait_st();
+// 32 rows x 64 channels from shared memory to o.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];\n" ::"l"(
+                   reinterpret_cast<uint64_t>(tmap)),
+               "r"(smem_u32(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
 }
 
-__device__ void weight_warps(const LinParams& p, uint8_t* sm, Small& s, int w, int lane) {
+// The output stage's gate, into q's tile when q is used.
+__device__ void gate_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
+  bool dead = false;
+  Jobs jobs(s, dead);
+  Job j;
+  uint32_t n = 0;
+  while (jobs.next(j)) {
+    if (lane == 0 && j.item.c0 < j.item.c1) {
+      tma_prefetch_3d(&p.tg, 0, j.head, j.item.first + j.item.c0 * kC);
+      tma_prefetch_3d(&p.tg, 64, j.head, j.item.first + j.item.c0 * kC);
+    }
+    for (int c = j.item.c0; c < j.item.c1; ++c, ++n) {
+      const Tiles<true> tile(n);
+      const int row = j.item.first + c * kC;
+      if (lane == 0 && c + 1 < j.item.c1) {  // the next chunk's, so that its copy comes from L2
+        tma_prefetch_3d(&p.tg, 0, j.head, row + kC);
+        tma_prefetch_3d(&p.tg, 64, j.head, row + kC);
+      }
+      LIN_WAIT(s.inter, n);
+      if (lane == 0 && !dead) {
+        mbar_arrive_expect_tx(&s.gate_full, kTile);
+        tma_load_3d(sm + tile.at(kQ), &p.tg, &s.gate_full, 0, j.head, row);
+        tma_load_3d(sm + tile.at(kQ) + kPanel, &p.tg, &s.gate_full, 64, j.head, row);
+      }
+      __syncwarp();
+      LIN_WAIT(s.gate_full, n);  // one at a time: the last has landed when the warp ends
+    }
+  }
+  if (dead && lane == 0) report_status(p.a.status, 6 /* KDA_ERR_TIMEOUT */);
+}
+
+// sigmoid(g): the approximations are within 2^-21 of it, and 1 / inf is 0.
+__device__ __forceinline__ float open_gate(float g) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + exp2_fast(-1.4426950408889634f * g)));
+  return y;
+}
+
+// 32 columns of a row times e, in place.
+__device__ __forceinline__ void scale_block(uint32_t at, float e) {
+  float x[32];
+  tmem_ld32(at, x);
+  const uint64_t e2 = f32x2(e, e);
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    const float2 y = unpack_f32x2(mul_f32x2(f32x2(x[i], x[i + 1]), e2));
+    x[i] = y.x;
+    x[i + 1] = y.y;
+  }
+  tmem_st32(at, x);
+}
+
+// NaN for the rows that see a value that is not finite, in its channel (cold).
+__device__ __noinline__ void poison(uint32_t tl, const uint32_t* noted, uint32_t n, int i) {
+#pragma unroll 1
+  for (int c = 0; c < kD; ++c) {
+    const uint32_t m = __ldcg(noted + c);
+    const bool hit = (m >> 8) == n && 255 - static_cast<int>(m & 255) <= i;
+    if (!__any_sync(0xffffffffu, hit)) continue;
+    uint32_t x;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;\n" : "=r"(x) : "r"(tl + c));
+    if (hit) x = 0x7fffffffu;
+    __syncwarp();
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\ntcgen05.wait::st.sync.aligned;\n" ::"r"(tl + c), "r"(x) : "memory");
+  }
+}
+
+// A row of the staged outputs, where not all of a warp's rows are the sequence's.
+__device__ __noinline__ void copy_row(uint32_t stage, uint4* dst, int i) {
+#pragma unroll 1
+  for (int q = 0; q < 16; ++q) dst[q] = lds128(stage + (q >> 3) * kPanel + sw128(i, 16 * (q & 7)));
+}
+
+template <bool kGate>
+__device__ void output_warps(const LinParams& p, uint8_t* sm, Small& s, int w, int lane) {
   const LinArgs& a = p.a;
   bool dead = false;
   Jobs jobs(s, dead);
   Job j;
   uint32_t n = 0;
-  const uint32_t tl = static_cast<uint32_t>(w) << 21;
+  const uint32_t ts = (static_cast<uint32_t>(w) << 21) + kTS, tl = (static_cast<uint32_t>(w) << 21) + kTO;
   const int i = 32 * w + lane;
+  int staged = -1;  // the buffer whose rows are on their way to o
+  auto release = [&] {
+    if (staged >= 0 && lane == 0) {
+      asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+      mbar_arrive(&s.free[kQ][staged]);
+    }
+    staged = -1;
+    __syncwarp();
+  };
   while (jobs.next(j)) {
     for (int c = j.item.c0; c < j.item.c1; ++c, ++n) {
+      const Tiles<true> tile(n);
       // ---- weights, 32 columns at a time, over the scores of columns that are read already
-      LIN_WAIT(s.dec_full[n & 1], n >> 1);
-      const Decays& d = s.dec[n & 1];
+      LIN_WAIT(s.dec_full, n);
+      const Decays& d = s.dec;
       const float G = d.G[i];
       LIN_WAIT(s.scores, n);
       tc_fence_after();
 #pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
-        float pk[16];
-        if (b > w) {
+      for (int b = 0; b < w; ++b) {  // D_ij = 2^{G_i - G at the block's end} 2^{G at the block's end - G_j}
+        float x[32];
+        uint32_t pk[16];
+        tmem_ld32(ts + 32 * b, x);
+        const float rf = exp2_fast(G - d.G[32 * b + 31]);
+        const uint64_t r2 = f32x2(rf, rf);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0.f;
-        } else {
-          float x[32];
-          tmem_ld32(tl + kTS + 32 * b, x);
-          if (b < w) {
-            const float rf = exp2_fast(G - d.G[32 * b + 31]);
-            const uint64_t r2 = f32x2(rf, rf);
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&d.cf[32 * b + e]);
-              pk[e / 2] = __uint_as_float(bf162_of(mul_f32x2(f32x2(x[e], x[e + 1]), mul_f32x2(r2, f32x2(f.x, f.y)))));
-              pk[e / 2 + 1] = __uint_as_float(bf162_of(mul_f32x2(f32x2(x[e + 2], x[e + 3]), mul_f32x2(r2, f32x2(f.z, f.w)))));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 f = *reinterpret_cast<const float4*>(&d.G[32 * b + e]);
-              const float y0 = e <= lane ? x[e] * exp2_fast(G - f.x) : 0.f;
-              const float y1 = e + 1 <= lane ? x[e + 1] * exp2_fast(G - f.y) : 0.f;
-              const float y2 = e + 2 <= lane ? x[e + 2] * exp2_fast(G - f.z) : 0.f;
-              const float y3 = e + 3 <= lane ? x[e + 3] * exp2_fast(G - f.w) : 0.f;
-              pk[e / 2] = __uint_as_float(pack_bf162(y0, y1));
-              pk[e / 2 + 1] = __uint_as_float(pack_bf162(y2, y3));
-            }
-          }
+        for (int e = 0; e < 32; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&d.cf[32 * b + e]);
+          pk[e / 2] = bf162_of(mul_f32x2(f32x2(x[e], x[e + 1]), mul_f32x2(r2, f32x2(f.x, f.y))));
+          pk[e / 2 + 1] = bf162_of(mul_f32x2(f32x2(x[e + 2], x[e + 3]), mul_f32x2(r2, f32x2(f.z, f.w))));
         }
-        tmem_st16(tl + kTS + 16 * b, pk);
+        tmem_st16(ts + 16 * b, reinterpret_cast<const float(&)[16]>(pk));
       }
+      {
+        float x[32];
+        uint32_t pk[16];
+        tmem_ld32(ts + 32 * w, x);
+#pragma unroll
+        for (int e = 0; e < 32; e += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&d.G[32 * w + e]);
+          const float y0 = e <= lane ? x[e] * exp2_fast(G - f.x) : 0.f;
+          const float y1 = e + 1 <= lane ? x[e + 1] * exp2_fast(G - f.y) : 0.f;
+          const float y2 = e + 2 <= lane ? x[e + 2] * exp2_fast(G - f.z) : 0.f;
+          const float y3 = e + 3 <= lane ? x[e + 3] * exp2_fast(G - f.w) : 0.f;
+          pk[e / 2] = pack_bf162(y0, y1);
+          pk[e / 2 + 1] = pack_bf162(y2, y3);
+        }
+        tmem_st16(ts + 16 * w, reinterpret_cast<const float(&)[16]>(pk));
+#pragma unroll
+        for (int e = 0; e < 16; ++e) pk[e] = 0;
+#pragma unroll 1
+        for (int b = w + 1; b < 4; ++b) tmem_st16(ts + 16 * b, reinterpret_cast<const float(&)[16]>(pk));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.dec_empty);
+      release();  // the last chunk's rows: here, since their copy takes as long as this
+      // ---- Q S times e^G
+      const float eg = exp2f(G);
+      LIN_WAIT(s.inter, n);
+      tc_fence_after();
+#pragma unroll 1
+      for (int b = 0; b < 4; ++b) scale_block(tl + 32 * b, eg);
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s.weights);
-        mbar_arrive(&s.dec_empty[n & 1]);
-      }
+      if (lane == 0) mbar_arrive(&s.ready);
       // ---- outputs
-      const uint32_t uv = 3 * n + 2, sv = uv % kSlots;
-      const bool live = i < live_rows(j.item, c);
+      const int live = live_rows(j.item, c);
       const int64_t t = static_cast<int64_t>(j.item.first) + c * kC + i;
-      const float eg = exp2_fast(G);
-      LIN_WAIT(s.full[sv], uv / kSlots);  // for the values, should they be needed
-      LIN_WAIT(s.out, n);
+      if constexpr (kGate) LIN_WAIT(s.gate_full, n);
+      LIN_WAIT(s.out[n & 1], n >> 1);
       tc_fence_after();
-      auto block = [&](int b, float (&x)[32]) {  // 32 columns of the row before scale
-        float y[32];
-        tmem_ld32_async(tl + kTO + 32 * b, x);
-        tmem_ld32_async(tl + kTI + 32 * b, y);
-        tmem_wait_ld32(x);
-        tmem_wait_ld32(y);
-        float z = 0.f;
-#pragma unroll
-        for (int e = 0; e < 32; ++e) z = fmaf(x[e], 0.f, z);
-        if (__any_sync(0xffffffffu, live && z != 0.f)) {
-          seen_only(smem_u32(sm) + sv * kTile, tl, i, b);
-          tmem_ld32(tl + kTO + 32 * b, x);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; ++e) x[e] = fmaf(eg, y[e], x[e]);
-      };
+      if (s.bad_chunk[n & 3] == n + 1) poison(tl, p.p.bad + 4 * kD * blockIdx.x + kD * (n & 3), n, i);
       float f = a.scale;
-      if (a.gate) {
-        float ss = 0.f;
+      if constexpr (kGate) {
+        float s0 = 0.f, s1 = 0.f;
 #pragma unroll 1
         for (int b = 0; b < 4; ++b) {
           float x[32];
-          block(b, x);
+          tmem_ld32(tl + 32 * b, x);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) { x[e] *= a.scale; ss = fmaf(x[e], x[e], ss); }
+          for (int e = 0; e < 32; e += 2) { s0 = fmaf(x[e], x[e], s0); s1 = fmaf(x[e + 1], x[e + 1], s1); }
         }
-        f *= 1.f / sqrtf(ss * (1.f / kD) + a.eps);
+        f *= 1.f / sqrtf((s0 + s1) * a.scale * a.scale * (1.f / kD) + a.eps);
       }
-      uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (t * a.H + j.head) * kD);
-      const uint4* gate = a.gate ? reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.gate) + t * a.gate_stride[1] + j.head * a.gate_stride[2]) : nullptr;
+      const uint32_t stage = smem_u32(sm) + tile.at(kQ);  // q is used: its tile takes the outputs
 #pragma unroll 1
       for (int b = 0; b < 4; ++b) {
         float x[32];
-        block(b, x);
+        tmem_ld32(tl + 32 * b, x);
         if (b == 3) {
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s.out_free);
         }
-        if (live) {
+        const uint32_t at = stage + (b >> 1) * kPanel + i * 128, turn = (i & 7) << 4;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
+          const uint32_t to = at + (((b & 1) * 64 + 16 * q) ^ turn);
           float y[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = x[8 * q + e] * f;
-          if (a.gate) {
-            const uint4 u = gate[4 * b + q];
+          for (int e = 0; e < 8; e += 2) {
+            const float2 z = unpack_f32x2(mul_f32x2(f32x2(x[8 * q + e], x[8 * q + e + 1]), f32x2(f, f)));
+            y[e] = z.x;
+            y[e + 1] = z.y;
+          }
+          if constexpr (kGate) {
+            const uint4 u = lds128(to);
             const uint32_t bits[4] = {u.x, u.y, u.z, u.w};
+            const float4 w0 = *reinterpret_cast<const float4*>(&s.weight[32 * b + 8 * q]);
+            const float4 w1 = *reinterpret_cast<const float4*>(&s.weight[32 * b + 8 * q + 4]);
+            const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              y[2 * e] = __fdividef(y[2 * e], 1.f + __expf(-__uint_as_float(bits[e] << 16)));
-              y[2 * e + 1] = __fdividef(y[2 * e + 1], 1.f + __expf(-__uint_as_float(bits[e] & 0xffff0000u)));
-            }
-            if (a.norm_weight) {
-              const float4 w0 = reinterpret_cast<const float4*>(a.norm_weight)[8 * b + 2 * q];
-              const float4 w1 = reinterpret_cast<const float4*>(a.norm_weight)[8 * b + 2 * q + 1];
-              y[0] *= w0.x; y[1] *= w0.y; y[2] *= w0.z; y[3] *= w0.w; y[4] *= w1.x; y[5] *= w1.y; y[6] *= w1.z; y[7] *= w1.w;
+              y[2 * e] *= wt[2 * e] * open_gate(__uint_as_float(bits[e] << 16));
+              y[2 * e + 1] *= wt[2 * e + 1] * open_gate(__uint_as_float(bits[e] & 0xffff0000u));
             }
           }
-          dst[4 * b + q] = make_uint4(pack_bf162(y[0], y[1]), pack_bf162(y[2], y[3]), pack_bf162(y[4], y[5]), pack_bf162(y[6], y[7]));
-        }
-        }
-        __syncwarp();
-      }
-    }
-  }
-  if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
-}
-
-// Decayed keys: hi = bf16(w k) in place, lo = bf16(w k - hi) in its own tile.  Rows past the sequence's end are
-// cleared, the values' too: what stands there must not meet the state.
-template <bool kFull>
-__device__ void key_warps(const LinParams& p, uint8_t* sm, Small& s, int tid) {
-  constexpr int kEach = kFull ? 3 : 2;
-  bool dead = false;
-  Jobs jobs(s, dead);
-  Job j;
-  uint32_t n = 0;
-  const int lane = tid & 31;
-  while (jobs.next(j)) {
-    for (int c = j.item.c0; c < j.item.c1; ++c, ++n) {
-      const uint32_t uk = kEach * n, uv = uk + kEach - 1, sk = uk % kSlots, sv = uv % kSlots;
-      const int live = live_rows(j.item, c);
-      LIN_WAIT(s.dec_full[n & 1], n >> 1);
-      LIN_WAIT(s.full[sk], uk / kSlots);
-      if constexpr (kFull) LIN_WAIT(s.scores, n);   // Q K^T has read the keys
-      if (n > 0) LIN_WAIT(s.kv, n - 1);             // the last K^T V has read the low parts
-      if (live < kC) LIN_WAIT(s.full[sv], uv / kSlots);
-      const Decays& d = s.dec[n & 1];
-      const uint32_t hi = smem_u32(sm) + sk * kTile, lo = smem_u32(sm) + kSmLo, v = smem_u32(sm) + sv * kTile;
-      if (!dead) {
-#pragma unroll 4
-        for (int it = 0; it < 16; ++it) {
-          const int row = 8 * it + (tid >> 4), ch = tid & 15;
-          const uint32_t at = (ch >> 3) * kPanel + sw128(row, 16 * (ch & 7));
-          if (row >= live) {
-            sts128(hi + at, make_uint4(0, 0, 0, 0));
-            sts128(lo + at, make_uint4(0, 0, 0, 0));
-            sts128(v + at, make_uint4(0, 0, 0, 0));
-            continue;
-          }
-          const float w = d.cf[row] * d.wb[row >> 5];
-          const uint4 u = lds128(hi + at);
-          const uint32_t x[4] = {u.x, u.y, u.z, u.w};
-          uint32_t h[4], l[4];
-          const uint64_t w2 = f32x2(w, w);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint64_t k2 = f32x2(__uint_as_float(x[e] << 16), __uint_as_float(x[e] & 0xffff0000u));
-            h[e] = bf162_of(mul_f32x2(k2, w2));
-            l[e] = bf162_of(fma_f32x2(k2, w2, f32x2(-__uint_as_float(h[e] << 16), -__uint_as_float(h[e] & 0xffff0000u))));
-          }
-          sts128(hi + at, make_uint4(h[0], h[1], h[2], h[3]));
-          sts128(lo + at, make_uint4(l[0], l[1], l[2], l[3]));
+          sts128(to, make_uint4(pack_bf162(y[0], y[1]), pack_bf162(y[2], y[3]), pack_bf162(y[4], y[5]), pack_bf162(y[6], y[7])));
         }
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&s.keys);
-        mbar_arrive(&s.dec_empty[n & 1]);
+      if (32 * w + 32 <= live) {
+        if (lane == 0 && !dead) {
+          const uint8_t* src = sm + tile.at(kQ) + w * 4096;
+          tma_store_3d(&p.to, src, 0, j.head, static_cast<int>(t));
+          tma_store_3d(&p.to, src + kPanel, 64, j.head, static_cast<int>(t));
+          asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+        }
+      } else if (i < live && !dead) {
+        copy_row(stage, reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (t * a.H + j.head) * kD), i);
       }
+      __syncwarp();
+      staged = static_cast<int>(tile.buf);
+    }
+  }
+  release();
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+  if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
+}
+
+// A pair of bf16 as two floats.
+__device__ __forceinline__ uint64_t floats(uint32_t u) {
+  return f32x2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// 8 x 8 tiles of 16-bit values, transposed: lanes 8 m .. 8 m + 7 point to the rows of tile m; of each tile a lane gets
+// column lane / 4, rows 2 (lane % 4) and the next.
+__device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// 16 lanes x 16 columns of tensor memory: registers 2 k and 2 k + 1 are column 4 k + lane % 4 of lanes lane / 4 and
+// lane / 4 + 8.
+__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&u)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(u[0]), "r"(u[1]),
+               "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+               : "memory");
+}
+
+// Values of a warp's 32 channels and 32 tokens that are not finite, cleared in the tile and noted (cold):
+// chunk number << 8 | 255 - the first such token of a channel.
+__device__ __noinline__ void clear_bad(uint32_t tile, uint32_t* noted, uint32_t* bad_chunk, uint32_t n, int w, int t0, int lane) {
+  const int ch = 32 * w + lane;
+  const uint32_t base = tile + (ch >> 6) * kPanel;
+  for (int t = t0; t < t0 + 32; ++t) {
+    const uint32_t at = base + sw128(t, 2 * (ch & 63));
+    uint16_t x;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
+    if ((x & 0x7f80) != 0x7f80) continue;
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0)) : "memory");
+    atomicMax(noted + kD * (n & 3) + ch, n << 8 | static_cast<uint32_t>(255 - t));
+  }
+  __threadfence();
+  __syncwarp();
+  if (lane == 0) bad_chunk[n & 3] = n + 1;
+}
+
+// Decayed values, transposed: y = 2^{G_last - G_t} v_t as hi + mid + low, each the nearest bf16 of what is left, in tensor
+// memory [channel][token].
+// Rows past the sequence's end are cleared in the tiles of k and v: what stands there must not meet the
+// state, or P V.
+template <bool kFull>
+__device__ void value_warps(const LinParams& p, uint8_t* sm, Small& s, int w, int lane) {
+  bool dead = false;
+  Jobs jobs(s, dead);
+  Job j;
+  uint32_t n = 0, u = 0;
+  const uint64_t minus = f32x2(-1.f, -1.f);
+  const int q = w & 3, side = w >> 2;  // channels 32 q .. + 31; tokens 32 side .. + 31 of each 64
+  uint32_t* noted = p.p.bad + 4 * kD * blockIdx.x;
+  while (jobs.next(j)) {
+    for (int c = j.item.c0; c < j.item.c1; ++c, ++n) {
+      const Tiles<kFull> tile(n);
+      const int live = live_rows(j.item, c);
+      const uint32_t v = smem_u32(sm) + tile.at(kV);
+      LIN_WAIT(s.full[1][tile.buf], tile.phase);
+      if (live < kC) {
+        LIN_WAIT(s.full[0][tile.buf], tile.phase);
+        if constexpr (kFull) LIN_WAIT(s.scores, n);  // Q K^T has read the keys
+        const uint32_t k = smem_u32(sm) + tile.at(kK);
+        if (!dead)
+          for (int e = lane; e < 4 * 64; e += 32) {  // the warp's tokens, 64 bytes of each
+            const int row = (e >> 2 & 31) + 32 * side + 64 * (e >> 7);
+            if (row < live) continue;
+            const uint32_t at = (q >> 1) * kPanel + sw128(row, 64 * (q & 1) + 16 * (e & 3));
+            sts128(k + at, make_uint4(0, 0, 0, 0));
+            sts128(v + at, make_uint4(0, 0, 0, 0));
+          }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      LIN_WAIT(s.w_full[n & 1], n >> 1);
+      const float* wp = &s.w[n & 1][2 * (lane & 3)];
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        const int t0 = 64 * h + 32 * side;
+        uint32_t part[3][2][8];  // [part][16 channels][..]
+        uint64_t any = f32x2(0.f, 0.f);  // NaN if a value is not finite: what is left of it is NaN
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {  // 8 tokens, 32 channels
+          uint32_t r[4];
+          const int ch = 32 * q + 8 * (lane >> 3);
+          ldsm4_trans(v + (ch >> 6) * kPanel + sw128(t0 + 8 * b + (lane & 7), 2 * (ch & 63)), r);
+          const uint64_t f = *reinterpret_cast<const uint64_t*>(wp + t0 + 8 * b);
+#pragma unroll
+          for (int m = 0; m < 4; ++m) {
+            uint64_t y = mul_f32x2(floats(r[m]), f);
+            const uint32_t hi = bf162_of(y);
+            y = fma_f32x2(floats(hi), minus, y);
+            const uint32_t mid = bf162_of(y);
+            y = fma_f32x2(floats(mid), minus, y);
+            any = add_f32x2(any, y);
+            part[0][m >> 1][2 * b + (m & 1)] = hi;
+            part[1][m >> 1][2 * b + (m & 1)] = mid;
+            part[2][m >> 1][2 * b + (m & 1)] = bf162_of(y);
+          }
+        }
+        const float2 left = unpack_f32x2(any);
+        if (kFull && __any_sync(0xffffffffu, left.x + left.y != left.x + left.y)) {
+          clear_bad(v, noted, s.bad_chunk, n, q, t0, lane);
+          fence_proxy_async_smem();
+        }
+        if constexpr (kFull) { if (u > 0) LIN_WAIT(s.half_free[0], 2 * n + h - 1); }
+        else { if (n > 0) LIN_WAIT(s.half_free[h], n - 1); }
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const uint32_t at = (static_cast<uint32_t>(q) << 21) + unit_column<kFull>(u + k) + 16 * side;
+          tmem_st_16x128b_x4(at, part[k][0]);
+          tmem_st_16x128b_x4(at + (16u << 16), part[k][1]);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.half_full[kFull ? 0 : h]);
+        u += 3;
+      }
+      if (lane == 0) {
+        mbar_arrive(&s.w_empty[n & 1]);
+        if (!kFull) mbar_arrive(&s.free[kV][tile.buf]);
+      }
+      __syncwarp();
     }
   }
   if (dead && lane == 0) report_status(p.a.status, 6 /* KDA_ERR_TIMEOUT */);
@@ -633,86 +831,103 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
   Jobs jobs(s, dead);
   Job j;
   uint32_t n = 0;
-  const int row = 32 * (w & 3) + lane, half = w >> 2;
-  const uint32_t tl = (static_cast<uint32_t>(w & 3) << 21) + kTKV + 64 * half;
+  const int ch = 32 * (w & 3) + lane, half = w >> 2;  // channel of v: a column of the state; rows 64 half ..
+  const uint32_t tl = (static_cast<uint32_t>(w & 3) << 21) + 64 * half;
   const uint32_t copy = smem_u32(sm) + kSmState + half * kPanel;
+  constexpr int kHalf = kD / 2;
   while (jobs.next(j)) {
     const Item& it = j.item;
-    const int64_t mine = row * kD + 64 * half;
+    const int mine = half * kHalf * kD + ch;
     auto slot = [&](int k) { return p.p.slots + (static_cast<int64_t>(it.base + k) * a.H + j.head) * kStateFloats + mine; };
-    float S[64], A = 1.f;
-#pragma unroll
-    for (int e = 0; e < 64; ++e) S[e] = 0.f;
+    const int64_t unit = (static_cast<int64_t>(it.seq) * a.H + j.head) * kStateFloats + mine;
+    float S[kHalf], A = 1.f;
     auto load = [&](const float* src) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const float4 x = reinterpret_cast<const float4*>(src)[e];
-        S[4 * e] = x.x; S[4 * e + 1] = x.y; S[4 * e + 2] = x.z; S[4 * e + 3] = x.w;
-      }
+      for (int e = 0; e < kHalf; ++e) S[e] = src[e * kD];
     };
     auto store = [&](float* dst) {
 #pragma unroll
-      for (int e = 0; e < 16; ++e) reinterpret_cast<float4*>(dst)[e] = make_float4(S[4 * e], S[4 * e + 1], S[4 * e + 2], S[4 * e + 3]);
+      for (int e = 0; e < kHalf; ++e) dst[e * kD] = S[e];
     };
-    if (it.seg == 0) {
-      if (a.S_in) {
-        // the second pass of a split sequence reads the copy: S_out may be S_in
-        load(kFull && it.base >= 0 ? slot(0) : a.S_in + (static_cast<int64_t>(it.seq) * a.H + j.head) * kStateFloats + mine);
-        if (!kFull) store(slot(0));
-      }
-    } else if (kFull) {
+    if (it.seg == 0 && a.S_in) {
+      // the second pass of a split sequence reads the copy: S_out may be S_in
+      load(kFull && it.base >= 0 ? slot(0) : a.S_in + unit);
+      if (!kFull) store(slot(0));
+    } else if (kFull && it.seg > 0) {
       load(slot(1));
 #pragma unroll 1
       for (int k = 1; k < it.seg; ++k) {
         const float f = p.p.decay[static_cast<int64_t>(it.base + 1 + k) * a.H + j.head];
-        const float4* src = reinterpret_cast<const float4*>(slot(1 + k));
+        const float* src = slot(1 + k);
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const float4 x = src[e];
-          S[4 * e] = fmaf(f, S[4 * e], x.x); S[4 * e + 1] = fmaf(f, S[4 * e + 1], x.y);
-          S[4 * e + 2] = fmaf(f, S[4 * e + 2], x.z); S[4 * e + 3] = fmaf(f, S[4 * e + 3], x.w);
-        }
+        for (int e = 0; e < kHalf; ++e) S[e] = fmaf(f, S[e], src[e * kD]);
       }
+    } else {
+#pragma unroll
+      for (int e = 0; e < kHalf; ++e) S[e] = 0.f;
     }
     for (int c = it.c0; c < it.c1; ++c, ++n) {
       if constexpr (kFull) {  // rounded to bf16 for Q S
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-          sts128(copy + sw128(row, 16 * e), make_uint4(pack_bf162(S[8 * e], S[8 * e + 1]), pack_bf162(S[8 * e + 2], S[8 * e + 3]),
-                                                       pack_bf162(S[8 * e + 4], S[8 * e + 5]), pack_bf162(S[8 * e + 6], S[8 * e + 7])));
+          sts128(copy + sw128(ch, 16 * e), make_uint4(pack_bf162(S[8 * e], S[8 * e + 1]), pack_bf162(S[8 * e + 2], S[8 * e + 3]),
+                                                      pack_bf162(S[8 * e + 4], S[8 * e + 5]), pack_bf162(S[8 * e + 6], S[8 * e + 7])));
         fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.state);
       }
-      tc_fence_before();
+      LIN_WAIT(s.w_full[n & 1], n >> 1);
+      const float f = s.a[n & 1];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&s.state);
-      LIN_WAIT(s.dec_full[n & 1], n >> 1);
-      const float f = s.dec[n & 1].a;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s.dec_empty[n & 1]);
+      if (lane == 0) mbar_arrive(&s.w_empty[n & 1]);
       A *= f;
-      LIN_WAIT(s.kv, n);
+      LIN_WAIT(s.kv[n & 1], n >> 1);
       tc_fence_after();
+      const uint32_t at = tl + kv_column<kFull>(n);
+      constexpr int kStep = kFull ? 32 : 16;  // columns at a time: what the registers of either instance take
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        float x[16];
-        tmem_ld16(tl + 16 * q, x);
+      for (int q = 0; q < kHalf; q += kStep) {
+        float x[kStep];
+        if constexpr (kFull) tmem_ld32(at + q, x);
+        else tmem_ld16(at + q, x);
+        if (!kFull && q + kStep == kHalf) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.kv_read[n & 1]);
+        }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) S[16 * q + e] = fmaf(f, S[16 * q + e], x[e]);
+        for (int e = 0; e < kStep; e += 2) {
+          const float2 y = unpack_f32x2(fma_f32x2(f32x2(f, f), f32x2(S[q + e], S[q + e + 1]), f32x2(x[e], x[e + 1])));
+          S[q + e] = y.x;
+          S[q + e + 1] = y.y;
+        }
       }
     }
     if constexpr (kFull) {
-      if (it.last && a.S_out && !dead) store(a.S_out + (static_cast<int64_t>(it.seq) * a.H + j.head) * kStateFloats + mine);
+      if (it.last && a.S_out && !dead) store(a.S_out + unit);
     } else {
       store(slot(1 + it.seg));
       if (w == 0 && lane == 0) p.p.decay[static_cast<int64_t>(it.base + 1 + it.seg) * a.H + j.head] = A;
     }
   }
   tc_fence_before();
+  if constexpr (kFull) {  // sequences without tokens: the final state is the entry state
+    if (a.S_out && a.S_in != a.S_out && !dead)
+      for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.p.counts[4]) * a.H; t += gridDim.x) {
+        const int seq = p.p.items[0][p.p.counts[0] + t / a.H].seq;
+        const int64_t at = (static_cast<int64_t>(seq) * a.H + t % a.H) * (kStateFloats / 4);
+        for (int e = 32 * w + lane; e < kStateFloats / 4; e += 256)
+          reinterpret_cast<float4*>(a.S_out)[at + e] =
+              a.S_in ? reinterpret_cast<const float4*>(a.S_in)[at + e] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+  }
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
-template <bool kFull>
+template <int kMode>
 __global__ void __launch_bounds__(kThreads, 1) lin_chunk_kernel(const __grid_constant__ LinParams p) {
+  constexpr bool kFull = kMode != kStates;
   extern __shared__ __align__(1024) uint8_t sm[];
   Small& s = *reinterpret_cast<Small*>(sm + kSmSmall);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -721,15 +936,27 @@ __global__ void __launch_bounds__(kThreads, 1) lin_chunk_kernel(const __grid_con
     return;
   }
   if (tid == 0) {
-    for (int i = 0; i < kSlots; ++i) { mbar_init(&s.full[i], 1); mbar_init(&s.empty[i], 1); }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(&s.full[0][i], kFull ? 2 : 1);
+      mbar_init(&s.full[1][i], 1);
+      mbar_init(&s.free[kK][i], 1);
+      mbar_init(&s.free[kV][i], 8);
+      mbar_init(&s.free[kQ][i], 4);
+    }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.job_full[i], 1);
-      mbar_init(&s.job_empty[i], kFull ? kReaders : kReaders - 4);
-      mbar_init(&s.dec_full[i], 1);
-      mbar_init(&s.dec_empty[i], kFull ? 16 : 12);
+      mbar_init(&s.job_empty[i], kMode == kGated ? 23 : kMode == kPlain ? 22 : 18);  // warps that read a job
+      mbar_init(&s.w_full[i], 1);
+      mbar_init(&s.w_empty[i], 16);
+      mbar_init(&s.kv[i], 1);
+      mbar_init(&s.out[i], 1);
+      mbar_init(&s.kv_read[i], 8);
     }
-    mbar_init(&s.scores, 1); mbar_init(&s.weights, 4); mbar_init(&s.keys, 4); mbar_init(&s.kv, 1);
-    mbar_init(&s.state, 8); mbar_init(&s.out, 1); mbar_init(&s.out_free, 4); mbar_init(&s.drain, 1);
+    for (int i = 0; i < 4; ++i) s.bad_chunk[i] = 0;
+    for (int i = 0; i < 2; ++i) { mbar_init(&s.half_full[i], 8); mbar_init(&s.half_free[i], 1); }
+    mbar_init(&s.dec_full, 1); mbar_init(&s.dec_empty, 4); mbar_init(&s.scores, 1); mbar_init(&s.inter, 1);
+    mbar_init(&s.ready, 4); mbar_init(&s.out_free, 4); mbar_init(&s.state, 8); mbar_init(&s.drain, 1);
+    mbar_init(&s.gate_full, 1);
     fence_mbar_init();
   }
   pdl_launch_dependents();
@@ -741,21 +968,27 @@ __global__ void __launch_bounds__(kThreads, 1) lin_chunk_kernel(const __grid_con
   __syncthreads();
   tc_fence_after();
   pdl_wait();
-  // registers: 96 a thread at launch, 480 over the five groups
+  if (kMode == kGated && tid < kD) s.weight[tid] = p.a.norm_weight ? p.a.norm_weight[tid] : 1.f;
+  if (kFull && tid < 4 * kD) p.p.bad[4 * kD * blockIdx.x + tid] = 0;  // chunk 0 has 255 - token > 0 added
+  __syncthreads();
+  // registers: kRegs a thread at launch, 480 over the six groups of four warps
   if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;\n" ::: "memory");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 48;\n" ::: "memory");
     if (warp == 0) load_warp<kFull>(p, sm, s, lane);
     else if (warp == 1) mma_warp<kFull>(p, sm, s, lane);
     else if (warp == 2) decay_warp<kFull>(p, s, lane);
+    else if constexpr (kMode == kGated) gate_warp(p, sm, s, lane);
   } else if (warp < 8) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;\n" ::: "memory");
-    if constexpr (kFull) weight_warps(p, sm, s, warp - 4, lane);
-  } else if (warp < 12) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n" ::: "memory");
-    key_warps<kFull>(p, sm, s, tid - 256);
+    if constexpr (kFull) output_warps<kMode == kGated>(p, sm, s, warp - 4, lane);
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 24;\n" ::: "memory");
+  } else if (warp < 16) {
+    if constexpr (kFull) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n" ::: "memory");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 88;\n" ::: "memory");
+    value_warps<kFull>(p, sm, s, warp - 8, lane);
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 120;\n" ::: "memory");
-    state_warps<kFull>(p, sm, s, warp - 12, lane);
+    if constexpr (kFull) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n" ::: "memory");
+    else asm volatile("setmaxnreg.inc.sync.aligned.u32 112;\n" ::: "memory");
+    state_warps<kFull>(p, sm, s, warp - 16, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -776,28 +1009,28 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Rows [tokens][heads][128] of bf16 in boxes of 128 tokens and 64 channels.
-bool rows_map(CUtensorMap* m, const void* base, const int64_t* stride, int heads, int64_t tokens) {
+// Rows [tokens][heads][128] of bf16 in boxes of some tokens and 64 channels.
+bool rows_map(CUtensorMap* m, const void* base, const int64_t* stride, int heads, int64_t tokens, int rows = kC) {
   const auto fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[3] = {kD, static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(tokens)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(stride[2]) * 2, static_cast<cuuint64_t>(stride[1]) * 2};
-  const cuuint32_t box[3] = {64, 1, kC}, es[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {64, 1, static_cast<cuuint32_t>(rows)}, es[3] = {1, 1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool kFull>
+template <int kMode>
 cudaError_t launch_chunks(const LinParams& p, int64_t items, int num_sms) {
   static SmemOptIn opt_in;
-  const auto kernel = lin_chunk_kernel<kFull>;
+  const auto kernel = lin_chunk_kernel<kMode>;
   cudaError_t e = opt_in(reinterpret_cast<const void*>(kernel), kSmBytes);
   if (e != cudaSuccess) return e;
   // setmaxnreg's shares add up to kRegs a thread: with fewer at launch the groups would wait for them forever
   static const int regs = [] {
     cudaFuncAttributes at;
-    return cudaFuncGetAttributes(&at, lin_chunk_kernel<kFull>) == cudaSuccess ? at.numRegs : 0;
+    return cudaFuncGetAttributes(&at, lin_chunk_kernel<kMode>) == cudaSuccess ? at.numRegs : 0;
   }();
   if (regs < kRegs) return cudaErrorLaunchOutOfResources;
   const unsigned grid = static_cast<unsigned>(items < num_sms ? items : num_sms);
@@ -816,18 +1049,21 @@ cudaError_t launch_lin_prefill(const LinArgs& a, int num_sms) {
   memset(&p, 0, sizeof(p));
   p.a = a;
   plan_layout(&p.p, a.workspace, a.n_seq, a.tokens, a.H, a.n_segments, num_sms);
+  const int64_t o_stride[3] = {0, static_cast<int64_t>(a.H) * kD, kD};
   if (a.tokens > 0 && (!rows_map(&p.tq, a.q, a.q_stride, a.H / a.group, a.tokens) || !rows_map(&p.tk, a.k, a.k_stride, a.H / a.group, a.tokens) ||
-                       !rows_map(&p.tv, a.v, a.v_stride, a.H, a.tokens)))
+                       !rows_map(&p.tv, a.v, a.v_stride, a.H, a.tokens) ||
+                       !rows_map(&p.to, a.o, o_stride, a.H, a.tokens, 32) ||
+                       (a.gate && !rows_map(&p.tg, a.gate, a.gate_stride, a.H, a.tokens))))
     return cudaErrorInvalidValue;
   cudaError_t e = launch_after(lin_plan_kernel, dim3(1), dim3(1024), 0, a.stream, a.cu, a.n_seq, a.tokens, a.H, num_sms,
                                a.n_segments, p.p, a.status);
   if (e != cudaSuccess) return e;
   // the first pass only where the rule can split: one sequence of all the tokens is cut most
   if (p.p.most[1] > 0 && segments_of(a.tokens, a.tokens, a.H, num_sms, a.n_segments) > 1) {
-    e = launch_chunks<false>(p, p.p.most[1] * a.H, num_sms);
+    e = launch_chunks<kStates>(p, p.p.most[1] * a.H, num_sms);
     if (e != cudaSuccess) return e;
   }
-  return launch_chunks<true>(p, p.p.most[0] * a.H, num_sms);
+  return a.gate ? launch_chunks<kGated>(p, p.p.most[0] * a.H, num_sms) : launch_chunks<kPlain>(p, p.p.most[0] * a.H, num_sms);
 }
 
 }  // namespace kda

@@ -155,8 +155,7 @@ def test_rows_as_they_lie():
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 @pytest.mark.parametrize("segments", [0, 2])
 def test_what_is_not_finite_stays_where_it_belongs(what, value, segments):
-    """One bad value in the middle of a chunk: earlier tokens, other heads and other sequences keep their bits,
-    but for a value's channel, which earlier tokens of its chunk sum in another order (128 products more)."""
+    """One bad value in the middle of a chunk: earlier tokens, other heads and other sequences keep their bits."""
     if what == "g" and value > 0:
         value = float("nan")
     p = Prefill([300, 300, 200], 2, 2, seed=8)
@@ -172,10 +171,6 @@ def test_what_is_not_finite_stays_where_it_belongs(what, value, segments):
         same[t, h] = False
     else:
         same[t:600, h] = False
-    if what == "v":
-        x, y = o[300:t, h, 5].float(), o0[300:t, h, 5].float()
-        assert bool(((x - y).abs() <= U16 * 2 * y.abs() + 1e-4).all())  # a step of bf16 and 128 U32 of sums below 10
-        o0[300:t, h, 5] = o[300:t, h, 5]
     assert torch.equal(o[same.cuda()], o0[same.cuda()])
     bad = ~torch.isfinite(o).all(-1).cpu()
     if what == "v":  # one channel
