@@ -20,7 +20,7 @@
 // products of operands in it take in full, is the block's bottleneck.  The parts go through a ring of four
 // units (a part of 64 tokens), so that they are made while the products of the units before them run.
 //
-// The products of a chunk: Q K^T | Q S | units of tokens 0 - 63 | units of tokens 64 - 127 | P V.  Weights are made
+// The products of a chunk: Q K^T | units of tokens 0 - 63 | Q S | units of tokens 64 - 127 | P V.  Weights are made
 // during the three in the middle, outputs and the next state during P V and the next Q K^T.
 //
 // A token's NaN or infinity must not reach earlier tokens, but 0 * NaN is NaN in P V: values that are not
@@ -358,16 +358,18 @@ __device__ void mma_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
         product_ss(who, kTS, d_k + tq, d_k + tk);
         mma_commit_if(who, &s.scores);
         LIN_WAIT(s.state, n);  // the state in front of the chunk is in shared memory, the last K^T V is read
-        if (n > 0) LIN_WAIT(s.out_free, n - 1);
-        tc_fence_after();
-        if (dead) break;
-        product_ss(who, kTO, d_k + tq, d_k + (kSmState >> 4));
-        mma_commit_if(who, &s.inter);
       }
       if (!kFull && n > 1) LIN_WAIT(s.kv_read[n & 1], (n >> 1) - 1);  // K^T V of the last chunk but one is read
       // (the values' parts)^T K, 64 tokens at a time
 #pragma unroll 1
       for (uint32_t h = 0; h < 2; ++h) {
+        if (kFull && h == 1) {
+          if (n > 0) LIN_WAIT(s.out_free, n - 1);
+          tc_fence_after();
+          if (dead) break;
+          product_ss(who, kTO, d_k + tq, d_k + (kSmState >> 4));
+          mma_commit_if(who, &s.inter);
+        }
         if constexpr (kFull) LIN_WAIT(s.half_full[0], 2 * n + h);
         else LIN_WAIT(s.half_full[h], n);
         tc_fence_after();
@@ -504,11 +506,20 @@ __device__ void gate_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
   if (dead && lane == 0) report_status(p.a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
-// sigmoid(g): the approximations are within 2^-21 of it, and 1 / inf is 0.
-__device__ __forceinline__ float open_gate(float g) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(1.f + exp2_fast(-1.4426950408889634f * g)));
-  return y;
+// A pair of bf16 as two floats.
+__device__ __forceinline__ uint64_t floats(uint32_t u) {
+  return f32x2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
+}
+
+// sigmoid of a pair of gates: the approximations are within 2^-21 of it, and 1 / inf is 0.
+__device__ __forceinline__ uint64_t open_gates(uint32_t g) {
+  const float l = -1.4426950408889634f;
+  const float2 y = unpack_f32x2(mul_f32x2(floats(g), f32x2(l, l)));
+  const float2 z = unpack_f32x2(add_f32x2(f32x2(exp2_fast(y.x), exp2_fast(y.y)), f32x2(1.f, 1.f)));
+  float r0, r1;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r0) : "f"(z.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r1) : "f"(z.y));
+  return f32x2(r0, r1);
 }
 
 // 32 columns of a row times e, in place.
@@ -526,9 +537,9 @@ __device__ __forceinline__ void scale_block(uint32_t at, float e) {
 }
 
 // NaN for the rows that see a value that is not finite, in its channel (cold).
-__device__ __noinline__ void poison(uint32_t tl, const uint32_t* noted, uint32_t n, int i) {
+__device__ __forceinline__ void poison(uint32_t tl, const uint32_t* noted, uint32_t n, int i, int half) {
 #pragma unroll 1
-  for (int c = 0; c < kD; ++c) {
+  for (int c = 64 * half; c < 64 * half + 64; ++c) {
     const uint32_t m = __ldcg(noted + c);
     const bool hit = (m >> 8) == n && 255 - static_cast<int>(m & 255) <= i;
     if (!__any_sync(0xffffffffu, hit)) continue;
@@ -540,14 +551,13 @@ __device__ __noinline__ void poison(uint32_t tl, const uint32_t* noted, uint32_t
   }
 }
 
-// A row of the staged outputs, where not all of a warp's rows are the sequence's.
-__device__ __noinline__ void copy_row(uint32_t stage, uint4* dst, int i) {
+// Half a row of the staged outputs, where not all of a warp's rows are the sequence's (cold).
+__device__ __forceinline__ void copy_row(uint32_t stage, uint4* dst, int i) {
 #pragma unroll 1
-  for (int q = 0; q < 16; ++q) dst[q] = lds128(stage + (q >> 3) * kPanel + sw128(i, 16 * (q & 7)));
+  for (int q = 0; q < 8; ++q) dst[q] = lds128(stage + sw128(i, 16 * q));
 }
 
-template <bool kGate>
-__device__ void output_warps(const LinParams& p, uint8_t* sm, Small& s, int w, int lane) {
+__device__ void weight_warps(const LinParams& p, Small& s, int w, int lane) {
   const LinArgs& a = p.a;
   bool dead = false;
   Jobs jobs(s, dead);
@@ -555,18 +565,8 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Small& s, int w, i
   uint32_t n = 0;
   const uint32_t ts = (static_cast<uint32_t>(w) << 21) + kTS, tl = (static_cast<uint32_t>(w) << 21) + kTO;
   const int i = 32 * w + lane;
-  int staged = -1;  // the buffer whose rows are on their way to o
-  auto release = [&] {
-    if (staged >= 0 && lane == 0) {
-      asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
-      mbar_arrive(&s.free[kQ][staged]);
-    }
-    staged = -1;
-    __syncwarp();
-  };
   while (jobs.next(j)) {
     for (int c = j.item.c0; c < j.item.c1; ++c, ++n) {
-      const Tiles<true> tile(n);
       // ---- weights, 32 columns at a time, over the scores of columns that are read already
       LIN_WAIT(s.dec_full, n);
       const Decays& d = s.dec;
@@ -610,7 +610,6 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Small& s, int w, i
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.dec_empty);
-      release();  // the last chunk's rows: here, since their copy takes as long as this
       // ---- Q S times e^G
       const float eg = exp2f(G);
       LIN_WAIT(s.inter, n);
@@ -621,85 +620,9 @@ __device__ void output_warps(const LinParams& p, uint8_t* sm, Small& s, int w, i
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.ready);
-      // ---- outputs
-      const int live = live_rows(j.item, c);
-      const int64_t t = static_cast<int64_t>(j.item.first) + c * kC + i;
-      if constexpr (kGate) LIN_WAIT(s.gate_full, n);
-      LIN_WAIT(s.out[n & 1], n >> 1);
-      tc_fence_after();
-      if (s.bad_chunk[n & 3] == n + 1) poison(tl, p.p.bad + 4 * kD * blockIdx.x + kD * (n & 3), n, i);
-      float f = a.scale;
-      if constexpr (kGate) {
-        float s0 = 0.f, s1 = 0.f;
-#pragma unroll 1
-        for (int b = 0; b < 4; ++b) {
-          float x[32];
-          tmem_ld32(tl + 32 * b, x);
-#pragma unroll
-          for (int e = 0; e < 32; e += 2) { s0 = fmaf(x[e], x[e], s0); s1 = fmaf(x[e + 1], x[e + 1], s1); }
-        }
-        f *= 1.f / sqrtf((s0 + s1) * a.scale * a.scale * (1.f / kD) + a.eps);
-      }
-      const uint32_t stage = smem_u32(sm) + tile.at(kQ);  // q is used: its tile takes the outputs
-#pragma unroll 1
-      for (int b = 0; b < 4; ++b) {
-        float x[32];
-        tmem_ld32(tl + 32 * b, x);
-        if (b == 3) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&s.out_free);
-        }
-        const uint32_t at = stage + (b >> 1) * kPanel + i * 128, turn = (i & 7) << 4;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint32_t to = at + (((b & 1) * 64 + 16 * q) ^ turn);
-          float y[8];
-#pragma unroll
-          for (int e = 0; e < 8; e += 2) {
-            const float2 z = unpack_f32x2(mul_f32x2(f32x2(x[8 * q + e], x[8 * q + e + 1]), f32x2(f, f)));
-            y[e] = z.x;
-            y[e + 1] = z.y;
-          }
-          if constexpr (kGate) {
-            const uint4 u = lds128(to);
-            const uint32_t bits[4] = {u.x, u.y, u.z, u.w};
-            const float4 w0 = *reinterpret_cast<const float4*>(&s.weight[32 * b + 8 * q]);
-            const float4 w1 = *reinterpret_cast<const float4*>(&s.weight[32 * b + 8 * q + 4]);
-            const float wt[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              y[2 * e] *= wt[2 * e] * open_gate(__uint_as_float(bits[e] << 16));
-              y[2 * e + 1] *= wt[2 * e + 1] * open_gate(__uint_as_float(bits[e] & 0xffff0000u));
-            }
-          }
-          sts128(to, make_uint4(pack_bf162(y[0], y[1]), pack_bf162(y[2], y[3]), pack_bf162(y[4], y[5]), pack_bf162(y[6], y[7])));
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (32 * w + 32 <= live) {
-        if (lane == 0 && !dead) {
-          const uint8_t* src = sm + tile.at(kQ) + w * 4096;
-          tma_store_3d(&p.to, src, 0, j.head, static_cast<int>(t));
-          tma_store_3d(&p.to, src + kPanel, 64, j.head, static_cast<int>(t));
-          asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
-        }
-      } else if (i < live && !dead) {
-        copy_row(stage, reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) + (t * a.H + j.head) * kD), i);
-      }
-      __syncwarp();
-      staged = static_cast<int>(tile.buf);
     }
   }
-  release();
-  if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
-}
-
-// A pair of bf16 as two floats.
-__device__ __forceinline__ uint64_t floats(uint32_t u) {
-  return f32x2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
 }
 
 // 8 x 8 tiles of 16-bit values, transposed: lanes 8 m .. 8 m + 7 point to the rows of tile m; of each tile a lane gets
@@ -708,20 +631,20 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-// 16 lanes x 16 columns of tensor memory: registers 2 k and 2 k + 1 are column 4 k + lane % 4 of lanes lane / 4 and
+// 16 lanes x 8 columns of tensor memory: registers 2 k and 2 k + 1 are column 4 k + lane % 4 of lanes lane / 4 and
 // lane / 4 + 8.
-__device__ __forceinline__ void tmem_st_16x128b_x4(uint32_t taddr, const uint32_t (&u)[8]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(u[0]), "r"(u[1]),
-               "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7])
+__device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_t (&u)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(taddr), "r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3])
                : "memory");
 }
 
-// Values of a warp's 32 channels and 32 tokens that are not finite, cleared in the tile and noted (cold):
+// Values of a warp's 32 channels and 16 tokens that are not finite, cleared in the tile and noted (cold):
 // chunk number << 8 | 255 - the first such token of a channel.
-__device__ __noinline__ void clear_bad(uint32_t tile, uint32_t* noted, uint32_t* bad_chunk, uint32_t n, int w, int t0, int lane) {
+__device__ __forceinline__ void clear_bad(uint32_t tile, uint32_t* noted, uint32_t* bad_chunk, uint32_t n, int w, int t0, int lane) {
   const int ch = 32 * w + lane;
   const uint32_t base = tile + (ch >> 6) * kPanel;
-  for (int t = t0; t < t0 + 32; ++t) {
+#pragma unroll 1
+  for (int t = t0; t < t0 + 16; ++t) {
     const uint32_t at = base + sw128(t, 2 * (ch & 63));
     uint16_t x;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
@@ -772,41 +695,46 @@ __device__ void value_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
       const float* wp = &s.w[n & 1][2 * (lane & 3)];
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        const int t0 = 64 * h + 32 * side;
-        uint32_t part[3][2][8];  // [part][16 channels][..]
-        uint64_t any = f32x2(0.f, 0.f);  // NaN if a value is not finite: what is left of it is NaN
+#pragma unroll 1
+        for (int piece = 0; piece < 2; ++piece) {
+          const int t0 = 64 * h + 32 * side + 16 * piece;
+          uint32_t part[3][2][4];  // [part][16 channels][..]
+          uint64_t any = f32x2(0.f, 0.f);  // NaN if a value is not finite: what is left of it is NaN
 #pragma unroll
-        for (int b = 0; b < 4; ++b) {  // 8 tokens, 32 channels
-          uint32_t r[4];
-          const int ch = 32 * q + 8 * (lane >> 3);
-          ldsm4_trans(v + (ch >> 6) * kPanel + sw128(t0 + 8 * b + (lane & 7), 2 * (ch & 63)), r);
-          const uint64_t f = *reinterpret_cast<const uint64_t*>(wp + t0 + 8 * b);
+          for (int b = 0; b < 2; ++b) {  // 8 tokens, 32 channels
+            uint32_t r[4];
+            const int ch = 32 * q + 8 * (lane >> 3);
+            ldsm4_trans(v + (ch >> 6) * kPanel + sw128(t0 + 8 * b + (lane & 7), 2 * (ch & 63)), r);
+            const uint64_t f = *reinterpret_cast<const uint64_t*>(wp + t0 + 8 * b);
 #pragma unroll
-          for (int m = 0; m < 4; ++m) {
-            uint64_t y = mul_f32x2(floats(r[m]), f);
-            const uint32_t hi = bf162_of(y);
-            y = fma_f32x2(floats(hi), minus, y);
-            const uint32_t mid = bf162_of(y);
-            y = fma_f32x2(floats(mid), minus, y);
-            any = add_f32x2(any, y);
-            part[0][m >> 1][2 * b + (m & 1)] = hi;
-            part[1][m >> 1][2 * b + (m & 1)] = mid;
-            part[2][m >> 1][2 * b + (m & 1)] = bf162_of(y);
+            for (int m = 0; m < 4; ++m) {
+              uint64_t y = mul_f32x2(floats(r[m]), f);
+              const uint32_t hi = bf162_of(y);
+              y = fma_f32x2(floats(hi), minus, y);
+              const uint32_t mid = bf162_of(y);
+              y = fma_f32x2(floats(mid), minus, y);
+              any = add_f32x2(any, y);
+              part[0][m >> 1][2 * b + (m & 1)] = hi;
+              part[1][m >> 1][2 * b + (m & 1)] = mid;
+              part[2][m >> 1][2 * b + (m & 1)] = bf162_of(y);
+            }
           }
-        }
-        const float2 left = unpack_f32x2(any);
-        if (kFull && __any_sync(0xffffffffu, left.x + left.y != left.x + left.y)) {
-          clear_bad(v, noted, s.bad_chunk, n, q, t0, lane);
-          fence_proxy_async_smem();
-        }
-        if constexpr (kFull) { if (u > 0) LIN_WAIT(s.half_free[0], 2 * n + h - 1); }
-        else { if (n > 0) LIN_WAIT(s.half_free[h], n - 1); }
-        tc_fence_after();
+          const float2 left = unpack_f32x2(any);
+          if (kFull && __any_sync(0xffffffffu, left.x + left.y != left.x + left.y)) {
+            clear_bad(v, noted, s.bad_chunk, n, q, t0, lane);
+            fence_proxy_async_smem();
+          }
+          if (piece == 0) {
+            if constexpr (kFull) { if (u > 0) LIN_WAIT(s.half_free[0], 2 * n + h - 1); }
+            else { if (n > 0) LIN_WAIT(s.half_free[h], n - 1); }
+            tc_fence_after();
+          }
 #pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const uint32_t at = (static_cast<uint32_t>(q) << 21) + unit_column<kFull>(u + k) + 16 * side;
-          tmem_st_16x128b_x4(at, part[k][0]);
-          tmem_st_16x128b_x4(at + (16u << 16), part[k][1]);
+          for (int k = 0; k < 3; ++k) {
+            const uint32_t at = (static_cast<uint32_t>(q) << 21) + unit_column<kFull>(u + k) + 16 * side + 8 * piece;
+            tmem_st_16x128b_x2(at, part[k][0]);
+            tmem_st_16x128b_x2(at + (16u << 16), part[k][1]);
+          }
         }
         tmem_wait_st();
         tc_fence_before();
@@ -824,8 +752,9 @@ __device__ void value_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
   if (dead && lane == 0) report_status(p.a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
 
-template <bool kFull>
+template <int kMode>
 __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, int lane) {
+  constexpr bool kFull = kMode != kStates, kGate = kMode == kGated;
   const LinArgs& a = p.a;
   bool dead = false;
   Jobs jobs(s, dead);
@@ -835,6 +764,79 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
   const uint32_t tl = (static_cast<uint32_t>(w & 3) << 21) + 64 * half;
   const uint32_t copy = smem_u32(sm) + kSmState + half * kPanel;
   constexpr int kHalf = kD / 2;
+  // ---- outputs of a chunk: 32 tokens, 64 channels
+  int staged = -1;  // the buffer whose rows are on their way to o
+  auto release = [&] {
+    if (staged >= 0 && lane == 0) {
+      asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+      mbar_arrive(&s.free[kQ][staged]);
+    }
+    staged = -1;
+    __syncwarp();
+  };
+  auto outputs = [&](const Item& it, int head, int c) {
+    const Tiles<kFull> tile(n);
+    const int i = ch;  // the thread's token in the chunk
+    const uint32_t to_q = (static_cast<uint32_t>(w & 3) << 21) + kTO, to = to_q + 64 * half;
+    release();  // with the output stage, what is left of the last chunk's
+    if constexpr (kGate) LIN_WAIT(s.gate_full, n);
+    LIN_WAIT(s.out[n & 1], n >> 1);
+    tc_fence_after();
+    if (s.bad_chunk[n & 3] == n + 1) poison(to_q, p.p.bad + 4 * kD * blockIdx.x + kD * (n & 3), n, i, half);
+    float f = a.scale;
+    if constexpr (kGate) {  // the row's sum of squares, by both warps that have it
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll 1
+      for (int b = 0; b < 8; ++b) {
+        float x[16];
+        tmem_ld16(to_q + 16 * b, x);
+#pragma unroll
+        for (int e = 0; e < 16; e += 2) { s0 = fmaf(x[e], x[e], s0); s1 = fmaf(x[e + 1], x[e + 1], s1); }
+      }
+      f *= 1.f / sqrtf((s0 + s1) * a.scale * a.scale * (1.f / kD) + a.eps);
+    }
+    const uint32_t stage = smem_u32(sm) + tile.at(kQ) + half * kPanel;  // q is used: its tile takes the outputs
+#pragma unroll 1
+    for (int b = 0; b < 4; ++b) {
+      float x[16];
+      tmem_ld16(to + 16 * b, x);
+      if (b == 3) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s.out_free);
+      }
+      const uint32_t at0 = stage + sw128(i, 32 * b), at1 = stage + sw128(i, 32 * b + 16);
+      uint32_t pk[8];
+      if constexpr (kGate) {
+        const uint4 u0 = lds128(at0), u1 = lds128(at1);
+        pk[0] = u0.x; pk[1] = u0.y; pk[2] = u0.z; pk[3] = u0.w; pk[4] = u1.x; pk[5] = u1.y; pk[6] = u1.z; pk[7] = u1.w;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; e += 2) {
+        uint64_t y = mul_f32x2(f32x2(x[e], x[e + 1]), f32x2(f, f));
+        if constexpr (kGate)
+          y = mul_f32x2(mul_f32x2(y, *reinterpret_cast<const uint64_t*>(&s.weight[64 * half + 16 * b + e])), open_gates(pk[e >> 1]));
+        pk[e >> 1] = bf162_of(y);
+      }
+      sts128(at0, make_uint4(pk[0], pk[1], pk[2], pk[3]));
+      sts128(at1, make_uint4(pk[4], pk[5], pk[6], pk[7]));
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    const int live = live_rows(it, c), row = it.first + c * kC + 32 * (w & 3);
+    if (32 * (w & 3) + 32 <= live) {
+      if (lane == 0 && !dead) {
+        tma_store_3d(&p.to, sm + tile.at(kQ) + half * kPanel + (w & 3) * 4096, 64 * half, head, row);
+        asm volatile("cp.async.bulk.commit_group;\n" ::: "memory");
+      }
+    } else if (i < live && !dead) {  // the next sequence's rows are not this one's to write
+      copy_row(stage, reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.o) +
+                                               ((static_cast<int64_t>(row) + lane) * a.H + head) * kD + 64 * half), i);
+    }
+    __syncwarp();
+    staged = static_cast<int>(tile.buf);
+    if constexpr (!kGate) release();  // nothing to do until K^T V of the next chunk
+  };
   while (jobs.next(j)) {
     const Item& it = j.item;
     const int mine = half * kHalf * kD + ch;
@@ -866,17 +868,18 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
 #pragma unroll
       for (int e = 0; e < kHalf; ++e) S[e] = 0.f;
     }
-    for (int c = it.c0; c < it.c1; ++c, ++n) {
-      if constexpr (kFull) {  // rounded to bf16 for Q S
+    auto publish = [&] {  // rounded to bf16 for Q S
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          sts128(copy + sw128(ch, 16 * e), make_uint4(pack_bf162(S[8 * e], S[8 * e + 1]), pack_bf162(S[8 * e + 2], S[8 * e + 3]),
-                                                      pack_bf162(S[8 * e + 4], S[8 * e + 5]), pack_bf162(S[8 * e + 6], S[8 * e + 7])));
-        fence_proxy_async_smem();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.state);
-      }
+      for (int e = 0; e < 8; ++e)
+        sts128(copy + sw128(ch, 16 * e), make_uint4(pack_bf162(S[8 * e], S[8 * e + 1]), pack_bf162(S[8 * e + 2], S[8 * e + 3]),
+                                                    pack_bf162(S[8 * e + 4], S[8 * e + 5]), pack_bf162(S[8 * e + 6], S[8 * e + 7])));
+      fence_proxy_async_smem();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.state);
+    };
+    if constexpr (kFull) publish();
+    for (int c = it.c0; c < it.c1; ++c, ++n) {
       LIN_WAIT(s.w_full[n & 1], n >> 1);
       const float f = s.a[n & 1];
       __syncwarp();
@@ -903,15 +906,22 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
           S[q + e + 1] = y.y;
         }
       }
+      if constexpr (kFull) {
+        if (c + 1 < it.c1) publish();
+        else if (it.last && a.S_out && !dead) store(a.S_out + unit);
+        outputs(it, j.head, c);
+      }
     }
-    if constexpr (kFull) {
-      if (it.last && a.S_out && !dead) store(a.S_out + unit);
-    } else {
+    if constexpr (!kFull) {
       store(slot(1 + it.seg));
       if (w == 0 && lane == 0) p.p.decay[static_cast<int64_t>(it.base + 1 + it.seg) * a.H + j.head] = A;
     }
   }
   tc_fence_before();
+  if constexpr (kFull) {
+    release();
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
+  }
   if constexpr (kFull) {  // sequences without tokens: the final state is the entry state
     if (a.S_out && a.S_in != a.S_out && !dead)
       for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.p.counts[4]) * a.H; t += gridDim.x) {
@@ -941,7 +951,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_chunk_kernel(const __grid_con
       mbar_init(&s.full[1][i], 1);
       mbar_init(&s.free[kK][i], 1);
       mbar_init(&s.free[kV][i], 8);
-      mbar_init(&s.free[kQ][i], 4);
+      mbar_init(&s.free[kQ][i], 8);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s.job_full[i], 1);
@@ -955,7 +965,7 @@ __global__ void __launch_bounds__(kThreads, 1) lin_chunk_kernel(const __grid_con
     for (int i = 0; i < 4; ++i) s.bad_chunk[i] = 0;
     for (int i = 0; i < 2; ++i) { mbar_init(&s.half_full[i], 8); mbar_init(&s.half_free[i], 1); }
     mbar_init(&s.dec_full, 1); mbar_init(&s.dec_empty, 4); mbar_init(&s.scores, 1); mbar_init(&s.inter, 1);
-    mbar_init(&s.ready, 4); mbar_init(&s.out_free, 4); mbar_init(&s.state, 8); mbar_init(&s.drain, 1);
+    mbar_init(&s.ready, 4); mbar_init(&s.out_free, 8); mbar_init(&s.state, 8); mbar_init(&s.drain, 1);
     mbar_init(&s.gate_full, 1);
     fence_mbar_init();
   }
@@ -979,16 +989,15 @@ __global__ void __launch_bounds__(kThreads, 1) lin_chunk_kernel(const __grid_con
     else if (warp == 2) decay_warp<kFull>(p, s, lane);
     else if constexpr (kMode == kGated) gate_warp(p, sm, s, lane);
   } else if (warp < 8) {
-    if constexpr (kFull) output_warps<kMode == kGated>(p, sm, s, warp - 4, lane);
+    if constexpr (kFull) weight_warps(p, s, warp - 4, lane);
     else asm volatile("setmaxnreg.dec.sync.aligned.u32 24;\n" ::: "memory");
   } else if (warp < 16) {
-    if constexpr (kFull) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;\n" ::: "memory");
+    if constexpr (kFull) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;\n" ::: "memory");
     else asm volatile("setmaxnreg.inc.sync.aligned.u32 88;\n" ::: "memory");
     value_warps<kFull>(p, sm, s, warp - 8, lane);
   } else {
-    if constexpr (kFull) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;\n" ::: "memory");
-    else asm volatile("setmaxnreg.inc.sync.aligned.u32 112;\n" ::: "memory");
-    state_warps<kFull>(p, sm, s, warp - 16, lane);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 112;\n" ::: "memory");
+    state_warps<kMode>(p, sm, s, warp - 16, lane);
   }
   tc_fence_before();
   __syncthreads();
