@@ -947,8 +947,13 @@ def _on(device, stream, *tensors):
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError(f"all tensors must be on one device, got cuda:{device} and {t.device}")
-    if device >= 0 and device != (_current_device() if stream is None else stream.device.index):
+    if device >= 0 and device != _here(stream):
         raise ValueError(f"the tensors are on cuda:{device}, which is not the device that the call runs on")
+
+
+def _here(stream):
+    """The device that the call runs on."""
+    return _current_device() if stream is None else stream.device.index
 
 
 def _decays(g, lead, H):
@@ -966,8 +971,27 @@ def _decays(g, lead, H):
     raise ValueError(f"g must have shape {lead + (H,)} or {(H,)}, got {tuple(g.shape)}")
 
 
-def _lin_rows(q, k, v, g, gate, norm_weight, n_lead, names, pack, pack_g):
-    """What the two calls share: sizes, and the rows' strides as the library takes them."""
+def _lin_rows(q, k, v, g, gate, norm_weight, stream, n_lead, names, pack):
+    """What the two calls share: sizes, and the rows' strides as the library takes them.  As for the
+    attention cache, what is checked for every call is checked in few steps."""
+    try:
+        shape, dev = q.shape, q.get_device()
+        lead, (H, d) = shape[:n_lead], v.shape[n_lead:]
+        Hk = shape[n_lead]
+        qs, ks, vs, gs = q.stride(), k.stride(), v.stride(), g.stride()
+        if len(gs) == 1:
+            gs = (0,) * n_lead + gs
+        if (gate is None and norm_weight is None and dev >= 0 and dev == k.get_device() == v.get_device() == g.get_device() == _here(stream)
+                and q.dtype is k.dtype is v.dtype is _BF16 and g.dtype is _F32 and d == HEAD_DIM and shape == k.shape
+                and shape[-1] == HEAD_DIM and len(shape) == n_lead + 2 and v.shape[:n_lead] == lead and H % Hk == 0
+                and (g.shape == lead + (H,) or g.shape == (H,)) and qs[-1] == ks[-1] == vs[-1] == 1):
+            return (lead, Hk, H, pack(*_sound(shape, qs)), pack(*_sound(shape, ks)), pack(*_sound(v.shape, vs)), pack(*gs), None)
+    except (AttributeError, ValueError, TypeError, IndexError, ZeroDivisionError):
+        pass
+    return _say_lin_rows(q, k, v, g, gate, norm_weight, n_lead, names, pack)
+
+
+def _say_lin_rows(q, k, v, g, gate, norm_weight, n_lead, names, pack):
     if not isinstance(q, torch.Tensor) or q.dim() != n_lead + 2:
         raise ValueError(f"q must be a tensor [{names}, heads, {HEAD_DIM}]")
     if not isinstance(v, torch.Tensor) or v.dim() != n_lead + 2:
@@ -985,7 +1009,7 @@ def _lin_rows(q, k, v, g, gate, norm_weight, n_lead, names, pack, pack_g):
             _need(norm_weight, "norm_weight", _F32, (HEAD_DIM,))
     elif norm_weight is not None:
         raise ValueError("norm_weight belongs to the output stage, which needs gate")
-    return lead, Hk, H, pack(*qs), pack(*ks), pack(*vs), pack_g(*gs), gates
+    return lead, Hk, H, pack(*qs), pack(*ks), pack(*vs), pack(*gs), gates
 
 
 def lin_prefill_workspace_size(n_seq, H, total_tokens, n_segments=0, d=HEAD_DIM) -> int:
@@ -1004,7 +1028,7 @@ def lin_prefill(q, k, v, g, cu_seqlens, S_in=None, scale=1.0, gate=None, norm_we
     ``sigmoid(gate) * norm_weight * o / sqrt(mean(o^2) + eps)``.  S_out may be S_in.
     Returns ``(o, S_out)``: ``[T, H, 128]`` bf16 and ``[N, H, 128, 128]`` fp32.
     """
-    (T,), Hk, H, qs, ks, vs, gs, gates = _lin_rows(q, k, v, g, gate, norm_weight, 1, "T", _pack2, _pack2)
+    (T,), Hk, H, qs, ks, vs, gs, gates = _lin_rows(q, k, v, g, gate, norm_weight, stream, 1, "T", _pack2)
     n_seq = cu_seqlens.shape[0] - 1 if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dim() == 1 else -1
     if n_seq < 0:
         raise ValueError("cu_seqlens must be a tensor [sequences + 1]")
@@ -1040,7 +1064,7 @@ def lin_decode(q, k, v, g, S_state, n_commit=None, scale=1.0, gate=None, norm_we
     q, k ``[B, n_tok, Hk, 128]``, v and gate ``[B, n_tok, H, 128]`` bf16 (leading dimensions may be
     strided); g ``[B, n_tok, H]`` or ``[H]`` fp32.  Returns o ``[B, n_tok, H, 128]`` fp32.
     """
-    (B, n_tok), Hk, H, qs, ks, vs, gs, gates = _lin_rows(q, k, v, g, gate, norm_weight, 2, "B, n_tok", _pack3, _pack3)
+    (B, n_tok), Hk, H, qs, ks, vs, gs, gates = _lin_rows(q, k, v, g, gate, norm_weight, stream, 2, "B, n_tok", _pack3)
     _on(q.get_device(), stream, k, v, g, gate, norm_weight, S_state, n_commit, o, dev_status)
     _need(S_state, "S_state", _F32, (B, H, HEAD_DIM, HEAD_DIM))
     commit = None if n_commit is None else _index(n_commit, "n_commit", (B,))
@@ -1081,27 +1105,50 @@ def block_norm(x, weight=None, y=None, post_norm=False, post_weight=None, gate=N
     fp32 or None (ones).  Rows may be strided; W a multiple of 8.  Returns ``(h, x')``: h ``[T, W]``
     bf16; x' of x's type, in ``x_out`` (which may be x) when given, and x itself without y.
     """
-    xs = _wide_rows(x, "x", (_BF16, _F32), None)
-    shape = x.shape
-    T, W = shape
-    ys = gs = 0
+    try:
+        shape, dev, dtype = x.shape, x.get_device(), x.dtype
+        T, W = shape
+        xs, one = x.stride()
+        ys = gs = 0
+        good = (dev >= 0 and dev == _here(stream) and one == 1 and T > 1 and (dtype is _BF16 or dtype is _F32)
+                and (weight is None or (weight.shape == (W,) and weight.dtype is _F32 and weight.get_device() == dev and weight.is_contiguous())))
+        if good and y is not None:
+            ys, one = y.stride()
+            good = y.shape == shape and y.dtype is _BF16 and y.get_device() == dev and one == 1
+            if post_weight is not None:
+                good = (good and post_weight.shape == (W,) and post_weight.dtype is _F32 and post_weight.get_device() == dev
+                        and post_weight.is_contiguous())
+            if gate is not None:
+                gs, one = gate.stride()
+                good = good and gate.shape == shape and gate.dtype is _BF16 and gate.get_device() == dev and one == 1
+        elif gate is not None or post_norm or post_weight is not None or x_out is not None:
+            good = False
+    except (AttributeError, ValueError):
+        good = False
+    if not good:  # say what is wrong, or take what the quick look does not
+        xs = _wide_rows(x, "x", (_BF16, _F32), None)
+        shape, dtype = x.shape, x.dtype
+        T, W = shape
+        ys = gs = 0
+        if y is not None:
+            ys = _wide_rows(y, "y", (_BF16,), shape)
+            if gate is not None:
+                gs = _wide_rows(gate, "gate", (_BF16,), shape)
+            if post_weight is not None:
+                _need(post_weight, "post_weight", _F32, (W,))
+        elif gate is not None or post_norm or post_weight is not None:
+            raise ValueError("post_norm, post_weight and gate belong to a block's output y")
+        elif x_out is not None:
+            raise ValueError("x_out needs a block's output y")
+        if weight is not None:
+            _need(weight, "weight", _F32, (W,))
+        _on(x.get_device(), stream, y, gate, weight, post_weight)
     if y is not None:
-        ys = _wide_rows(y, "y", (_BF16,), shape)
-        if gate is not None:
-            gs = _wide_rows(gate, "gate", (_BF16,), shape)
-        if post_weight is not None:
-            _need(post_weight, "post_weight", _F32, (W,))
-        x_out = _output(shape, x.dtype, x.device, stream) if x_out is None else _need(x_out, "x_out", x.dtype, shape)
-    elif gate is not None or post_norm or post_weight is not None:
-        raise ValueError("post_norm, post_weight and gate belong to a block's output y")
-    elif x_out is not None:
-        raise ValueError("x_out needs a block's output y")
-    if weight is not None:
-        _need(weight, "weight", _F32, (W,))
-    _on(x.get_device(), stream, y, gate, weight, post_weight, h, x_out)
+        x_out = _output(shape, dtype, x.device, stream) if x_out is None else _need(x_out, "x_out", dtype, shape)
     h = _output(shape, _BF16, x.device, stream) if h is None else _need(h, "h", _BF16, shape)
+    _on(x.get_device(), stream, h, x_out)
     st = (_lib or library()).kda_block_norm(
-        x.data_ptr(), 0 if x.dtype is _BF16 else 1, xs, _ptr(weight), _ptr(y), ys, post_norm, _ptr(post_weight), _ptr(gate),
+        x.data_ptr(), 0 if dtype is _BF16 else 1, xs, _ptr(weight), _ptr(y), ys, post_norm, _ptr(post_weight), _ptr(gate),
         gs, scale, eps, h.data_ptr(), _ptr(x_out), T, W, _stream_of(stream))
     if st != 0:
         raise KdaError(st, "kda_block_norm")

@@ -51,6 +51,47 @@ def test_sizes(T, W, wide):
     verify(a, *run(a))
 
 
+@pytest.mark.parametrize("T,W", [(640, 8), (700, 24), (1000, 264), (650, 1000), (1500, 1928), (650, 2056), (700, 4096), (650, 4104),
+                                 (620, 6144), (640, 8192), (620, 8200), (610, 12288), (610, 12296), (609, 16384)])
+@pytest.mark.parametrize("wide,parts", [(False, "wynpgs"), (True, "wynpgs"), (False, ""), (True, "wyp"), (False, "yn"), (True, "w")])
+def test_many_rows(T, W, wide, parts):
+    """Enough rows for blocks that walk over several: some of them against the statement, all against a call of few."""
+    a = make(T, W, wide, T + W, parts)
+    h, x = run(a)
+    some = torch.cat([torch.arange(5), torch.randperm(T, generator=torch.Generator().manual_seed(1))[:20], torch.arange(T - 5, T)])
+    few = {n: t[some] if isinstance(t, torch.Tensor) and t.dim() == 2 else t for n, t in a.items()}
+    verify(few, h[some.cuda()], x[some.cuda()])
+    assert bool(torch.isfinite(h).all()) and bool(torch.isfinite(x).all())
+    rms = lambda t: t.float().square().mean(-1).sqrt()  # noqa: E731
+    want, _ = run({n: t[:600] if isinstance(t, torch.Tensor) and t.dim() == 2 else t for n, t in a.items()})
+    assert float((rms(h[:600]) - rms(want)).abs().max()) < 1e-3 and int((h[:600] != want).sum()) <= h.numel() // 1000
+
+
+@pytest.mark.parametrize("wide", [False, True])
+def test_many_strided_rows_in_place_and_bad_ones(wide):
+    T, W = 900, 520
+    a = make(T, W, wide, 5, "wynpgs")
+    h0, x0 = run(a)
+
+    def spread(t):
+        b = torch.full((T, W + 24), float("nan"), dtype=t.dtype, device="cuda")
+        b[:, 8:W + 8] = t.cuda()
+        return b[:, 8:W + 8]
+
+    h, x = run({n: spread(a[n]) if n in ("x", "y", "gate") else t for n, t in a.items()})
+    assert torch.equal(h, h0) and torch.equal(x, x0)
+    x = a["x"].cuda()
+    h, x1 = run({**a, "x": x}, x_out=x)
+    assert x1 is x and torch.equal(h, h0) and torch.equal(x, x0)
+    bad = [0, 3, 500, 611, T - 1]
+    a["y"][bad] = float("nan")
+    h, x = run(a)
+    same = torch.ones(T, dtype=torch.bool)
+    same[bad] = False
+    assert torch.equal(h[same.cuda()], h0[same.cuda()]) and torch.equal(x[same.cuda()], x0[same.cuda()])
+    assert not bool(torch.isfinite(h[~same.cuda()]).any())
+
+
 def test_no_rows():
     a = make(0, 64, False, 1, "wynpgs")
     h, x = run(a)
