@@ -39,9 +39,25 @@ __global__ void __launch_bounds__(kThreads, 2) lin_decode_kernel(const __grid_co
   float4 s[kRows];
 #pragma unroll
   for (int m = 0; m < kRows; ++m) s[m] = S[((r0 + 8 * m) * kD + col) >> 2];
-  // the state of the unit that starts about half the resident blocks later, into L2 (a hint)
-  if (tid == 0 && unit + lookahead < static_cast<int>(gridDim.x))
-    bulk_prefetch_l2(a.S_out + (static_cast<int64_t>(unit) + lookahead) * kStateFloats, kStateFloats * sizeof(float));
+  // the state and the rows of the unit that starts about half the resident blocks later, into L2 (a hint)
+  if (warp == 1 && unit + lookahead < static_cast<int>(gridDim.x)) {
+    const int next = unit + lookahead, nb = next / a.H, nh = next - nb * a.H, nq = nh / a.group;
+    if (lane == 0) bulk_prefetch_l2(a.S_out + next * kStateFloats, kStateFloats * sizeof(float));
+    const int i = lane >> 3, which = (lane >> 1) & 3;  // token; q, k, v, gate, two lines each
+    if (i < kTok && (which < 3 || a.gate)) {
+      const void* base = which == 0 ? a.q : which == 1 ? a.k : which == 2 ? a.v : a.gate;
+      const int64_t* st = which == 0 ? a.q_stride : which == 1 ? a.k_stride : which == 2 ? a.v_stride : a.gate_stride;
+      prefetch_l2(static_cast<const __nv_bfloat16*>(base) + nb * st[0] + i * st[1] + (which < 2 ? nq : nh) * st[2] + 64 * (lane & 1));
+    }
+  }
+  // the output stage's gate of token `warp`, for the end
+  uint2 gb = make_uint2(0, 0);
+  float4 w4 = make_float4(1.f, 1.f, 1.f, 1.f);
+  if (a.gate && warp < kTok) {
+    gb = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.gate) + b * a.gate_stride[0] + warp * a.gate_stride[1] +
+                                         h * a.gate_stride[2] + 4 * lane);
+    if (a.norm_weight) w4 = *reinterpret_cast<const float4*>(a.norm_weight + 4 * lane);
+  }
   int nc = a.n_commit ? a.n_commit[b] : kTok;
   if (nc < 0 || nc > kTok) {
     if (tid == 0) report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
@@ -96,7 +112,6 @@ __global__ void __launch_bounds__(kThreads, 2) lin_decode_kernel(const __grid_co
       E[i] = expf(sum);
     }
   }
-  __syncthreads();
 
   uint64_t s2[kRows][2];
 #pragma unroll
@@ -104,6 +119,7 @@ __global__ void __launch_bounds__(kThreads, 2) lin_decode_kernel(const __grid_co
     s2[m][0] = f32x2(s[m].x, s[m].y);
     s2[m][1] = f32x2(s[m].z, s[m].w);
   }
+  float p[kTok][4];  // S^T q
 #pragma unroll
   for (int i = 0; i < kTok; ++i) {
     uint64_t p01 = f32x2(0.f, 0.f), p23 = p01;
@@ -119,21 +135,27 @@ __global__ void __launch_bounds__(kThreads, 2) lin_decode_kernel(const __grid_co
       }
     }
     const float2 lo = unpack_f32x2(p01), hi = unpack_f32x2(p23);
-    float p[4] = {lo.x, lo.y, hi.x, hi.y};
+    p[i][0] = lo.x; p[i][1] = lo.y; p[i][2] = hi.x; p[i][3] = hi.y;
+  }
 #pragma unroll
-    for (int off = 4; off < 32; off <<= 1)
+  for (int off = 4; off < 32; off <<= 1)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] += __shfl_xor_sync(0xffffffffu, p[e], off);
-    if (r0 == 0) {
+    for (int i = 0; i < kTok; ++i)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) p[e] *= E[i];
+      for (int e = 0; e < 4; ++e) p[i][e] += __shfl_xor_sync(0xffffffffu, p[i][e], off);
+  __syncthreads();  // the products of q and k
+  if (r0 == 0) {
+#pragma unroll
+    for (int i = 0; i < kTok; ++i) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) p[i][e] *= E[i];
 #pragma unroll
       for (int j = 0; j <= i; ++j) {
         const float f = w[j][i] * sqk[i][j];
         const float4 x = *reinterpret_cast<const float4*>(&sv[j][col]);
-        p[0] = fmaf(f, x.x, p[0]); p[1] = fmaf(f, x.y, p[1]); p[2] = fmaf(f, x.z, p[2]); p[3] = fmaf(f, x.w, p[3]);
+        p[i][0] = fmaf(f, x.x, p[i][0]); p[i][1] = fmaf(f, x.y, p[i][1]); p[i][2] = fmaf(f, x.z, p[i][2]); p[i][3] = fmaf(f, x.w, p[i][3]);
       }
-      const float4 o4 = make_float4(p[0] * a.scale, p[1] * a.scale, p[2] * a.scale, p[3] * a.scale);
+      const float4 o4 = make_float4(p[i][0] * a.scale, p[i][1] * a.scale, p[i][2] * a.scale, p[i][3] * a.scale);
       if (a.gate) *reinterpret_cast<float4*>(&so[i][col]) = o4;
       else *reinterpret_cast<float4*>(static_cast<float*>(a.o) + ((static_cast<int64_t>(b) * kTok + i) * a.H + h) * kD + col) = o4;
     }
@@ -177,14 +199,11 @@ __global__ void __launch_bounds__(kThreads, 2) lin_decode_kernel(const __grid_co
   if (a.gate) {  // output stage: warp i normalises and gates token i's row
     __syncthreads();
     if (warp < kTok) {
-      const auto* gate = static_cast<const __nv_bfloat16*>(a.gate) + b * a.gate_stride[0] + warp * a.gate_stride[1] + h * a.gate_stride[2];
       const float4 x = *reinterpret_cast<const float4*>(&so[warp][4 * lane]);
       float ss = x.x * x.x + x.y * x.y + x.z * x.z + x.w * x.w;
 #pragma unroll
       for (int off = 16; off; off >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, off);
       const float inv = 1.f / sqrtf(ss * (1.f / kD) + a.eps);
-      const float4 w4 = a.norm_weight ? *reinterpret_cast<const float4*>(a.norm_weight + 4 * lane) : make_float4(1.f, 1.f, 1.f, 1.f);
-      const uint2 gb = *reinterpret_cast<const uint2*>(gate + 4 * lane);
       const float2 g01 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gb.x));
       const float2 g23 = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&gb.y));
       float4 y;
