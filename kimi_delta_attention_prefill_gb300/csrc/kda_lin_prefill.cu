@@ -8,11 +8,13 @@
 // One block walks the chunks of a (sequence, head) or of a segment of one; its warps:
 //     0        copies (TMA; two tiles each of q, k and v) and the line of work items
 //     1        products (tcgen05)
-//     2        decays (3: the output stage's gate, into q's tile when q is used): sums in 64-bit fixed point (2^-32 of a factor of 2), so that no difference loses bits
+//     2        decays: sums in 64-bit fixed point (2^-32 of a factor of 2), so that no difference loses bits
+//     3        the output stage's gate, into q's tile when q is used
 //     4 - 7    weights P = (Q K^T) o D to bf16 over their scores; Q S times e^G in place, on which P V is then
-//              added; outputs (thread = token)
+//              added (thread = token)
 //     8 - 15   decayed values, transposed into tensor memory as three bf16 parts (24 bits together)
-//     16 - 23  the state, in fp32 registers (thread = half a column); its bf16 copy for Q S in shared memory
+//     16 - 23  the state, in fp32 registers (thread = half a column); its bf16 copy for Q S in shared memory;
+//              outputs (thread = half a token's row), through q's tile
 //
 // Rounded to bf16: P and the copy of S, for o only, which is bf16 itself.  The state sees 24-bit products:
 // S^T gets three products, one for each part of the values, with K as it lies.  The decay is on the values'
@@ -22,6 +24,14 @@
 //
 // The products of a chunk: Q K^T | units of tokens 0 - 63 | Q S | units of tokens 64 - 127 | P V.  Weights are made
 // during the three in the middle, outputs and the next state during P V and the next Q K^T.
+//
+// What bounds it: instructions of the warps that make weights, parts, states and outputs; each of the SM's four
+// schedulers issues for about 4500 cycles a chunk, and waits for one another make it 5700 (3 us), where the
+// products take 3100.  With all SMs at it 128 KB a chunk are 5.7 TB/s.  Tried and slower than 190 us at 8192
+// tokens x 96 heads: scores a chunk ahead in columns of their own with a ring of half the size (232), eight warps for
+// weights and outputs (226 - 249), outputs stored from registers (221), loops not unrolled (199 - 587), products
+// issued from rolled loops (212), parts by bf16x2 arithmetic (2 cycles an instruction, like the conversions that
+// they replace).  Two parts of the values instead of three leave states off by 2e-6.
 //
 // A token's NaN or infinity must not reach earlier tokens, but 0 * NaN is NaN in P V: values that are not
 // finite are cleared in the tile, and the rows that see one get NaN in its channel when they are written.
@@ -536,10 +546,10 @@ __device__ __forceinline__ void scale_block(uint32_t at, float e) {
   tmem_st32(at, x);
 }
 
-// NaN for the rows that see a value that is not finite, in its channel (cold).
-__device__ __forceinline__ void poison(uint32_t tl, const uint32_t* noted, uint32_t n, int i, int half) {
+// NaN for the rows that see a value that is not finite, in its channel, of some channels (cold).
+__device__ __forceinline__ void poison(uint32_t tl, const uint32_t* noted, uint32_t n, int i, int first, int channels) {
 #pragma unroll 1
-  for (int c = 64 * half; c < 64 * half + 64; ++c) {
+  for (int c = first; c < first + channels; ++c) {
     const uint32_t m = __ldcg(noted + c);
     const bool hit = (m >> 8) == n && 255 - static_cast<int>(m & 255) <= i;
     if (!__any_sync(0xffffffffu, hit)) continue;
@@ -782,7 +792,9 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
     if constexpr (kGate) LIN_WAIT(s.gate_full, n);
     LIN_WAIT(s.out[n & 1], n >> 1);
     tc_fence_after();
-    if (s.bad_chunk[n & 3] == n + 1) poison(to_q, p.p.bad + 4 * kD * blockIdx.x + kD * (n & 3), n, i, half);
+    // with the output stage all 128: both warps of a row sum its squares, and neither waits for the other's mark
+    if (s.bad_chunk[n & 3] == n + 1)
+      poison(to_q, p.p.bad + 4 * kD * blockIdx.x + kD * (n & 3), n, i, kGate ? 0 : 64 * half, kGate ? kD : 64);
     float f = a.scale;
     if constexpr (kGate) {  // the row's sum of squares, by both warps that have it
       float s0 = 0.f, s1 = 0.f;

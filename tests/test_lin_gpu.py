@@ -186,6 +186,22 @@ def test_what_is_not_finite_stays_where_it_belongs(what, value, segments):
     assert torch.equal(S[1, 1], S0[1, 1]) if what == "q" else not bool(torch.isfinite(S[1, 1]).all())
 
 
+@pytest.mark.parametrize("channel", [3, 70])
+def test_a_bad_value_takes_its_whole_row_through_the_output_stage(channel):
+    """The row's root mean square is not finite then, whichever warps have the channel."""
+    p = Prefill([300, 257], 12, 4, seed=9, gated=True)
+    o0, S0 = p.run()
+    t = [20 * h + 9 for h in range(12)]
+    for h in range(12):
+        p.v[t[h], h, channel] = float("nan") if h % 2 else float("inf")
+    o, S = p.run()
+    for h in range(12):
+        assert torch.equal(o[:t[h], h], o0[:t[h], h]) and torch.equal(o[300:, h], o0[300:, h])
+        assert not bool(torch.isfinite(o[t[h]:300, h]).any())
+    rest = torch.arange(D, device="cuda") != channel
+    assert torch.equal(S[:, :, :, rest], S0[:, :, :, rest]) and not bool(torch.isfinite(S[0, :, :, channel]).any())
+
+
 def test_neighbours_and_rows_outside_do_not_reach_a_sequence():
     """The tail of a chunk holds the next sequence's rows, here NaN; another sequence is all infinities."""
     p = Prefill([130, 140, 90], 2, 1, seed=12)
