@@ -3,13 +3,15 @@
 // With G_i the sum of the step's decays g_0 .. g_i, the recurrence over n <= 4 tokens unrolls to
 //     o_i = scale (e^{G_i} S^T q_i + sum_{j <= i} e^{G_i - G_j} (q_i . k_j) v_j)
 //     S  <- e^{G_m} S + sum_{j < m} e^{G_m - G_j} k_j v_j^T        (m accepted tokens)
-// so every output needs the old state only, and the state is read once and written once: the
-// step is bound by those 128 KiB a (sequence, head).  The dot products of all tokens run
-// side by side over the state in registers instead of one token after the other.
+// so every output needs the old state only, and the state is read once and written once: the step is
+// bound by those 128 KiB a (sequence, head).  One pass over the state's rows takes S^T q of all tokens from what
+// comes in and sends the new rows out at once; the rest of the outputs follows while they are on their way.
 //
-// Work split as the delta rule's step (kda_decode.cu): 256 threads a (sequence, head), warp w owns
-// columns [16 w, 16 w + 16), lane 4 r + c the columns 16 w + 4 c .. + 3 of rows r, r + 8, ..: 16 loads of
-// 16 bytes a thread in flight, sums over rows by three shuffles.
+// Work split: 256 threads a (sequence, head), warp w owns columns [16 w, 16 w + 16), lane 4 r + c the columns
+// 16 w + 4 c .. + 3 of rows r, r + 8, ..: eight loads of 16 bytes a thread in flight, three blocks an SM.
+// Measured (of copy bandwidth): 256 sequences x 96 heads, one token 459 us (104 %); 61 x 64, four tokens with the output
+// stage 79 us (89 %).  With the whole state in registers and two blocks an SM the latter took 94 us, and
+// 82 with this pass and two blocks.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cstdint>
@@ -28,18 +30,21 @@ constexpr int kRows = 16;  // of the state, a thread
 __device__ constexpr int at_row(int i) { return (i & 7) * 16 + (i >> 3); }
 
 template <int kTok>
-__global__ void __launch_bounds__(kThreads, 2) lin_decode_kernel(const __grid_constant__ LinArgs a, int lookahead) {
+__global__ void __launch_bounds__(kThreads, 3) lin_decode_kernel(const __grid_constant__ LinArgs a, int lookahead) {
+  constexpr int kP = kTok == 3 ? 4 : kTok;  // tokens whose sums are spread over the lanes
   __shared__ __align__(16) float sq[kTok][kD], sk[kTok][kD];  // by at_row
   __shared__ __align__(16) float sv[kTok][kD], so[kTok][kD];
-  __shared__ float sqk[kTok][kTok];  // q_i . k_j
+  __shared__ float sE[kP];             // e^{g up to token i}
+  __shared__ float sqk[kP][kTok];      // q_i . k_j times the decay between them
   const int unit = blockIdx.x, b = unit / a.H, h = unit - b * a.H, hq = h / a.group;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = lane >> 2, col = warp * 16 + (lane & 3) * 4;
-  float4* S = reinterpret_cast<float4*>(a.S_out + unit * kStateFloats);
-  float4 s[kRows];
+  float4* S = reinterpret_cast<float4*>(a.S_out + unit * kStateFloats) + ((r0 * kD + col) >> 2);
+  float4 s[8];  // rows r0 + 8 m on their way, eight at a time
 #pragma unroll
-  for (int m = 0; m < kRows; ++m) s[m] = S[((r0 + 8 * m) * kD + col) >> 2];
-  // the state and the rows of the unit that starts about half the resident blocks later, into L2 (a hint)
+  for (int m = 0; m < 8; ++m) s[m] = S[m * 2 * kD];
+  // the state and the rows of the unit that starts about a third of the resident blocks later, into L2 (a hint;
+  // from a third of a wave to one and a half they measured alike)
   if (warp == 1 && unit + lookahead < static_cast<int>(gridDim.x)) {
     const int next = unit + lookahead, nb = next / a.H, nh = next - nb * a.H, nq = nh / a.group;
     if (lane == 0) bulk_prefetch_l2(a.S_out + next * kStateFloats, kStateFloats * sizeof(float));
@@ -50,20 +55,11 @@ __global__ void __launch_bounds__(kThreads, 2) lin_decode_kernel(const __grid_co
       prefetch_l2(static_cast<const __nv_bfloat16*>(base) + nb * st[0] + i * st[1] + (which < 2 ? nq : nh) * st[2] + 64 * (lane & 1));
     }
   }
-  // the output stage's gate of token `warp`, for the end
-  uint2 gb = make_uint2(0, 0);
-  float4 w4 = make_float4(1.f, 1.f, 1.f, 1.f);
-  if (a.gate && warp < kTok) {
-    gb = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.gate) + b * a.gate_stride[0] + warp * a.gate_stride[1] +
-                                         h * a.gate_stride[2] + 4 * lane);
-    if (a.norm_weight) w4 = *reinterpret_cast<const float4*>(a.norm_weight + 4 * lane);
-  }
   int nc = a.n_commit ? a.n_commit[b] : kTok;
   if (nc < 0 || nc > kTok) {
     if (tid == 0) report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
     nc = 0;  // the state stays; outputs are made all the same
   }
-  // decays up to each token, in every thread
   float G[kTok];
 #pragma unroll
   for (int i = 0; i < kTok; ++i) G[i] = a.g[b * a.g_stride[0] + i * a.g_stride[1] + h * a.g_stride[2]];
@@ -82,6 +78,15 @@ __global__ void __launch_bounds__(kThreads, 2) lin_decode_kernel(const __grid_co
       }
     }
   }
+  // e^{g_{j+1} + .. + g_{i}}: a sum from its own first term, so that -inf before it does not touch it
+  auto decay = [&](int j, int i) {
+    float sum = 0.f;
+#pragma unroll
+    for (int t = 0; t < kTok; ++t)
+      if (t > j && t <= i) sum += G[t];
+    return expf(sum);
+  };
+  if (tid < kTok) sE[tid] = decay(-1, tid);
   __syncthreads();
   for (int p = warp; p < kTok * kTok; p += kThreads / 32) {
     const int i = p / kTok, j = p - i * kTok;
@@ -90,111 +95,118 @@ __global__ void __launch_bounds__(kThreads, 2) lin_decode_kernel(const __grid_co
     float d = x.x * y.x + x.y * y.y + x.z * y.z + x.w * y.w;
 #pragma unroll
     for (int off = 16; off; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-    if (lane == 0) sqk[i][j] = d;
+    if (lane == 0) sqk[i][j] = d * decay(j, i);
   }
-  // w[j][i] = e^{g_{j+1} + .. + g_i}: a sum from its own first term, so that -inf before it does not touch it
-  float w[kTok][kTok], E[kTok];
+  // the state after nc tokens: e times the one before, and each token's values times f = its decay up to there
+  const float e = decay(-1, nc - 1);
+  const uint64_t e2 = f32x2(e, e);
+  uint64_t x[kTok][2];
 #pragma unroll
   for (int j = 0; j < kTok; ++j) {
-    float sum = 0.f;
-    w[j][j] = 1.f;
-#pragma unroll
-    for (int i = j + 1; i < kTok; ++i) {
-      sum += G[i];
-      w[j][i] = expf(sum);
-    }
+    const float4 u = *reinterpret_cast<const float4*>(&sv[j][col]);
+    const float f = decay(j, nc - 1);
+    x[j][0] = f32x2(u.x * f, u.y * f);
+    x[j][1] = f32x2(u.z * f, u.w * f);
   }
-  {
-    float sum = 0.f;
+  // one pass over the state's rows: S^T q of what comes in, the new rows on their way out at once
+  uint64_t p2[kTok][2];
+#pragma unroll
+  for (int i = 0; i < kTok; ++i) p2[i][0] = p2[i][1] = f32x2(0.f, 0.f);
+#pragma unroll
+  for (int m = 0; m < kRows; m += 4) {
+    uint64_t y[4][2];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const float4 u = s[(m & 7) + t];
+      y[t][0] = f32x2(u.x, u.y);
+      y[t][1] = f32x2(u.z, u.w);
+    }
 #pragma unroll
     for (int i = 0; i < kTok; ++i) {
-      sum += G[i];
-      E[i] = expf(sum);
-    }
-  }
-
-  uint64_t s2[kRows][2];
-#pragma unroll
-  for (int m = 0; m < kRows; ++m) {
-    s2[m][0] = f32x2(s[m].x, s[m].y);
-    s2[m][1] = f32x2(s[m].z, s[m].w);
-  }
-  float p[kTok][4];  // S^T q
-#pragma unroll
-  for (int i = 0; i < kTok; ++i) {
-    uint64_t p01 = f32x2(0.f, 0.f), p23 = p01;
-#pragma unroll
-    for (int m = 0; m < kRows; m += 4) {
       const float4 q4 = *reinterpret_cast<const float4*>(&sq[i][r0 * 16 + m]);
       const float qv[4] = {q4.x, q4.y, q4.z, q4.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint64_t q2 = f32x2(qv[e], qv[e]);
-        p01 = fma_f32x2(q2, s2[m + e][0], p01);
-        p23 = fma_f32x2(q2, s2[m + e][1], p23);
+      for (int t = 0; t < 4; ++t) {
+        const uint64_t q2 = f32x2(qv[t], qv[t]);
+        p2[i][0] = fma_f32x2(q2, y[t][0], p2[i][0]);
+        p2[i][1] = fma_f32x2(q2, y[t][1], p2[i][1]);
       }
     }
-    const float2 lo = unpack_f32x2(p01), hi = unpack_f32x2(p23);
-    p[i][0] = lo.x; p[i][1] = lo.y; p[i][2] = hi.x; p[i][3] = hi.y;
-  }
+    if (nc > 0) {
 #pragma unroll
-  for (int off = 4; off < 32; off <<= 1)
+      for (int t = 0; t < 4; ++t) { y[t][0] = mul_f32x2(y[t][0], e2); y[t][1] = mul_f32x2(y[t][1], e2); }
 #pragma unroll
-    for (int i = 0; i < kTok; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) p[i][e] += __shfl_xor_sync(0xffffffffu, p[i][e], off);
-  __syncthreads();  // the products of q and k
-  if (r0 == 0) {
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) p[i][e] *= E[i];
-#pragma unroll
-      for (int j = 0; j <= i; ++j) {
-        const float f = w[j][i] * sqk[i][j];
-        const float4 x = *reinterpret_cast<const float4*>(&sv[j][col]);
-        p[i][0] = fmaf(f, x.x, p[i][0]); p[i][1] = fmaf(f, x.y, p[i][1]); p[i][2] = fmaf(f, x.z, p[i][2]); p[i][3] = fmaf(f, x.w, p[i][3]);
-      }
-      const float4 o4 = make_float4(p[i][0] * a.scale, p[i][1] * a.scale, p[i][2] * a.scale, p[i][3] * a.scale);
-      if (a.gate) *reinterpret_cast<float4*>(&so[i][col]) = o4;
-      else *reinterpret_cast<float4*>(static_cast<float*>(a.o) + ((static_cast<int64_t>(b) * kTok + i) * a.H + h) * kD + col) = o4;
-    }
-  }
-  if (nc > 0) {
-    float f[kTok], e = 0.f;  // of each token in the state after nc of them
-#pragma unroll
-    for (int i = 0; i < kTok; ++i) {
-      f[i] = 0.f;
-      if (i == nc - 1) e = E[i];
-#pragma unroll
-      for (int t = i; t < kTok; ++t)
-        if (t == nc - 1) f[i] = w[i][t];
-    }
-    const uint64_t e2 = f32x2(e, e);
-#pragma unroll
-    for (int m = 0; m < kRows; ++m) { s2[m][0] = mul_f32x2(s2[m][0], e2); s2[m][1] = mul_f32x2(s2[m][1], e2); }
-#pragma unroll
-    for (int j = 0; j < kTok; ++j) {
-      if (j >= nc) break;  // a later token's values, whatever they are, do not meet the state
-      const float4 x = *reinterpret_cast<const float4*>(&sv[j][col]);
-      const uint64_t x01 = f32x2(x.x * f[j], x.y * f[j]), x23 = f32x2(x.z * f[j], x.w * f[j]);
-#pragma unroll
-      for (int m = 0; m < kRows; m += 4) {
+      for (int j = 0; j < kTok; ++j) {
+        if (j >= nc) break;  // a later token's values, whatever they are, do not meet the state
         const float4 k4 = *reinterpret_cast<const float4*>(&sk[j][r0 * 16 + m]);
         const float kv[4] = {k4.x, k4.y, k4.z, k4.w};
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
           const uint64_t k2 = f32x2(kv[t], kv[t]);
-          s2[m + t][0] = fma_f32x2(k2, x01, s2[m + t][0]);
-          s2[m + t][1] = fma_f32x2(k2, x23, s2[m + t][1]);
+          y[t][0] = fma_f32x2(k2, x[j][0], y[t][0]);
+          y[t][1] = fma_f32x2(k2, x[j][1], y[t][1]);
         }
+      }
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        const float2 lo = unpack_f32x2(y[t][0]), hi = unpack_f32x2(y[t][1]);
+        __stcs(&S[(m + t) * 2 * kD], make_float4(lo.x, lo.y, hi.x, hi.y));
       }
     }
 #pragma unroll
-    for (int m = 0; m < kRows; ++m) {
-      const float2 lo = unpack_f32x2(s2[m][0]), hi = unpack_f32x2(s2[m][1]);
-      __stcs(&S[((r0 + 8 * m) * kD + col) >> 2], make_float4(lo.x, lo.y, hi.x, hi.y));
+    for (int t = 0; t < 4; ++t)
+      if (m < kRows - 8) s[(m & 7) + t] = S[(m + 8 + t) * 2 * kD];
+  }
+  // the output stage's gate of token `warp`
+  uint2 gb = make_uint2(0, 0);
+  float4 w4 = make_float4(1.f, 1.f, 1.f, 1.f);
+  if (a.gate && warp < kTok) {
+    gb = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.gate) + b * a.gate_stride[0] + warp * a.gate_stride[1] +
+                                         h * a.gate_stride[2] + 4 * lane);
+    if (a.norm_weight) w4 = *reinterpret_cast<const float4*>(a.norm_weight + 4 * lane);
+  }
+  // sums over the eight lanes of a column, halving what a lane keeps: value i * 4 + c is column col + c of token i
+  float p[kP * 4];
+#pragma unroll
+  for (int i = 0; i < kP; ++i) {
+    const float2 lo = i < kTok ? unpack_f32x2(p2[i % kTok][0]) : make_float2(0.f, 0.f), hi = i < kTok ? unpack_f32x2(p2[i % kTok][1]) : make_float2(0.f, 0.f);
+    p[4 * i] = lo.x; p[4 * i + 1] = lo.y; p[4 * i + 2] = hi.x; p[4 * i + 3] = hi.y;
+  }
+  int first = 0;
+  constexpr int kKept = kP == 4 ? 2 : 1;
+#pragma unroll
+  for (int off = 16, n = kP * 4; off >= 4; off >>= 1) {
+    if (n > 1) {
+      n >>= 1;
+      const bool up = lane & off;
+#pragma unroll
+      for (int t = 0; t < kP * 2; ++t)
+        if (t < n) {
+          const float other = __shfl_xor_sync(0xffffffffu, up ? p[t] : p[t + n], off);
+          p[t] = (up ? p[t + n] : p[t]) + other;
+        }
+      if (up) first += n;
+    } else {
+      p[0] += __shfl_xor_sync(0xffffffffu, p[0], off);
     }
+  }
+  __syncthreads();  // the products of q and k
+  const int tok = first >> 2, c0 = col + (first & 3);
+  if (tok < kTok && (kP > 1 || r0 % 2 == 0)) {
+    const float E = sE[tok];
+    float y[kKept];
+#pragma unroll
+    for (int t = 0; t < kKept; ++t) y[t] = p[t] * E;
+#pragma unroll
+    for (int j = 0; j < kTok; ++j) {
+      if (j > tok) break;
+      const float f = sqk[tok][j];
+#pragma unroll
+      for (int t = 0; t < kKept; ++t) y[t] = fmaf(f, sv[j][c0 + t], y[t]);
+    }
+    float* dst = a.gate ? &so[tok][c0] : static_cast<float*>(a.o) + ((static_cast<int64_t>(b) * kTok + tok) * a.H + h) * kD + c0;
+#pragma unroll
+    for (int t = 0; t < kKept; ++t) dst[t] = y[t] * a.scale;
   }
   if (a.gate) {  // output stage: warp i normalises and gates token i's row
     __syncthreads();
