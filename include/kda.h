@@ -494,8 +494,8 @@ kda_status kda_attn_decode_paged(const kda_bf16* q, const int64_t* q_stride, con
  *   workspace   kda_lin_prefill_workspace_size(...) bytes (never 0), 256-byte aligned; its contents need
  *               no preparation and mean nothing between calls
  * The same call gives the same bits; a split sequence's last bits may depend on what else is in the call.
- * Products take bf16 operands: q, k, v as they are, the decayed weights of a chunk and the state in front
- * of it rounded to bf16 for o only.  The states themselves are carried in fp32, from decayed values of 24 bits.
+ * Products take bf16 operands: q, k, v as they are, the state in front of a chunk rounded to bf16 and the
+ * chunk's decayed weights to 16 bits, for o only.  The states themselves are carried in fp32, from decayed values of 24 bits.
  */
 size_t kda_lin_prefill_workspace_size(int n_seq, int H, int d, int64_t total_tokens, int n_segments);
 kda_status kda_lin_prefill(const kda_bf16* q, const int64_t* q_stride, const kda_bf16* k, const int64_t* k_stride,

@@ -10,13 +10,15 @@
 //     1        products (tcgen05)
 //     2        decays: sums in 64-bit fixed point (2^-32 of a factor of 2), so that no difference loses bits
 //     3        the output stage's gate, into q's tile when q is used
-//     4 - 7    weights P = (Q K^T) o D to bf16 over their scores; Q S times e^G in place, on which P V is then
+//     4 - 7    weights P = (Q K^T) o D as two bf16 parts over their scores; Q S times e^G in place, on which P V is then
 //              added (thread = token)
 //     8 - 15   decayed values, transposed into tensor memory as three bf16 parts (24 bits together)
 //     16 - 23  the state, in fp32 registers (thread = half a column); its bf16 copy for Q S in shared memory;
 //              outputs (thread = half a token's row), through q's tile
 //
-// Rounded to bf16: P and the copy of S, for o only, which is bf16 itself.  The state sees 24-bit products:
+// Rounded to bf16: the copy of S, for o only, which is bf16 itself.  P has 16 bits: with 8 a row that few weights
+// make is off by as much again as its own rounding (o off by 0.0023 instead of 0.0017 of its norm on short
+// sequences, by 0.0026 on a few tokens; the second parts' product costs 3 %).  The state sees 24-bit products:
 // S^T gets three products, one for each part of the values, with K as it lies.  The decay is on the values'
 // side because they can then be an operand in tensor memory: shared memory, whose 128 bytes a cycle the
 // products of operands in it take in full, is the block's bottleneck.  The parts go through a ring of four
@@ -25,13 +27,14 @@
 // The products of a chunk: Q K^T | units of tokens 0 - 63 | Q S | units of tokens 64 - 127 | P V.  Weights are made
 // during the three in the middle, outputs and the next state during P V and the next Q K^T.
 //
-// What bounds it: instructions of the warps that make weights, parts, states and outputs; each of the SM's four
-// schedulers issues for about 4500 cycles a chunk, and waits for one another make it 5700 (3 us), where the
-// products take 3100.  With all SMs at it 128 KB a chunk are 5.7 TB/s.  Tried and slower than 190 us at 8192
-// tokens x 96 heads: scores a chunk ahead in columns of their own with a ring of half the size (232), eight warps for
-// weights and outputs (226 - 249), outputs stored from registers (221), loops not unrolled (199 - 587), products
-// issued from rolled loops (212), parts by bf16x2 arithmetic (2 cycles an instruction, like the conversions that
-// they replace).  Two parts of the values instead of three leave states off by 2e-6.
+// What bounds it: the chain of a chunk.  8192 tokens x 96 heads, one block each on 96 of 152 SMs: 200 us, 3.1 us
+// a chunk, of which the products take 1.9 and each scheduler's instructions 1.6 to 2.4; 8 heads x 262144 tokens on all SMs: 3.6 us
+// a chunk, 128 KB of it at 5.5 TB/s.  Tried and slower than the 190 us of before the second parts: scores
+// a chunk ahead in columns of their own with a ring of half the size (232), eight warps for weights and outputs
+// (226 - 249), outputs stored from registers (221), loops not unrolled (199 - 587), products issued from rolled
+// loops (212), parts by bf16x2 arithmetic (2 cycles an instruction, like the conversions that they
+// replace); cutting each of 96 heads into 2 - 6 segments (235 - 275: the rule cuts only what fits the SMs at once;
+// 64 heads into 2: 190 -> 167).  Two parts of the values instead of three leave states off by 2e-6.
 //
 // A token's NaN or infinity must not reach earlier tokens, but 0 * NaN is NaN in P V: values that are not
 // finite are cleared in the tile, and the rows that see one get NaN in its channel when they are written.
@@ -347,6 +350,16 @@ __device__ __forceinline__ void product_ts(uint32_t who, uint32_t d, uint32_t a,
   for (uint32_t kk = 0; kk < kSteps; ++kk) mma_f16_ta_if(who, d, a + 8 * kk, b + 128 * kk, id, more | kk);
 }
 
+// D += P B: of each 32 tokens' weights 16 columns are the first parts, the next 16 the second.
+__device__ __forceinline__ void product_weights(uint32_t who, uint32_t d, uint32_t a, uint64_t b) {
+  constexpr uint32_t id = idesc_f16(128, 128, true, false, true);
+#pragma unroll
+  for (uint32_t kk = 0; kk < 16; ++kk) {
+    const uint32_t step = 2 * (kk >> 2) + (kk & 1);  // 16 tokens
+    mma_f16_ta_if(who, d, a + 8 * kk, b + 128 * step, id, 1);
+  }
+}
+
 template <bool kFull>
 __device__ void mma_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
   bool dead = false;
@@ -397,7 +410,7 @@ __device__ void mma_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
         LIN_WAIT(s.ready, n);  // v has landed before its parts were made
         tc_fence_after();
         if (dead) break;
-        product_ts<8>(who, kTO, kTS, d_m + tv, 1);
+        product_weights(who, kTO, kTS, d_m + tv);
         mma_commit_if(who, &s.out[n & 1]);
       }
     }
@@ -532,6 +545,12 @@ __device__ __forceinline__ uint64_t open_gates(uint32_t g) {
   return f32x2(r0, r1);
 }
 
+// A pair of floats as bf16 and what that leaves of them.
+__device__ __forceinline__ void two_parts(uint64_t y, uint32_t& hi, uint32_t& low) {
+  hi = bf162_of(y);
+  low = bf162_of(fma_f32x2(floats(hi), f32x2(-1.f, -1.f), y));
+}
+
 // 32 columns of a row times e, in place.
 __device__ __forceinline__ void scale_block(uint32_t at, float e) {
   float x[32];
@@ -586,21 +605,21 @@ __device__ void weight_warps(const LinParams& p, Small& s, int w, int lane) {
 #pragma unroll 1
       for (int b = 0; b < w; ++b) {  // D_ij = 2^{G_i - G at the block's end} 2^{G at the block's end - G_j}
         float x[32];
-        uint32_t pk[16];
         tmem_ld32(ts + 32 * b, x);
         const float rf = exp2_fast(G - d.G[32 * b + 31]);
         const uint64_t r2 = f32x2(rf, rf);
+        uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&d.cf[32 * b + e]);
-          pk[e / 2] = bf162_of(mul_f32x2(f32x2(x[e], x[e + 1]), mul_f32x2(r2, f32x2(f.x, f.y))));
-          pk[e / 2 + 1] = bf162_of(mul_f32x2(f32x2(x[e + 2], x[e + 3]), mul_f32x2(r2, f32x2(f.z, f.w))));
+          two_parts(mul_f32x2(f32x2(x[e], x[e + 1]), mul_f32x2(r2, f32x2(f.x, f.y))), pk[e / 2], pk[16 + e / 2]);
+          two_parts(mul_f32x2(f32x2(x[e + 2], x[e + 3]), mul_f32x2(r2, f32x2(f.z, f.w))), pk[e / 2 + 1], pk[17 + e / 2]);
         }
-        tmem_st16(ts + 16 * b, reinterpret_cast<const float(&)[16]>(pk));
+        tmem_st32(ts + 32 * b, reinterpret_cast<const float(&)[32]>(pk));
       }
       {
         float x[32];
-        uint32_t pk[16];
+        uint32_t pk[32];
         tmem_ld32(ts + 32 * w, x);
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
@@ -609,14 +628,14 @@ __device__ void weight_warps(const LinParams& p, Small& s, int w, int lane) {
           const float y1 = e + 1 <= lane ? x[e + 1] * exp2_fast(G - f.y) : 0.f;
           const float y2 = e + 2 <= lane ? x[e + 2] * exp2_fast(G - f.z) : 0.f;
           const float y3 = e + 3 <= lane ? x[e + 3] * exp2_fast(G - f.w) : 0.f;
-          pk[e / 2] = pack_bf162(y0, y1);
-          pk[e / 2 + 1] = pack_bf162(y2, y3);
+          two_parts(f32x2(y0, y1), pk[e / 2], pk[16 + e / 2]);
+          two_parts(f32x2(y2, y3), pk[e / 2 + 1], pk[17 + e / 2]);
         }
-        tmem_st16(ts + 16 * w, reinterpret_cast<const float(&)[16]>(pk));
+        tmem_st32(ts + 32 * w, reinterpret_cast<const float(&)[32]>(pk));
 #pragma unroll
-        for (int e = 0; e < 16; ++e) pk[e] = 0;
+        for (int e = 0; e < 32; ++e) pk[e] = 0;
 #pragma unroll 1
-        for (int b = w + 1; b < 4; ++b) tmem_st16(ts + 16 * b, reinterpret_cast<const float(&)[16]>(pk));
+        for (int b = w + 1; b < 4; ++b) tmem_st32(ts + 32 * b, reinterpret_cast<const float(&)[32]>(pk));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.dec_empty);

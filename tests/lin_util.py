@@ -45,14 +45,15 @@ def stage_far(o, far, gate, weight, eps):
 
 def prefill_far(q, k, v, g, S, scale):
     """(o, final state): how far before o's own rounding.  With absolute values in their places the recurrence gives
-    the sums that the errors are relative to.  o: the weights of a chunk and the state in front of it are rounded to
-    bf16 (a half step each, on parts that add up to the sum), a state has its own error, sums and decays of 32 bits: a twentieth
-    of a half step more; exponents up to E have lost E 2^-24 twice, in units of ln 2.  States: decayed
+    the sums that the errors are relative to.  o: the state in front of a chunk is rounded to bf16 (a half step),
+    the chunk's weights to two bf16 parts (a half step of what the first leaves; a part that is zero is exact), a state has its
+    own error, sums and decays of 32 bits: a twentieth of a half step more; exponents up to E have lost E 2^-24 twice, in units of ln 2.  States: decayed
     values in three bf16 parts (2^-21 left over at most), 128 products a chunk and one step a chunk in 32 bits, decays within 2^-21."""
     A, states = tokens(q.abs(), k.abs(), v.abs(), g, None if S is None else S.abs(), abs(scale))
     n = v.shape[0]
     deepest = max((float(-g[i:i + GROUP].double().clamp(min=-192 * math.log(2)).sum(0).min()) for i in range(0, n, GROUP)), default=0.0)
-    return A * (1.05 * U16 + 4 * deepest * U32), states[-1] * (2.0 ** -21 + GROUP * 2 * U32 + (n // GROUP + 2) * 2.0 ** -21)
+    state = 0.0 if S is None and n <= GROUP else 1.0  # none in front of a first chunk
+    return A * ((state + 0.05) * U16 + U16 * U16 + 4 * deepest * U32), states[-1] * (2.0 ** -21 + GROUP * 2 * U32 + (n // GROUP + 2) * 2.0 ** -21)
 
 
 def decode_far(q, k, v, g, S, scale):
