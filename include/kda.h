@@ -491,8 +491,10 @@ kda_status kda_attn_decode_paged(const kda_bf16* q, const int64_t* q_stride, con
  *   S_out       [n_seq, H, d, d] fp32 final states, or NULL; may be S_in (in place)
  *   n_segments  0: a sequence is split over the SMs by the library's rule when there are few heads and
  *               sequences; k >= 1: every sequence into min(k, its chunks) segments
- *   workspace   kda_lin_prefill_workspace_size(...) bytes (never 0), 256-byte aligned; its contents need
- *               no preparation and mean nothing between calls
+ *   workspace   kda_lin_prefill_workspace_size(...) bytes, 256-byte aligned; its contents need no
+ *               preparation and mean nothing between calls.  Calls with no more (sequence, head) pairs than SMs
+ *               and nothing to split need none: the size is 0 and the workspace may be NULL
+ * Outputs must not overlap inputs, but for S_out = S_in.
  * The same call gives the same bits; a split sequence's last bits may depend on what else is in the call.
  * Products take bf16 operands: q, k, v as they are, the state in front of a chunk rounded to bf16 and the
  * chunk's decayed weights to 16 bits, for o only.  The states themselves are carried in fp32, from decayed values of 24 bits.

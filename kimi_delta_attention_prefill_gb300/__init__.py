@@ -655,7 +655,8 @@ def combine_pairs(M, S_tilde, S_in=None, entry=None, stream=None):
 # is wrong run only when something is.
 _BF16, _E4M3, _I32 = torch.bfloat16, torch.float8_e4m3fn, torch.int32
 _pack_cache = struct.Struct("4q 3q 3q 2q 2q q 3i 4x").pack  # kda_kv_cache
-_pack2, _pack3 = struct.Struct("2q").pack, struct.Struct("3q").pack
+_pack2, _pack3, _pack4 = (struct.Struct(n).pack for n in ("2q", "3q", "4q"))
+_ALIGNMENT = 3  # KDA_ERR_ALIGNMENT
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
@@ -971,27 +972,20 @@ def _decays(g, lead, H):
     raise ValueError(f"g must have shape {lead + (H,)} or {(H,)}, got {tuple(g.shape)}")
 
 
-def _lin_rows(q, k, v, g, gate, norm_weight, stream, n_lead, names, pack):
-    """What the two calls share: sizes, and the rows' strides as the library takes them.  As for the
-    attention cache, what is checked for every call is checked in few steps."""
-    try:
-        shape, dev = q.shape, q.get_device()
-        lead, (H, d) = shape[:n_lead], v.shape[n_lead:]
-        Hk = shape[n_lead]
-        qs, ks, vs, gs = q.stride(), k.stride(), v.stride(), g.stride()
-        if len(gs) == 1:
-            gs = (0,) * n_lead + gs
-        if (gate is None and norm_weight is None and dev >= 0 and dev == k.get_device() == v.get_device() == g.get_device() == _here(stream)
-                and q.dtype is k.dtype is v.dtype is _BF16 and g.dtype is _F32 and d == HEAD_DIM and shape == k.shape
-                and shape[-1] == HEAD_DIM and len(shape) == n_lead + 2 and v.shape[:n_lead] == lead and H % Hk == 0
-                and (g.shape == lead + (H,) or g.shape == (H,)) and qs[-1] == ks[-1] == vs[-1] == 1):
-            return (lead, Hk, H, pack(*_sound(shape, qs)), pack(*_sound(shape, ks)), pack(*_sound(v.shape, vs)), pack(*gs), None)
-    except (AttributeError, ValueError, TypeError, IndexError, ZeroDivisionError):
-        pass
-    return _say_lin_rows(q, k, v, g, gate, norm_weight, n_lead, names, pack)
+def _stage_rows(gate, norm_weight, shape, dev, pack):
+    """(whether they are what they should be at a quick look, gate's strides)"""
+    if gate is None:
+        return norm_weight is None, None
+    st = gate.stride()
+    return (gate.shape == shape and gate.dtype is _BF16 and gate.get_device() == dev and st[-1] == 1
+            and (norm_weight is None or (norm_weight.shape == (HEAD_DIM,) and norm_weight.dtype is _F32
+                                         and norm_weight.get_device() == dev and norm_weight.is_contiguous()))), pack(*st)
 
 
 def _say_lin_rows(q, k, v, g, gate, norm_weight, n_lead, names, pack):
+    """What the two calls share: sizes, and the rows' strides as the library takes them; says what is wrong.  The calls
+    look at well-formed arguments in fewer steps, as for the attention cache, and come here with the others: torch gives
+    dimensions of extent 1 any stride, which the library may refuse."""
     if not isinstance(q, torch.Tensor) or q.dim() != n_lead + 2:
         raise ValueError(f"q must be a tensor [{names}, heads, {HEAD_DIM}]")
     if not isinstance(v, torch.Tensor) or v.dim() != n_lead + 2:
@@ -1028,28 +1022,51 @@ def lin_prefill(q, k, v, g, cu_seqlens, S_in=None, scale=1.0, gate=None, norm_we
     ``sigmoid(gate) * norm_weight * o / sqrt(mean(o^2) + eps)``.  S_out may be S_in.
     Returns ``(o, S_out)``: ``[T, H, 128]`` bf16 and ``[N, H, 128, 128]`` fp32.
     """
-    (T,), Hk, H, qs, ks, vs, gs, gates = _lin_rows(q, k, v, g, gate, norm_weight, stream, 1, "T", _pack2)
+    good, lib = False, _lib or library()
+    try:
+        shape, dev = q.shape, q.get_device()
+        T, Hk, d = shape
+        full = v.shape
+        H = full[1]
+        qs, ks, vs, gs = q.stride(), k.stride(), v.stride(), g.stride()
+        if (dev >= 0 and dev == _here(stream) and dev == k.get_device() == v.get_device() == g.get_device() == cu_seqlens.get_device()
+                and q.dtype is k.dtype is v.dtype is _BF16 and g.dtype is _F32 and d == HEAD_DIM and shape == k.shape
+                and full == (T, H, d) and g.shape == ((T, H) if len(gs) == 2 else (H,)) and qs[2] == ks[2] == vs[2] == 1 and H % Hk == 0):
+            good, gates = _stage_rows(gate, norm_weight, full, dev, _pack3)
+            qs, ks, vs, gs = _pack3(*qs), _pack3(*ks), _pack3(*vs), _pack2(*gs) if len(gs) == 2 else _pack2(0, gs[0])
+    except (AttributeError, ValueError, TypeError, IndexError, ZeroDivisionError):
+        good = False
+    if not good:
+        (T,), Hk, H, qs, ks, vs, gs, gates = _say_lin_rows(q, k, v, g, gate, norm_weight, 1, "T", _pack2)
+        _on(q.get_device(), stream, k, v, g, gate, norm_weight, cu_seqlens if isinstance(cu_seqlens, torch.Tensor) else None)
     n_seq = cu_seqlens.shape[0] - 1 if isinstance(cu_seqlens, torch.Tensor) and cu_seqlens.dim() == 1 else -1
     if n_seq < 0:
         raise ValueError("cu_seqlens must be a tensor [sequences + 1]")
-    _on(q.get_device(), stream, k, v, g, gate, norm_weight, S_in, cu_seqlens, o, S_out, workspace, dev_status)
-    shape, states = (T, H, HEAD_DIM), (n_seq, H, HEAD_DIM, HEAD_DIM)
+    states = (n_seq, H, HEAD_DIM, HEAD_DIM)
     cu = _index(cu_seqlens, "cu_seqlens", (n_seq + 1,))
     if S_in is not None:
         _need(S_in, "S_in", _F32, states)
-    o = _output(shape, _BF16, q.device, stream) if o is None else _need(o, "o", _BF16, shape)
+    _on(q.get_device(), stream, S_in, o, S_out, workspace, dev_status)
+    if o is None:
+        o = _output((T, H, HEAD_DIM), _BF16, q.device, stream)
+    else:
+        _need(o, "o", _BF16, (T, H, HEAD_DIM))
     S_out = _output(states, _F32, q.device, stream) if S_out is None else _need(S_out, "S_out", _F32, states)
-    lib = _lib or library()
     if workspace is None:
-        ws_bytes = lib.kda_lin_prefill_workspace_size(n_seq, H, HEAD_DIM, T, n_segments)
-        workspace = _scratch(ws_bytes, q.device, stream)
-        ws = workspace.data_ptr()
+        ws, ws_bytes = None, lib.kda_lin_prefill_workspace_size(n_seq, H, HEAD_DIM, T, n_segments)
+        if ws_bytes:
+            workspace = _scratch(ws_bytes, q.device, stream)
+            ws = workspace.data_ptr()
     else:
         ws, ws_bytes = _workspace(workspace)
-    st = lib.kda_lin_prefill(
-        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs, scale, _ptr(gate), gates,
-        _ptr(norm_weight), eps, _ptr(S_in), cu, n_seq, T, o.data_ptr(), S_out.data_ptr(), Hk, H, HEAD_DIM, n_segments, ws,
-        ws_bytes, _status_ptr(dev_status), _stream_of(stream))
+    for good in (good, False):
+        st = lib.kda_lin_prefill(
+            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs, scale, _ptr(gate), gates,
+            _ptr(norm_weight), eps, _ptr(S_in), cu, n_seq, T, o.data_ptr(), S_out.data_ptr(), Hk, H, HEAD_DIM, n_segments, ws,
+            ws_bytes, _status_ptr(dev_status), _stream_of(stream))
+        if st != _ALIGNMENT or not good:
+            break
+        _, _, _, qs, ks, vs, gs, gates = _say_lin_rows(q, k, v, g, gate, norm_weight, 1, "T", _pack2)
     if st != 0:
         raise KdaError(st, "kda_lin_prefill")
     return o, S_out
@@ -1064,16 +1081,39 @@ def lin_decode(q, k, v, g, S_state, n_commit=None, scale=1.0, gate=None, norm_we
     q, k ``[B, n_tok, Hk, 128]``, v and gate ``[B, n_tok, H, 128]`` bf16 (leading dimensions may be
     strided); g ``[B, n_tok, H]`` or ``[H]`` fp32.  Returns o ``[B, n_tok, H, 128]`` fp32.
     """
-    (B, n_tok), Hk, H, qs, ks, vs, gs, gates = _lin_rows(q, k, v, g, gate, norm_weight, stream, 2, "B, n_tok", _pack3)
-    _on(q.get_device(), stream, k, v, g, gate, norm_weight, S_state, n_commit, o, dev_status)
+    good = False
+    try:
+        shape, dev = q.shape, q.get_device()
+        B, n_tok, Hk, d = shape
+        full = v.shape
+        H = full[2]
+        qs, ks, vs, gs = q.stride(), k.stride(), v.stride(), g.stride()
+        if (dev >= 0 and dev == _here(stream) and dev == k.get_device() == v.get_device() == g.get_device() == S_state.get_device()
+                and q.dtype is k.dtype is v.dtype is _BF16 and g.dtype is _F32 and d == HEAD_DIM and shape == k.shape
+                and full == (B, n_tok, H, d) and g.shape == ((B, n_tok, H) if len(gs) == 3 else (H,))
+                and qs[3] == ks[3] == vs[3] == 1 and H % Hk == 0):
+            good, gates = _stage_rows(gate, norm_weight, full, dev, _pack4)
+            qs, ks, vs, gs = _pack4(*qs), _pack4(*ks), _pack4(*vs), _pack3(*gs) if len(gs) == 3 else _pack3(0, 0, gs[0])
+    except (AttributeError, ValueError, TypeError, IndexError, ZeroDivisionError):
+        good = False
+    if not good:
+        (B, n_tok), Hk, H, qs, ks, vs, gs, gates = _say_lin_rows(q, k, v, g, gate, norm_weight, 2, "B, n_tok", _pack3)
+        _on(q.get_device(), stream, k, v, g, gate, norm_weight)
     _need(S_state, "S_state", _F32, (B, H, HEAD_DIM, HEAD_DIM))
     commit = None if n_commit is None else _index(n_commit, "n_commit", (B,))
-    shape = (B, n_tok, H, HEAD_DIM)
-    o = _output(shape, _F32, q.device, stream) if o is None else _need(o, "o", _F32, shape)
-    st = (_lib or library()).kda_lin_decode(
-        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs, scale, _ptr(gate), gates,
-        _ptr(norm_weight), eps, S_state.data_ptr(), commit, o.data_ptr(), B, n_tok, Hk, H, HEAD_DIM,
-        _status_ptr(dev_status), _stream_of(stream))
+    _on(q.get_device(), stream, S_state, n_commit, o, dev_status)
+    if o is None:
+        o = _output((B, n_tok, H, HEAD_DIM), _F32, q.device, stream)
+    else:
+        _need(o, "o", _F32, (B, n_tok, H, HEAD_DIM))
+    for good in (good, False):
+        st = (_lib or library()).kda_lin_decode(
+            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, g.data_ptr(), gs, scale, _ptr(gate), gates,
+            _ptr(norm_weight), eps, S_state.data_ptr(), commit, o.data_ptr(), B, n_tok, Hk, H, HEAD_DIM,
+            _status_ptr(dev_status), _stream_of(stream))
+        if st != _ALIGNMENT or not good:
+            break
+        _, _, _, qs, ks, vs, gs, gates = _say_lin_rows(q, k, v, g, gate, norm_weight, 2, "B, n_tok", _pack3)
     if st != 0:
         raise KdaError(st, "kda_lin_decode")
     return o
@@ -1143,10 +1183,11 @@ def block_norm(x, weight=None, y=None, post_norm=False, post_weight=None, gate=N
         if weight is not None:
             _need(weight, "weight", _F32, (W,))
         _on(x.get_device(), stream, y, gate, weight, post_weight)
+    if h is not None or x_out is not None:
+        _on(x.get_device(), stream, h, x_out)
     if y is not None:
         x_out = _output(shape, dtype, x.device, stream) if x_out is None else _need(x_out, "x_out", dtype, shape)
     h = _output(shape, _BF16, x.device, stream) if h is None else _need(h, "h", _BF16, shape)
-    _on(x.get_device(), stream, h, x_out)
     st = (_lib or library()).kda_block_norm(
         x.data_ptr(), 0 if dtype is _BF16 else 1, xs, _ptr(weight), _ptr(y), ys, post_norm, _ptr(post_weight), _ptr(gate),
         gs, scale, eps, h.data_ptr(), _ptr(x_out), T, W, _stream_of(stream))

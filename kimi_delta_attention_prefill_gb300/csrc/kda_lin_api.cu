@@ -81,8 +81,8 @@ kda_status kda_lin_prefill(const kda_bf16* q, const int64_t* q_stride, const kda
   int sms = 152;
   const kda_status dev = static_cast<kda_status>(kda::current_device_status(&sms));
   if (dev != KDA_OK) sms = 152;
-  if (!workspace || workspace_bytes < kda::lin_prefill_workspace(n_seq, total_tokens, H, n_segments, sms))
-    return KDA_ERR_WORKSPACE;
+  const size_t need = kda::lin_prefill_workspace(n_seq, total_tokens, H, n_segments, sms);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
   if (dev != KDA_OK) return dev;
   a.S_in = S_in; a.S_out = S_out; a.cu = cu_seqlens; a.n_segments = n_segments; a.workspace = workspace;
   a.status = dev_status; a.stream = stream;

@@ -39,7 +39,7 @@
 // A token's NaN or infinity must not reach earlier tokens, but 0 * NaN is NaN in P V: values that are not
 // finite are cleared in the tile, and the rows that see one get NaN in its channel when they are written.
 //
-// Few heads: plan_segments' rule cuts a sequence into as many segments as its share of the work is worth
+// Few heads: segments_of's rule cuts a sequence into as many segments as its share of the work is worth
 // in SMs.  A first pass (the same kernel without q and o) leaves each segment's state from zeros, the second
 // begins with the sum over the segments before it.
 #include <cuda.h>
@@ -81,11 +81,10 @@ struct Item {
 };
 
 struct Plan {
-  int* counts = nullptr;  // items of pass 2, of pass 1; next item of pass 2, of pass 1; items without tokens, after pass 2's
+  int* counts = nullptr;  // (null: block i has head i % H of sequence i / H) items of pass 2, of pass 1; next item of pass 2, of pass 1; items without tokens, after pass 2's
   Item* items[2] = {nullptr, nullptr};
   float* decay = nullptr;  // [slots][H] factor of a segment's decay
   float* slots = nullptr;  // [slots][H][128][128]: slot base: the sequence's entry state; base + 1 + j: segment j's exit
-  uint32_t* bad = nullptr; // [blocks][4][128] values that are not finite, of a block's chunks (clear_bad)
   int64_t most[2] = {0, 0}, n_slots = 0;
 };
 
@@ -100,7 +99,17 @@ __host__ __device__ inline int segments_of(int64_t len, int64_t tokens, int H, i
   return n < 1 ? 1 : static_cast<int>(n);
 }
 
+// A block for each (sequence, head) and nothing to split: no plan, no workspace (48 items of 97 tokens: 10 us on the
+// device instead of 15, and an allocation less).
+bool one_item_a_block(int n_seq, int64_t tokens, int H, int forced, int sms) {
+  return static_cast<int64_t>(n_seq) * H <= sms && segments_of(tokens, tokens, H, sms, forced) == 1;
+}
+
 size_t plan_layout(Plan* p, void* ws, int n_seq, int64_t tokens, int H, int forced, int sms) {
+  if (one_item_a_block(n_seq, tokens, H, forced, sms)) {
+    p->most[0] = n_seq;
+    return 0;
+  }
   // Segments beyond a sequence's first.  The rule's counts add up to no more than sms / H, and to one for
   // each kMinSegment chunks of a sequence that has twice as many (its last chunk may hold one token).
   int64_t extra = sms / H - 1;
@@ -119,9 +128,6 @@ size_t plan_layout(Plan* p, void* ws, int n_seq, int64_t tokens, int H, int forc
     p->items[i] = reinterpret_cast<Item*>(b + at);
     at = up(at + sizeof(Item) * static_cast<size_t>(p->most[i]));
   }
-  p->bad = reinterpret_cast<uint32_t*>(b + at);
-  const int64_t blocks = p->most[0] * H < sms ? p->most[0] * H : sms;
-  at += sizeof(uint32_t) * 4 * kD * static_cast<size_t>(blocks);
   p->decay = reinterpret_cast<float*>(b + at);
   at = up(at + sizeof(float) * static_cast<size_t>(p->n_slots) * H);
   p->slots = reinterpret_cast<float*>(b + at);
@@ -273,12 +279,30 @@ struct Jobs {
 
 __device__ __forceinline__ int live_rows(const Item& it, int c) { return min(kC, it.len - c * kC); }
 
+// The offsets of all sequences, looked at by one warp.
+__device__ __forceinline__ bool offsets_hold(const LinArgs& a, int lane) {
+  bool bad = a.cu[0] != 0 || a.cu[a.n_seq] != a.tokens;
+  for (int s = lane; s < a.n_seq; s += 32) bad |= a.cu[s + 1] < a.cu[s] || a.cu[s] < 0 || a.cu[s + 1] > a.tokens;
+  if (!__any_sync(0xffffffffu, bad)) return true;
+  if (lane == 0) report_status(a.status, 7 /* KDA_ERR_DEVICE_CHECK */);
+  return false;
+}
+
+__device__ __forceinline__ Item whole_sequence(const int32_t* cu, int s) {
+  Item it;
+  it.seq = s; it.first = cu[s]; it.len = cu[s + 1] - cu[s];
+  it.c0 = 0; it.c1 = static_cast<int>((static_cast<int64_t>(it.len) + kC - 1) / kC);
+  it.seg = 0; it.base = -1; it.last = 1;
+  return it;
+}
+
 template <bool kFull>
 __device__ void load_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
   bool dead = false;
   uint32_t u = 0, n = 0, jobs = 0;
   const int pass = kFull ? 0 : 1;
-  const int64_t total = static_cast<int64_t>(p.p.counts[pass]) * p.a.H;
+  const bool planned = !kFull || p.p.counts != nullptr;
+  const int64_t total = planned ? static_cast<int64_t>(p.p.counts[pass]) * p.a.H : offsets_hold(p.a, lane) ? gridDim.x : 0;
   int64_t t = blockIdx.x;
   for (;; ++jobs) {
     LIN_WAIT(s.job_empty[jobs & 1], (jobs >> 1) + 1);
@@ -286,8 +310,9 @@ __device__ void load_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
     Item it = {};
     int head = -1;
     if (more) {
-      it = p.p.items[pass][t / p.a.H];
       head = static_cast<int>(t % p.a.H);
+      if (planned) it = p.p.items[pass][t / p.a.H];
+      else it = whole_sequence(p.a.cu, static_cast<int>(t / p.a.H));
     }
     if (lane == 0) {
       s.job[jobs & 1].item = it;
@@ -297,7 +322,7 @@ __device__ void load_warp(const LinParams& p, uint8_t* sm, Small& s, int lane) {
     if (!more) break;
     // the next item's number, known by the time that this one's copies are under way
     int next = 0;
-    if (lane == 0) next = atomicAdd(&p.p.counts[2 + pass], 1);
+    if (planned && lane == 0) next = atomicAdd(&p.p.counts[2 + pass], 1);
     const int hq = head / p.a.group;
     for (int c = it.c0; c < it.c1; ++c, ++n) {
       const int row = it.first + c * kC;
@@ -565,18 +590,26 @@ __device__ __forceinline__ void scale_block(uint32_t at, float e) {
   tmem_st32(at, x);
 }
 
-// NaN for the rows that see a value that is not finite, in its channel, of some channels (cold).
-__device__ __forceinline__ void poison(uint32_t tl, const uint32_t* noted, uint32_t n, int i, int first, int channels) {
+// NaN for the rows that see a value that is not finite, in its channel, of some channels (cold).  The values were
+// cleared in the tile: they are looked at where they came from.
+__device__ __forceinline__ void poison(uint32_t tl, const LinArgs& a, const Item& it, int head, int c, int i, int first, int channels) {
+  const int live = live_rows(it, c), lane = threadIdx.x & 31;
+  const auto* v = static_cast<const uint16_t*>(a.v) + (static_cast<int64_t>(it.first) + c * kC) * a.v_stride[1] + head * a.v_stride[2];
 #pragma unroll 1
-  for (int c = first; c < first + channels; ++c) {
-    const uint32_t m = __ldcg(noted + c);
-    const bool hit = (m >> 8) == n && 255 - static_cast<int>(m & 255) <= i;
-    if (!__any_sync(0xffffffffu, hit)) continue;
+  for (int ch = first; ch < first + channels; ++ch) {
+    int seen = kC;  // the first such token
+#pragma unroll 1
+    for (int t = 96; t >= 0; t -= 32) {
+      const uint32_t bits = t + lane < live ? v[(t + lane) * a.v_stride[1] + ch] : 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, (bits & 0x7f80) == 0x7f80);
+      if (m) seen = t + __ffs(m) - 1;
+    }
+    if (!__any_sync(0xffffffffu, seen <= i)) continue;
     uint32_t x;
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;\n" : "=r"(x) : "r"(tl + c));
-    if (hit) x = 0x7fffffffu;
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];\ntcgen05.wait::ld.sync.aligned;\n" : "=r"(x) : "r"(tl + ch));
+    if (seen <= i) x = 0x7fffffffu;
     __syncwarp();
-    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\ntcgen05.wait::st.sync.aligned;\n" ::"r"(tl + c), "r"(x) : "memory");
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x1.b32 [%0], {%1};\ntcgen05.wait::st.sync.aligned;\n" ::"r"(tl + ch), "r"(x) : "memory");
   }
 }
 
@@ -667,9 +700,8 @@ __device__ __forceinline__ void tmem_st_16x128b_x2(uint32_t taddr, const uint32_
                : "memory");
 }
 
-// Values of a warp's 32 channels and 16 tokens that are not finite, cleared in the tile and noted (cold):
-// chunk number << 8 | 255 - the first such token of a channel.
-__device__ __forceinline__ void clear_bad(uint32_t tile, uint32_t* noted, uint32_t* bad_chunk, uint32_t n, int w, int t0, int lane) {
+// Values of a warp's 32 channels and 16 tokens that are not finite, cleared in the tile (cold).
+__device__ __forceinline__ void clear_bad(uint32_t tile, uint32_t* bad_chunk, uint32_t n, int w, int t0, int lane) {
   const int ch = 32 * w + lane;
   const uint32_t base = tile + (ch >> 6) * kPanel;
 #pragma unroll 1
@@ -677,11 +709,8 @@ __device__ __forceinline__ void clear_bad(uint32_t tile, uint32_t* noted, uint32
     const uint32_t at = base + sw128(t, 2 * (ch & 63));
     uint16_t x;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at) : "memory");
-    if ((x & 0x7f80) != 0x7f80) continue;
-    asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0)) : "memory");
-    atomicMax(noted + kD * (n & 3) + ch, n << 8 | static_cast<uint32_t>(255 - t));
+    if ((x & 0x7f80) == 0x7f80) asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"(static_cast<uint16_t>(0)) : "memory");
   }
-  __threadfence();
   __syncwarp();
   if (lane == 0) bad_chunk[n & 3] = n + 1;
 }
@@ -698,7 +727,6 @@ __device__ void value_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
   uint32_t n = 0, u = 0;
   const uint64_t minus = f32x2(-1.f, -1.f);
   const int q = w & 3, side = w >> 2;  // channels 32 q .. + 31; tokens 32 side .. + 31 of each 64
-  uint32_t* noted = p.p.bad + 4 * kD * blockIdx.x;
   while (jobs.next(j)) {
     for (int c = j.item.c0; c < j.item.c1; ++c, ++n) {
       const Tiles<kFull> tile(n);
@@ -750,7 +778,7 @@ __device__ void value_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
           }
           const float2 left = unpack_f32x2(any);
           if (kFull && __any_sync(0xffffffffu, left.x + left.y != left.x + left.y)) {
-            clear_bad(v, noted, s.bad_chunk, n, q, t0, lane);
+            clear_bad(v, s.bad_chunk, n, q, t0, lane);
             fence_proxy_async_smem();
           }
           if (piece == 0) {
@@ -779,6 +807,14 @@ __device__ void value_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
     }
   }
   if (dead && lane == 0) report_status(p.a.status, 6 /* KDA_ERR_TIMEOUT */);
+}
+
+// The final state of a sequence without tokens is its entry state (256 threads).
+__device__ __forceinline__ void entry_to_exit(const LinArgs& a, int seq, int head, int thread) {
+  if (!a.S_out || a.S_in == a.S_out) return;
+  const int64_t at = (static_cast<int64_t>(seq) * a.H + head) * (kStateFloats / 4);
+  for (int e = thread; e < kStateFloats / 4; e += 256)
+    reinterpret_cast<float4*>(a.S_out)[at + e] = a.S_in ? reinterpret_cast<const float4*>(a.S_in)[at + e] : make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 template <int kMode>
@@ -813,7 +849,7 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
     tc_fence_after();
     // with the output stage all 128: both warps of a row sum its squares, and neither waits for the other's mark
     if (s.bad_chunk[n & 3] == n + 1)
-      poison(to_q, p.p.bad + 4 * kD * blockIdx.x + kD * (n & 3), n, i, kGate ? 0 : 64 * half, kGate ? kD : 64);
+      poison(to_q, a, it, head, c, i, kGate ? 0 : 64 * half, kGate ? kD : 64);
     float f = a.scale;
     if constexpr (kGate) {  // the row's sum of squares, by both warps that have it
       float s0 = 0.f, s1 = 0.f;
@@ -873,6 +909,10 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
     const int mine = half * kHalf * kD + ch;
     auto slot = [&](int k) { return p.p.slots + (static_cast<int64_t>(it.base + k) * a.H + j.head) * kStateFloats + mine; };
     const int64_t unit = (static_cast<int64_t>(it.seq) * a.H + j.head) * kStateFloats + mine;
+    if (kFull && it.c0 == it.c1) {  // without a plan an item may be a sequence without tokens
+      if (!dead) entry_to_exit(a, it.seq, j.head, 32 * w + lane);
+      continue;
+    }
     float S[kHalf], A = 1.f;
     auto load = [&](const float* src) {
 #pragma unroll
@@ -953,15 +993,10 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
     release();
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   }
-  if constexpr (kFull) {  // sequences without tokens: the final state is the entry state
-    if (a.S_out && a.S_in != a.S_out && !dead)
-      for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.p.counts[4]) * a.H; t += gridDim.x) {
-        const int seq = p.p.items[0][p.p.counts[0] + t / a.H].seq;
-        const int64_t at = (static_cast<int64_t>(seq) * a.H + t % a.H) * (kStateFloats / 4);
-        for (int e = 32 * w + lane; e < kStateFloats / 4; e += 256)
-          reinterpret_cast<float4*>(a.S_out)[at + e] =
-              a.S_in ? reinterpret_cast<const float4*>(a.S_in)[at + e] : make_float4(0.f, 0.f, 0.f, 0.f);
-      }
+  if constexpr (kFull) {  // sequences without tokens, which the plan puts last
+    if (p.p.counts && !dead)
+      for (int64_t t = blockIdx.x; t < static_cast<int64_t>(p.p.counts[4]) * a.H; t += gridDim.x)
+        entry_to_exit(a, p.p.items[0][p.p.counts[0] + t / a.H].seq, static_cast<int>(t % a.H), 32 * w + lane);
   }
   if (dead && lane == 0) report_status(a.status, 6 /* KDA_ERR_TIMEOUT */);
 }
@@ -1010,7 +1045,6 @@ __global__ void __launch_bounds__(kThreads, 1) lin_chunk_kernel(const __grid_con
   tc_fence_after();
   pdl_wait();
   if (kMode == kGated && tid < kD) s.weight[tid] = p.a.norm_weight ? p.a.norm_weight[tid] : 1.f;
-  if (kFull && tid < 4 * kD) p.p.bad[4 * kD * blockIdx.x + tid] = 0;  // chunk 0 has 255 - token > 0 added
   __syncthreads();
   // registers: kRegs a thread at launch, 480 over the six groups of four warps
   if (warp < 4) {
@@ -1088,16 +1122,19 @@ cudaError_t launch_lin_prefill(const LinArgs& a, int num_sms) {
   LinParams p;
   memset(&p, 0, sizeof(p));
   p.a = a;
-  plan_layout(&p.p, a.workspace, a.n_seq, a.tokens, a.H, a.n_segments, num_sms);
+  const size_t need = plan_layout(&p.p, a.workspace, a.n_seq, a.tokens, a.H, a.n_segments, num_sms);
   const int64_t o_stride[3] = {0, static_cast<int64_t>(a.H) * kD, kD};
   if (a.tokens > 0 && (!rows_map(&p.tq, a.q, a.q_stride, a.H / a.group, a.tokens) || !rows_map(&p.tk, a.k, a.k_stride, a.H / a.group, a.tokens) ||
                        !rows_map(&p.tv, a.v, a.v_stride, a.H, a.tokens) ||
                        !rows_map(&p.to, a.o, o_stride, a.H, a.tokens, 32) ||
                        (a.gate && !rows_map(&p.tg, a.gate, a.gate_stride, a.H, a.tokens))))
     return cudaErrorInvalidValue;
-  cudaError_t e = launch_after(lin_plan_kernel, dim3(1), dim3(1024), 0, a.stream, a.cu, a.n_seq, a.tokens, a.H, num_sms,
-                               a.n_segments, p.p, a.status);
-  if (e != cudaSuccess) return e;
+  cudaError_t e = cudaSuccess;
+  if (need > 0) {
+    e = launch_after(lin_plan_kernel, dim3(1), dim3(1024), 0, a.stream, a.cu, a.n_seq, a.tokens, a.H, num_sms, a.n_segments,
+                     p.p, a.status);
+    if (e != cudaSuccess) return e;
+  }
   // the first pass only where the rule can split: one sequence of all the tokens is cut most
   if (p.p.most[1] > 0 && segments_of(a.tokens, a.tokens, a.H, num_sms, a.n_segments) > 1) {
     e = launch_chunks<kStates>(p, p.p.most[1] * a.H, num_sms);

@@ -77,14 +77,17 @@ def test_prefill_refusals(lib):
     assert _prefill(lib, S_in=0x5008) == ALIGNMENT
     assert _prefill(lib, S_out=0x5008) == ALIGNMENT
     assert _prefill(lib, ws=0x100080) == ALIGNMENT
-    assert _prefill(lib, ws=0) == WORKSPACE
-    need = lib.kda_lin_prefill_workspace_size(1, 4, 128, 5, 0)
+    planned = dict(n_seq=60, T=500)  # more heads of sequences than SMs
+    need = lib.kda_lin_prefill_workspace_size(60, 4, 128, 500, 0)
     assert need > 0
-    assert _prefill(lib, ws_bytes=need - 1) == WORKSPACE
+    assert _prefill(lib, ws=0, **planned) == WORKSPACE
+    assert _prefill(lib, ws_bytes=need - 1, **planned) == WORKSPACE
+    assert lib.kda_lin_prefill_workspace_size(1, 4, 128, 5, 0) == 0
     assert _prefill(lib, n_seq=0, T=0, q=0, k=0, v=0, g=0, o=0, cu=0) == OK
     if not HAS_GPU:
         assert _prefill(lib) in (CUDA, UNSUPPORTED)
-        assert _prefill(lib, ws_bytes=need) in (CUDA, UNSUPPORTED)
+        assert _prefill(lib, ws=0, ws_bytes=0) in (CUDA, UNSUPPORTED)
+        assert _prefill(lib, ws_bytes=need, **planned) in (CUDA, UNSUPPORTED)
 
 
 def test_decode_refusals(lib):
@@ -102,7 +105,8 @@ def test_decode_refusals(lib):
 def test_prefill_workspace_size(lib):
     size = lambda *a: int(lib.kda_lin_prefill_workspace_size(*a))  # noqa: E731
     assert size(1, 4, 64, 5, 0) == size(-1, 4, 128, 5, 0) == size(1, 0, 128, 5, 0) == size(1, 4, 128, -1, 0) == size(1, 4, 128, 5, -1) == 0
-    assert 0 < size(1, 96, 128, 8192, 0) < 1 << 20                # as many heads as fill the GPU: no split
+    assert size(1, 96, 128, 8192, 0) == size(3, 16, 128, 291, 0) == size(1, 8, 128, 900, 1) == 0  # a block each, no split
+    assert 0 < size(2, 96, 128, 8192, 0) < 1 << 20                # more than the SMs: a plan
     assert size(1, 8, 128, 1 << 20, 0) < 32 << 20                 # at most a state for each SM
     assert size(4, 8, 128, 4096, 3) <= size(4, 8, 128, 4096, 8)
 

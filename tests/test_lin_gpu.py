@@ -225,6 +225,40 @@ def test_bad_offsets_write_nothing(cu):
     assert bool((o == 7).all()) and bool((S == 7).all())
 
 
+@pytest.mark.parametrize("H", [4, 40])
+@pytest.mark.parametrize("gated", [False, True])
+def test_a_block_each_and_a_plan(H, gated):
+    """As many (sequence, head) pairs as there are blocks, and more: sequences without tokens, a bad value, the state
+    in place, and offsets that are wrong."""
+    p = Prefill([130, 0, 70, 0, 1, 257], H, 4, seed=51, gated=gated)
+    size = kda.lin_prefill_workspace_size(6, H, 458)
+    assert (size > 0) == (6 * H > torch.cuda.get_device_properties(0).multi_processor_count)
+    o, S = p.run()
+    p.check(o, S, heads=(0, H - 1))
+    assert torch.equal(S[1].cpu(), p.S[1]) and torch.equal(S[3].cpu(), p.S[3])
+    states = p.S.cuda()
+    o1, S1 = p.run(S_in=states, S_out=states)
+    assert S1 is states and torch.equal(o, o1) and torch.equal(S, S1)
+    o1, S1 = p.run(S_in=None)
+    assert not bool(S1[1].any()) and not bool(S1[3].any())
+    p.v[130 + 40, H - 1, 9] = float("nan")
+    o1, S1 = p.run()
+    bad = torch.zeros(458, H, dtype=torch.bool)
+    bad[170:200, H - 1] = True
+    assert torch.equal(o1[~bad], o[~bad]) and bool(o1[bad][:, 9].isnan().all())
+    assert bool(o1[bad].isnan().all()) == gated
+    assert bool(S1[2, H - 1, :, 9].isnan().all()) and torch.equal(S1[5], S[5])
+    a, b = p.args()
+    for i, wrong in ((2, 129), (6, 457), (0, 1), (4, 10 ** 9)):
+        cu = a[4].clone()
+        cu[i] = wrong
+        st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        keep = [torch.full_like(t, 7) for t in (o, S)]
+        kda.lin_prefill(*a[:4], cu, **b, o=keep[0], S_out=keep[1], dev_status=st)
+        torch.cuda.synchronize()
+        assert int(st) == CHECK and bool((keep[0] == 7).all()) and bool((keep[1] == 7).all())
+
+
 @pytest.mark.parametrize("n", [0, 3])
 def test_no_tokens(n):
     S0 = torch.randn(n, 2, D, D, device="cuda")
