@@ -27,14 +27,17 @@
 // The products of a chunk: Q K^T | units of tokens 0 - 63 | Q S | units of tokens 64 - 127 | P V.  Weights are made
 // during the three in the middle, outputs and the next state during P V and the next Q K^T.
 //
-// What bounds it: the chain of a chunk.  8192 tokens x 96 heads, one block each on 96 of 152 SMs: 200 us, 3.1 us
-// a chunk, of which the products take 1.9 and each scheduler's instructions 1.6 to 2.4; 8 heads x 262144 tokens on all SMs: 3.6 us
-// a chunk, 128 KB of it at 5.5 TB/s.  Tried and slower than the 190 us of before the second parts: scores
-// a chunk ahead in columns of their own with a ring of half the size (232), eight warps for weights and outputs
-// (226 - 249), outputs stored from registers (221), loops not unrolled (199 - 587), products issued from rolled
-// loops (212), parts by bf16x2 arithmetic (2 cycles an instruction, like the conversions that they
-// replace); cutting each of 96 heads into 2 - 6 segments (235 - 275: the rule cuts only what fits the SMs at once;
-// 64 heads into 2: 190 -> 167).  Two parts of the values instead of three leave states off by 2e-6.
+// What bounds it: the chain of a chunk and the issue of the warps around it.  8192 tokens x 96 heads, one block each
+// on 96 of 152 SMs: 196 us, 3 us a chunk, of which the products take 1.9 (tensor pipe 61 %), each scheduler's arithmetic
+// pipes 1.3 and 0.9; 8 heads x 262144 tokens on all SMs: 3.5 us a chunk, 128 KB of it at 5.5 TB/s; with the output
+// stage 4.2 us alone, 3.6 beside others (12 ragged prompts x 64 heads: 437 us).  Tried and slower than 196 (or 190,
+// before the weights' second parts): scores a chunk ahead in columns of their own with a ring of half the size (232),
+// eight warps for weights and outputs (226 - 249), outputs stored from registers (221), loops not unrolled
+// (199 - 587), products issued from rolled loops (212), parts by bf16x2 arithmetic (2 cycles an instruction, like the
+// conversions that they replace), eight units of 32 tokens (205), with Q S first or last (207, 241), weights made by
+// the state's warps too (211); the output stage's sums of squares made by the weights' warps (437 -> 463);
+// each of 96 heads in 2 - 6 segments (235 - 275: the rule cuts only what fits the SMs at once; 64 heads
+// into 2: 190 -> 167).  Two parts of the values instead of three leave states off by 2e-6.
 //
 // A token's NaN or infinity must not reach earlier tokens, but 0 * NaN is NaN in P V: values that are not
 // finite are cleared in the tile, and the rows that see one get NaN in its channel when they are written.
@@ -830,20 +833,10 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
   const uint32_t copy = smem_u32(sm) + kSmState + half * kPanel;
   constexpr int kHalf = kD / 2;
   // ---- outputs of a chunk: 32 tokens, 64 channels
-  int staged = -1;  // the buffer whose rows are on their way to o
-  auto release = [&] {
-    if (staged >= 0 && lane == 0) {
-      asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
-      mbar_arrive(&s.free[kQ][staged]);
-    }
-    staged = -1;
-    __syncwarp();
-  };
   auto outputs = [&](const Item& it, int head, int c) {
     const Tiles<kFull> tile(n);
     const int i = ch;  // the thread's token in the chunk
     const uint32_t to_q = (static_cast<uint32_t>(w & 3) << 21) + kTO, to = to_q + 64 * half;
-    release();  // with the output stage, what is left of the last chunk's
     if constexpr (kGate) LIN_WAIT(s.gate_full, n);
     LIN_WAIT(s.out[n & 1], n >> 1);
     tc_fence_after();
@@ -852,15 +845,20 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
       poison(to_q, a, it, head, c, i, kGate ? 0 : 64 * half, kGate ? kD : 64);
     float f = a.scale;
     if constexpr (kGate) {  // the row's sum of squares, by both warps that have it
-      float s0 = 0.f, s1 = 0.f;
+      uint64_t s0 = f32x2(0.f, 0.f), s1 = s0;
 #pragma unroll 1
-      for (int b = 0; b < 8; ++b) {
-        float x[16];
-        tmem_ld16(to_q + 16 * b, x);
+      for (int b = 0; b < 4; ++b) {
+        float x[32];
+        tmem_ld32(to_q + 32 * b, x);
 #pragma unroll
-        for (int e = 0; e < 16; e += 2) { s0 = fmaf(x[e], x[e], s0); s1 = fmaf(x[e + 1], x[e + 1], s1); }
+        for (int e = 0; e < 32; e += 4) {
+          const uint64_t x0 = f32x2(x[e], x[e + 1]), x1 = f32x2(x[e + 2], x[e + 3]);
+          s0 = fma_f32x2(x0, x0, s0);
+          s1 = fma_f32x2(x1, x1, s1);
+        }
       }
-      f *= 1.f / sqrtf((s0 + s1) * a.scale * a.scale * (1.f / kD) + a.eps);
+      const float2 sum = unpack_f32x2(add_f32x2(s0, s1));
+      f *= 1.f / sqrtf((sum.x + sum.y) * a.scale * a.scale * (1.f / kD) + a.eps);
     }
     const uint32_t stage = smem_u32(sm) + tile.at(kQ) + half * kPanel;  // q is used: its tile takes the outputs
 #pragma unroll 1
@@ -901,8 +899,11 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
                                                ((static_cast<int64_t>(row) + lane) * a.H + head) * kD + 64 * half), i);
     }
     __syncwarp();
-    staged = static_cast<int>(tile.buf);
-    if constexpr (!kGate) release();  // nothing to do until K^T V of the next chunk
+    if (lane == 0) {  // nothing to do until K^T V of the next chunk, and the next but one's q waits for its place
+      asm volatile("cp.async.bulk.wait_group.read 0;\n" ::: "memory");
+      mbar_arrive(&s.free[kQ][tile.buf]);
+    }
+    __syncwarp();
   };
   while (jobs.next(j)) {
     const Item& it = j.item;
@@ -990,7 +991,6 @@ __device__ void state_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
   }
   tc_fence_before();
   if constexpr (kFull) {
-    release();
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;\n" ::: "memory");
   }
   if constexpr (kFull) {  // sequences without tokens, which the plan puts last
