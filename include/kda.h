@@ -492,7 +492,8 @@ kda_status kda_attn_decode_paged(const kda_bf16* q, const int64_t* q_stride, con
  *   n_segments  0: a sequence is split over the SMs by the library's rule when there are few heads and
  *               sequences; k >= 1: every sequence into min(k, its chunks) segments
  *   workspace   kda_lin_prefill_workspace_size(...) bytes, 256-byte aligned; its contents need no
- *               preparation and mean nothing between calls.  Calls with no more (sequence, head) pairs than SMs
+ *               preparation and mean nothing between calls; calls that may run at the same time (captured
+ *               ones, too) need one each.  Calls with no more (sequence, head) pairs than SMs
  *               and nothing to split need none: the size is 0 and the workspace may be NULL
  * Outputs must not overlap inputs, but for S_out = S_in.
  * The same call gives the same bits; a split sequence's last bits may depend on what else is in the call.
