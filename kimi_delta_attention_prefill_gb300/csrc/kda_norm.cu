@@ -334,7 +334,11 @@ cudaError_t launch_rows(const NormArgs& a, int num_sms) {
   const int threads = threads_for(a.width >> 3, kVec);
   const int bytes = kStages * 16 * threads * kVec * ((kF32 ? 2 : 1) + (a.y ? 1 : 0) + (a.gate ? 1 : 0));
   // as many blocks as an SM holds at once: their rows are then spread evenly
-  const int blocks = max(1, min(min(32, 2048 / threads), min(65536 / (regs * threads), (kMaxSmem + 1024) / (bytes + 1536))));
+  int blocks = max(1, min(min(32, 2048 / threads), min(65536 / (regs * threads), (kMaxSmem + 1024) / (bytes + 1536))));
+  // A stream of 32 bits that is read and written: about 43 KB of it under way on an SM, two blocks at least.  More
+  // slows it (30000 rows; blocks an SM: us.  2048 wide 2: 130, 3: 122, 4: 134; 1792 wide 3: 101, 4: 116; 1280 wide 4: 72, 5: 84;
+  // 1024 wide 4: 64, 5: 57, 8: 69; 4096 wide 2: 257, 3: 263), a stream of 16 bits or one that is only read does not mind.
+  if (kF32 && a.y) blocks = min(blocks, max(2, (43 * 1024 + 4 * a.width) / (8 * a.width)));
   const int64_t most = static_cast<int64_t>(num_sms) * blocks;
   kernel<<<static_cast<unsigned>(a.rows < most ? a.rows : most), threads, bytes, a.stream>>>(a);
   return cudaGetLastError();
@@ -348,7 +352,7 @@ cudaError_t launch_rows(const NormArgs& a, int num_sms) {
 
 // What both ways took, in us (8192 x 12288 with all parts in bf16; 30001 x 1928 with an fp32 residual, no gate;
 // 4001 x 5128, the norm alone; 1200, 304 and 152 x 4096 with all parts): a row a block 270 / 137 / 42 / 15.5 / 5.0 /
-// 3.4, rows in a line 158 / 129 / 19 / 13 / 5.8 / 4.0.
+// 3.4, rows in a line 158 / 110 / 19 / 13 / 5.8 / 4.0.
 cudaError_t launch_block_norm(const NormArgs& a, int num_sms) {
   const int n = a.width >> 3, part_bytes = 16 * ((a.x_f32 ? 2 : 1) + (a.y ? 1 : 0) + (a.gate ? 1 : 0));
   // Blocks of up to 256 threads, several on an SM, whose waits overlap; of up to 512 where only one fits
