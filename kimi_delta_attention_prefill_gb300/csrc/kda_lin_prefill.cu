@@ -30,12 +30,13 @@
 // What bounds it: the chain of a chunk and the issue of the warps around it.  8192 tokens x 96 heads, one block each
 // on 96 of 152 SMs: 196 us, 3 us a chunk, of which the products take 1.9 (tensor pipe 61 %), each scheduler's arithmetic
 // pipes 1.3 and 0.9; 8 heads x 262144 tokens on all SMs: 3.5 us a chunk, 128 KB of it at 5.5 TB/s; with the output
-// stage 4.2 us alone, 3.6 beside others (12 ragged prompts x 64 heads: 437 us).  Tried and slower than 196 (or 190,
+// stage 3.9 us (12 ragged prompts x 64 heads: 432 us).  Tried and slower than 196 (or 190,
 // before the weights' second parts): scores a chunk ahead in columns of their own with a ring of half the size (232),
 // eight warps for weights and outputs (226 - 249), outputs stored from registers (221), loops not unrolled
 // (199 - 587), products issued from rolled loops (212), parts by bf16x2 arithmetic (2 cycles an instruction, like the
 // conversions that they replace), eight units of 32 tokens (205), with Q S first or last (207, 241), weights made by
-// the state's warps too (211); the output stage's sums of squares made by the weights' warps (437 -> 463);
+// the state's warps too (211); the output stage's sums of squares made by the weights' warps (432 -> 463), q's rows fetched into L2
+// before their place is free (no change);
 // each of 96 heads in 2 - 6 segments (235 - 275: the rule cuts only what fits the SMs at once; 64 heads
 // into 2: 190 -> 167).  Two parts of the values instead of three leave states off by 2e-6.
 //
