@@ -976,8 +976,10 @@ def _stage_rows(gate, norm_weight, shape, dev, pack):
     """(whether they are what they should be at a quick look, gate's strides)"""
     if gate is None:
         return norm_weight is None, None
+    if gate.shape != shape:
+        return False, None  # its strides may be any number
     st = gate.stride()
-    return (gate.shape == shape and gate.dtype is _BF16 and gate.get_device() == dev and st[-1] == 1
+    return (gate.dtype is _BF16 and gate.get_device() == dev and st[-1] == 1
             and (norm_weight is None or (norm_weight.shape == (HEAD_DIM,) and norm_weight.dtype is _F32
                                          and norm_weight.get_device() == dev and norm_weight.is_contiguous()))), pack(*st)
 
