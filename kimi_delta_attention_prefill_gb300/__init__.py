@@ -944,9 +944,10 @@ _F32 = torch.float32
 
 
 def _on(device, stream, *tensors):
-    """All tensors are on one device, and it is the one that the call runs on."""
+    """All tensors are on one device, and it is the one that the call runs on.  What is no tensor is refused by name
+    where its type is looked at."""
     for t in tensors:
-        if t is not None and t.get_device() != device:
+        if isinstance(t, torch.Tensor) and t.get_device() != device:
             raise ValueError(f"all tensors must be on one device, got cuda:{device} and {t.device}")
     if device >= 0 and device != _here(stream):
         raise ValueError(f"the tensors are on cuda:{device}, which is not the device that the call runs on")

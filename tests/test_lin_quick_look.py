@@ -71,3 +71,16 @@ def test_ranks_and_shapes(fakes, call, name, bad):  # noqa: F811
     """A projection's rows before they are split into heads, a dimension too many, and the like."""
     with pytest.raises(ValueError, match=name):
         call(**{name: bad})
+
+
+@pytest.mark.parametrize("call,name", [
+    (prefill, "q"), (prefill, "k"), (prefill, "v"), (prefill, "g"), (prefill, "cu_seqlens"), (prefill, "gate"), (prefill, "norm_weight"),
+    (prefill, "S_in"), (prefill, "o"), (prefill, "S_out"), (prefill, "workspace"), (prefill, "dev_status"),
+    (decode, "q"), (decode, "k"), (decode, "v"), (decode, "g"), (decode, "gate"), (decode, "norm_weight"), (decode, "S_state"),
+    (decode, "n_commit"), (decode, "o"), (decode, "dev_status"),
+    (norm, "x"), (norm, "weight"), (norm, "y"), (norm, "gate"), (norm, "post_weight"), (norm, "h"), (norm, "x_out"),
+])
+@pytest.mark.parametrize("bad", [[1.0], 1, "rows"])
+def test_what_is_no_tensor(fakes, call, name, bad):  # noqa: F811
+    with pytest.raises((TypeError, ValueError), match=name):
+        call(**{name: bad})
