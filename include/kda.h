@@ -535,7 +535,9 @@ kda_status kda_lin_decode(const kda_bf16* q, const int64_t* q_stride, const kda_
  *                in front of the first block); gate NULL: no gate
  *   weight, post_weight  [width] fp32, or NULL for ones
  *   h            [rows, width] bf16, contiguous, or NULL
- *   x_out        [rows, width] of x's type, contiguous, or NULL: x'; may be x itself.  NULL without y
+ *   x_out        [rows, width] of x's type, contiguous, or NULL: x'; may be x itself where x's rows are
+ *                contiguous (KDA_ERR_INVALID_ARG where they are not).  NULL without y
+ * Outputs must not overlap inputs or one another, but for x_out = x.
  * h is made from x' before x' is rounded to x's type.  Strides are positive whole 16-byte units; width is a
  * multiple of 8, at most 32768 (KDA_ERR_UNSUPPORTED).  Sums of squares are of 32 bits.
  */

@@ -120,6 +120,7 @@ kda_status kda_block_norm(const void* x, int x_dtype, int64_t x_stride, const fl
   if (!h && !x_out) return KDA_ERR_INVALID_ARG;
   if (!y && x_out) return KDA_ERR_INVALID_ARG;  // a copy is not this call's work
   if (!x) return KDA_ERR_INVALID_ARG;
+  if (x_out == x && rows > 1 && x_stride != width) return KDA_ERR_INVALID_ARG;  // it would come upon rows not read yet
   const bool f32 = x_dtype == KDA_ROWS_F32;
   int64_t s[3];
   if (!aligned(x, 16) || !aligned(y, 16) || !aligned(gate, 16) || !aligned(weight, 16) || !aligned(post_weight, 16) ||
