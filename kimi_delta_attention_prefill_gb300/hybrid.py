@@ -129,7 +129,8 @@ class HybridStack:
         new = cu.diff()
         kv_len = self.length + new
         if self.norms is not None:
-            h, x = kda.block_norm(x.float(), self.norms[0]["pre"])
+            x = x.to(torch.float32, copy=True)  # the stack's own: the blocks' outputs are added in place
+            h, x = kda.block_norm(x, self.norms[0]["pre"])
         for i, layer in enumerate(self.layers):
             if self.norms is None:
                 h = torch.nn.functional.rms_norm(x.float(), (self.width,)).to(torch.bfloat16)
