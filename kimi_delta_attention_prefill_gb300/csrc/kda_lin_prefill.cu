@@ -8,7 +8,8 @@
 // One block walks the chunks of a (sequence, head) or of a segment of one; its warps:
 //     0        copies (TMA; two tiles each of q, k and v) and the line of work items
 //     1        products (tcgen05)
-//     2        decays: sums in 64-bit fixed point (2^-32 of a factor of 2), so that no difference loses bits
+//     2        decays: sums in 64-bit fixed point (2^-32 of a factor of 2); the weights get them as a whole number and
+//              a fraction of 32 bits each, so that a small difference of large sums keeps its bits
 //     3        the output stage's gate, into q's tile when q is used
 //     4 - 7    weights P = (Q K^T) o D as two bf16 parts over their scores; Q S times e^G in place, on which P V is then
 //              added (thread = token)
@@ -203,9 +204,10 @@ struct Job {
   int head;  // -1: no more
 };
 
-struct Decays {  // of a chunk, in units of log2
-  float G[kC];   // G_i
-  float cf[kC];  // 2^{G at the end of the token's block of 32 - G_i}
+// G_i of a chunk, in units of log2, as whole + part with 0 <= part <= 1.  A reset counts 192: one float for the sum would
+// have a step of up to 2^-9, and after 90 resets weights off by 2^-10 (o off by 20 times what its own roundings leave where values cancel).
+struct Decays {
+  float whole[kC], part[kC];
 };
 
 enum { kK, kV, kQ };  // tiles
@@ -218,9 +220,10 @@ template <bool kFull> constexpr uint32_t kBufs = kFull ? 2 : 3;
 
 struct Small {
   Decays dec;
-  float w[2][kC];            // 2^{G_last - G_t}, by the chunk's parity
+  // by the chunk's parity
+  float cf[2][kC];           // 2^{G at the end of the token's block of 32 - G_t}
+  float end[2][4];           // 2^{G_last - G at the end of a block}
   float a[2];                // 2^{G_last}
-  float pad[2];
   float weight[kD];          // the output stage's
   Job job[2];
   uint64_t full[2][3];  // [k and q; v][buffer]
@@ -494,23 +497,29 @@ __device__ void decay_warp(const LinParams& p, Small& s, int lane) {
       const long long end = __shfl_sync(0xffffffffu, sum, lane | 7);  // of the block of 32 tokens
       auto real = [](long long d) { return static_cast<float>(d) * (1.f / kUnit); };
       const float none = __int_as_float(0x7fffffff);
-      float v[4], f[4], w[4];
+      float f[4], e = exp2f(real(last - end));
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         G[i] += sum - own;
-        v[i] = 4 * lane + i >= nan_at ? none : real(G[i]);
         f[i] = exp2f(real(end - G[i]));
-        w[i] = exp2f(real(last - G[i]));
       }
+      // the weights' warps are done with these places too: the last chunk but one's dec_empty has been waited for
       LIN_WAIT(s.w_empty[n & 1], (n >> 1) + 1);
-      *reinterpret_cast<float4*>(&s.w[n & 1][4 * lane]) = make_float4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<float4*>(&s.cf[n & 1][4 * lane]) = make_float4(f[0], f[1], f[2], f[3]);
+      if ((lane & 7) == 0) s.end[n & 1][lane >> 3] = e;
       if (lane == 0) s.a[n & 1] = nan_at < kC ? none : exp2f(real(last));
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.w_full[n & 1]);
       if constexpr (kFull) {
+        float whole[4], part[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          whole[i] = 4 * lane + i >= nan_at ? none : static_cast<float>(static_cast<int>(G[i] >> 32));
+          part[i] = static_cast<float>(static_cast<uint32_t>(G[i])) * (1.f / kUnit);
+        }
         LIN_WAIT(s.dec_empty, n + 1);
-        *reinterpret_cast<float4*>(&s.dec.G[4 * lane]) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(&s.dec.cf[4 * lane]) = make_float4(f[0], f[1], f[2], f[3]);
+        *reinterpret_cast<float4*>(&s.dec.whole[4 * lane]) = make_float4(whole[0], whole[1], whole[2], whole[3]);
+        *reinterpret_cast<float4*>(&s.dec.part[4 * lane]) = make_float4(part[0], part[1], part[2], part[3]);
         __syncwarp();
         if (lane == 0) mbar_arrive(&s.dec_full);
       }
@@ -636,19 +645,20 @@ __device__ void weight_warps(const LinParams& p, Small& s, int w, int lane) {
       // ---- weights, 32 columns at a time, over the scores of columns that are read already
       LIN_WAIT(s.dec_full, n);
       const Decays& d = s.dec;
-      const float G = d.G[i];
+      const float* cf = s.cf[n & 1];
+      const float whole = d.whole[i], part = d.part[i];
       LIN_WAIT(s.scores, n);
       tc_fence_after();
 #pragma unroll 1
       for (int b = 0; b < w; ++b) {  // D_ij = 2^{G_i - G at the block's end} 2^{G at the block's end - G_j}
         float x[32];
         tmem_ld32(ts + 32 * b, x);
-        const float rf = exp2_fast(G - d.G[32 * b + 31]);
+        const float rf = exp2_fast((whole - d.whole[32 * b + 31]) + (part - d.part[32 * b + 31]));
         const uint64_t r2 = f32x2(rf, rf);
         uint32_t pk[32];
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&d.cf[32 * b + e]);
+          const float4 f = *reinterpret_cast<const float4*>(&cf[32 * b + e]);
           two_parts(mul_f32x2(f32x2(x[e], x[e + 1]), mul_f32x2(r2, f32x2(f.x, f.y))), pk[e / 2], pk[16 + e / 2]);
           two_parts(mul_f32x2(f32x2(x[e + 2], x[e + 3]), mul_f32x2(r2, f32x2(f.z, f.w))), pk[e / 2 + 1], pk[17 + e / 2]);
         }
@@ -657,14 +667,17 @@ __device__ void weight_warps(const LinParams& p, Small& s, int w, int lane) {
       {
         float x[32];
         uint32_t pk[32];
+        const uint64_t whole2 = f32x2(whole, whole), part2 = f32x2(part, part), minus = f32x2(-1.f, -1.f);
         tmem_ld32(ts + 32 * w, x);
 #pragma unroll
         for (int e = 0; e < 32; e += 4) {
-          const float4 f = *reinterpret_cast<const float4*>(&d.G[32 * w + e]);
-          const float y0 = e <= lane ? x[e] * exp2_fast(G - f.x) : 0.f;
-          const float y1 = e + 1 <= lane ? x[e + 1] * exp2_fast(G - f.y) : 0.f;
-          const float y2 = e + 2 <= lane ? x[e + 2] * exp2_fast(G - f.z) : 0.f;
-          const float y3 = e + 3 <= lane ? x[e + 3] * exp2_fast(G - f.w) : 0.f;
+          const float4 f = *reinterpret_cast<const float4*>(&d.whole[32 * w + e]), h = *reinterpret_cast<const float4*>(&d.part[32 * w + e]);
+          const float2 g0 = unpack_f32x2(add_f32x2(fma_f32x2(f32x2(f.x, f.y), minus, whole2), fma_f32x2(f32x2(h.x, h.y), minus, part2)));
+          const float2 g1 = unpack_f32x2(add_f32x2(fma_f32x2(f32x2(f.z, f.w), minus, whole2), fma_f32x2(f32x2(h.z, h.w), minus, part2)));
+          const float y0 = e <= lane ? x[e] * exp2_fast(g0.x) : 0.f;
+          const float y1 = e + 1 <= lane ? x[e + 1] * exp2_fast(g0.y) : 0.f;
+          const float y2 = e + 2 <= lane ? x[e + 2] * exp2_fast(g1.x) : 0.f;
+          const float y3 = e + 3 <= lane ? x[e + 3] * exp2_fast(g1.y) : 0.f;
           two_parts(f32x2(y0, y1), pk[e / 2], pk[16 + e / 2]);
           two_parts(f32x2(y2, y3), pk[e / 2 + 1], pk[17 + e / 2]);
         }
@@ -677,7 +690,7 @@ __device__ void weight_warps(const LinParams& p, Small& s, int w, int lane) {
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.dec_empty);
       // ---- Q S times e^G
-      const float eg = exp2f(G);
+      const float eg = exp2f(whole + part);
       LIN_WAIT(s.inter, n);
       tc_fence_after();
 #pragma unroll 1
@@ -753,9 +766,11 @@ __device__ void value_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
         __syncwarp();
       }
       LIN_WAIT(s.w_full[n & 1], n >> 1);
-      const float* wp = &s.w[n & 1][2 * (lane & 3)];
+      const float* wp = &s.cf[n & 1][2 * (lane & 3)];
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
+        const float e = s.end[n & 1][2 * h + side];
+        const uint64_t e2 = f32x2(e, e);
 #pragma unroll 1
         for (int piece = 0; piece < 2; ++piece) {
           const int t0 = 64 * h + 32 * side + 16 * piece;
@@ -766,7 +781,7 @@ __device__ void value_warps(const LinParams& p, uint8_t* sm, Small& s, int w, in
             uint32_t r[4];
             const int ch = 32 * q + 8 * (lane >> 3);
             ldsm4_trans(v + (ch >> 6) * kPanel + sw128(t0 + 8 * b + (lane & 7), 2 * (ch & 63)), r);
-            const uint64_t f = *reinterpret_cast<const uint64_t*>(wp + t0 + 8 * b);
+            const uint64_t f = mul_f32x2(*reinterpret_cast<const uint64_t*>(wp + t0 + 8 * b), e2);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
               uint64_t y = mul_f32x2(floats(r[m]), f);
