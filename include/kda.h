@@ -539,7 +539,9 @@ kda_status kda_lin_decode(const kda_bf16* q, const int64_t* q_stride, const kda_
  *                contiguous (KDA_ERR_INVALID_ARG where they are not).  NULL without y
  * Outputs must not overlap inputs or one another, but for x_out = x.
  * h is made from x' before x' is rounded to x's type.  Strides are positive whole 16-byte units; width is a
- * multiple of 8, at most 32768 (KDA_ERR_UNSUPPORTED).  Sums of squares are of 32 bits.
+ * multiple of 8, at most 32768 (KDA_ERR_UNSUPPORTED).  Sums of squares are of 32 bits: a row whose sum passes 2^128
+ * is taken for one of infinite norm.  The same call gives the same bits; a row's last bits may depend on how many rows
+ * the call has, since few and many rows take sums and products in other orders.
  */
 enum { KDA_ROWS_BF16 = 0, KDA_ROWS_F32 = 1 };
 kda_status kda_block_norm(const void* x, int x_dtype, int64_t x_stride, const float* weight, const kda_bf16* y,

@@ -1146,7 +1146,8 @@ def block_norm(x, weight=None, y=None, post_norm=False, post_weight=None, gate=N
     x ``[T, W]`` the residual stream, bf16 or fp32; y ``[T, W]`` bf16 the block's output, or None (the
     norm in front of the first block); gate ``[T, W]`` bf16 logits or None; weight, post_weight ``[W]``
     fp32 or None (ones).  Rows may be strided; W a multiple of 8.  Returns ``(h, x')``: h ``[T, W]``
-    bf16; x' of x's type, in ``x_out`` (which may be x) when given, and x itself without y.
+    bf16; x' of x's type, in ``x_out`` (contiguous; may be x) when given, and x itself without y.  A row's last bits
+    may depend on the number of rows in the call.
     """
     try:
         shape, dev, dtype = x.shape, x.get_device(), x.dtype

@@ -30,8 +30,8 @@
 //
 // What bounds it: the chain of a chunk and the issue of the warps around it.  8192 tokens x 96 heads, one block each
 // on 96 of 152 SMs: 196 us, 3 us a chunk, of which the products take 1.9 (tensor pipe 61 %), each scheduler's arithmetic
-// pipes 1.3 and 0.9; 8 heads x 262144 tokens on all SMs: 3.5 us a chunk, 128 KB of it at 5.5 TB/s; with the output
-// stage 3.9 us (12 ragged prompts x 64 heads: 432 us).  Tried and slower than 196 (or 190,
+// pipes 1.2 each; 8 heads x 262144 tokens on all SMs: 3.5 us a chunk, 128 KB of it at 5.5 TB/s; with the output
+// stage 3.9 us (12 ragged prompts x 64 heads: 432 - 441 us).  Tried and slower than 196 (or 190,
 // before the weights' second parts): scores a chunk ahead in columns of their own with a ring of half the size (232),
 // eight warps for weights and outputs (226 - 249), outputs stored from registers (221), loops not unrolled
 // (199 - 587), products issued from rolled loops (212), parts by bf16x2 arithmetic (2 cycles an instruction, like the
@@ -46,7 +46,8 @@
 //
 // Few heads: segments_of's rule cuts a sequence into as many segments as its share of the work is worth
 // in SMs.  A first pass (the same kernel without q and o) leaves each segment's state from zeros, the second
-// begins with the sum over the segments before it.
+// begins with the sum over the segments before it, which it takes one after another: cheap for the 19 segments of
+// 8 heads, but one head of 100000 tokens in the rule's 97 takes 207 us (in 64: 165; 32: 171; 16: 251), 262144 tokens 396.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>

@@ -352,7 +352,8 @@ cudaError_t launch_rows(const NormArgs& a, int num_sms) {
 
 // What both ways took, in us (8192 x 12288 with all parts in bf16; 30001 x 1928 with an fp32 residual, no gate;
 // 4001 x 5128, the norm alone; 1200, 304 and 152 x 4096 with all parts): a row a block 270 / 137 / 42 / 15.5 / 5.0 /
-// 3.4, rows in a line 158 / 110 / 19 / 13 / 5.8 / 4.0.
+// 3.4, rows in a line 158 / 109 / 18 / 13 / 5.8 / 4.0.  Where no line fits, many rows go a row a block (all parts; of what their bytes
+// take at the copy rate: bf16 8192 x 12296 282 us (148), 8192 x 16384 327 (198); fp32 8192 x 12288 223 (208), x 16384 321 (277)).
 cudaError_t launch_block_norm(const NormArgs& a, int num_sms) {
   const int n = a.width >> 3, part_bytes = 16 * ((a.x_f32 ? 2 : 1) + (a.y ? 1 : 0) + (a.gate ? 1 : 0));
   // Blocks of up to 256 threads, several on an SM, whose waits overlap; of up to 512 where only one fits
